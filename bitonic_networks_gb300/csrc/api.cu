@@ -90,18 +90,11 @@ cudaError_t blocks_per_sm(const void *kernel, int threads, size_t smem, int *out
 
 namespace {
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 // Two ranges of `bytes` each: identical, disjoint, or (bad) partially overlapping.
 bool partial_overlap(const void *a, const void *b, size_t bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     if (x == y) return false;
     return x < y + bytes && y < x + bytes;
-}
-
-bool ranges_overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + b_bytes && y < x + a_bytes;
 }
 
 bool overlap(const void *a, const void *b, size_t bytes) { return ranges_overlap(a, bytes, b, bytes); }

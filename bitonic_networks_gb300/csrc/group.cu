@@ -1,0 +1,204 @@
+// group.cu -- stable grouping of (token, slot) pairs by expert: one pass of a
+// counting sort with up to 1024 bins, giving each expert's padded segment.
+//
+// With n the pair's index and e its expert (anything outside [0, E) drops the
+// pair), c_e the expert's pairs and A the alignment:
+//   offsets[e + 1] = offsets[e] + roundup(c_e, A)
+//   positions[n]   = offsets[e] + pairs of e before n   (-1: dropped)
+//   rows[positions[n]] = n, every other entry of rows is -1
+//
+// Up to one tile (4096 pairs): one CTA.  More: a counting kernel, then a
+// placing kernel whose CTAs each add up the counts of the CTAs before them
+// (a few hundred rows of counts, read from L2), so no CTA waits on another.
+// Ranks are warp multisplits (match_any) over consecutive pairs, and every sum
+// is an integer sum: the result does not depend on the order of execution.
+#include <algorithm>
+
+#include "model_ops.cuh"
+
+namespace gsort {
+namespace {
+
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupWarps = kGroupThreads / 32;
+constexpr int kGroupItems = 4;                                   // pairs per thread and tile
+constexpr uint32_t kGroupTile = kGroupThreads * kGroupItems;
+constexpr uint32_t kGroupMaxTiles = 148;   // CTAs of one launch: all resident at once, and a bound on the counts each one reads
+
+struct GroupArgs {
+    const int32_t *experts_in;
+    uint32_t pairs, span;     // pairs per CTA, a multiple of the tile
+    uint32_t experts, align, capacity, tiles;
+    int32_t *offsets, *counts, *rows, *positions;
+    uint32_t *ws;             // [tiles][experts]
+};
+
+__global__ void __launch_bounds__(kGroupThreads) k_group_count(const GroupArgs a) {
+    extern __shared__ uint32_t s_hist[];   // [experts]
+    for (uint32_t e = threadIdx.x; e < a.experts; e += kGroupThreads) s_hist[e] = 0;
+    __syncthreads();
+    const uint32_t begin = blockIdx.x * a.span;
+    const uint32_t end = min(a.pairs, begin + a.span);
+    for (uint32_t n = begin + threadIdx.x; n < end; n += kGroupThreads) {
+        const uint32_t e = static_cast<uint32_t>(a.experts_in[n]);
+        if (e < a.experts) atomicAdd(&s_hist[e], 1u);
+    }
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < a.experts; e += kGroupThreads) a.ws[blockIdx.x * a.experts + e] = s_hist[e];
+}
+
+// Shared memory of the placing kernel: u32 total[E], base[E], scan[33], then
+// u16 counts[warps][E].
+__global__ void __launch_bounds__(kGroupThreads) k_group_place(const GroupArgs a) {
+    extern __shared__ uint32_t s_mem[];
+    uint32_t *s_total = s_mem, *s_base = s_mem + a.experts, *s_scan = s_mem + 2 * a.experts;
+    uint16_t *s_count = reinterpret_cast<uint16_t *>(s_scan + 33);
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t E = a.experts;
+    const uint32_t begin = blockIdx.x * a.span;
+    const uint32_t end = min(a.pairs, begin + a.span);
+
+    for (uint32_t tile = begin;; tile += kGroupTile) {
+        // ranks of the tile's pairs among their expert's pairs in the warp
+        for (uint32_t i = tid; i < E * kGroupWarps / 2; i += kGroupThreads) reinterpret_cast<uint32_t *>(s_count)[i] = 0;
+        __syncthreads();
+        uint32_t key[kGroupItems], rank[kGroupItems];
+        const uint32_t first = tile + warp * (32 * kGroupItems) + lane;
+#pragma unroll
+        for (int i = 0; i < kGroupItems; ++i) {
+            const uint32_t n = first + i * 32;
+            key[i] = n < end ? min(static_cast<uint32_t>(a.experts_in[n]), E) : E;   // E: dropped or beyond the end
+        }
+        uint16_t *count = s_count + warp * E;
+#pragma unroll
+        for (int i = 0; i < kGroupItems; ++i) {
+            const uint32_t peers = __match_any_sync(kFullMask, key[i]);
+            const uint32_t before = __popc(peers & lanemask_lt());
+            const uint32_t had = key[i] < E ? count[key[i]] : 0u;
+            rank[i] = had + before;
+            __syncwarp();
+            if (key[i] < E && before == 0) count[key[i]] = static_cast<uint16_t>(had + __popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        // exclusive scan over the warps, expert by expert
+        uint32_t tile_total = 0;     // of expert `tid`
+        if (tid < E) {
+#pragma unroll 8
+            for (int w = 0; w < kGroupWarps; ++w) {
+                const uint32_t c = s_count[w * E + tid];
+                s_count[w * E + tid] = static_cast<uint16_t>(tile_total);
+                tile_total += c;
+            }
+        }
+        if (tile == begin) {
+            // counts of every expert over all CTAs, and over the CTAs before this one
+            if (a.tiles > 1) {
+                if (tid < E) s_total[tid] = 0, s_base[tid] = 0;
+                __syncthreads();
+                const uint32_t parts = kGroupThreads / E, part = tid / E, e = tid % E;
+                if (part < parts) {
+                    uint32_t total = 0, before = 0;
+#pragma unroll 8
+                    for (uint32_t b = part; b < a.tiles; b += parts) {
+                        const uint32_t c = a.ws[b * E + e];
+                        total += c;
+                        if (b < blockIdx.x) before += c;
+                    }
+                    if (total) atomicAdd(&s_total[e], total);
+                    if (before) atomicAdd(&s_base[e], before);
+                }
+            } else if (tid < E) {
+                s_total[tid] = tile_total;
+                s_base[tid] = 0;
+            }
+            __syncthreads();
+            // padded segments: block-wide exclusive scan, one expert per thread
+            const uint32_t have = tid < E ? s_total[tid] : 0u;
+            const uint32_t padded = (have + a.align - 1) / a.align * a.align;
+            const uint32_t incl = warp_inclusive_scan(padded, lane);
+            if (lane == 31) s_scan[warp] = incl;
+            __syncthreads();
+            if (warp == 0) {
+                const uint32_t v = s_scan[lane];
+                s_scan[lane] = warp_inclusive_scan(v, lane) - v;
+            }
+            __syncthreads();
+            const uint32_t start = s_scan[warp] + incl - padded;
+            if (tid < E) {
+                s_base[tid] += start;
+                if (blockIdx.x == 0) {
+                    a.counts[tid] = static_cast<int32_t>(have);
+                    a.offsets[tid] = static_cast<int32_t>(start);
+                    if (tid == E - 1) a.offsets[E] = static_cast<int32_t>(start + padded);
+                }
+                // padding of this expert's segment
+                if (tid % a.tiles == blockIdx.x)
+                    for (uint32_t p = start + have; p < start + padded; ++p) a.rows[p] = -1;
+                if (tid == E - 1) s_scan[32] = start + padded;
+            }
+            __syncthreads();
+            for (uint32_t p = s_scan[32] + blockIdx.x * kGroupThreads + tid; p < a.capacity; p += a.tiles * kGroupThreads) a.rows[p] = -1;
+        } else {
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < kGroupItems; ++i) {
+            const uint32_t n = first + i * 32;
+            if (n < end) {
+                int32_t p = -1;
+                if (key[i] < E) {
+                    p = static_cast<int32_t>(s_base[key[i]] + count[key[i]] + rank[i]);
+                    a.rows[p] = static_cast<int32_t>(n);
+                }
+                a.positions[n] = p;
+            }
+        }
+        if (tile + kGroupTile >= end) break;   // the same for the whole CTA
+        __syncthreads();
+        if (tid < E) s_base[tid] += tile_total;
+    }
+}
+
+size_t place_smem(uint32_t experts) { return (2 * experts + 33) * 4 + static_cast<size_t>(kGroupWarps) * experts * 2; }
+
+uint32_t group_tiles(uint32_t pairs) {
+    return std::max(1u, std::min(kGroupMaxTiles, (pairs + kGroupTile - 1) / kGroupTile));
+}
+
+}  // namespace
+
+size_t group_workspace_bytes(uint32_t pairs, int experts) {
+    const uint32_t tiles = group_tiles(pairs);
+    return tiles > 1 ? static_cast<size_t>(tiles) * experts * 4 : 0;
+}
+
+int launch_group(const GroupLaunch &L) {
+    GroupArgs a{};
+    a.experts_in = L.experts_in;
+    a.pairs = L.pairs;
+    a.experts = L.experts;
+    a.align = L.align;
+    a.capacity = L.capacity;
+    a.offsets = L.offsets;
+    a.counts = L.counts;
+    a.rows = L.rows;
+    a.positions = L.positions;
+    a.ws = L.ws;
+    const uint32_t most = group_tiles(L.pairs);
+    const uint32_t per = (L.pairs + most - 1) / most;
+    a.span = std::max(kGroupTile, (per + kGroupTile - 1) / kGroupTile * kGroupTile);
+    a.tiles = std::max(1u, (L.pairs + a.span - 1) / a.span);
+    // the limit is the kernel's largest need: it is set once, for every number of experts
+    if (set_smem_limit(reinterpret_cast<const void *>(&k_group_place), place_smem(GSORT_ROUTE_MAX_EXPERTS)) != cudaSuccess)
+        return GSORT_ECUDA;
+    const size_t smem = place_smem(a.experts);
+    if (a.tiles > 1) {
+        k_group_count<<<a.tiles, kGroupThreads, a.experts * 4, L.stream>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
+    }
+    k_group_place<<<a.tiles, kGroupThreads, smem, L.stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? GSORT_OK : GSORT_ECUDA;
+}
+
+}  // namespace gsort

@@ -162,6 +162,14 @@ cudaError_t blocks_per_sm(const void *kernel, int threads, size_t smem, int *out
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Argument checks shared by the entry points.
+inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+inline bool ranges_overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
 // ------------------------------------------------------------ launch plans
 // Order map of a key kind and direction: ordered = (float ? float_map(bits)
 // : bits) ^ flip, on key words of key_bytes bytes.

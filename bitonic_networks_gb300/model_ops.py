@@ -1,0 +1,309 @@
+"""torch-facing wrappers of libgsort's language-model operators (argument
+marshalling only): routing to experts, grouping by expert, moving rows to the
+experts and back, and log probabilities of given tokens, with their gradients.
+
+Every call takes CUDA tensors (there is no CPU fallback), runs on the current
+stream of their device without synchronising, and returns newly allocated
+tensors unless an output is given.  Activations and logits are float32,
+bfloat16 or float16; all arithmetic is in 32 bits.  Rows may be strided
+(tensor[:, :n] of a wider tensor); the elements of a row are consecutive.
+Arguments of a wrong type or shape raise TypeError or ValueError, what the
+library refuses raises GsortError.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import _lib
+from .gsort import GsortError, _workspace
+
+_FLOATS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+
+
+class ExpertGroups(NamedTuple):
+    """Pairs (token, slot), numbered token * slots + slot, grouped by expert.
+
+    offsets    [experts + 1] int32  first row of each expert's segment, a multiple of the alignment
+    counts     [experts] int32      pairs of each expert
+    rows       [capacity] int32     the pair in each row of the layout, -1 where there is none
+    positions  [tokens, slots] int32  each pair's row, -1 for a dropped pair
+    """
+    offsets: torch.Tensor
+    counts: torch.Tensor
+    rows: torch.Tensor
+    positions: torch.Tensor
+
+
+class TokenLogprobs(NamedTuple):
+    """logprobs [rows] and entropy [rows] float32; top_logprobs and top_ids
+    [rows, top] (None without alternatives); stats [rows, 2] float32: each
+    row's largest logit and its sum of exponentials relative to it."""
+    logprobs: torch.Tensor | None
+    entropy: torch.Tensor
+    top_logprobs: torch.Tensor | None
+    top_ids: torch.Tensor | None
+    stats: torch.Tensor
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name: str, device: torch.device, *args):
+    """Calls the entry point on the device's current stream."""
+    fn = getattr(_lib.load(), name)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise GsortError(rc, name)
+
+
+def _rows2d(t: torch.Tensor, name: str) -> int:
+    """Checks a 2-D float CUDA tensor with consecutive row elements; returns its dtype code."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _FLOATS.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the elements of a row of {name} must be consecutive")
+    return code
+
+
+def _flat(t: torch.Tensor, name: str, dtype, shape, device):
+    """Checks a contiguous tensor of the given dtype and shape on the device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _choice(value, table, name):
+    code = table.get(value)
+    if code is None:
+        raise ValueError(f"{name} must be one of {', '.join(table)}, got {value!r}")
+    return code
+
+
+def _stride(t: torch.Tensor) -> int:
+    # the stride of a tensor with one row (or none) means nothing
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+# ----------------------------------------------------------------- routing
+def route_experts(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None,
+                  score: str = "softmax", groups: int = 1, groups_kept: int | None = None,
+                  group_score: str = "max", renormalise: bool = False, scale: float = 1.0):
+    """Chooses k experts for every token from router logits [tokens, experts].
+
+    Scores are a softmax over the experts or a sigmoid each; `bias` [experts]
+    float32 is added to the scores for the choice alone; with groups > 1 only
+    experts of the groups_kept best groups (by their largest choice value, or
+    the sum of their two largest scores) can be chosen.  Experts with a logit
+    of -inf or NaN are never chosen.  Returns (weights [tokens, k] float32,
+    experts [tokens, k] int32), best first and ties to the lower index; a token
+    with fewer candidates has experts -1 with weight 0."""
+    code = _rows2d(logits, "logits")
+    tokens, experts = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _flat(bias, "bias", torch.float32, (experts,), dev)
+    k = int(k)
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
+    chosen = torch.empty((tokens, k), dtype=torch.int32, device=dev)
+    _call("gsort_route_experts", dev, logits.data_ptr(), code, tokens, experts, _stride(logits),
+          _ptr(bias), _choice(score, _SCORES, "score"), groups, groups if groups_kept is None else groups_kept,
+          _choice(group_score, _GROUP_SCORES, "group_score"), k, 1 if renormalise else 0, scale,
+          weights.data_ptr(), chosen.data_ptr())
+    return weights, chosen
+
+
+def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, *,
+                           score: str = "softmax", renormalise: bool = False,
+                           scale: float = 1.0) -> torch.Tensor:
+    """Gradient of route_experts' weights by the logits, for the experts it
+    chose; [tokens, experts] of the logits' dtype."""
+    code = _rows2d(logits, "logits")
+    tokens, number = logits.shape
+    dev = logits.device
+    if experts.dim() != 2:
+        raise ValueError("experts must have two dimensions")
+    k = experts.shape[1]
+    _flat(experts, "experts", torch.int32, (tokens, k), dev)
+    _flat(d_weights, "d_weights", torch.float32, (tokens, k), dev)
+    out = torch.empty((tokens, number), dtype=logits.dtype, device=dev)
+    _call("gsort_route_experts_backward", dev, d_weights.data_ptr(), logits.data_ptr(), code, tokens,
+          number, _stride(logits), experts.data_ptr(), k, _choice(score, _SCORES, "score"),
+          1 if renormalise else 0, scale, out.data_ptr())
+    return out
+
+
+# ---------------------------------------------------- grouping and row moves
+def group_capacity(pairs: int, num_experts: int, align: int = 1) -> int:
+    """Rows of the grouped layout that any choice of experts fits into."""
+    return int(_lib.load().gsort_group_capacity(pairs, num_experts, align))
+
+
+def group_workspace_bytes(pairs: int, num_experts: int) -> int:
+    return int(_lib.load().gsort_group_workspace_bytes(pairs, num_experts))
+
+
+def group_by_expert(experts: torch.Tensor, num_experts: int, *, align: int = 1,
+                    workspace: torch.Tensor | None = None) -> ExpertGroups:
+    """Stable grouping of the pairs of experts [tokens, slots] int32 by expert,
+    each expert's segment starting at a multiple of `align`.  Pairs whose expert
+    is not in 0..num_experts-1 are dropped."""
+    if not experts.is_cuda:
+        raise ValueError("experts must be a CUDA tensor")
+    if experts.dim() != 2:
+        raise ValueError("experts must have two dimensions")
+    dev = experts.device
+    _flat(experts, "experts", torch.int32, experts.shape, dev)
+    lib = _lib.load()
+    pairs = experts.numel()
+    capacity = lib.gsort_group_capacity(pairs, num_experts, align)
+    nbytes = lib.gsort_group_workspace_bytes(pairs, num_experts)
+    ws = _workspace(nbytes, dev, workspace) if nbytes else None
+    offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int32, device=dev)
+    counts = torch.empty(max(num_experts, 0), dtype=torch.int32, device=dev)
+    rows = torch.empty(capacity, dtype=torch.int32, device=dev)
+    positions = torch.empty_like(experts)
+    _call("gsort_group_by_expert", dev, experts.data_ptr(), pairs, num_experts, align, offsets.data_ptr(),
+          counts.data_ptr(), rows.data_ptr(), capacity, positions.data_ptr(), _ptr(ws),
+          ws.numel() * ws.element_size() if ws is not None else 0)
+    return ExpertGroups(offsets, counts, rows, positions)
+
+
+def _layout(groups: ExpertGroups, device):
+    tokens, k = groups.positions.shape
+    capacity = groups.rows.shape[0]
+    _flat(groups.positions, "groups.positions", torch.int32, (tokens, k), device)
+    _flat(groups.rows, "groups.rows", torch.int32, (capacity,), device)
+    return tokens, k, capacity
+
+
+def dispatch_rows(x: torch.Tensor, groups: ExpertGroups) -> torch.Tensor:
+    """Copies each token's row of x [tokens, width] to its pairs' rows of the
+    grouped layout; rows without a pair are zero.  Returns [capacity, width]."""
+    code = _rows2d(x, "x")
+    dev = x.device
+    tokens, k, capacity = _layout(groups, dev)
+    if x.shape[0] != tokens:
+        raise ValueError(f"x must have {tokens} rows, got {x.shape[0]}")
+    out = torch.empty((capacity, x.shape[1]), dtype=x.dtype, device=dev)
+    _call("gsort_dispatch_rows", dev, x.data_ptr(), code, tokens, x.shape[1], _stride(x),
+          groups.positions.data_ptr(), k, groups.rows.data_ptr(), capacity, out.data_ptr())
+    return out
+
+
+def combine_rows(y: torch.Tensor, groups: ExpertGroups, weights: torch.Tensor | None = None) -> torch.Tensor:
+    """Sums each token's rows of y [capacity, width] in the grouped layout, with
+    weights [tokens, slots] float32 (None: ones, dispatch_rows' gradient).
+    Dropped pairs add nothing.  Returns [tokens, width]."""
+    code = _rows2d(y, "y")
+    dev = y.device
+    tokens, k, capacity = _layout(groups, dev)
+    if y.shape[0] != capacity:
+        raise ValueError(f"y must have {capacity} rows, got {y.shape[0]}")
+    if weights is not None:
+        _flat(weights, "weights", torch.float32, (tokens, k), dev)
+    out = torch.empty((tokens, y.shape[1]), dtype=y.dtype, device=dev)
+    _call("gsort_combine_rows", dev, y.data_ptr(), code, capacity, y.shape[1], _stride(y), _ptr(weights),
+          groups.positions.data_ptr(), tokens, k, out.data_ptr())
+    return out
+
+
+def combine_rows_backward(d_out: torch.Tensor, y: torch.Tensor, groups: ExpertGroups, weights: torch.Tensor):
+    """Gradients of combine_rows by y and by the weights: (d_y [capacity,
+    width], zero where a row holds no pair; d_weights [tokens, slots])."""
+    code = _rows2d(d_out, "d_out")
+    dev = d_out.device
+    if _rows2d(y, "y") != code:
+        raise TypeError("d_out and y must have one dtype")
+    tokens, k, capacity = _layout(groups, dev)
+    if tuple(d_out.shape) != (tokens, y.shape[1]) or y.shape[0] != capacity or y.device != dev:
+        raise ValueError("d_out must be [tokens, width] and y [capacity, width] on one device")
+    _flat(weights, "weights", torch.float32, (tokens, k), dev)
+    d_y = torch.empty((capacity, y.shape[1]), dtype=y.dtype, device=dev)
+    d_weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
+    _call("gsort_combine_rows_backward", dev, d_out.data_ptr(), code, tokens, y.shape[1], _stride(d_out),
+          y.data_ptr(), capacity, _stride(y), weights.data_ptr(), groups.positions.data_ptr(), k,
+          groups.rows.data_ptr(), d_y.data_ptr(), d_weights.data_ptr())
+    return d_y, d_weights
+
+
+# ------------------------------------------------------- log probabilities
+def _targets(targets, rows, device):
+    if targets is None:
+        return None, 0
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"targets must be int32 or int64, got {targets.dtype}")
+    _flat(targets, "targets", targets.dtype, (rows,), device)
+    return targets.data_ptr(), targets.element_size()
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, *, top: int = 0) -> TokenLogprobs:
+    """Log probabilities of targets [rows] under softmax(logits [rows, vocab]),
+    each row's entropy, and its `top` (at most 32) most likely tokens, from one
+    read of the logits.  Logits of -inf are masked.  A negative target gives 0,
+    one beyond the vocabulary NaN; alternatives come best first, ties to the
+    lower index, with -inf and -1 where a row has too few unmasked logits."""
+    code = _rows2d(logits, "logits")
+    rows, vocab = logits.shape
+    dev = logits.device
+    at, size = _targets(targets, rows, dev)
+    if top < 0:
+        raise ValueError("top must not be negative")
+    lp = None if targets is None else torch.empty(rows, dtype=torch.float32, device=dev)
+    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+    stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    top_lp = torch.empty((rows, top), dtype=torch.float32, device=dev) if top else None
+    top_ids = torch.empty((rows, top), dtype=torch.int32, device=dev) if top else None
+    _call("gsort_token_logprobs", dev, logits.data_ptr(), code, rows, vocab, _stride(logits), at, size, top,
+          _ptr(lp), entropy.data_ptr(), stats.data_ptr(), _ptr(top_lp), _ptr(top_ids))
+    return TokenLogprobs(lp, entropy, top_lp, top_ids, stats)
+
+
+def token_logprobs_backward(d_logprobs: torch.Tensor | None, d_entropy: torch.Tensor | None,
+                            logits: torch.Tensor, targets: torch.Tensor | None, result: TokenLogprobs, *,
+                            out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient by the logits of sum(d_logprobs * logprobs + d_entropy *
+    entropy), [rows, vocab] of the logits' dtype; `result` is the forward
+    call's.  `out` may be the logits themselves.  Without it the gradient's rows
+    are laid out as the logits' are."""
+    code = _rows2d(logits, "logits")
+    rows, vocab = logits.shape
+    dev = logits.device
+    at, size = _targets(targets, rows, dev)
+    if d_logprobs is not None:
+        if targets is None:
+            raise ValueError("d_logprobs needs targets")
+        _flat(d_logprobs, "d_logprobs", torch.float32, (rows,), dev)
+    if d_entropy is not None:
+        _flat(d_entropy, "d_entropy", torch.float32, (rows,), dev)
+    _flat(result.entropy, "result.entropy", torch.float32, (rows,), dev)
+    _flat(result.stats, "result.stats", torch.float32, (rows, 2), dev)
+    if out is None:
+        out = torch.empty((rows, _stride(logits)), dtype=logits.dtype, device=dev)[:, :vocab]
+    elif _rows2d(out, "out") != code or out.shape != logits.shape or out.device != dev:
+        raise ValueError("out must have the logits' dtype, shape and device")
+    _call("gsort_token_logprobs_backward", dev, _ptr(d_logprobs), _ptr(d_entropy), logits.data_ptr(), code,
+          rows, vocab, _stride(logits), at, size, result.entropy.data_ptr(), result.stats.data_ptr(),
+          out.data_ptr(), _stride(out))
+    return out

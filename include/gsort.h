@@ -1,6 +1,7 @@
 /*
  * gsort.h -- C ABI of libgsort.so: GB300 (sm_103a) stable LSD radix sort,
- * stream compaction and segmented bitonic sort.
+ * stream compaction, segmented bitonic sort, and the selection and grouping
+ * operators of language models (expert routing, token log probabilities).
  *
  * Sources of the operations (reference pages, by title and section):
  *   [PMPP10]  "Parallel Patterns: Sorting on the GPU" (textbook chapter 10):
@@ -304,6 +305,146 @@ int gsort_segmented_sort(const void *d_keys_in, void *d_keys_out,
                          const uint32_t *d_offsets, int64_t num_segments,
                          int kind, int flags, void *d_ws, size_t ws_bytes,
                          cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Language-model operators: the selection, grouping and row moves around a
+ * layer of experts, and the selection over a model's output.
+ *
+ * Element types of activations and logits; arithmetic and sums are in 32
+ * bits whatever the type, rounded once when stored.  Pointers are aligned to
+ * their element (else GSORT_EALIGN); rows and bases that are also 16-byte
+ * aligned move as 16-byte vectors.  Strides count elements, from one row to
+ * the next; elements of a row are consecutive.  A count of zero rows is a
+ * no-op returning GSORT_OK.  Outputs must not overlap inputs or each other
+ * (GSORT_EINVAL), except where a call allows it.  Indices that the device
+ * reads (experts, positions, targets) are checked there: one outside its
+ * range takes no part, as each call states, and touches no memory.
+ * ---------------------------------------------------------------------- */
+typedef enum gsort_float {
+    GSORT_F32 = 0,
+    GSORT_BF16 = 1,
+    GSORT_F16 = 2
+} gsort_float;
+
+/* Routing of tokens to experts.  Per token, with logits x of `experts`
+ * experts (1..GSORT_ROUTE_MAX_EXPERTS):
+ *   candidates  experts whose logit is above -inf (masked and NaN are none)
+ *   score s     GSORT_SCORE_SOFTMAX: softmax over the candidates;
+ *               GSORT_SCORE_SIGMOID: 1 / (1 + exp(-x))
+ *   choice c    x if d_bias is NULL (s grows with x), else s + d_bias[e]; an
+ *               expert whose choice value is -inf or NaN is no candidate
+ *   groups      groups > 1 (a divisor of experts, at most 32): consecutive
+ *               experts form groups of equal size; a group's value is
+ *               GSORT_GROUP_MAX: its largest c, or GSORT_GROUP_TOP2: the sum
+ *               of its two largest s (+ bias); experts outside the
+ *               groups_kept best groups are no candidates
+ *   chosen      the `chosen` (1..GSORT_ROUTE_MAX_CHOSEN, at most experts)
+ *               largest c in descending order; ties, here and between groups,
+ *               go to the lower index
+ *   weight      scale * s, or with renormalise != 0 scale * s / (sum of the
+ *               chosen s)
+ * d_weights and d_experts are [tokens][chosen]; where a token has fewer
+ * candidates, the rest are expert -1 with weight 0. */
+#define GSORT_SCORE_SOFTMAX 0
+#define GSORT_SCORE_SIGMOID 1
+#define GSORT_GROUP_MAX 0
+#define GSORT_GROUP_TOP2 1
+#define GSORT_ROUTE_MAX_EXPERTS 1024
+#define GSORT_ROUTE_MAX_CHOSEN 32
+
+int gsort_route_experts(const void *d_logits, int dtype, int64_t tokens, int experts,
+                        int64_t row_stride, const float *d_bias, int score, int groups,
+                        int groups_kept, int group_score, int chosen, int renormalise, float scale,
+                        float *d_weights, int32_t *d_experts, cudaStream_t stream);
+
+/* Gradient of the weights by the logits, for the chosen experts given: the
+ * choice, the groups and the bias have none.  d_grad_logits is contiguous
+ * [tokens][experts] of the logits' type and is written whole.  A token's
+ * experts are distinct (or outside the range: no part). */
+int gsort_route_experts_backward(const float *d_grad_weights, const void *d_logits, int dtype,
+                                 int64_t tokens, int experts, int64_t row_stride,
+                                 const int32_t *d_experts, int chosen, int score, int renormalise,
+                                 float scale, void *d_grad_logits, cudaStream_t stream);
+
+/* Stable grouping of (token, slot) pairs by expert.  With pair n's expert
+ * e = d_experts[n] (outside 0..experts-1: the pair is dropped) and c_e pairs
+ * of expert e:
+ *   d_counts[e] = c_e                                       experts entries
+ *   d_offsets[0] = 0, d_offsets[e + 1] = d_offsets[e] + c_e rounded up to a
+ *                 multiple of align                          experts + 1 entries
+ *   d_positions[n] = d_offsets[e] + pairs of e before n; -1: dropped
+ *   d_rows[d_positions[n]] = n, every other entry -1        capacity entries
+ * capacity = gsort_group_capacity(), the most rows that any experts can need
+ * (0 where an argument is out of range or the result exceeds GSORT_MAX_N).
+ * The workspace comes from gsort_group_workspace_bytes() and may be NULL where
+ * that is 0. */
+int64_t gsort_group_capacity(int64_t pairs, int experts, int align);
+size_t gsort_group_workspace_bytes(int64_t pairs, int experts);
+
+int gsort_group_by_expert(const int32_t *d_experts, int64_t pairs, int experts, int align,
+                          int32_t *d_offsets, int32_t *d_counts, int32_t *d_rows, int64_t capacity,
+                          int32_t *d_positions, void *d_ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Rows to the experts and back.  `width` elements to a row, `chosen` slots to
+ * a token, positions and rows as gsort_group_by_expert gives them (a position
+ * outside 0..capacity-1 takes no part).  Outputs are contiguous.
+ *   dispatch          d_out[positions[t][j]] = d_x[t]; rows that no pair
+ *                     holds (d_rows < 0) are zero
+ *   combine           d_out[t] = sum over j of weights[t][j] *
+ *                     d_y[positions[t][j]]; d_weights NULL: ones.  With ones
+ *                     it is dispatch's gradient.
+ *   combine_backward  d_grad_y[positions[t][j]] = weights[t][j] *
+ *                     d_grad_out[t], rows that no pair holds are zero;
+ *                     d_grad_weights[t][j] = sum of d_grad_out[t] *
+ *                     d_y[positions[t][j]] (0 without a position) */
+int gsort_dispatch_rows(const void *d_x, int dtype, int64_t tokens, int64_t width, int64_t row_stride,
+                        const int32_t *d_positions, int chosen, const int32_t *d_rows,
+                        int64_t capacity, void *d_out, cudaStream_t stream);
+
+int gsort_combine_rows(const void *d_y, int dtype, int64_t capacity, int64_t width, int64_t row_stride,
+                       const float *d_weights, const int32_t *d_positions, int64_t tokens, int chosen,
+                       void *d_out, cudaStream_t stream);
+
+int gsort_combine_rows_backward(const void *d_grad_out, int dtype, int64_t tokens, int64_t width,
+                                int64_t grad_stride, const void *d_y, int64_t capacity,
+                                int64_t row_stride, const float *d_weights,
+                                const int32_t *d_positions, int chosen, const int32_t *d_rows,
+                                void *d_grad_y, float *d_grad_weights, cudaStream_t stream);
+
+/* Log probabilities of given tokens.  Per row of `vocab` logits x (1 ..
+ * GSORT_MAX_N; -inf: masked):
+ *   d_logprobs[r]      log softmax(x) at d_targets[r] (4- or 8-byte signed
+ *                      integers, target_bytes); 0 for a negative target, NaN
+ *                      for one beyond the vocabulary, -inf for a masked one;
+ *                      both pointers NULL: not wanted
+ *   d_entropy[r]       - sum of p log p (NULL: not wanted)
+ *   d_stats[r][2]      max x and sum of exp(x - max x): the log of the sum of
+ *                      exponentials is max + log(sum)
+ *   d_top_logprobs[r][top], d_top_ids[r][top]   the `top` (0 ..
+ *                      GSORT_LOGPROBS_MAX_TOP) largest logits' log
+ *                      probabilities and indices, descending, ties to the
+ *                      lower index; -inf and -1 where a row has fewer logits
+ *                      above -inf
+ * A row that is masked whole has log probabilities -inf and entropy 0.  A row
+ * with NaN or +inf has NaN results (NaN is no alternative). */
+#define GSORT_LOGPROBS_MAX_TOP 32
+
+int gsort_token_logprobs(const void *d_logits, int dtype, int64_t rows, int64_t vocab,
+                         int64_t row_stride, const void *d_targets, int target_bytes, int top,
+                         float *d_logprobs, float *d_entropy, float *d_stats, float *d_top_logprobs,
+                         int32_t *d_top_ids, cudaStream_t stream);
+
+/* Gradient by the logits of sum over rows of grad_logprobs[r] * logprobs[r] +
+ * grad_entropy[r] * entropy[r] (either gradient may be NULL: zeros), from the
+ * forward call's entropy and stats.  d_grad_logits has rows grad_stride apart;
+ * it may be the logits themselves (same pointer and stride).  A row without a
+ * target takes no part through its log probability; a row that is masked whole
+ * gets zeros. */
+int gsort_token_logprobs_backward(const float *d_grad_logprobs, const float *d_grad_entropy,
+                                  const void *d_logits, int dtype, int64_t rows, int64_t vocab,
+                                  int64_t row_stride, const void *d_targets, int target_bytes,
+                                  const float *d_entropy, const float *d_stats, void *d_grad_logits,
+                                  int64_t grad_stride, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Device-side status: synchronises `stream`, then returns GSORT_OK or the

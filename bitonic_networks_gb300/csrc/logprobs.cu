@@ -22,12 +22,20 @@
 namespace gsort {
 namespace {
 
-constexpr int kLpThreads = 512;
+#ifndef LP_THREADS
+#define LP_THREADS 256
+#define LP_VECTORS 4
+#define LP_CTAS 4
+#endif
+constexpr int kLpThreads = LP_THREADS;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpVectors = 4;              // 16-byte vectors per thread and step
+constexpr int kLpVectors = LP_VECTORS;     // 16-byte vectors per thread and step
+constexpr int kLpCtas = LP_CTAS;           // CTAs per SM that the registers allow
 constexpr uint32_t kLpStep = kLpThreads * kLpVectors;
+constexpr int kGroupLanes = kLpThreads / 32;   // 32 groups of lanes give the first threshold
 constexpr uint32_t kCandidates = 2048;     // shared buffer of candidates
 constexpr int kMaxCluster = 8;
+constexpr float kLowLogit = -1e37f;        // x - max above it: the exponent does not overflow
 constexpr float kTinyExponent = -256.0f;   // 2^-256 is 0 in 32 bits: masked logits add e^d * d = 0 * -256
 
 // A candidate: order key of the logit, then the lower index first.
@@ -84,23 +92,10 @@ __device__ __forceinline__ void rescale(RowSums &s, float to) {
     s.max = to;
 }
 
-__device__ __forceinline__ RowSums join(RowSums a, RowSums b) {
-    const float m = fmaxf(a.max, b.max);
-    rescale(a, m);
-    rescale(b, m);
-    return {m, a.sum + b.sum, a.dot + b.dot};
-}
-
+// Sums over the lanes of a warp: all to the largest maximum, then added.
 __device__ __forceinline__ RowSums warp_join(RowSums s) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        RowSums t;
-        t.max = __shfl_xor_sync(kFullMask, s.max, o);
-        t.sum = __shfl_xor_sync(kFullMask, s.sum, o);
-        t.dot = __shfl_xor_sync(kFullMask, s.dot, o);
-        s = join(s, t);
-    }
-    return s;
+    rescale(s, order_key_value(__reduce_max_sync(kFullMask, order_key(s.max))));
+    return {s.max, warp_sum(s.sum), warp_sum(s.dot)};
 }
 
 // Two 32-bit numbers that move through one packed instruction.
@@ -150,11 +145,12 @@ struct ThreadSums {
         dot = pair(a.dot, b.dot);
     }
 
-    template <int N> __device__ __forceinline__ void add(const float (&x)[N]) {
+    // low: some logit is so low that its exponent needs the bound
+    template <int N> __device__ __forceinline__ void add(const float (&x)[N], bool low) {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
             Pair y = mul2(add2(pair(x[i], x[i + 1]), minus), pair(kLog2e, kLog2e));
-            y = pair(max_nan(y.f.x, kTinyExponent), max_nan(y.f.y, kTinyExponent));
+            if (low) y = pair(max_nan(y.f.x, kTinyExponent), max_nan(y.f.y, kTinyExponent));
             const Pair e = pair(exp2_approx(y.f.x), exp2_approx(y.f.y));
             sum = add2(sum, e);
             dot = fma2(e, y, dot);
@@ -194,6 +190,11 @@ template <typename T> struct RowView {
         vectors = (end + N - 1) / N;
     }
 
+    __device__ __forceinline__ typename Wide<T>::type load_full(uint32_t v) const {
+        const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(row - shift) + v);
+        return *reinterpret_cast<const typename Wide<T>::type *>(&q);
+    }
+
     // Vector v, -inf where it is not of the row or not below `last`.
     __device__ __forceinline__ typename Wide<T>::type load(uint32_t v, uint32_t last) const {
         using V = typename Wide<T>::type;
@@ -214,12 +215,40 @@ template <typename T> struct RowView {
     }
 };
 
+// Largest and smallest of a vector's logits, NaN left out.
+template <typename T> __device__ __forceinline__ float2 vector_range(const typename Wide<T>::type &v) {
+    float lo = to_f32(v.e[0]), hi = lo;
+#pragma unroll
+    for (int i = 1; i < Wide<T>::kCount; ++i) {
+        const float x = to_f32(v.e[i]);
+        lo = fminf(lo, x);
+        hi = fmaxf(hi, x);
+    }
+    return make_float2(lo, hi);
+}
+
+// 16-bit types: two at a time, before they are widened.
+template <> __device__ __forceinline__ float2 vector_range<__nv_bfloat16>(const Wide<__nv_bfloat16>::type &v) {
+    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&v);
+    const __nv_bfloat162 lo = __hmin2(__hmin2(p[0], p[1]), __hmin2(p[2], p[3]));
+    const __nv_bfloat162 hi = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+    return make_float2(fminf(to_f32(lo.x), to_f32(lo.y)), fmaxf(to_f32(hi.x), to_f32(hi.y)));
+}
+
+template <> __device__ __forceinline__ float2 vector_range<__half>(const Wide<__half>::type &v) {
+    const __half2 *p = reinterpret_cast<const __half2 *>(&v);
+    const __half2 lo = __hmin2(__hmin2(p[0], p[1]), __hmin2(p[2], p[3]));
+    const __half2 hi = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+    return make_float2(fminf(to_f32(lo.x), to_f32(lo.y)), fmaxf(to_f32(hi.x), to_f32(hi.y)));
+}
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsArgs a) {
+__global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const LogprobsArgs a) {
     constexpr int N = Wide<T>::kCount;
     using V = typename Wide<T>::type;
     __shared__ RowSums s_sums[kLpWarps], s_cluster[kMaxCluster];
-    __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];        // warps' lists, and half-warp maxima
+    __shared__ uint32_t s_group[32];                           // the groups' largest keys
+    __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];        // the warps' lists
     __shared__ uint64_t s_remote[TOP ? kMaxCluster : 1][32];   // the cluster's lists
     __shared__ uint64_t s_buffer[TOP ? kCandidates : 1];
     __shared__ uint32_t s_count;
@@ -231,8 +260,9 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsArgs a) {
     if (a.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
     const RowView<T> view(static_cast<const T *>(a.logits) + row * a.row_stride, a.vocab);
-    const uint32_t per = (view.vectors + a.split - 1) / a.split;
-    const uint32_t first = part * per, last = min(view.vectors, first + per);
+    const uint32_t full = view.full_end > view.full_begin ? view.full_end - view.full_begin : 0;
+    const uint32_t per = (full + a.split - 1) / a.split;
+    const uint32_t first = view.full_begin + min(full, part * per), last = view.full_begin + min(full, (part + 1) * per);
 
     float given = kNegInf;
     int64_t target = -1;
@@ -244,7 +274,10 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsArgs a) {
     ThreadSums mine;
     float threshold = kNegInf;
     uint64_t kept = 0;           // warp 0: the running list of the row's part, descending
-    if (TOP && tid == 0) s_count = 0;
+    if (TOP) {
+        if (tid == 0) s_count = 0;
+        __syncthreads();
+    }
 
     // sorts the buffer (and, where it overflowed, the candidates still held in
     // registers, given by `more`) into warp 0's list
@@ -275,89 +308,100 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const LogprobsArgs a) {
         threshold = s_threshold;
     };
 
-    V next[kLpVectors];
-#pragma unroll
-    for (int u = 0; u < kLpVectors; ++u) next[u] = view.load(first + u * kLpThreads + tid, last);
     for (uint32_t base = first; base < last; base += kLpStep) {
         V now[kLpVectors];
-#pragma unroll
-        for (int u = 0; u < kLpVectors; ++u) now[u] = next[u];
-        if (base + kLpStep < last) {
-#pragma unroll
-            for (int u = 0; u < kLpVectors; ++u) next[u] = view.load(base + kLpStep + u * kLpThreads + tid, last);
-        }
         const uint32_t v0 = base + tid;
-        uint64_t floor64 = 1;    // every candidate
-        if (TOP && base == first) {
-            // the largest candidate of each half warp; `top` of those 32 reach their top-th
-            uint64_t c = 0;
-#pragma unroll
-            for (int u = 0; u < kLpVectors; ++u)
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float x = to_f32(now[u].e[i]);
-                    if (x > kNegInf) c = max64(c, candidate(x, (v0 + u * kLpThreads) * N + i - view.shift));
-                }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) c = max64(c, __shfl_xor_sync(kFullMask, c, o));
-            if ((lane & 15) == 0) s_list[0][tid >> 4] = c;
-            __syncthreads();
-            c = bitonic_sort_desc(s_list[0][lane], lane);
-            floor64 = __shfl_sync(kFullMask, c, a.top - 1);
-            threshold = kNegInf;
-            __syncthreads();     // s_list is used again
-        }
-        uint32_t held = 0;       // candidates of this step that found a place in the buffer
-        bool full = false;
 #pragma unroll
         for (int u = 0; u < kLpVectors; ++u) {
+            if (v0 + u * kLpThreads < last) {
+                now[u] = view.load_full(v0 + u * kLpThreads);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) now[u].e[i] = neg_inf<T>();
+            }
+        }
+        float bound = threshold;     // candidates are above it
+        if (TOP && base == first) {
+            // the largest logit of each of 32 groups of threads: `top` logits reach their top-th
+            float hi = kNegInf;
+#pragma unroll
+            for (int u = 0; u < kLpVectors; ++u) hi = fmaxf(hi, vector_range<T>(now[u]).y);
+#pragma unroll
+            for (int o = kGroupLanes / 2; o > 0; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, o));
+            if (tid % kGroupLanes == 0) s_group[tid / kGroupLanes] = hi > kNegInf ? order_key(hi) : 0u;
+            __syncthreads();
+            const uint32_t key = s_group[lane];
+            uint32_t rank = 0;       // groups before this one
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t o = __shfl_sync(kFullMask, key, i);
+                rank += (o > key || (o == key && i < lane)) ? 1u : 0u;
+            }
+            const uint32_t cut = __reduce_max_sync(kFullMask, rank == static_cast<uint32_t>(a.top - 1) ? key : 0u);
+            // logits of this step that equal it may belong to the best; later ones have
+            // higher indices: only a greater logit displaces one of this step
+            threshold = cut ? order_key_value(cut) : kNegInf;
+            bound = cut ? order_key_value(cut - (cut == 0x80000000u ? 2u : 1u)) : kNegInf;   // the key below zero's is unused
+        }
+        uint32_t held = 0;       // candidates of this step that found a place in the buffer
+        bool full_buffer = false;
+#pragma unroll
+        for (int u = 0; u < kLpVectors; ++u) {
+            const float2 range = vector_range<T>(now[u]);
+            if (range.y > mine.max) mine.raise(range.y);
             float x[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) x[i] = to_f32(now[u].e[i]);
-            float vmax = x[0];
-#pragma unroll
-            for (int i = 1; i < N; ++i) vmax = fmaxf(vmax, x[i]);
-            if (vmax > mine.max) mine.raise(vmax);
-            mine.add<N>(x);
-            if (TOP && vmax > threshold) {
+            if (range.x - mine.max > kLowLogit) mine.template add<N>(x, false);
+            else mine.template add<N>(x, true);
+            if (TOP && range.y > bound) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    if (x[i] > threshold) {
-                        const uint64_t c = candidate(x[i], (v0 + u * kLpThreads) * N + i - view.shift);
-                        if (c >= floor64) {
-                            const uint32_t at = atomicAdd(&s_count, 1u);
-                            if (at < kCandidates) {
-                                s_buffer[at] = c;
-                                held |= 1u << (u * N + i);
-                            }
-                            full |= at >= kCandidates / 2;
+                    if (x[i] > bound) {
+                        const uint32_t at = atomicAdd(&s_count, 1u);
+                        if (at < kCandidates) {
+                            s_buffer[at] = candidate(x[i], (v0 + u * kLpThreads) * N + i - view.shift);
+                            held |= 1u << (u * N + i);
                         }
+                        full_buffer |= at >= kCandidates / 2;
                     }
                 }
             }
         }
-        if (TOP) {
-            if (__syncthreads_or(full)) {
-                const bool over = s_count > kCandidates;
-                compress([&](uint64_t &list) {
-                    if (!over) return;
+        if (TOP && __syncthreads_or(full_buffer)) {
+            const bool over = s_count > kCandidates;
+            compress([&](uint64_t &list) {
+                if (!over) return;
 #pragma unroll 1
-                    for (int b = 0; b < kLpVectors * N; ++b) {
-                        float x = kNegInf;
+                for (int b = 0; b < kLpVectors * N; ++b) {
+                    float x = kNegInf;
 #pragma unroll
-                        for (int u = 0; u < kLpVectors; ++u)
+                    for (int u = 0; u < kLpVectors; ++u)
 #pragma unroll
-                            for (int i = 0; i < N; ++i)
-                                if (u * N + i == b) x = to_f32(now[u].e[i]);
-                        uint64_t c = 0;
-                        if (x > threshold && !((held >> b) & 1u))
-                            c = candidate(x, (v0 + (b / N) * kLpThreads) * N + b % N - view.shift);
-                        if (__any_sync(kFullMask, c != 0)) list = merge_lists(list, bitonic_sort_desc(c, lane), lane);
-                    }
-                });
-            } else if (base == first) {
-                // later logits have higher indices: only a greater one displaces a candidate
-                threshold = floor64 > 1 ? order_key_value(static_cast<uint32_t>(floor64 >> 32)) : kNegInf;
+                        for (int i = 0; i < N; ++i)
+                            if (u * N + i == b) x = to_f32(now[u].e[i]);
+                    uint64_t c = 0;
+                    if (x > bound && !((held >> b) & 1u))
+                        c = candidate(x, (v0 + (b / N) * kLpThreads) * N + b % N - view.shift);
+                    if (__any_sync(kFullMask, c != 0)) list = merge_lists(list, bitonic_sort_desc(c, lane), lane);
+                }
+            });
+        }
+    }
+
+    // the row's ends, up to N - 1 logits each that do not fill a vector
+    if (part == 0 && warp == 0) {
+        const uint32_t head = full ? view.full_begin * N : view.end;    // without a full vector: everything
+        uint32_t e = view.shift + lane;
+        if (e >= head) e = e - head + (full ? view.full_end * N : view.end);
+        if (e < view.end) {
+            const float x = to_f32((view.row - view.shift)[e]);
+            if (x > mine.max) mine.raise(x);
+            const float xs[2] = {x, kNegInf};
+            mine.template add<2>(xs, true);
+            if (TOP && x > kNegInf && x >= threshold) {    // less than half of the buffer is taken
+                const uint32_t at = atomicAdd(&s_count, 1u);
+                s_buffer[at] = candidate(x, e - view.shift);
             }
         }
     }

@@ -98,44 +98,18 @@ __device__ __forceinline__ RowSums warp_join(RowSums s) {
     return {s.max, warp_sum(s.sum), warp_sum(s.dot)};
 }
 
-// Two 32-bit numbers that move through one packed instruction.
-union Pair {
-    uint64_t u;
-    float2 f;
-};
-
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-    Pair c;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c.u) : "l"(a.u), "l"(b.u));
-    return c;
-}
-
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair c;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c.u) : "l"(a.u), "l"(b.u));
-    return c;
-}
-
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(a.u), "l"(b.u), "l"(c.u));
-    return d;
-}
-
-__device__ __forceinline__ Pair pair(float x, float y) {
-    Pair p;
-    p.f = make_float2(x, y);
-    return p;
-}
-
-// A thread's running sums, even and odd logits apart.
-struct ThreadSums {
+// A lane's running sums at its warp's running maximum, even and odd logits apart.
+struct LaneSums {
     float max;
     Pair minus, sum, dot;    // minus: -max twice; 0 before the first logit above -inf, so that -inf - 0 stays -inf
 
-    __device__ ThreadSums() : max(kNegInf), minus(pair(0.0f, 0.0f)), sum(pair(0.0f, 0.0f)), dot(pair(0.0f, 0.0f)) {}
+    __device__ LaneSums() : max(kNegInf), minus(pair(0.0f, 0.0f)), sum(pair(0.0f, 0.0f)), dot(pair(0.0f, 0.0f)) {}
 
-    __device__ __forceinline__ void raise(float to) {
+    // Raises the warp's maximum to the largest of the lanes' `hi`.  It grows
+    // about ln(steps) times in a row, so this is rarely more than one vote.
+    __device__ __forceinline__ void raise(float hi) {
+        if (!__any_sync(kFullMask, hi > max)) return;
+        const float to = order_key_value(__reduce_max_sync(kFullMask, order_key(hi > max ? hi : max)));
         RowSums a{max, sum.f.x, dot.f.x}, b{max, sum.f.y, dot.f.y};
         rescale(a, to);
         rescale(b, to);
@@ -146,15 +120,12 @@ struct ThreadSums {
     }
 
     // low: some logit is so low that its exponent needs the bound
-    template <int N> __device__ __forceinline__ void add(const float (&x)[N], bool low) {
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            Pair y = mul2(add2(pair(x[i], x[i + 1]), minus), pair(kLog2e, kLog2e));
-            if (low) y = pair(max_nan(y.f.x, kTinyExponent), max_nan(y.f.y, kTinyExponent));
-            const Pair e = pair(exp2_approx(y.f.x), exp2_approx(y.f.y));
-            sum = add2(sum, e);
-            dot = fma2(e, y, dot);
-        }
+    __device__ __forceinline__ void add(Pair x, bool low) {
+        Pair y = mul2(add2(x, minus), pair(kLog2e, kLog2e));
+        if (low) y = pair(max_nan(y.f.x, kTinyExponent), max_nan(y.f.y, kTinyExponent));
+        const Pair e = pair(exp2_approx(y.f.x), exp2_approx(y.f.y));
+        sum = add2(sum, e);
+        dot = fma2(e, y, dot);
     }
 
     __device__ __forceinline__ RowSums total() const { return {max, sum.f.x + sum.f.y, dot.f.x + dot.f.y}; }
@@ -190,37 +161,28 @@ template <typename T> struct RowView {
         vectors = (end + N - 1) / N;
     }
 
-    __device__ __forceinline__ typename Wide<T>::type load_full(uint32_t v) const {
-        const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(row - shift) + v);
-        return *reinterpret_cast<const typename Wide<T>::type *>(&q);
+    __device__ __forceinline__ uint4 load(uint32_t v) const {
+        return __ldcs(reinterpret_cast<const uint4 *>(row - shift) + v);
     }
 
-    // Vector v, -inf where it is not of the row or not below `last`.
-    __device__ __forceinline__ typename Wide<T>::type load(uint32_t v, uint32_t last) const {
-        using V = typename Wide<T>::type;
-        constexpr int N = Wide<T>::kCount;
-        V x;
-        const T *base = row - shift;
-        if (v < last && v >= full_begin && v < full_end) {
-            const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(base) + v);
-            x = *reinterpret_cast<const V *>(&q);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t e = v * N + i;
-                x.e[i] = v < last && e >= shift && e < end ? base[e] : neg_inf<T>();
-            }
-        }
-        return x;
+    // Element that lane `i` takes of the row's ends (up to kCount - 1 at each
+    // end do not fill a vector; without a full vector it is the whole row);
+    // `end` where there is none.
+    __device__ __forceinline__ uint32_t edge(uint32_t i) const {
+        const bool some = full_end > full_begin;
+        const uint32_t head = some ? full_begin * Wide<T>::kCount : end;
+        const uint32_t e = shift + i;
+        if (e < head) return e;
+        return min(end, e - head + (some ? full_end * Wide<T>::kCount : end));
     }
 };
 
-// Largest and smallest of a vector's logits, NaN left out.
-template <typename T> __device__ __forceinline__ float2 vector_range(const typename Wide<T>::type &v) {
-    float lo = to_f32(v.e[0]), hi = lo;
+// Smallest and largest of a thread's logits, NaN left out.
+template <typename T, int U> __device__ __forceinline__ float2 logit_range(const uint4 (&q)[U]) {
+    float lo = __uint_as_float(q[0].x), hi = lo;
 #pragma unroll
-    for (int i = 1; i < Wide<T>::kCount; ++i) {
-        const float x = to_f32(v.e[i]);
+    for (int i = 1; i < 4 * U; ++i) {
+        const float x = __uint_as_float((&q[i / 4].x)[i % 4]);
         lo = fminf(lo, x);
         hi = fmaxf(hi, x);
     }
@@ -228,24 +190,28 @@ template <typename T> __device__ __forceinline__ float2 vector_range(const typen
 }
 
 // 16-bit types: two at a time, before they are widened.
-template <> __device__ __forceinline__ float2 vector_range<__nv_bfloat16>(const Wide<__nv_bfloat16>::type &v) {
-    const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&v);
-    const __nv_bfloat162 lo = __hmin2(__hmin2(p[0], p[1]), __hmin2(p[2], p[3]));
-    const __nv_bfloat162 hi = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+template <typename T2, int U> __device__ __forceinline__ float2 logit_range2(const uint4 (&q)[U]) {
+    T2 lo = *reinterpret_cast<const T2 *>(&q[0].x), hi = lo;
+#pragma unroll
+    for (int i = 1; i < 4 * U; ++i) {
+        const T2 x = *reinterpret_cast<const T2 *>(&q[i / 4].x + i % 4);
+        lo = __hmin2(lo, x);
+        hi = __hmax2(hi, x);
+    }
     return make_float2(fminf(to_f32(lo.x), to_f32(lo.y)), fmaxf(to_f32(hi.x), to_f32(hi.y)));
 }
 
-template <> __device__ __forceinline__ float2 vector_range<__half>(const Wide<__half>::type &v) {
-    const __half2 *p = reinterpret_cast<const __half2 *>(&v);
-    const __half2 lo = __hmin2(__hmin2(p[0], p[1]), __hmin2(p[2], p[3]));
-    const __half2 hi = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
-    return make_float2(fminf(to_f32(lo.x), to_f32(lo.y)), fmaxf(to_f32(hi.x), to_f32(hi.y)));
+template <> __device__ __forceinline__ float2 logit_range<__nv_bfloat16>(const uint4 (&q)[kLpVectors]) {
+    return logit_range2<__nv_bfloat162>(q);
+}
+
+template <> __device__ __forceinline__ float2 logit_range<__half>(const uint4 (&q)[kLpVectors]) {
+    return logit_range2<__half2>(q);
 }
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const LogprobsArgs a) {
     constexpr int N = Wide<T>::kCount;
-    using V = typename Wide<T>::type;
     __shared__ RowSums s_sums[kLpWarps], s_cluster[kMaxCluster];
     __shared__ uint32_t s_group[32];                           // the groups' largest keys
     __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];        // the warps' lists
@@ -271,7 +237,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
         if (target >= 0 && target < a.vocab) given = to_f32(view.row[target]);
     }
 
-    ThreadSums mine;
+    LaneSums mine;
     float threshold = kNegInf;
     uint64_t kept = 0;           // warp 0: the running list of the row's part, descending
     if (TOP) {
@@ -309,23 +275,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
     };
 
     for (uint32_t base = first; base < last; base += kLpStep) {
-        V now[kLpVectors];
+        uint4 now[kLpVectors];
         const uint32_t v0 = base + tid;
 #pragma unroll
         for (int u = 0; u < kLpVectors; ++u) {
-            if (v0 + u * kLpThreads < last) {
-                now[u] = view.load_full(v0 + u * kLpThreads);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) now[u].e[i] = neg_inf<T>();
-            }
+            constexpr uint32_t w = Wide<T>::kNegInfWord;
+            now[u] = make_uint4(w, w, w, w);
+            if (v0 + u * kLpThreads < last) now[u] = view.load(v0 + u * kLpThreads);
         }
+        const float2 range = logit_range<T>(now);
+        mine.raise(range.y);
         float bound = threshold;     // candidates are above it
         if (TOP && base == first) {
             // the largest logit of each of 32 groups of threads: `top` logits reach their top-th
-            float hi = kNegInf;
-#pragma unroll
-            for (int u = 0; u < kLpVectors; ++u) hi = fmaxf(hi, vector_range<T>(now[u]).y);
+            float hi = range.y > kNegInf ? range.y : kNegInf;
 #pragma unroll
             for (int o = kGroupLanes / 2; o > 0; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, o));
             if (tid % kGroupLanes == 0) s_group[tid / kGroupLanes] = hi > kNegInf ? order_key(hi) : 0u;
@@ -343,28 +306,31 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
             threshold = cut ? order_key_value(cut) : kNegInf;
             bound = cut ? order_key_value(cut - (cut == 0x80000000u ? 2u : 1u)) : kNegInf;   // the key below zero's is unused
         }
+        if (range.x - mine.max > kLowLogit) {
+#pragma unroll
+            for (int u = 0; u < kLpVectors; ++u)
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) mine.add(Wide<T>::pair_of(now[u], i), false);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kLpVectors; ++u)
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) mine.add(Wide<T>::pair_of(now[u], i), true);
+        }
         uint32_t held = 0;       // candidates of this step that found a place in the buffer
         bool full_buffer = false;
+        if (TOP && range.y > bound) {
 #pragma unroll
-        for (int u = 0; u < kLpVectors; ++u) {
-            const float2 range = vector_range<T>(now[u]);
-            if (range.y > mine.max) mine.raise(range.y);
-            float x[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = to_f32(now[u].e[i]);
-            if (range.x - mine.max > kLowLogit) mine.template add<N>(x, false);
-            else mine.template add<N>(x, true);
-            if (TOP && range.y > bound) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    if (x[i] > bound) {
-                        const uint32_t at = atomicAdd(&s_count, 1u);
-                        if (at < kCandidates) {
-                            s_buffer[at] = candidate(x[i], (v0 + u * kLpThreads) * N + i - view.shift);
-                            held |= 1u << (u * N + i);
-                        }
-                        full_buffer |= at >= kCandidates / 2;
+            for (int b = 0; b < kLpVectors * N; ++b) {
+                const Pair p = Wide<T>::pair_of(now[b / N], b % N / 2);
+                const float x = b % 2 ? p.f.y : p.f.x;
+                if (x > bound) {
+                    const uint32_t at = atomicAdd(&s_count, 1u);
+                    if (at < kCandidates) {
+                        s_buffer[at] = candidate(x, (v0 + b / N * kLpThreads) * N + b % N - view.shift);
+                        held |= 1u << b;
                     }
+                    full_buffer |= at >= kCandidates / 2;
                 }
             }
         }
@@ -376,10 +342,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
                 for (int b = 0; b < kLpVectors * N; ++b) {
                     float x = kNegInf;
 #pragma unroll
-                    for (int u = 0; u < kLpVectors; ++u)
-#pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            if (u * N + i == b) x = to_f32(now[u].e[i]);
+                    for (int o = 0; o < kLpVectors * N; ++o) {
+                        const Pair p = Wide<T>::pair_of(now[o / N], o % N / 2);
+                        if (o == b) x = o % 2 ? p.f.y : p.f.x;
+                    }
                     uint64_t c = 0;
                     if (x > bound && !((held >> b) & 1u))
                         c = candidate(x, (v0 + (b / N) * kLpThreads) * N + b % N - view.shift);
@@ -389,20 +355,15 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
         }
     }
 
-    // the row's ends, up to N - 1 logits each that do not fill a vector
+    // the row's ends
     if (part == 0 && warp == 0) {
-        const uint32_t head = full ? view.full_begin * N : view.end;    // without a full vector: everything
-        uint32_t e = view.shift + lane;
-        if (e >= head) e = e - head + (full ? view.full_end * N : view.end);
-        if (e < view.end) {
-            const float x = to_f32((view.row - view.shift)[e]);
-            if (x > mine.max) mine.raise(x);
-            const float xs[2] = {x, kNegInf};
-            mine.template add<2>(xs, true);
-            if (TOP && x > kNegInf && x >= threshold) {    // less than half of the buffer is taken
-                const uint32_t at = atomicAdd(&s_count, 1u);
-                s_buffer[at] = candidate(x, e - view.shift);
-            }
+        const uint32_t e = view.edge(lane);
+        const float x = e < view.end ? to_f32((view.row - view.shift)[e]) : kNegInf;
+        mine.raise(x);
+        mine.add(pair(x, kNegInf), true);
+        if (TOP && x > kNegInf && x >= threshold) {    // less than half of the buffer is taken
+            const uint32_t at = atomicAdd(&s_count, 1u);
+            s_buffer[at] = candidate(x, e - view.shift);
         }
     }
 
@@ -479,10 +440,30 @@ struct LogprobsBackwardArgs {
     uint32_t blocks_per_row;
 };
 
+// A row's gradient as a function of x: with e = 2^y, y = (x - m) log2(e),
+//   -p (g + h (ln p + H)) = e * (q1 y + q0),  q1 = -h ln2 / S,  q0 = -(g + h (H - ln S)) / S
+struct RowGradient {
+    Pair minus, q0, q1;
+
+    // FLAT: q1 = 0, no entropy in the loss
+    template <bool FLAT> __device__ __forceinline__ Pair at(Pair x) const {
+        Pair y = mul2(add2(x, minus), pair(kLog2e, kLog2e));
+        if (FLAT) return mul2(pair(exp2_approx(y.f.x), exp2_approx(y.f.y)), q0);
+        y = pair(max_nan(y.f.x, kTinyExponent), max_nan(y.f.y, kTinyExponent));
+        return mul2(pair(exp2_approx(y.f.x), exp2_approx(y.f.y)), fma2(q1, y, q0));
+    }
+
+    template <typename T, bool FLAT> __device__ __forceinline__ uint4 vector(const uint4 &x) const {
+        uint4 o;
+#pragma unroll
+        for (int i = 0; i < Wide<T>::kCount / 2; ++i) Wide<T>::set_pair(o, i, at<FLAT>(Wide<T>::pair_of(x, i)));
+        return o;
+    }
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const LogprobsBackwardArgs a) {
     constexpr int N = Wide<T>::kCount;
-    using V = typename Wide<T>::type;
     const int64_t row = blockIdx.x / a.blocks_per_row;
     const uint32_t block = blockIdx.x % a.blocks_per_row;
     const RowView<T> view(static_cast<const T *>(a.logits) + row * a.row_stride, a.vocab);
@@ -491,47 +472,58 @@ __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const Logpro
     const bool same = (reinterpret_cast<uintptr_t>(out) & 15) == (reinterpret_cast<uintptr_t>(view.row) & 15);
     out -= view.shift;
 
-    V x[kGradVectors];
-    const uint32_t v0 = block * (kGradThreads * kGradVectors) + threadIdx.x;
+    uint4 x[kGradVectors];
+    const uint32_t v0 = view.full_begin + block * (kGradThreads * kGradVectors) + threadIdx.x;
 #pragma unroll
-    for (int u = 0; u < kGradVectors; ++u) x[u] = view.load(v0 + u * kGradThreads, view.vectors);
+    for (int u = 0; u < kGradVectors; ++u)
+        if (v0 + u * kGradThreads < view.full_end) x[u] = view.load(v0 + u * kGradThreads);
 
     const float2 stats = reinterpret_cast<const float2 *>(a.stats)[row];
-    const float m = stats.x, sum = stats.y;
     float g = a.grad_logprobs != nullptr ? a.grad_logprobs[row] : 0.0f;
     const float h = a.grad_entropy != nullptr ? a.grad_entropy[row] : 0.0f;
     int64_t t = -1;
     if (a.targets != nullptr) t = target_of(a.targets, a.wide_targets, row);
     if (t < 0) g = 0.0f;
     if (t >= static_cast<int64_t>(a.vocab)) g = __int_as_float(0x7FC00000);
-    const bool empty = sum == 0.0f;
-    const float inv = empty ? 0.0f : 1.0f / sum;
-    const float cb = h * kLn2, ca = empty ? 0.0f : g + h * (a.entropy[row] - logf(sum));
+    const bool empty = stats.y == 0.0f;      // every logit is -inf: -inf - 0 stays -inf, and e = 0
+    const float m = empty ? 0.0f : stats.x, inv = empty ? 0.0f : -1.0f / stats.y;
+    const float q0 = empty ? 0.0f : (h == 0.0f ? g : g + h * (a.entropy[row] - logf(stats.y))) * inv, q1 = h * kLn2 * inv;
+    RowGradient f;
+    f.minus = pair(-m, -m);
+    f.q0 = pair(q0, q0);
+    f.q1 = pair(q1, q1);
+    // the target's element; 0xFFFFFFFF: none
     const uint32_t at = t >= 0 && t < static_cast<int64_t>(a.vocab) && !empty ? static_cast<uint32_t>(t) + view.shift : 0xFFFFFFFFu;
+
+    // read before the stores: they may be to the same memory
+    const uint32_t tv = at / N;
+    const bool own = tv >= v0 && tv < view.full_end && (tv - v0) % kGradThreads == 0 && (tv - v0) / kGradThreads < kGradVectors;
+    float xt = 0.0f;
+    if (own) xt = to_f32((view.row - view.shift)[at]);
 
 #pragma unroll
     for (int u = 0; u < kGradVectors; ++u) {
         const uint32_t v = v0 + u * kGradThreads;
-        if (v >= view.vectors) break;
-        V o;
+        if (v < view.full_end) {
+            const uint4 o = h == 0.0f ? f.vector<T, true>(x[u]) : f.vector<T, false>(x[u]);
+            if (same) {
+                __stcs(reinterpret_cast<uint4 *>(out) + v, o);
+            } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float xi = to_f32(x[u].e[i]);
-            // in a row that is masked whole x - m is NaN, and so masked apart
-            const float y = empty ? kTinyExponent : max_nan((xi - m) * kLog2e, kTinyExponent);
-            const float p = exp2_approx(y) * inv;
-            float d = -p * fmaf(cb, y, ca);
-            if (v * N + i == at) d += g;
-            o.e[i] = from_f32<T>(d);
-        }
-        if (same && v >= view.full_begin && v < view.full_end) {
-            __stcs(reinterpret_cast<uint4 *>(out) + v, *reinterpret_cast<const uint4 *>(&o));
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t e = v * N + i;
-                if (e >= view.shift && e < view.end) out[e] = o.e[i];
+                for (int i = 0; i < N; ++i) out[v * N + i] = Wide<T>::element(o, i);
             }
+        }
+    }
+    if (own) {                                   // over this thread's own vector, rounded once
+        const Pair p = pair(xt, kNegInf);
+        out[at] = from_f32<T>((h == 0.0f ? f.at<true>(p) : f.at<false>(p)).f.x + g);
+    }
+    if (block == 0 && threadIdx.x < 32) {        // the row's ends
+        const uint32_t e = view.edge(threadIdx.x);
+        if (e < view.end) {
+            const Pair p = pair(to_f32((view.row - view.shift)[e]), kNegInf);
+            const Pair d = h == 0.0f ? f.at<true>(p) : f.at<false>(p);
+            out[e] = from_f32<T>(d.f.x + (e == at ? g : 0.0f));
         }
     }
 }
@@ -590,8 +582,7 @@ int launch_logprobs_backward(const LogprobsBackwardLaunch &L) {
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int64_t per_block = static_cast<int64_t>(kGradThreads) * kGradVectors * Wide<T>::kCount;
-        // a row can start inside a vector: up to kCount - 1 elements more
-        a.blocks_per_row = static_cast<uint32_t>((L.vocab + Wide<T>::kCount - 1 + per_block - 1) / per_block);
+        a.blocks_per_row = static_cast<uint32_t>((L.vocab + per_block - 1) / per_block);
         if (L.rows * a.blocks_per_row > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
         k_logprobs_backward<T><<<static_cast<uint32_t>(L.rows * a.blocks_per_row), kGradThreads, 0, L.stream>>>(a);
         return cudaGetLastError() == cudaSuccess ? static_cast<int>(GSORT_OK) : static_cast<int>(GSORT_ECUDA);

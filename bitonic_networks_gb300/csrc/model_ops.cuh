@@ -28,18 +28,88 @@ template <> __device__ __forceinline__ float from_f32<float>(float x) { return x
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
-template <typename T> __device__ __forceinline__ T neg_inf();
-template <> __device__ __forceinline__ float neg_inf<float>() { return __uint_as_float(0xFF800000u); }
-template <> __device__ __forceinline__ __nv_bfloat16 neg_inf<__nv_bfloat16>() { return __ushort_as_bfloat16(0xFF80); }
-template <> __device__ __forceinline__ __half neg_inf<__half>() { return __ushort_as_half(0xFC00); }
-
 // N elements that move as one aligned access.
 template <typename T, int N> struct alignas(sizeof(T) * N) Vec {
     T e[N];
 };
-template <typename T> struct Wide {
-    static constexpr int kCount = 16 / sizeof(T);
-    using type = Vec<T, kCount>;
+// Two 32-bit numbers that move through one packed instruction.
+union Pair {
+    uint64_t u;
+    float2 f;
+};
+
+__device__ __forceinline__ Pair pair(float x, float y) {
+    Pair p;
+    p.f = make_float2(x, y);
+    return p;
+}
+
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair c;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c.u) : "l"(a.u), "l"(b.u));
+    return c;
+}
+
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair c;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c.u) : "l"(a.u), "l"(b.u));
+    return c;
+}
+
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return d;
+}
+
+// 16-byte vectors as pairs of 32-bit numbers and back, two elements at a time.
+template <typename T> struct Wide;
+
+template <> struct Wide<float> {
+    static constexpr int kCount = 4;
+    static constexpr uint32_t kNegInfWord = 0xFF800000u;
+    static __device__ __forceinline__ float element(const uint4 &q, int i) { return __uint_as_float((&q.x)[i]); }
+    static __device__ __forceinline__ Pair pair_of(const uint4 &q, int i) {
+        const uint32_t *w = &q.x;
+        return pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    static __device__ __forceinline__ void set_pair(uint4 &q, int i, Pair p) {
+        uint32_t *w = &q.x;
+        w[2 * i] = __float_as_uint(p.f.x);
+        w[2 * i + 1] = __float_as_uint(p.f.y);
+    }
+};
+
+template <> struct Wide<__nv_bfloat16> {
+    static constexpr int kCount = 8;
+    static constexpr uint32_t kNegInfWord = 0xFF80FF80u;
+    static __device__ __forceinline__ __nv_bfloat16 element(const uint4 &q, int i) {
+        return __ushort_as_bfloat16(static_cast<unsigned short>((&q.x)[i / 2] >> (16 * (i % 2))));
+    }
+    static __device__ __forceinline__ Pair pair_of(const uint4 &q, int i) {
+        const uint32_t w = (&q.x)[i];
+        return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ void set_pair(uint4 &q, int i, Pair p) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(p.f.x, p.f.y);
+        (&q.x)[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+};
+
+template <> struct Wide<__half> {
+    static constexpr int kCount = 8;
+    static constexpr uint32_t kNegInfWord = 0xFC00FC00u;
+    static __device__ __forceinline__ __half element(const uint4 &q, int i) {
+        return __ushort_as_half(static_cast<unsigned short>((&q.x)[i / 2] >> (16 * (i % 2))));
+    }
+    static __device__ __forceinline__ Pair pair_of(const uint4 &q, int i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&q.x + i));
+        return pair(f.x, f.y);
+    }
+    static __device__ __forceinline__ void set_pair(uint4 &q, int i, Pair p) {
+        const __half2 v = __floats2half2_rn(p.f.x, p.f.y);
+        (&q.x)[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
 };
 
 // Order key of a float: greater floats have greater keys; both zeros have one

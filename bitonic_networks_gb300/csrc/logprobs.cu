@@ -10,11 +10,12 @@
 //
 // The forward pass keeps a running maximum per thread and rescales its sums
 // when the maximum grows, so a row is read once.  The largest logits are found
-// in the same pass: the first 16,384 16-bit (8,192 32-bit) logits give a
+// in the same pass: the first 8,192 16-bit (4,096 32-bit) logits give a
 // threshold that at least `top` of them reach, and only logits above it are
 // written to a shared buffer, which is sorted by warps (bitonic networks of 32)
-// when the row ends or the buffer fills.  Few rows are split over a cluster of
-// CTAs, joined through distributed shared memory.
+// when the row ends; where the buffer is full, a warp sorts into a list of its
+// own.  Few rows are split over a cluster of CTAs, joined through distributed
+// shared memory.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -22,15 +23,13 @@
 namespace gsort {
 namespace {
 
-#ifndef LP_THREADS
-#define LP_THREADS 256
-#define LP_VECTORS 4
-#define LP_CTAS 4
-#endif
-constexpr int kLpThreads = LP_THREADS;
-constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpVectors = LP_VECTORS;     // 16-byte vectors per thread and step
-constexpr int kLpCtas = LP_CTAS;           // CTAs per SM that the registers allow
+// 256 threads with 4 vectors each in flight and 5 CTAs per SM keep the memory
+// busy: 4096 x 100003 bf16 with one alternative takes 158 us (5.2 TB/s); 4 CTAs
+// 165, 2 vectors 182, CTAs of 512 threads 190.
+constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;   // at most 8: join_lists
+constexpr int kLpVectors = 4;               // 16-byte vectors per thread and step
+constexpr int kLpCtas = 5;                  // CTAs per SM that the registers allow
 constexpr uint32_t kLpStep = kLpThreads * kLpVectors;
 constexpr int kGroupLanes = kLpThreads / 32;   // 32 groups of lanes give the first threshold
 constexpr uint32_t kCandidates = 2048;     // shared buffer of candidates
@@ -72,6 +71,22 @@ __device__ __forceinline__ uint64_t bitonic_sort_desc(uint64_t v, int lane) {
 // The 32 largest of two descending lists, descending.
 __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane) {
     return bitonic_merge_desc(max64(a, __shfl_sync(kFullMask, b, 31 - lane)), lane);
+}
+
+// Joins `count` (1..8) lists of 32, one after another in shared memory, by a
+// tree: the merges of a level do not wait on each other.
+__device__ __forceinline__ uint64_t join_lists(const uint64_t (*lists)[32], int count, int lane) {
+    uint64_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < count ? lists[i][lane] : 0;
+#pragma unroll
+    for (int w = 4; w > 0; w >>= 1) {
+        if (count > w) {
+#pragma unroll
+            for (int i = 0; i < w; ++i) v[i] = merge_lists(v[i], v[i + w], lane);
+        }
+    }
+    return v[0];
 }
 
 // Sums over a part of a row with running maximum `max`, in powers of two:
@@ -213,12 +228,11 @@ template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const LogprobsArgs a) {
     constexpr int N = Wide<T>::kCount;
     __shared__ RowSums s_sums[kLpWarps], s_cluster[kMaxCluster];
-    __shared__ uint32_t s_group[32];                           // the groups' largest keys
+    __shared__ __align__(16) uint32_t s_group[32];             // the groups' largest keys
     __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];        // the warps' lists
     __shared__ uint64_t s_remote[TOP ? kMaxCluster : 1][32];   // the cluster's lists
     __shared__ uint64_t s_buffer[TOP ? kCandidates : 1];
     __shared__ uint32_t s_count;
-    __shared__ float s_threshold;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / a.split;
@@ -239,40 +253,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
 
     LaneSums mine;
     float threshold = kNegInf;
-    uint64_t kept = 0;           // warp 0: the running list of the row's part, descending
-    if (TOP) {
-        if (tid == 0) s_count = 0;
-        __syncthreads();
-    }
-
-    // sorts the buffer (and, where it overflowed, the candidates still held in
-    // registers, given by `more`) into warp 0's list
-    auto compress = [&](auto &&more) {
-        const uint32_t have = min(s_count, kCandidates);
-        uint64_t list = warp == 0 ? kept : 0;
-        for (uint32_t b = warp * 32; b < have; b += kLpThreads) {
-            const uint64_t c = b + lane < have ? s_buffer[b + lane] : 0;
-            list = merge_lists(list, bitonic_sort_desc(c, lane), lane);
-        }
-        more(list);
-        s_list[warp][lane] = list;
-        __syncthreads();
-        for (int w = kLpWarps / 2; w > 0; w >>= 1) {
-            if (warp < w) {
-                list = merge_lists(list, s_list[warp + w][lane], lane);
-                s_list[warp][lane] = list;
-            }
-            __syncthreads();
-        }
-        if (warp == 0) kept = list;
-        if (tid == 0) {
-            const uint64_t c = s_list[0][a.top - 1];
-            s_threshold = c ? order_key_value(static_cast<uint32_t>(c >> 32)) : kNegInf;
-            s_count = 0;
-        }
-        __syncthreads();
-        threshold = s_threshold;
-    };
+    uint64_t kept = 0;           // the warp's list, descending: candidates that found the buffer full
+    if (TOP && tid == 0) s_count = 0;
 
     for (uint32_t base = first; base < last; base += kLpStep) {
         uint4 now[kLpVectors];
@@ -291,16 +273,18 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
             float hi = range.y > kNegInf ? range.y : kNegInf;
 #pragma unroll
             for (int o = kGroupLanes / 2; o > 0; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, o));
-            if (tid % kGroupLanes == 0) s_group[tid / kGroupLanes] = hi > kNegInf ? order_key(hi) : 0u;
+            // the key's last five bits make room for the group's number, so that no two are equal
+            const uint32_t group = tid / kGroupLanes;
+            if (tid % kGroupLanes == 0) s_group[group] = hi > kNegInf ? (order_key(hi) & ~31u) | group : 0u;
             __syncthreads();
             const uint32_t key = s_group[lane];
-            uint32_t rank = 0;       // groups before this one
+            uint32_t above = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const uint32_t o = __shfl_sync(kFullMask, key, i);
-                rank += (o > key || (o == key && i < lane)) ? 1u : 0u;
+            for (int i = 0; i < 32; i += 4) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(s_group + i);
+                above += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
             }
-            const uint32_t cut = __reduce_max_sync(kFullMask, rank == static_cast<uint32_t>(a.top - 1) ? key : 0u);
+            const uint32_t cut = __reduce_max_sync(kFullMask, above == static_cast<uint32_t>(a.top - 1) ? key : 0u) & ~31u;
             // logits of this step that equal it may belong to the best; later ones have
             // higher indices: only a greater logit displaces one of this step
             threshold = cut ? order_key_value(cut) : kNegInf;
@@ -317,27 +301,22 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
 #pragma unroll
                 for (int i = 0; i < N / 2; ++i) mine.add(Wide<T>::pair_of(now[u], i), true);
         }
-        uint32_t held = 0;       // candidates of this step that found a place in the buffer
-        bool full_buffer = false;
-        if (TOP && range.y > bound) {
+        if (TOP) {
+            uint32_t lost = 0;   // candidates that found the buffer full
+            if (range.y > bound) {
 #pragma unroll
-            for (int b = 0; b < kLpVectors * N; ++b) {
-                const Pair p = Wide<T>::pair_of(now[b / N], b % N / 2);
-                const float x = b % 2 ? p.f.y : p.f.x;
-                if (x > bound) {
-                    const uint32_t at = atomicAdd(&s_count, 1u);
-                    if (at < kCandidates) {
-                        s_buffer[at] = candidate(x, (v0 + b / N * kLpThreads) * N + b % N - view.shift);
-                        held |= 1u << b;
+                for (int b = 0; b < kLpVectors * N; ++b) {
+                    const Pair p = Wide<T>::pair_of(now[b / N], b % N / 2);
+                    const float x = b % 2 ? p.f.y : p.f.x;
+                    if (x > bound) {
+                        const uint32_t at = atomicAdd(&s_count, 1u);
+                        if (at < kCandidates) s_buffer[at] = candidate(x, (v0 + b / N * kLpThreads) * N + b % N - view.shift);
+                        else lost |= 1u << b;
                     }
-                    full_buffer |= at >= kCandidates / 2;
                 }
             }
-        }
-        if (TOP && __syncthreads_or(full_buffer)) {
-            const bool over = s_count > kCandidates;
-            compress([&](uint64_t &list) {
-                if (!over) return;
+            if (__any_sync(kFullMask, lost != 0)) {
+                // rare: the warp sorts them into a list of its own, which raises its threshold
 #pragma unroll 1
                 for (int b = 0; b < kLpVectors * N; ++b) {
                     float x = kNegInf;
@@ -346,31 +325,43 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
                         const Pair p = Wide<T>::pair_of(now[o / N], o % N / 2);
                         if (o == b) x = o % 2 ? p.f.y : p.f.x;
                     }
-                    uint64_t c = 0;
-                    if (x > bound && !((held >> b) & 1u))
-                        c = candidate(x, (v0 + (b / N) * kLpThreads) * N + b % N - view.shift);
-                    if (__any_sync(kFullMask, c != 0)) list = merge_lists(list, bitonic_sort_desc(c, lane), lane);
+                    const uint64_t c = (lost >> b) & 1u ? candidate(x, (v0 + b / N * kLpThreads) * N + b % N - view.shift) : 0;
+                    if (__any_sync(kFullMask, c != 0)) kept = merge_lists(kept, bitonic_sort_desc(c, lane), lane);
                 }
-            });
+                const uint64_t c = __shfl_sync(kFullMask, kept, a.top - 1);
+                if (c) threshold = fmaxf(threshold, order_key_value(static_cast<uint32_t>(c >> 32)));
+            }
         }
     }
 
+    if (TOP && first >= last) __syncthreads();     // s_count is set; with a step, its barrier has come
     // the row's ends
     if (part == 0 && warp == 0) {
         const uint32_t e = view.edge(lane);
         const float x = e < view.end ? to_f32((view.row - view.shift)[e]) : kNegInf;
         mine.raise(x);
         mine.add(pair(x, kNegInf), true);
-        if (TOP && x > kNegInf && x >= threshold) {    // less than half of the buffer is taken
-            const uint32_t at = atomicAdd(&s_count, 1u);
-            s_buffer[at] = candidate(x, e - view.shift);
+        if (TOP) {
+            const uint64_t c = x > kNegInf ? candidate(x, e - view.shift) : 0;
+            kept = merge_lists(kept, bitonic_sort_desc(c, lane), lane);
         }
     }
 
     RowSums s = warp_join(mine.total());
     if (lane == 0) s_sums[warp] = s;
     __syncthreads();
-    if (TOP && s_count > 0) compress([](uint64_t &) {});
+    if (TOP) {
+        // each warp sorts its share of the buffer into its list; warp 0 joins the lists
+        const uint32_t have = min(s_count, kCandidates);
+        for (uint32_t b = warp * 32; b < have; b += kLpThreads)
+            kept = merge_lists(kept, bitonic_sort_desc(b + lane < have ? s_buffer[b + lane] : 0, lane), lane);
+        const int lists = s_count > kCandidates ? kLpWarps : min(kLpWarps, static_cast<int>((have + 31) / 32));
+        if (lists > 1) {
+            s_list[warp][lane] = kept;
+            __syncthreads();
+            if (warp == 0) kept = join_lists(s_list, lists, lane);
+        }
+    }
     if (warp == 0) s = warp_join(lane < kLpWarps ? s_sums[lane] : RowSums{kNegInf, 0.0f, 0.0f});
 
     if (a.split > 1) {
@@ -395,8 +386,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
         if (part != 0) return;
         if (warp == 0) {
             s = warp_join(lane < static_cast<int>(a.split) ? s_cluster[lane] : RowSums{kNegInf, 0.0f, 0.0f});
-            if (TOP)
-                for (uint32_t p = 1; p < a.split; ++p) kept = merge_lists(kept, s_remote[p][lane], lane);
+            if (TOP) kept = join_lists(s_remote, static_cast<int>(a.split), lane);
         }
     }
     if (warp != 0) return;

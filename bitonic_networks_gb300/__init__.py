@@ -27,5 +27,6 @@ __all__ += _MODEL_OPS
 def __getattr__(name):
     if name in __all__:
         mod = importlib.import_module(".model_ops" if name in _MODEL_OPS else ".gsort", __name__)
-        return getattr(mod, name)
+        value = globals()[name] = getattr(mod, name)   # the next access finds it at once
+        return value
     raise AttributeError(name)

@@ -53,15 +53,27 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_entry_points = {}
+
+
+def _entry(name: str):
+    fn = _entry_points.get(name)
+    if fn is None:
+        fn = _entry_points[name] = getattr(_lib.load(), name)
+    return fn
+
+
 def _call(name: str, device: torch.device, *args):
-    """Calls the entry point on the device's current stream."""
-    fn = getattr(_lib.load(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, stream)
+    """Calls the entry point on the device's current stream.  A single-token
+    call costs little more than its launch: the stream's handle is read without
+    making a stream object, and the device is switched only where it is another."""
+    fn = _entry(name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         raise GsortError(rc, name)
 
@@ -84,7 +96,7 @@ def _flat(t: torch.Tensor, name: str, dtype, shape, device):
     """Checks a contiguous tensor of the given dtype and shape on the device."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
@@ -157,11 +169,11 @@ def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, expert
 # ---------------------------------------------------- grouping and row moves
 def group_capacity(pairs: int, num_experts: int, align: int = 1) -> int:
     """Rows of the grouped layout that any choice of experts fits into."""
-    return int(_lib.load().gsort_group_capacity(pairs, num_experts, align))
+    return int(_entry("gsort_group_capacity")(pairs, num_experts, align))
 
 
 def group_workspace_bytes(pairs: int, num_experts: int) -> int:
-    return int(_lib.load().gsort_group_workspace_bytes(pairs, num_experts))
+    return int(_entry("gsort_group_workspace_bytes")(pairs, num_experts))
 
 
 def group_by_expert(experts: torch.Tensor, num_experts: int, *, align: int = 1,
@@ -175,10 +187,9 @@ def group_by_expert(experts: torch.Tensor, num_experts: int, *, align: int = 1,
         raise ValueError("experts must have two dimensions")
     dev = experts.device
     _flat(experts, "experts", torch.int32, experts.shape, dev)
-    lib = _lib.load()
     pairs = experts.numel()
-    capacity = lib.gsort_group_capacity(pairs, num_experts, align)
-    nbytes = lib.gsort_group_workspace_bytes(pairs, num_experts)
+    capacity = group_capacity(pairs, num_experts, align)
+    nbytes = group_workspace_bytes(pairs, num_experts)
     ws = _workspace(nbytes, dev, workspace) if nbytes else None
     offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int32, device=dev)
     counts = torch.empty(max(num_experts, 0), dtype=torch.int32, device=dev)

@@ -10,10 +10,12 @@
 //   chosen      the k largest c, ties to the lower index
 //   weight      s * scale, or s / (sum of the chosen s) * scale
 //
-// One warp holds one token: lane l keeps experts [l * C, (l + 1) * C) in
-// registers, so lower lanes hold lower indices and the tie rule is "lowest
-// lane, then lowest slot".  A pick is one warp-wide integer maximum
-// (redux.sync) of 32-bit order keys, one ballot and one shuffle.
+// L lanes (a power of two, at least k) hold one token, C experts each: lane l
+// keeps experts [l * C, (l + 1) * C) in registers, so lower lanes hold lower
+// indices and the tie rule is "lowest lane, then lowest slot".  C is 8 up to 256
+// experts, so that 64 experts take 8 lanes and a warp works on 4 tokens at once.
+// A pick is a maximum of 32-bit order keys over the lanes (redux.sync for a
+// whole warp), one ballot and one shuffle.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -21,28 +23,90 @@
 namespace gsort {
 namespace {
 
-constexpr int kRouteWarps = 4;
+constexpr int kRouteThreads = 128;
 
-// A warp's row of E values, C per lane, -inf beyond the row's end.
-template <typename T, int C>
-__device__ __forceinline__ void load_row(const T *row, int experts, bool wide, int lane, float (&x)[C]) {
-    const int e0 = lane * C;
-    constexpr int N = C * sizeof(T) <= 16 ? C : static_cast<int>(16 / sizeof(T));
-    if (wide && e0 + C <= experts) {
+// A lane's C values of a row, -inf beyond the row's end.  `access` (1..16
+// bytes): what the rows' alignment allows at once.
+template <typename T, int C, int N>
+__device__ __forceinline__ void load_values(const T *row, int experts, int e0, float (&x)[C]) {
 #pragma unroll
-        for (int b = 0; b < C; b += N) {
+    for (int b = 0; b < C; b += N) {
+        if (e0 + b + N <= experts) {
             const Vec<T, N> v = *reinterpret_cast<const Vec<T, N> *>(row + e0 + b);
 #pragma unroll
             for (int i = 0; i < N; ++i) x[b + i] = to_f32(v.e[i]);
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int i = 0; i < C; ++i) x[i] = e0 + i < experts ? to_f32(row[e0 + i]) : kNegInf;
+            for (int i = 0; i < N; ++i) x[b + i] = N > 1 && e0 + b + i < experts ? to_f32(row[e0 + b + i]) : kNegInf;
+        }
     }
 }
 
-// Sum over the warp's row in one fixed order: neighbours first.
-template <int C> __device__ __forceinline__ float row_sum(const float (&v)[C]) {
+template <typename T, int C>
+__device__ __forceinline__ void load_row(const T *row, int experts, int access, int e0, float (&x)[C]) {
+    constexpr int kMost = 16 / sizeof(T) < C ? 16 / sizeof(T) : C;
+    if (access >= 16) load_values<T, C, kMost>(row, experts, e0, x);
+    else if (access >= 8) load_values<T, C, 8 / sizeof(T)>(row, experts, e0, x);
+    else if (access >= 4) load_values<T, C, 4 / sizeof(T)>(row, experts, e0, x);
+    else load_values<T, C, 1>(row, experts, e0, x);
+}
+
+template <typename T, int C, int N>
+__device__ __forceinline__ void store_values(T *row, int experts, int e0, const float (&x)[C]) {
+#pragma unroll
+    for (int b = 0; b < C; b += N) {
+        if (e0 + b + N <= experts) {
+            Vec<T, N> v;
+#pragma unroll
+            for (int i = 0; i < N; ++i) v.e[i] = from_f32<T>(x[b + i]);
+            *reinterpret_cast<Vec<T, N> *>(row + e0 + b) = v;
+        } else if (N > 1) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (e0 + b + i < experts) row[e0 + b + i] = from_f32<T>(x[b + i]);
+        }
+    }
+}
+
+template <typename T, int C>
+__device__ __forceinline__ void store_row(T *row, int experts, int access, int e0, const float (&x)[C]) {
+    constexpr int kMost = 16 / sizeof(T) < C ? 16 / sizeof(T) : C;
+    if (access >= 16) store_values<T, C, kMost>(row, experts, e0, x);
+    else if (access >= 8) store_values<T, C, 8 / sizeof(T)>(row, experts, e0, x);
+    else if (access >= 4) store_values<T, C, 4 / sizeof(T)>(row, experts, e0, x);
+    else store_values<T, C, 1>(row, experts, e0, x);
+}
+
+// Reductions over a token's L lanes.
+template <int L> __device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+
+template <int L> __device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
+    return v;
+}
+
+template <int L> __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+    if (L == 32) return __reduce_max_sync(kFullMask, v);
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) v = max(v, __shfl_xor_sync(kFullMask, v, o));
+    return v;
+}
+
+// The token's first lane for which `p` holds, as a lane of the warp; one must.
+template <int L> __device__ __forceinline__ int first_lane(bool p, int lane) {
+    const uint32_t votes = __ballot_sync(kFullMask, p);
+    if (L == 32) return __ffs(votes) - 1;
+    const int base = lane & ~(L - 1);
+    return base + __ffs((votes >> base) & ((1u << (L & 31)) - 1)) - 1;
+}
+
+// Sum over a token's row in one fixed order: neighbours first.
+template <int C, int L> __device__ __forceinline__ float row_sum(const float (&v)[C]) {
     float t[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) t[i] = v[i];
@@ -50,29 +114,30 @@ template <int C> __device__ __forceinline__ float row_sum(const float (&v)[C]) {
     for (int w = 1; w < C; w *= 2)
 #pragma unroll
         for (int i = 0; i < C; i += 2 * w) t[i] += t[i + w];
-    float s = t[0];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) s += __shfl_xor_sync(kFullMask, s, o);
-    return s;
+    return lanes_sum<L>(t[0]);
 }
 
-// Exponentials e^(x - m) of a row's candidates; x - m is exact enough because
-// it is formed before the multiplication inside expf.
+// e^(x - m) of a candidate: the difference is formed before expf multiplies it.
+// The largest candidate has 1 even at +inf.
+__device__ __forceinline__ float exp_from(float x, float m) { return x == m ? 1.0f : expf(x - m); }
+
 template <int C>
 __device__ __forceinline__ void row_exp(const float (&x)[C], float m, float (&e)[C]) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) e[i] = x[i] > kNegInf ? (x[i] == m ? 1.0f : expf(x[i] - m)) : 0.0f;
+    for (int i = 0; i < C; ++i) e[i] = x[i] > kNegInf ? exp_from(x[i], m) : 0.0f;
 }
 
 // Largest candidate of the row (NaN is none); -inf where there is no candidate.
-template <int C> __device__ __forceinline__ float row_max(const float (&x)[C]) {
+template <int C, int L> __device__ __forceinline__ float row_max(const float (&x)[C]) {
     float m = x[0] > kNegInf ? x[0] : kNegInf;
 #pragma unroll
     for (int i = 1; i < C; ++i) m = x[i] > m ? x[i] : m;
-    return warp_max(m);
+    return lanes_max<L>(m);
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// 1 / (1 + e^-x), each operation rounded to nearest: a choice among biased
+// scores does not depend on how the quotient is formed.
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
 
 struct RouteArgs {
     const void *logits;
@@ -82,139 +147,187 @@ struct RouteArgs {
     int32_t *experts_out;
     float scale;
     int experts, groups, groups_kept, group_size, chosen;
+    int group_lanes;         // lanes to a group where each lane's experts are of one group, else 0
     uint32_t group_magic;    // ceil(2^21 / group_size): e / group_size = e * magic >> 21 for e < 1024
-    bool softmax, top2, renormalise, wide;
+    int access, bias_access;
+    bool softmax, top2, renormalise;
 };
 
-template <typename T, int C>
-__global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
-    // group values are read by other lanes; one word of padding for 32
-    __shared__ float s_value[kRouteWarps][C * 33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-    if (token >= a.tokens) return;   // whole warp: no block-wide barrier below
-    const T *row = static_cast<const T *>(a.logits) + token * a.row_stride;
-    const int e0 = lane * C;
+// The two largest order keys of a lane's candidates and their slots; ties to
+// the lower slot.  0: none.
+struct LaneBest {
+    uint32_t first, second;
+    int slot, next;
 
-    float x[C], c[C];
-    load_row<T, C>(row, a.experts, a.wide, lane, x);
+    template <int C> __device__ __forceinline__ void find(const uint32_t (&key)[C]) {
+        first = second = 0u;
+        slot = next = 0;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const bool best = key[i] > first, better = key[i] > second;
+            second = best ? first : better ? key[i] : second;
+            next = best ? slot : better ? i : next;
+            first = best ? key[i] : first;
+            slot = best ? i : slot;
+        }
+    }
+
+    // The two that follow (last, at) in order.
+    template <int C> __device__ __forceinline__ void find_after(const uint32_t (&key)[C], uint32_t last, int at) {
+        uint32_t rest[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) rest[i] = key[i] < last || (key[i] == last && i > at) ? key[i] : 0u;
+        find<C>(rest);
+    }
+};
+
+template <typename T, int C, int L>
+__global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
+    // group values that other lanes read; one word of padding for 32
+    __shared__ float s_value[kRouteThreads / 32][32 * C + C];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1);
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / L) + threadIdx.x / L;
+    const bool live = token < a.tokens;      // every lane goes through the warp's votes
+    const T *row = static_cast<const T *>(a.logits) + (live ? token : 0) * a.row_stride;
+    const int e0 = sub * C;
+
+    float x[C];
+    load_row<T, C>(row, a.experts, a.access, e0, x);
 
     const bool biased = a.bias != nullptr;
-    const bool by_score = a.groups > 1 && a.top2;
     float m = kNegInf, sum = 0.0f;
-    if (a.softmax && (biased || by_score || !a.renormalise)) {
-        m = row_max<C>(x);
+    if (a.softmax && (biased || !a.renormalise || (a.groups > 1 && a.top2))) {
+        m = row_max<C, L>(x);
         float e[C];
         row_exp<C>(x, m, e);
-        sum = row_sum<C>(e);
-#pragma unroll
-        for (int i = 0; i < C; ++i) c[i] = e[i] / sum;
-    } else if (!a.softmax && (biased || by_score)) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) c[i] = sigmoid(x[i]);
+        sum = row_sum<C, L>(e);
     }
-    if (biased) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) c[i] += e0 + i < a.experts ? a.bias[e0 + i] : 0.0f;
-    }
+    auto score = [&](float v) { return a.softmax ? exp_from(v, m) / sum : sigmoid(v); };
+
     // order keys of the choice values; 0: no candidate
     uint32_t key[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const float v = biased ? c[i] : x[i];
-        key[i] = x[i] > kNegInf && v > kNegInf ? order_key(v) : 0u;
-    }
-
-    if (a.groups > 1) {
-        float *sv = s_value[warp];
+    if (biased) {
+        float b[C];
+        load_row<float, C>(a.bias, a.experts, a.bias_access, e0, b);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int e = e0 + i;
-            sv[e + (e >> 5)] = key[i] == 0u ? kNegInf : (biased || by_score) ? c[i] : x[i];
-        }
-        __syncwarp();
-        // `per` lanes to a group, a power of two
-        int per = 1;
-        while (per * 2 * a.groups <= 32) per *= 2;
-        const int g = lane / per, sub = lane % per;
-        float first = kNegInf, second = kNegInf;
-        if (g < a.groups) {
-            for (int i = sub; i < a.group_size; i += per) {
-                const int e = g * a.group_size + i;
-                const float v = sv[e + (e >> 5)];
-                second = fmaxf(second, fminf(first, v));
-                first = fmaxf(first, v);
-            }
-        }
-        for (int o = 1; o < per; o <<= 1) {
-            const float f = __shfl_xor_sync(kFullMask, first, o), s = __shfl_xor_sync(kFullMask, second, o);
-            second = fmaxf(fmaxf(second, s), fminf(first, f));
-            first = fmaxf(first, f);
-        }
-        float value = first;
-        if (a.top2 && second > kNegInf) value += second;
-        uint32_t gkey = g < a.groups && sub == 0 && first > kNegInf ? order_key(value) : 0u;
-        uint32_t kept = 0;
-        for (int r = 0; r < a.groups_kept; ++r) {
-            const uint32_t best = __reduce_max_sync(kFullMask, gkey);
-            if (best == 0u) break;
-            const int src = __ffs(__ballot_sync(kFullMask, gkey == best)) - 1;
-            kept |= 1u << (src / per);
-            if (lane == src) gkey = 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const uint32_t gi = (static_cast<uint32_t>(e0 + i) * a.group_magic) >> 21;
-            if (gi >= 32u || !((kept >> gi) & 1u)) key[i] = 0u;
-        }
-    }
-
-    // k picks: the lane's best candidate, then the warp's
-    int mine = -1;           // the pick that this lane keeps: number `lane`
-    uint32_t best = 0u;
-    int slot = 0;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-        if (key[i] > best) best = key[i], slot = i;
-    for (int r = 0; r < a.chosen; ++r) {
-        const uint32_t top = __reduce_max_sync(kFullMask, best);
-        if (top == 0u) break;
-        const int src = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
-        const int e = __shfl_sync(kFullMask, e0 + slot, src);
-        if (lane == r) mine = e;
-        if (lane == src) {
-            const int old = slot;
-            best = 0u;
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                if (i == old) key[i] = 0u;
-                if (key[i] > best) best = key[i], slot = i;
-            }
-        }
-    }
-
-    // the chosen experts' weights, pick r in lane r
-    float w = 0.0f;
-    const float xe = mine >= 0 ? to_f32(row[mine]) : kNegInf;
-    if (a.softmax) {
-        if (a.renormalise) {     // a softmax over the chosen alone
-            const float mc = warp_max(xe);
-            const float e = mine >= 0 ? (xe == mc ? 1.0f : expf(xe - mc)) : 0.0f;
-            const float total = warp_sum(e);
-            w = total > 0.0f ? e / total : 0.0f;
-        } else if (mine >= 0) {
-            w = (xe == m ? 1.0f : expf(xe - m)) / sum;
+            const float c = score(x[i]) + b[i];
+            key[i] = x[i] > kNegInf && c > kNegInf ? order_key(c) : 0u;
         }
     } else {
-        w = mine >= 0 ? sigmoid(xe) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) key[i] = x[i] > kNegInf ? order_key(x[i]) : 0u;
+    }
+    LaneBest best;
+    best.find<C>(key);
+
+    if (a.groups > 1) {
+        // the largest keys of a group; scores grow with their keys
+        const int per = a.group_lanes > 0 ? a.group_lanes : 1;
+        int g;
+        uint32_t first, second;
+        if (a.group_lanes > 0) {
+            g = sub / per;
+            first = best.first;
+            second = best.second;
+        } else {
+            // groups that end inside a lane: one lane reads a group's keys
+            uint32_t *sk = reinterpret_cast<uint32_t *>(s_value[warp]);
+            const int w0 = (lane & ~(L - 1)) * C;
+#pragma unroll
+            for (int i = 0; i < C; ++i) sk[w0 + e0 + i + ((w0 + e0 + i) >> 5)] = key[i];
+            __syncwarp();
+            first = second = 0u;
+            g = sub;                 // at least as many lanes as groups
+            if (g < a.groups)
+                for (int i = 0; i < a.group_size; ++i) {
+                    const int e = w0 + g * a.group_size + i;
+                    const uint32_t v = sk[e + (e >> 5)];
+                    second = max(second, min(first, v));
+                    first = max(first, v);
+                }
+        }
+        for (int o = 1; o < per; o <<= 1) {
+            const uint32_t f = __shfl_xor_sync(kFullMask, first, o), s = __shfl_xor_sync(kFullMask, second, o);
+            second = max(max(second, s), min(first, f));
+            first = max(first, f);
+        }
+        uint32_t gkey = 0u;
+        if (g < a.groups && first != 0u && sub % per == 0) {
+            if (!a.top2) {
+                gkey = first;
+            } else {
+                float value = order_key_value(first), other = order_key_value(second);
+                if (!biased) value = score(value), other = score(other);
+                gkey = order_key(second != 0u ? value + other : value);
+            }
+        }
+        uint32_t kept = 0;
+        for (int r = 0; r < a.groups_kept; ++r) {
+            const uint32_t top = lanes_max<L>(gkey);
+            const int src = first_lane<L>(gkey == top, lane);
+            if (top != 0u) kept |= 1u << ((src & (L - 1)) / per);
+            if (lane == src) gkey = 0u;
+        }
+        if (a.group_lanes > 0) {
+            if (!((kept >> g) & 1u)) {
+                best.first = best.second = 0u;
+#pragma unroll
+                for (int i = 0; i < C; ++i) key[i] = 0u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const uint32_t gi = (static_cast<uint32_t>(e0 + i) * a.group_magic) >> 21;
+                if (gi >= 32u || !((kept >> gi) & 1u)) key[i] = 0u;
+            }
+            best.find<C>(key);
+        }
+    }
+
+    // k picks, pick r kept by the token's lane r.  A lane has its two best at
+    // hand; one that wins a third time looks again.
+    int mine = -1;
+    uint32_t mine_key = 0u;
+    for (int r = 0; r < a.chosen; ++r) {
+        const uint32_t top = lanes_max<L>(best.first);
+        const int src = first_lane<L>(best.first == top, lane);
+        const int e = __shfl_sync(kFullMask, e0 + best.slot, src);
+        if (sub == r && top != 0u) mine = e, mine_key = top;
+        const bool won = lane == src && top != 0u;
+        const uint32_t last = best.first;
+        const int at = best.slot;
+        if (won) {
+            best.first = best.second;
+            best.slot = best.next;
+            best.second = 0u;
+        }
+        if (won && best.first == 0u) best.find_after<C>(key, last, at);
+    }
+
+    // the chosen experts' weights
+    float w = 0.0f;
+    const bool there = mine >= 0;
+    const float xe = !there ? kNegInf : biased ? to_f32(row[mine]) : order_key_value(mine_key);
+    if (a.softmax) {
+        if (a.renormalise) {     // a softmax over the chosen alone
+            const float mc = lanes_max<L>(xe);
+            const float e = there ? exp_from(xe, mc) : 0.0f;
+            const float total = lanes_sum<L>(e);
+            w = total > 0.0f ? e / total : 0.0f;
+        } else if (there) {
+            w = exp_from(xe, m) / sum;
+        }
+    } else {
+        w = there ? sigmoid(xe) : 0.0f;
         if (a.renormalise) {
-            const float total = warp_sum(w);
+            const float total = lanes_sum<L>(w);
             w = total > 0.0f ? w / total : 0.0f;
         }
     }
-    if (lane < a.chosen) {
-        a.weights[token * a.chosen + lane] = w * a.scale;
-        a.experts_out[token * a.chosen + lane] = mine;
+    if (live && sub < a.chosen) {
+        a.weights[token * a.chosen + sub] = w * a.scale;
+        a.experts_out[token * a.chosen + sub] = mine;
     }
 }
 
@@ -225,38 +338,37 @@ struct RouteBackwardArgs {
     const int32_t *experts_in;
     void *grad_logits;
     float scale;
-    int experts, chosen;
-    bool softmax, renormalise, wide, wide_out;
+    int experts, chosen, access, access_out;
+    bool softmax, renormalise;
 };
 
-// Gradient of the weights by the logits, pick j in lane j, with dw scaled:
+// Gradient of the weights by the logits, pick j in the token's lane j, with dw
+// scaled:
 //   softmax                 dx_e = p_e * (dw_e [chosen] - sum_j dw_j p_j)
 //   softmax, renormalised   dx_j = q_j * (dw_j - sum_i dw_i q_i), chosen only
 //   sigmoid                 dx_j = dw_j * s_j (1 - s_j), chosen only
 //   sigmoid, renormalised   dx_j = (dw_j - sum_i dw_i q_i) / S * s_j (1 - s_j)
 // The choice itself, the groups and the bias have no gradient.  The dense row
 // is written first (zeros, or -p_e times the sum), then the chosen entries.
-template <typename T, int C>
-__global__ void __launch_bounds__(kRouteWarps * 32) k_route_backward(const RouteBackwardArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-    if (token >= a.tokens) return;
-    const T *row = static_cast<const T *>(a.logits) + token * a.row_stride;
-    T *out = static_cast<T *>(a.grad_logits) + token * a.experts;
-    const int e0 = lane * C;
+template <typename T, int C, int L>
+__global__ void __launch_bounds__(kRouteThreads) k_route_backward(const RouteBackwardArgs a) {
+    const int sub = threadIdx.x & (L - 1);
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / L) + threadIdx.x / L;
+    const bool live = token < a.tokens;
+    const T *row = static_cast<const T *>(a.logits) + (live ? token : 0) * a.row_stride;
+    T *out = static_cast<T *>(a.grad_logits) + (live ? token : 0) * a.experts;
+    const int e0 = sub * C;
 
     int e = -1;
     float d = 0.0f, xe = kNegInf;
-    if (lane < a.chosen) {
-        e = a.experts_in[token * a.chosen + lane];
+    if (live && sub < a.chosen) {
+        e = a.experts_in[token * a.chosen + sub];
         if (e >= 0 && e < a.experts) {
             xe = to_f32(row[e]);
-            d = a.grad_weights[token * a.chosen + lane] * a.scale;
-        } else {
-            e = -1;
+            d = a.grad_weights[token * a.chosen + sub] * a.scale;
         }
     }
-    const bool there = e >= 0 && xe > kNegInf;
+    const bool there = xe > kNegInf;
     if (!there) d = 0.0f;
 
     float g = 0.0f;          // gradient of the chosen entry
@@ -265,68 +377,57 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route_backward(const Route
     for (int i = 0; i < C; ++i) dense[i] = 0.0f;
     if (!a.softmax) {
         const float s = there ? sigmoid(xe) : 0.0f;
-        const float slope = there ? s * (1.0f / (1.0f + expf(xe))) : 0.0f;   // s (1 - s) without cancellation
+        const float slope = there ? s * __frcp_rn(1.0f + expf(xe)) : 0.0f;   // s (1 - s) without cancellation
         if (a.renormalise) {
-            const float total = warp_sum(s);
-            const float mean = warp_sum(total > 0.0f ? d * (s / total) : 0.0f);
+            const float total = lanes_sum<L>(s);
+            const float mean = lanes_sum<L>(total > 0.0f ? d * (s / total) : 0.0f);
             g = total > 0.0f ? (d - mean) / total * slope : 0.0f;
         } else {
             g = d * slope;
         }
     } else if (a.renormalise) {
-        const float m = warp_max(there ? xe : kNegInf);
-        const float q0 = there ? (xe == m ? 1.0f : expf(xe - m)) : 0.0f;
-        const float total = warp_sum(q0);
+        const float m = lanes_max<L>(there ? xe : kNegInf);
+        const float q0 = there ? exp_from(xe, m) : 0.0f;
+        const float total = lanes_sum<L>(q0);
         const float q = total > 0.0f ? q0 / total : 0.0f;
-        const float mean = warp_sum(d * q);
+        const float mean = lanes_sum<L>(d * q);
         g = q * (d - mean);
     } else {
-        float x[C], ex[C];
-        load_row<T, C>(row, a.experts, a.wide, lane, x);
-        const float m = row_max<C>(x);
-        row_exp<C>(x, m, ex);
-        const float sum = row_sum<C>(ex);
+        float x[C];
+        load_row<T, C>(row, a.experts, a.access, e0, x);
+        const float m = row_max<C, L>(x);
+        row_exp<C>(x, m, dense);
+        const float sum = row_sum<C, L>(dense);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const float p = there ? (xe == m ? 1.0f : expf(xe - m)) * inv : 0.0f;
-        const float mean = warp_sum(d * p);
+        const float p = there ? exp_from(xe, m) * inv : 0.0f;
+        const float mean = lanes_sum<L>(d * p);
         g = p * (d - mean);
 #pragma unroll
-        for (int i = 0; i < C; ++i) dense[i] = -(ex[i] * inv) * mean;
+        for (int i = 0; i < C; ++i) dense[i] = -(dense[i] * inv) * mean;
     }
-
-    constexpr int N = C * sizeof(T) <= 16 ? C : static_cast<int>(16 / sizeof(T));
-    if (a.wide_out && e0 + C <= a.experts) {
-#pragma unroll
-        for (int b = 0; b < C; b += N) {
-            Vec<T, N> v;
-#pragma unroll
-            for (int i = 0; i < N; ++i) v.e[i] = from_f32<T>(dense[b + i]);
-            *reinterpret_cast<Vec<T, N> *>(out + e0 + b) = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (e0 + i < a.experts) out[e0 + i] = from_f32<T>(dense[i]);
-    }
-    __syncwarp();            // the row's stores come before the chosen entries'
+    if (live) store_row<T, C>(out, a.experts, a.access_out, e0, dense);
+    __syncwarp();            // the rows' stores come before the chosen entries'
     if (there) out[e] = from_f32<T>(g);
 }
 
-// Whether rows of `experts` T at `base`, `stride` apart, can move as the
-// vectors of a lane with `per_lane` experts.
-template <typename T> bool wide_rows(const void *base, int64_t stride, int per_lane) {
-    const size_t bytes = std::min<size_t>(16, per_lane * sizeof(T));
-    return aligned(base, bytes) && (static_cast<size_t>(stride) * sizeof(T)) % bytes == 0;
+// Bytes, up to 16, that rows of T at `base`, `stride` apart, can move at once.
+template <typename T> int access_of(const void *base, int64_t stride) {
+    int bytes = 16;
+    while (bytes > static_cast<int>(sizeof(T)) && !(aligned(base, bytes) && static_cast<size_t>(stride) * sizeof(T) % bytes == 0)) bytes /= 2;
+    return bytes;
 }
 
-// Calls f with the smallest power of two C for which 32 * C >= experts.
-template <typename F> int with_slots(int experts, F &&f) {
-    if (experts <= 32) return f(std::integral_constant<int, 1>{});
-    if (experts <= 64) return f(std::integral_constant<int, 2>{});
-    if (experts <= 128) return f(std::integral_constant<int, 4>{});
-    if (experts <= 256) return f(std::integral_constant<int, 8>{});
-    if (experts <= 512) return f(std::integral_constant<int, 16>{});
-    return f(std::integral_constant<int, 32>{});
+// Calls f with (C, L): 8 experts to a lane up to 256 experts, and at least
+// `lanes` lanes.
+template <typename F> int with_shape(int experts, int lanes, F &&f) {
+    using std::integral_constant;
+    const int need = std::max((experts + 7) / 8, lanes);
+    if (need <= 4) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+    if (need <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    if (need <= 16) return f(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+    if (need <= 32) return f(integral_constant<int, 8>{}, integral_constant<int, 32>{});
+    if (need <= 64) return f(integral_constant<int, 16>{}, integral_constant<int, 32>{});
+    return f(integral_constant<int, 32>{}, integral_constant<int, 32>{});
 }
 
 }  // namespace
@@ -349,13 +450,17 @@ int launch_route(const RouteLaunch &L) {
     a.softmax = L.score == GSORT_SCORE_SOFTMAX;
     a.top2 = L.group_score == GSORT_GROUP_TOP2;
     a.renormalise = L.renormalise;
-    const uint32_t grid = static_cast<uint32_t>((L.tokens + kRouteWarps - 1) / kRouteWarps);
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
-        return with_slots(L.experts, [&](auto slots) {
-            constexpr int C = decltype(slots)::value;
-            a.wide = wide_rows<T>(L.logits, L.row_stride, C);
-            k_route<T, C><<<grid, kRouteWarps * 32, 0, L.stream>>>(a);
+        // without whole lanes to a group, a lane reads each group: as many lanes as groups
+        return with_shape(L.experts, std::max(L.chosen, L.groups), [&](auto slots, auto lanes) {
+            constexpr int C = decltype(slots)::value, W = decltype(lanes)::value;
+            a.access = access_of<T>(L.logits, L.row_stride);
+            a.bias_access = access_of<float>(L.bias, 0);
+            const int per = a.group_size / C;
+            a.group_lanes = a.group_size % C == 0 && (per & (per - 1)) == 0 ? per : 0;
+            const uint32_t grid = static_cast<uint32_t>((L.tokens + kRouteThreads / W - 1) / (kRouteThreads / W));
+            k_route<T, C, W><<<grid, kRouteThreads, 0, L.stream>>>(a);
             return cudaGetLastError() == cudaSuccess ? GSORT_OK : GSORT_ECUDA;
         });
     });
@@ -374,14 +479,14 @@ int launch_route_backward(const RouteBackwardLaunch &L) {
     a.chosen = L.chosen;
     a.softmax = L.score == GSORT_SCORE_SOFTMAX;
     a.renormalise = L.renormalise;
-    const uint32_t grid = static_cast<uint32_t>((L.tokens + kRouteWarps - 1) / kRouteWarps);
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
-        return with_slots(L.experts, [&](auto slots) {
-            constexpr int C = decltype(slots)::value;
-            a.wide = wide_rows<T>(L.logits, L.row_stride, C);
-            a.wide_out = wide_rows<T>(L.grad_logits, L.experts, C);
-            k_route_backward<T, C><<<grid, kRouteWarps * 32, 0, L.stream>>>(a);
+        return with_shape(L.experts, L.chosen, [&](auto slots, auto lanes) {
+            constexpr int C = decltype(slots)::value, W = decltype(lanes)::value;
+            a.access = access_of<T>(L.logits, L.row_stride);
+            a.access_out = access_of<T>(L.grad_logits, L.experts);
+            const uint32_t grid = static_cast<uint32_t>((L.tokens + kRouteThreads / W - 1) / (kRouteThreads / W));
+            k_route_backward<T, C, W><<<grid, kRouteThreads, 0, L.stream>>>(a);
             return cudaGetLastError() == cudaSuccess ? GSORT_OK : GSORT_ECUDA;
         });
     });

@@ -97,12 +97,16 @@ template <int L> __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
     return v;
 }
 
-// The token's first lane for which `p` holds, as a lane of the warp; one must.
-template <int L> __device__ __forceinline__ int first_lane(bool p, int lane) {
+// The lanes below this one that hold the same token.
+template <int L> __device__ __forceinline__ uint32_t lanes_before(int lane) {
+    return lanemask_lt() & ~((1u << (lane & ~(L - 1))) - 1u);
+}
+
+// Whether this is the token's first lane for which `p` holds.  The vote is the
+// whole warp's: it is taken before `p` is looked at.
+__device__ __forceinline__ bool is_first(bool p, uint32_t before) {
     const uint32_t votes = __ballot_sync(kFullMask, p);
-    if (L == 32) return __ffs(votes) - 1;
-    const int base = lane & ~(L - 1);
-    return base + __ffs((votes >> base) & ((1u << (L & 31)) - 1)) - 1;
+    return p && (votes & before) == 0u;
 }
 
 // Sum over a token's row in one fixed order: neighbours first.
@@ -121,10 +125,12 @@ template <int C, int L> __device__ __forceinline__ float row_sum(const float (&v
 // The largest candidate has 1 even at +inf.
 __device__ __forceinline__ float exp_from(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
+// The same for a whole row, where only sums and a gradient's dense part are
+// formed from it: 2 ulp and (x - m) 2^-24, and a third of the instructions.
 template <int C>
 __device__ __forceinline__ void row_exp(const float (&x)[C], float m, float (&e)[C]) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) e[i] = x[i] > kNegInf ? exp_from(x[i], m) : 0.0f;
+    for (int i = 0; i < C; ++i) e[i] = x[i] > kNegInf ? (x[i] == m ? 1.0f : exp2_approx((x[i] - m) * kLog2e)) : 0.0f;
 }
 
 // Largest candidate of the row (NaN is none); -inf where there is no candidate.
@@ -153,38 +159,86 @@ struct RouteArgs {
     bool softmax, top2, renormalise;
 };
 
-// The two largest order keys of a lane's candidates and their slots; ties to
-// the lower slot.  0: none.
-struct LaneBest {
-    uint32_t first, second;
-    int slot, next;
-
-    template <int C> __device__ __forceinline__ void find(const uint32_t (&key)[C]) {
-        first = second = 0u;
-        slot = next = 0;
+// Sorts C words in registers, largest first (Batcher's odd-even merge sort).
+template <int C> __device__ __forceinline__ void sort_desc(uint32_t (&v)[C]) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const bool best = key[i] > first, better = key[i] > second;
-            second = best ? first : better ? key[i] : second;
-            next = best ? slot : better ? i : next;
-            first = best ? key[i] : first;
-            slot = best ? i : slot;
+    for (int p = 1; p < C; p <<= 1)
+#pragma unroll
+        for (int k = p; k > 0; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < C; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < C && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t a = v[i + j], b = v[i + j + k];
+                        v[i + j] = max(a, b);
+                        v[i + j + k] = min(a, b);
+                    }
+}
+
+// The k best candidates by their full keys, each lane looking through all of
+// its own for every pick; pick r's expert is left in picks[r], -1 beyond the
+// candidates.
+template <int C, int L>
+__device__ __noinline__ void pick_exactly(const uint32_t (&key)[C], int chosen, int lane, int32_t *picks) {
+    const int e0 = (lane & (L - 1)) * C;
+    const uint32_t before = lanes_before<L>(lane);
+    uint32_t last = 0xFFFFFFFFu;     // this lane's last pick: candidates that follow it are left
+    int at = -1;
+    for (int r = 0; r < chosen; ++r) {
+        uint32_t best = 0u;
+        int slot = 0;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if ((key[i] < last || (key[i] == last && i > at)) && key[i] > best) best = key[i], slot = i;
+        const uint32_t top = lanes_max<L>(best);
+        if (is_first(best == top, before)) {
+            picks[r] = top != 0u ? e0 + slot : -1;
+            last = best;
+            at = slot;
         }
     }
+}
 
-    // The two that follow (last, at) in order.
-    template <int C> __device__ __forceinline__ void find_after(const uint32_t (&key)[C], uint32_t last, int at) {
-        uint32_t rest[C];
+// The same with one word for a candidate: its key with the last bits given to
+// the slot, lower slots first.  Each lane sorts its words beforehand and keeps
+// them in shared memory, so that a pick is a maximum, a vote, and the winner's
+// next word.  Returns whether keys that differ in the bits given up met: two
+// picks one after the other, or the last and what is left, are then equal in
+// the others.
+template <int C, int L>
+__device__ __forceinline__ bool pick_sorted(const uint32_t (&key)[C], int chosen, int lane, uint32_t *words, int32_t *picks) {
+    constexpr uint32_t kSlot = C - 1;
+    const int e0 = (lane & (L - 1)) * C;
+    const uint32_t before = lanes_before<L>(lane);
+    uint32_t v[C];
 #pragma unroll
-        for (int i = 0; i < C; ++i) rest[i] = key[i] < last || (key[i] == last && i > at) ? key[i] : 0u;
-        find<C>(rest);
+    for (int i = 0; i < C; ++i) v[i] = (key[i] & ~kSlot) | (kSlot - i);    // up to kSlot: no candidate
+    sort_desc<C>(v);
+    uint32_t *mine = words + lane * (C + 1);
+#pragma unroll
+    for (int i = 0; i < C; ++i) mine[i] = v[i];
+    mine[C] = 0u;
+    uint32_t head = v[0], last = ~0u;
+    int next = 1;
+    bool met = false;
+#pragma unroll 1
+    for (int r = 0; r < chosen; ++r) {
+        const uint32_t top = lanes_max<L>(head);
+        met |= (top ^ last) <= kSlot;
+        last = top > kSlot ? top : ~0u;
+        if (is_first((head ^ top) <= kSlot, before)) {
+            picks[r] = head > kSlot ? e0 + static_cast<int>(kSlot - (head & kSlot)) : -1;
+            head = mine[min(next++, C)];
+        }
     }
-};
+    return met | ((lanes_max<L>(head) ^ last) <= kSlot);
+}
 
 template <typename T, int C, int L>
 __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
-    // group values that other lanes read; one word of padding for 32
-    __shared__ float s_value[kRouteThreads / 32][32 * C + C];
+    __shared__ uint32_t s_words[kRouteThreads / 32][32 * (C + 1)];
+    __shared__ int32_t s_picks[kRouteThreads];       // a token's picks, one for each of its lanes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (L - 1);
     const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRouteThreads / L) + threadIdx.x / L;
     const bool live = token < a.tokens;      // every lane goes through the warp's votes
@@ -218,39 +272,36 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
 #pragma unroll
         for (int i = 0; i < C; ++i) key[i] = x[i] > kNegInf ? order_key(x[i]) : 0u;
     }
-    LaneBest best;
-    best.find<C>(key);
 
     if (a.groups > 1) {
-        // the largest keys of a group; scores grow with their keys
-        const int per = a.group_lanes > 0 ? a.group_lanes : 1;
-        int g;
-        uint32_t first, second;
+        // the two largest keys of a group; scores grow with their keys
+        const int per = a.group_lanes > 0 ? a.group_lanes : 1, g = sub / per;
+        uint32_t first = 0u, second = 0u;
         if (a.group_lanes > 0) {
-            g = sub / per;
-            first = best.first;
-            second = best.second;
-        } else {
-            // groups that end inside a lane: one lane reads a group's keys
-            uint32_t *sk = reinterpret_cast<uint32_t *>(s_value[warp]);
-            const int w0 = (lane & ~(L - 1)) * C;
 #pragma unroll
-            for (int i = 0; i < C; ++i) sk[w0 + e0 + i + ((w0 + e0 + i) >> 5)] = key[i];
+            for (int i = 0; i < C; ++i) {
+                second = max(second, min(first, key[i]));
+                first = max(first, key[i]);
+            }
+            for (int o = 1; o < per; o <<= 1) {
+                const uint32_t f = __shfl_xor_sync(kFullMask, first, o), s = __shfl_xor_sync(kFullMask, second, o);
+                second = max(max(second, s), min(first, f));
+                first = max(first, f);
+            }
+        } else {
+            // groups that end inside a lane: lane g reads group g's keys (there are as many lanes)
+            uint32_t *sk = s_words[warp];
+#pragma unroll
+            for (int i = 0; i < C; ++i) sk[lane * (C + 1) + i] = key[i];
             __syncwarp();
-            first = second = 0u;
-            g = sub;                 // at least as many lanes as groups
             if (g < a.groups)
                 for (int i = 0; i < a.group_size; ++i) {
-                    const int e = w0 + g * a.group_size + i;
-                    const uint32_t v = sk[e + (e >> 5)];
+                    const int e = (lane & ~(L - 1)) * C + g * a.group_size + i;
+                    const uint32_t v = sk[e / C * (C + 1) + e % C];
                     second = max(second, min(first, v));
                     first = max(first, v);
                 }
-        }
-        for (int o = 1; o < per; o <<= 1) {
-            const uint32_t f = __shfl_xor_sync(kFullMask, first, o), s = __shfl_xor_sync(kFullMask, second, o);
-            second = max(max(second, s), min(first, f));
-            first = max(first, f);
+            __syncwarp();
         }
         uint32_t gkey = 0u;
         if (g < a.groups && first != 0u && sub % per == 0) {
@@ -262,53 +313,43 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
                 gkey = order_key(second != 0u ? value + other : value);
             }
         }
-        uint32_t kept = 0;
+        bool keep = false;       // in a group's first lane: it is one of the best
+        const uint32_t before = lanes_before<L>(lane);
         for (int r = 0; r < a.groups_kept; ++r) {
             const uint32_t top = lanes_max<L>(gkey);
-            const int src = first_lane<L>(gkey == top, lane);
-            if (top != 0u) kept |= 1u << ((src & (L - 1)) / per);
-            if (lane == src) gkey = 0u;
+            if (is_first(gkey == top, before) && top != 0u) {
+                keep = true;
+                gkey = 0u;
+            }
         }
         if (a.group_lanes > 0) {
-            if (!((kept >> g) & 1u)) {
-                best.first = best.second = 0u;
+            keep = __shfl_sync(kFullMask, keep, lane & ~(per - 1));
 #pragma unroll
-                for (int i = 0; i < C; ++i) key[i] = 0u;
-            }
+            for (int i = 0; i < C; ++i) key[i] = keep ? key[i] : 0u;
         } else {
+            const uint32_t kept = __ballot_sync(kFullMask, keep) >> (lane & ~(L - 1));
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 const uint32_t gi = (static_cast<uint32_t>(e0 + i) * a.group_magic) >> 21;
-                if (gi >= 32u || !((kept >> gi) & 1u)) key[i] = 0u;
+                if (gi >= static_cast<uint32_t>(L) || !((kept >> gi) & 1u)) key[i] = 0u;
             }
-            best.find<C>(key);
         }
     }
 
-    // k picks, pick r kept by the token's lane r.  A lane has its two best at
-    // hand; one that wins a third time looks again.
-    int mine = -1;
-    uint32_t mine_key = 0u;
-    for (int r = 0; r < a.chosen; ++r) {
-        const uint32_t top = lanes_max<L>(best.first);
-        const int src = first_lane<L>(best.first == top, lane);
-        const int e = __shfl_sync(kFullMask, e0 + best.slot, src);
-        if (sub == r && top != 0u) mine = e, mine_key = top;
-        const bool won = lane == src && top != 0u;
-        const uint32_t last = best.first;
-        const int at = best.slot;
-        if (won) {
-            best.first = best.second;
-            best.slot = best.next;
-            best.second = 0u;
-        }
-        if (won && best.first == 0u) best.find_after<C>(key, last, at);
+    int32_t *picks = s_picks + (threadIdx.x & ~(L - 1));
+    const bool met = pick_sorted<C, L>(key, a.chosen, lane, s_words[warp], picks);
+    // 16-bit logits have no bits there: equal words are equal logits
+    __syncwarp();
+    if ((sizeof(T) == 4 || biased) && __any_sync(kFullMask, met)) {
+        pick_exactly<C, L>(key, a.chosen, lane, picks);
+        __syncwarp();
     }
+    const int mine = sub < a.chosen ? picks[sub] : -1;
 
     // the chosen experts' weights
     float w = 0.0f;
     const bool there = mine >= 0;
-    const float xe = !there ? kNegInf : biased ? to_f32(row[mine]) : order_key_value(mine_key);
+    const float xe = there ? to_f32(row[mine]) : kNegInf;
     if (a.softmax) {
         if (a.renormalise) {     // a softmax over the chosen alone
             const float mc = lanes_max<L>(xe);

@@ -12,10 +12,14 @@
 //
 // L lanes (a power of two, at least k) hold one token, C experts each: lane l
 // keeps experts [l * C, (l + 1) * C) in registers, so lower lanes hold lower
-// indices and the tie rule is "lowest lane, then lowest slot".  C is 8 up to 256
-// experts, so that 64 experts take 8 lanes and a warp works on 4 tokens at once.
-// A pick is a maximum of 32-bit order keys over the lanes (redux.sync for a
-// whole warp), one ballot and one shuffle.
+// indices and the tie rule is "lowest lane, then lowest slot".  64 experts take 4
+// lanes, and a warp works on 8 tokens at once.  Each lane sorts its candidates;
+// a pick is then a maximum over the lanes' best (redux.sync for a whole warp),
+// one vote and the winner's next candidate.
+//
+// Bound by instructions, about 550 a token at 256 experts and k = 8, not by its
+// bytes: 16384 x 256 32-bit logits with bias and groups take 15.5 us, where
+// reading them takes 2.5.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -159,44 +163,64 @@ struct RouteArgs {
     bool softmax, top2, renormalise;
 };
 
-// Sorts C words in registers, largest first (Batcher's odd-even merge sort).
-template <int C> __device__ __forceinline__ void sort_desc(uint32_t (&v)[C]) {
-#pragma unroll
-    for (int p = 1; p < C; p <<= 1)
-#pragma unroll
-        for (int k = p; k > 0; k >>= 1)
-#pragma unroll
-            for (int j = k % p; j + k < C; j += 2 * k)
-#pragma unroll
-                for (int i = 0; i < k; ++i)
-                    if (i + j + k < C && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-                        const uint32_t a = v[i + j], b = v[i + j + k];
-                        v[i + j] = max(a, b);
-                        v[i + j + k] = min(a, b);
-                    }
+// Batcher's odd-even merge sort of C words in registers, largest first.  The
+// recursion is over constants, so that every index is one.
+template <int A, int B, int C> __device__ __forceinline__ void exchange(uint32_t (&v)[C]) {
+    const uint32_t a = v[A], b = v[B];
+    v[A] = max(a, b);
+    v[B] = min(a, b);
+}
+
+template <int LO, int N, int STEP, int C, int I = LO + STEP> __device__ __forceinline__ void exchange_odd(uint32_t (&v)[C]) {
+    if constexpr (I + STEP < LO + N) {
+        exchange<I, I + STEP>(v);
+        exchange_odd<LO, N, STEP, C, I + 2 * STEP>(v);
+    }
+}
+
+// Merges the sorted halves of every STEP-th word of [LO, LO + N).
+template <int LO, int N, int STEP, int C> __device__ __forceinline__ void merge_halves(uint32_t (&v)[C]) {
+    if constexpr (2 * STEP < N) {
+        merge_halves<LO, N, 2 * STEP>(v);
+        merge_halves<LO + STEP, N, 2 * STEP>(v);
+        exchange_odd<LO, N, STEP>(v);
+    } else {
+        exchange<LO, LO + STEP>(v);
+    }
+}
+
+template <int LO, int N, int C> __device__ __forceinline__ void sort_desc(uint32_t (&v)[C]) {
+    if constexpr (N > 1) {
+        sort_desc<LO, N / 2>(v);
+        sort_desc<LO + N / 2, N / 2>(v);
+        merge_halves<LO, N, 1>(v);
+    }
 }
 
 // The k best candidates by their full keys, each lane looking through all of
 // its own for every pick; pick r's expert is left in picks[r], -1 beyond the
-// candidates.
+// candidates.  Rarely needed, but a whole launch may wait for one warp that
+// does: without a branch in the loop over the slots it takes about a
+// microsecond, with some it took eight.
 template <int C, int L>
-__device__ __noinline__ void pick_exactly(const uint32_t (&key)[C], int chosen, int lane, int32_t *picks) {
+__device__ __forceinline__ void pick_exactly(uint32_t (&key)[C], int chosen, int lane, int32_t *picks) {
     const int e0 = (lane & (L - 1)) * C;
     const uint32_t before = lanes_before<L>(lane);
-    uint32_t last = 0xFFFFFFFFu;     // this lane's last pick: candidates that follow it are left
-    int at = -1;
+#pragma unroll 1
     for (int r = 0; r < chosen; ++r) {
         uint32_t best = 0u;
         int slot = 0;
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            if ((key[i] < last || (key[i] == last && i > at)) && key[i] > best) best = key[i], slot = i;
-        const uint32_t top = lanes_max<L>(best);
-        if (is_first(best == top, before)) {
-            picks[r] = top != 0u ? e0 + slot : -1;
-            last = best;
-            at = slot;
+        for (int i = 0; i < C; ++i) {
+            slot = key[i] > best ? i : slot;
+            best = max(best, key[i]);
         }
+        const uint32_t top = lanes_max<L>(best);
+        const bool won = is_first(best == top, before);
+        if (won) picks[r] = top != 0u ? e0 + slot : -1;
+        slot = won ? slot : -1;
+#pragma unroll
+        for (int i = 0; i < C; ++i) key[i] = i == slot ? 0u : key[i];
     }
 }
 
@@ -214,7 +238,7 @@ __device__ __forceinline__ bool pick_sorted(const uint32_t (&key)[C], int chosen
     uint32_t v[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] = (key[i] & ~kSlot) | (kSlot - i);    // up to kSlot: no candidate
-    sort_desc<C>(v);
+    sort_desc<0, C>(v);
     uint32_t *mine = words + lane * (C + 1);
 #pragma unroll
     for (int i = 0; i < C; ++i) mine[i] = v[i];
@@ -249,24 +273,31 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
     load_row<T, C>(row, a.experts, a.access, e0, x);
 
     const bool biased = a.bias != nullptr;
-    float m = kNegInf, sum = 0.0f;
+    float m = kNegInf, inv = 0.0f;       // softmax: the row's largest logit and 1 / sum
+    float c[C];
     if (a.softmax && (biased || !a.renormalise || (a.groups > 1 && a.top2))) {
         m = row_max<C, L>(x);
-        float e[C];
-        row_exp<C>(x, m, e);
-        sum = row_sum<C, L>(e);
+        row_exp<C>(x, m, c);
+        const float sum = row_sum<C, L>(c);
+        inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    auto score = [&](float v) { return a.softmax ? exp_from(v, m) / sum : sigmoid(v); };
 
     // order keys of the choice values; 0: no candidate
     uint32_t key[C];
     if (biased) {
+        if (a.softmax) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) c[i] *= inv;
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; ++i) c[i] = sigmoid(x[i]);
+        }
         float b[C];
         load_row<float, C>(a.bias, a.experts, a.bias_access, e0, b);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const float c = score(x[i]) + b[i];
-            key[i] = x[i] > kNegInf && c > kNegInf ? order_key(c) : 0u;
+            const float v = c[i] + b[i];
+            key[i] = x[i] > kNegInf && v > kNegInf ? order_key(v) : 0u;
         }
     } else {
 #pragma unroll
@@ -309,7 +340,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
                 gkey = first;
             } else {
                 float value = order_key_value(first), other = order_key_value(second);
-                if (!biased) value = score(value), other = score(other);
+                if (!biased && a.softmax) value = exp_from(value, m) * inv, other = exp_from(other, m) * inv;
+                if (!biased && !a.softmax) value = sigmoid(value), other = sigmoid(other);
                 gkey = order_key(second != 0u ? value + other : value);
             }
         }
@@ -353,18 +385,16 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
     if (a.softmax) {
         if (a.renormalise) {     // a softmax over the chosen alone
             const float mc = lanes_max<L>(xe);
-            const float e = there ? exp_from(xe, mc) : 0.0f;
-            const float total = lanes_sum<L>(e);
-            w = total > 0.0f ? e / total : 0.0f;
+            w = there ? exp_from(xe, mc) : 0.0f;
         } else if (there) {
-            w = exp_from(xe, m) / sum;
+            w = exp_from(xe, m) * inv;
         }
     } else {
         w = there ? sigmoid(xe) : 0.0f;
-        if (a.renormalise) {
-            const float total = lanes_sum<L>(w);
-            w = total > 0.0f ? w / total : 0.0f;
-        }
+    }
+    if (a.renormalise) {
+        const float total = lanes_sum<L>(w);
+        w *= total > 0.0f ? 1.0f / total : 0.0f;    // one quotient a token, none of zero
     }
     if (live && sub < a.chosen) {
         a.weights[token * a.chosen + sub] = w * a.scale;
@@ -420,9 +450,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(const RouteBac
         const float s = there ? sigmoid(xe) : 0.0f;
         const float slope = there ? s * __frcp_rn(1.0f + expf(xe)) : 0.0f;   // s (1 - s) without cancellation
         if (a.renormalise) {
-            const float total = lanes_sum<L>(s);
-            const float mean = lanes_sum<L>(total > 0.0f ? d * (s / total) : 0.0f);
-            g = total > 0.0f ? (d - mean) / total * slope : 0.0f;
+            const float total = lanes_sum<L>(s), inv = total > 0.0f ? 1.0f / total : 0.0f;
+            g = (d - lanes_sum<L>(d * (s * inv))) * inv * slope;
         } else {
             g = d * slope;
         }
@@ -430,7 +459,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(const RouteBac
         const float m = lanes_max<L>(there ? xe : kNegInf);
         const float q0 = there ? exp_from(xe, m) : 0.0f;
         const float total = lanes_sum<L>(q0);
-        const float q = total > 0.0f ? q0 / total : 0.0f;
+        const float q = q0 * (total > 0.0f ? 1.0f / total : 0.0f);
         const float mean = lanes_sum<L>(d * q);
         g = q * (d - mean);
     } else {
@@ -458,16 +487,23 @@ template <typename T> int access_of(const void *base, int64_t stride) {
     return bytes;
 }
 
-// Calls f with (C, L): 8 experts to a lane up to 256 experts, and at least
-// `lanes` lanes.
-template <typename F> int with_shape(int experts, int lanes, F &&f) {
+// Calls f with (C, L), at least `lanes` lanes to a token.  Measured, routing of
+// bf16 logits with k = 8 in us:
+//   up to 1024 tokens every one gets a warp (128 experts: 3.0 for 8 tokens, 4.2
+//   with 16 lanes each: redux.sync instead of shuffles);
+//   16 experts to a lane from 33 experts on (65536 x 128: 15 against 23 with 8,
+//   x 256: 31 against 40), 8 up to 32 experts (x 16, k = 2: 5.2 against 7.3),
+//   32 only where they must be.
+template <typename F> int with_shape(int64_t tokens, int experts, int lanes, F &&f) {
     using std::integral_constant;
-    const int need = std::max((experts + 7) / 8, lanes);
-    if (need <= 4) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
-    if (need <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
-    if (need <= 16) return f(integral_constant<int, 8>{}, integral_constant<int, 16>{});
-    if (need <= 32) return f(integral_constant<int, 8>{}, integral_constant<int, 32>{});
-    if (need <= 64) return f(integral_constant<int, 16>{}, integral_constant<int, 32>{});
+    if (tokens <= 1024 && experts <= 256) return f(integral_constant<int, 8>{}, integral_constant<int, 32>{});
+    if (experts <= 32 && lanes <= 4) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+    if (experts <= 32 && lanes <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    const int need = std::max((experts + 15) / 16, lanes);
+    if (need <= 4) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    if (need <= 8) return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    if (need <= 16) return f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    if (need <= 32) return f(integral_constant<int, 16>{}, integral_constant<int, 32>{});
     return f(integral_constant<int, 32>{}, integral_constant<int, 32>{});
 }
 
@@ -494,7 +530,7 @@ int launch_route(const RouteLaunch &L) {
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
         // without whole lanes to a group, a lane reads each group: as many lanes as groups
-        return with_shape(L.experts, std::max(L.chosen, L.groups), [&](auto slots, auto lanes) {
+        return with_shape(L.tokens, L.experts, std::max(L.chosen, L.groups), [&](auto slots, auto lanes) {
             constexpr int C = decltype(slots)::value, W = decltype(lanes)::value;
             a.access = access_of<T>(L.logits, L.row_stride);
             a.bias_access = access_of<float>(L.bias, 0);
@@ -522,7 +558,7 @@ int launch_route_backward(const RouteBackwardLaunch &L) {
     a.renormalise = L.renormalise;
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
-        return with_shape(L.experts, L.chosen, [&](auto slots, auto lanes) {
+        return with_shape(L.tokens, L.experts, L.chosen, [&](auto slots, auto lanes) {
             constexpr int C = decltype(slots)::value, W = decltype(lanes)::value;
             a.access = access_of<T>(L.logits, L.row_stride);
             a.access_out = access_of<T>(L.grad_logits, L.experts);

@@ -265,7 +265,10 @@ int gsort_combine_rows_backward(const void *d_grad_out, int dtype, int64_t token
                        {d_weights, pairs * 4}, {d_positions, pairs * 4}, {d_rows, static_cast<size_t>(capacity) * 4}};
     const Span out[] = {rows_span(d_grad_y, capacity, width, width, size), {d_grad_weights, pairs * 4}};
     if (clash(in, out)) return GSORT_EINVAL;
+    DeviceInfo dev;
+    if (device_info(&dev) != GSORT_OK) return GSORT_ECUDA;
     RowsLaunch L{};
+    L.sm_count = dev.sm_count;
     L.dtype = dtype;
     L.tokens = tokens;
     L.width = width;

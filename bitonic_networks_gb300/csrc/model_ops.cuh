@@ -208,6 +208,7 @@ struct RowsLaunch {
     void *out;                  // contiguous
     float *grad_weights;
     cudaStream_t stream;
+    int sm_count;
 };
 int launch_dispatch(const RowsLaunch &L);
 int launch_combine(const RowsLaunch &L);

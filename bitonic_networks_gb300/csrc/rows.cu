@@ -9,7 +9,16 @@
 //
 // Every kernel walks the tokens, not the grouped rows: a token's row is read
 // once and written to (or summed from) its k places, so the traffic is the
-// algorithm's own.  Sums run over j in order, in 32 bits, rounded once.
+// algorithm's own, and the memory bounds it.  Sums run over j in order, in 32
+// bits, rounded once.
+//
+// Rows move in 16-byte vectors.  Where the width, a stride or a base is not a
+// multiple of 16 bytes, rows start anywhere: a row that is written is cut at its
+// own 16-byte boundaries (its first and last elements are written one by one),
+// and a row that is read gives 16 bytes at any element from the two aligned
+// vectors around them.  Those may hold elements of the neighbouring rows, which
+// are not used, but never bytes outside the array: at its ends elements are read
+// one by one.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -18,129 +27,292 @@ namespace gsort {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kDotThreads = 128;
+// CTAs per SM that a kernel's registers leave room for where rows start
+// anywhere: loads wait for memory, and more of them do with more CTAs (8191 x 6
+// rows of 1001 32-bit elements: combine 45 us with 4 CTAs of 2 x 2 loads per
+// thread, 67 with 3 of 4; backward 84 with 6 CTAs, 89 with 4).
+constexpr int kShiftedCombine = 4, kShiftedBackward = 6;
+
+// Addresses at which 32 bytes of an array can be read; none where last < first.
+struct ReadSpan {
+    uintptr_t first, last;
+};
 
 template <typename T> struct RowArgs {
     const T *by_token;
     const T *by_row;
+    ReadSpan token_span, row_span;
     T *out;
     const int32_t *positions;
     const int32_t *rows;
     const float *weights;
     float *grad_weights;
-    int64_t tokens, token_stride, row_stride, out_stride;
-    uint32_t chosen, capacity, vectors;   // vectors per row
-    uint32_t row_blocks;                  // CTAs that move rows; the rest fill with zeros
+    int64_t token_stride, row_stride;
+    uint32_t tokens, chosen, capacity, width;
+    uint32_t vectors;        // vectors that a written row touches, at most
+    uint32_t log_lanes;      // 2^log_lanes threads side by side on a row
+    uint32_t chunks;         // a row's pieces of lanes * U vectors
+    uint32_t fill_rows, fill_blocks;   // rows that a CTA looks over to zero them; such CTAs: the rest move rows
 };
 
-template <typename T, int N> __device__ __forceinline__ Vec<T, N> load_vec(const T *row, uint32_t v) {
-    return reinterpret_cast<const Vec<T, N> *>(row)[v];
+// How rows are read: every row starts and ends at 16 bytes; anywhere; or element
+// by element, for arrays that hold no two aligned vectors.
+enum RowMode { kAligned, kShifted, kElements };
+
+// 16 bytes of a row from element e on, in two steps, so that several can be in
+// flight: the loads, which do not branch, and the shift.  Elements outside the
+// row have any value.
+struct Loaded {
+    uint4 q, r;
+};
+
+template <typename T> __device__ __forceinline__ uintptr_t address_of(const T *row, int32_t e) {
+    return reinterpret_cast<uintptr_t>(row) + static_cast<int64_t>(e) * static_cast<int64_t>(sizeof(T));
 }
 
-// Zeros the rows that no pair holds: a warp looks over 32 rows at a time.
-template <typename T, int N>
-__device__ __forceinline__ void fill_rows(const RowArgs<T> &a, uint32_t block) {
-    Vec<T, N> zero;
-#pragma unroll
-    for (int i = 0; i < N; ++i) zero.e[i] = from_f32<T>(0.0f);
-    const uint32_t lane = threadIdx.x & 31;
-    const uint32_t first = (block * (blockDim.x >> 5) + (threadIdx.x >> 5)) * 32;
-    const uint32_t r = first + lane;
-    uint32_t empty = __ballot_sync(kFullMask, r < a.capacity && a.rows[r] < 0);
-    while (empty) {
-        const uint32_t b = __ffs(empty) - 1;
-        empty &= empty - 1;
-        Vec<T, N> *o = reinterpret_cast<Vec<T, N> *>(a.out + static_cast<int64_t>(first + b) * a.out_stride);
-        for (uint32_t v = lane; v < a.vectors; v += 32) o[v] = zero;
+template <typename T, int MODE>
+__device__ __forceinline__ Loaded start_read(const T *row, int32_t e, const ReadSpan &span) {
+    Loaded x;
+    if (MODE == kAligned) {
+        x.q = *reinterpret_cast<const uint4 *>(row + e);
+    } else if (MODE == kShifted) {
+        const uintptr_t low = address_of(row, e) & ~static_cast<uintptr_t>(15);
+        const uint4 *p = reinterpret_cast<const uint4 *>(min(max(low, span.first), span.last));
+        x.q = p[0];
+        x.r = p[1];
     }
+    return x;
 }
 
-template <typename T, int N>
-__global__ void __launch_bounds__(kRowThreads) k_dispatch(const RowArgs<T> a) {
-    if (blockIdx.x >= a.row_blocks) {
-        fill_rows<T, N>(a, blockIdx.x - a.row_blocks);
-        return;
+template <typename T, int MODE>
+__device__ __forceinline__ uint4 end_read(const Loaded &x, const T *row, int32_t e, uint32_t width, const ReadSpan &span) {
+    constexpr int N = Wide<T>::kCount;
+    if (MODE == kAligned) return x.q;
+    const uintptr_t at = address_of(row, e), low = at & ~static_cast<uintptr_t>(15);
+    uint4 q;
+    if (MODE == kShifted) {
+        uint32_t w[5] = {x.q.x, x.q.y, x.q.z, x.q.w, x.r.x};
+        const bool two = at & 8, one = at & 4;
+        w[0] = two ? x.q.z : x.q.x;
+        w[1] = two ? x.q.w : x.q.y;
+        w[2] = two ? x.r.x : x.q.z;
+        w[3] = two ? x.r.y : x.q.w;
+        w[4] = two ? x.r.z : x.r.x;
+        const uint32_t after = two ? x.r.w : x.r.y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = one ? w[i + 1] : w[i];
+        w[4] = one ? after : w[4];
+        if (sizeof(T) == 2) {
+            const uint32_t bits = (at & 2) * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+        }
+        q = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-    const uint64_t t = i / a.vectors;
-    const uint32_t v = static_cast<uint32_t>(i - t * a.vectors);
-    if (t >= static_cast<uint64_t>(a.tokens)) return;
-    const Vec<T, N> x = load_vec<T, N>(a.by_token + t * a.token_stride, v);
-    const int32_t *pos = a.positions + t * a.chosen;
-    for (uint32_t j = 0; j < a.chosen; ++j) {
-        const uint32_t p = static_cast<uint32_t>(pos[j]);
-        if (p < a.capacity) reinterpret_cast<Vec<T, N> *>(a.out + p * a.out_stride)[v] = x;
+    if (MODE == kElements || low < span.first || low > span.last) {      // the array's ends
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = static_cast<uint32_t>(e + i) < width ? to_f32(row[e + i]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, pair(f[2 * i], f[2 * i + 1]));
     }
+    return q;
 }
 
-template <typename T, int N>
-__global__ void __launch_bounds__(kRowThreads) k_combine(const RowArgs<T> a) {
-    const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-    const uint64_t t = i / a.vectors;
-    const uint32_t v = static_cast<uint32_t>(i - t * a.vectors);
-    if (t >= static_cast<uint64_t>(a.tokens)) return;
-    const int32_t *pos = a.positions + t * a.chosen;
-    const float *w = a.weights ? a.weights + t * a.chosen : nullptr;
-    float acc[N];
+// A row that is written: vector v holds its elements from first(v) on.
+template <typename T, int MODE> struct OutRow {
+    T *row;
+    int32_t shift;           // elements between the boundary at or before the row and the row
+
+    __device__ __forceinline__ explicit OutRow(T *r)
+        : row(r), shift(MODE == kAligned ? 0 : static_cast<int32_t>((reinterpret_cast<uintptr_t>(r) & 15) / sizeof(T))) {}
+    __device__ __forceinline__ int32_t first(uint32_t v) const { return static_cast<int32_t>(v * Wide<T>::kCount) - shift; }
+    __device__ __forceinline__ void write(int32_t e, uint32_t width, const uint4 &q) const {
+        constexpr int N = Wide<T>::kCount;
+        if (MODE == kAligned || (e >= 0 && e + N <= static_cast<int32_t>(width))) {
+            *reinterpret_cast<uint4 *>(row + e) = q;
+        } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-#pragma unroll 8
-    for (uint32_t j = 0; j < a.chosen; ++j) {
-        const uint32_t p = static_cast<uint32_t>(pos[j]);
-        if (p < a.capacity) {
-            const Vec<T, N> y = load_vec<T, N>(a.by_row + p * a.row_stride, v);
-            const float wj = w ? w[j] : 1.0f;
-#pragma unroll
-            for (int e = 0; e < N; ++e) acc[e] = fmaf(wj, to_f32(y.e[e]), acc[e]);
+            for (int i = 0; i < N; ++i)
+                if (static_cast<uint32_t>(e + i) < width) row[e + i] = Wide<T>::element(q, i);
         }
     }
-    Vec<T, N> o;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o.e[e] = from_f32<T>(acc[e]);
-    reinterpret_cast<Vec<T, N> *>(a.out + t * a.out_stride)[v] = o;
+};
+
+// Zeros the rows that no pair holds.  A warp looks over 32 rows; of wide ones
+// (2 KB and more) the CTA's warps look over the same and take them in turn.
+// These CTAs come first, so that a long run of such rows (the end of the layout)
+// is under way while the others are moved (256 experts padded to 16, 16384 x 8
+// rows of 8 KB: 189 us, and 220 when they came last with 32 rows to a warp).
+template <typename T, int MODE> __device__ __forceinline__ void fill_rows(const RowArgs<T> &a) {
+    constexpr uint32_t kWarps = kRowThreads / 32;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t first = a.fill_rows == 32 ? blockIdx.x * 32 : (blockIdx.x * kWarps + warp) * 32;
+    uint32_t empty = __ballot_sync(kFullMask, first + lane < a.capacity && a.rows[first + lane] < 0);
+    for (uint32_t n = 0; empty; ++n, empty &= empty - 1) {
+        if (a.fill_rows == 32 && n % kWarps != warp) continue;
+        const OutRow<T, MODE> o(a.out + static_cast<int64_t>(first + __ffs(empty) - 1) * a.width);
+        for (uint32_t v = lane; v < a.vectors; v += 32) o.write(o.first(v), a.width, make_uint4(0, 0, 0, 0));
+    }
 }
 
-// One CTA per token: dy rows are written and the dot products are summed over
-// the CTA in a fixed order.
-template <typename T, int N>
-__global__ void __launch_bounds__(kDotThreads) k_combine_backward(const RowArgs<T> a) {
-    if (blockIdx.x >= a.row_blocks) {
-        fill_rows<T, N>(a, blockIdx.x - a.row_blocks);
+// The token and the first vector of this thread: 2^log_lanes threads walk a
+// chunk of U vectors each of a token's row side by side.
+struct RowPlace {
+    uint32_t token, v;
+};
+
+template <int U, typename T> __device__ __forceinline__ RowPlace row_place(const RowArgs<T> &a) {
+    const uint32_t lanes = 1u << a.log_lanes;
+    const uint32_t block = blockIdx.x - a.fill_blocks, group = block / a.chunks, chunk = block % a.chunks;
+    return {group * (kRowThreads >> a.log_lanes) + (threadIdx.x >> a.log_lanes), chunk * lanes * U + (threadIdx.x & (lanes - 1))};
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kRowThreads) k_dispatch(const RowArgs<T> a) {
+    if (blockIdx.x < a.fill_blocks) {
+        fill_rows<T, MODE>(a);
         return;
     }
-    __shared__ float s_dot[kDotThreads / 32];
-    const int64_t t = blockIdx.x;
-    const T *d_row = a.by_token + t * a.token_stride;
+    const RowPlace at = row_place<1>(a);
+    if (at.token >= a.tokens || at.v >= a.vectors) return;
+    const T *row = a.by_token + at.token * a.token_stride;
+    uint4 q;
+    if (MODE == kAligned) q = start_read<T, MODE>(row, at.v * Wide<T>::kCount, a.token_span).q;
+    const int32_t *pos = a.positions + static_cast<int64_t>(at.token) * a.chosen;
+#pragma unroll 4
     for (uint32_t j = 0; j < a.chosen; ++j) {
-        const uint32_t p = static_cast<uint32_t>(a.positions[t * a.chosen + j]);
-        float dot = 0.0f;
-        if (p < a.capacity) {
-            const float w = a.weights[t * a.chosen + j];
-            const T *y_row = a.by_row + p * a.row_stride;
-            Vec<T, N> *o = reinterpret_cast<Vec<T, N> *>(a.out + p * a.out_stride);
-            for (uint32_t v = threadIdx.x; v < a.vectors; v += kDotThreads) {
-                const Vec<T, N> d = load_vec<T, N>(d_row, v), y = load_vec<T, N>(y_row, v);
-                Vec<T, N> g;
+        const uint32_t p = static_cast<uint32_t>(pos[j]);
+        if (p >= a.capacity) continue;
+        const OutRow<T, MODE> o(a.out + static_cast<int64_t>(p) * a.width);
+        const int32_t e = o.first(at.v);
+        // from L1: each place has its own boundaries
+        if (MODE != kAligned) q = end_read<T, MODE>(start_read<T, MODE>(row, e, a.token_span), row, e, a.width, a.token_span);
+        o.write(e, a.width, q);
+    }
+}
+
+// J slots' rows are loaded together, U vectors of each.
+template <typename T, int MODE, int J, int U>
+__global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedCombine : 1) k_combine(const RowArgs<T> a) {
+    constexpr int N = Wide<T>::kCount;
+    const RowPlace at = row_place<U>(a);
+    if (at.token >= a.tokens) return;
+    const uint32_t lanes = 1u << a.log_lanes;
+    const int64_t pair0 = static_cast<int64_t>(at.token) * a.chosen;
+    const OutRow<T, MODE> out(a.out + static_cast<int64_t>(at.token) * a.width);
+    Pair acc[U][N / 2];
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float x = to_f32(d.e[e]);
-                    dot = fmaf(x, to_f32(y.e[e]), dot);
-                    g.e[e] = from_f32<T>(w * x);
-                }
-                o[v] = g;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) acc[u][i] = pair(0.0f, 0.0f);
+    for (uint32_t j0 = 0; j0 < a.chosen; j0 += J) {
+        Loaded y[J][U];
+        const T *row[J];
+        float w[J];
+        bool there[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const uint32_t p = j0 + j < a.chosen ? static_cast<uint32_t>(a.positions[pair0 + j0 + j]) : a.capacity;
+            there[j] = p < a.capacity;
+            w[j] = !there[j] ? 0.0f : a.weights ? a.weights[pair0 + j0 + j] : 1.0f;
+            row[j] = a.by_row + static_cast<int64_t>(there[j] ? p : 0) * a.row_stride;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t v = min(at.v + u * lanes, a.vectors - 1);     // no branch around the loads
+                y[j][u] = start_read<T, MODE>(row[j], out.first(v), a.row_span);
             }
         }
-        dot = warp_sum(dot);
-        if ((threadIdx.x & 31) == 0) s_dot[threadIdx.x >> 5] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kDotThreads / 32; ++i) sum += s_dot[i];
-            a.grad_weights[t * a.chosen + j] = sum;
-        }
-        __syncthreads();
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t v = at.v + u * lanes;
+                if (!there[j] || v >= a.vectors) continue;
+                const uint4 q = end_read<T, MODE>(y[j][u], row[j], out.first(v), a.width, a.row_span);
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) acc[u][i] = fma2(pair(w[j], w[j]), Wide<T>::pair_of(q, i), acc[u][i]);
+            }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t v = at.v + u * lanes;
+        if (v >= a.vectors) continue;
+        uint4 o;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(o, i, acc[u][i]);
+        out.write(out.first(v), a.width, o);
+    }
+}
+
+// 2^log_lanes threads hold a pair: they write its row of dy and sum its product
+// in a fixed order.  Pairs of a token are neighbours, so that its row of dout
+// comes from the caches after the first.
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedBackward : 1) k_combine_backward(const RowArgs<T> a) {
+    if (blockIdx.x < a.fill_blocks) {
+        fill_rows<T, MODE>(a);
+        return;
+    }
+    constexpr int N = Wide<T>::kCount, U = MODE == kShifted ? 1 : 2;
+    __shared__ float s_dot[kRowThreads / 32];
+    const uint32_t lanes = 1u << a.log_lanes, warp = threadIdx.x >> 5;
+    const uint32_t pr = (blockIdx.x - a.fill_blocks) * (kRowThreads >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
+    const uint32_t pairs = a.tokens * a.chosen;
+    const uint32_t p = pr < pairs ? static_cast<uint32_t>(a.positions[pr]) : a.capacity;
+    Pair dots = pair(0.0f, 0.0f);
+    if (p < a.capacity) {
+        const float w = a.weights[pr];
+        const T *d_row = a.by_token + static_cast<int64_t>(pr / a.chosen) * a.token_stride;
+        const T *y_row = a.by_row + static_cast<int64_t>(p) * a.row_stride;
+        const OutRow<T, MODE> out(a.out + static_cast<int64_t>(p) * a.width);
+        for (uint32_t v0 = threadIdx.x & (lanes - 1); v0 < a.vectors; v0 += lanes * U) {
+            Loaded d[U], y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t v = min(v0 + u * lanes, a.vectors - 1);       // no branch around the loads
+                d[u] = start_read<T, MODE>(d_row, out.first(v), a.token_span);
+                y[u] = start_read<T, MODE>(y_row, out.first(v), a.row_span);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t v = v0 + u * lanes;
+                if (v >= a.vectors) continue;
+                const int32_t e = out.first(v);
+                const uint4 dq = end_read<T, MODE>(d[u], d_row, e, a.width, a.token_span);
+                const uint4 yq = end_read<T, MODE>(y[u], y_row, e, a.width, a.row_span);
+                const bool whole = MODE == kAligned || (e >= 0 && e + N <= static_cast<int32_t>(a.width));
+                uint4 g;
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    Pair x = Wide<T>::pair_of(dq, i), z = Wide<T>::pair_of(yq, i);
+                    if (!whole) {          // what is beside the row is no part of the product
+                        if (static_cast<uint32_t>(e + 2 * i) >= a.width) x.f.x = z.f.x = 0.0f;
+                        if (static_cast<uint32_t>(e + 2 * i + 1) >= a.width) x.f.y = z.f.y = 0.0f;
+                    }
+                    dots = fma2(x, z, dots);
+                    Wide<T>::set_pair(g, i, mul2(pair(w, w), x));
+                }
+                out.write(e, a.width, g);
+            }
+        }
+    }
+    float dot = dots.f.x + dots.f.y;
+    for (uint32_t o = 1; o < min(lanes, 32u); o <<= 1) dot += __shfl_xor_sync(kFullMask, dot, o);
+    if (lanes > 32) {
+        if ((threadIdx.x & 31) == 0) s_dot[warp] = dot;
+        __syncthreads();
+        dot = 0.0f;
+        for (uint32_t i = 0; i < lanes / 32; ++i) dot += s_dot[(warp & ~(lanes / 32 - 1)) + i];
+    }
+    if ((threadIdx.x & (lanes - 1)) == 0 && pr < pairs) a.grad_weights[pr] = dot;
+}
+
+template <typename T> ReadSpan span_of(const void *p, int64_t rows, int64_t stride, int64_t width) {
+    if (p == nullptr || rows == 0) return {1, 0};
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(p), end = begin + ((rows - 1) * stride + width) * sizeof(T);
+    const uintptr_t first = (begin + 15) & ~static_cast<uintptr_t>(15), last = end & ~static_cast<uintptr_t>(15);
+    return last >= first + 32 ? ReadSpan{first, last - 32} : ReadSpan{1, 0};
 }
 
 template <typename T> RowArgs<T> row_args(const RowsLaunch &L) {
@@ -152,87 +324,105 @@ template <typename T> RowArgs<T> row_args(const RowsLaunch &L) {
     a.rows = L.rows;
     a.weights = L.weights;
     a.grad_weights = L.grad_weights;
-    a.tokens = L.tokens;
+    a.tokens = static_cast<uint32_t>(L.tokens);
     a.token_stride = L.token_stride;
     a.row_stride = L.row_stride;
-    a.out_stride = L.width;
     a.chosen = L.chosen;
     a.capacity = static_cast<uint32_t>(L.capacity);
+    a.width = static_cast<uint32_t>(L.width);
+    a.token_span = span_of<T>(L.by_token, L.tokens, L.token_stride, L.width);
+    a.row_span = span_of<T>(L.by_row, L.capacity, L.row_stride, L.width);
     return a;
 }
 
-// Elements that every row of every array can move at once: 16 bytes' worth
-// where the bases, the strides and the width allow it, else less, down to one.
-template <typename T> int vector_of(const RowsLaunch &L) {
-    for (int n = 16 / sizeof(T); n > 1; n /= 2) {
-        const size_t bytes = n * sizeof(T);
-        auto fits = [&](const void *p, int64_t stride) {
-            return p == nullptr || (aligned(p, bytes) && stride % n == 0);
-        };
-        if (L.width % n == 0 && fits(L.by_token, L.token_stride) && fits(L.by_row, L.row_stride) && fits(L.out, L.width))
-            return n;
-    }
-    return 1;
-}
-
-template <typename F> int with_vector(const RowsLaunch &L, F &&f) {
+// Calls f(arguments, mode).
+template <typename F> int with_rows(const RowsLaunch &L, F &&f) {
+    using std::integral_constant;
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
-        switch (vector_of<T>(L)) {
-            case 8: return f(t, std::integral_constant<int, 16 / sizeof(T)>{});
-            case 4: return f(t, std::integral_constant<int, 4>{});
-            case 2: return f(t, std::integral_constant<int, 2>{});
-            default: return f(t, std::integral_constant<int, 1>{});
+        constexpr int N = Wide<T>::kCount;
+        RowArgs<T> a = row_args<T>(L);
+        auto fits = [&](const void *p, int64_t stride) { return p == nullptr || (aligned(p, 16) && stride % N == 0); };
+        auto spans = [&](const void *p, const ReadSpan &s) { return p == nullptr || s.first <= s.last; };
+        const bool some = L.tokens > 0 && L.capacity > 0;
+        if (some && L.width % N == 0 && fits(L.by_token, L.token_stride) && fits(L.by_row, L.row_stride) && fits(L.out, L.width)) {
+            a.vectors = a.width / N;
+            return f(a, integral_constant<int, kAligned>{});
         }
+        a.vectors = (a.width + 2 * (N - 1)) / N;     // a row of `width` can touch so many
+        if (some && spans(L.by_token, a.token_span) && spans(L.by_row, a.row_span)) return f(a, integral_constant<int, kShifted>{});
+        return f(a, integral_constant<int, kElements>{});
     });
 }
 
-// CTAs that look for rows to zero, one row per thread.
-uint32_t zero_blocks(const RowsLaunch &L, int threads) {
-    return static_cast<uint32_t>((L.capacity + threads - 1) / threads);
+// As many threads side by side as the row's vectors need at `per_thread` each,
+// a power of two up to the CTA.
+uint32_t lanes_for(uint32_t vectors, int per_thread) {
+    uint32_t log_lanes = 0;
+    while ((1 << log_lanes) < kRowThreads && (static_cast<uint64_t>(per_thread) << log_lanes) < vectors) ++log_lanes;
+    return log_lanes;
+}
+
+// CTAs that walk all tokens' rows so.
+template <typename T> int64_t split_rows(RowArgs<T> &a, int per_thread) {
+    a.log_lanes = lanes_for(a.vectors, per_thread);
+    const uint32_t step = per_thread << a.log_lanes, tokens = kRowThreads >> a.log_lanes;
+    a.chunks = (a.vectors + step - 1) / step;
+    return static_cast<int64_t>((a.tokens + tokens - 1) / tokens) * a.chunks;
+}
+
+template <typename T> void set_fill(RowArgs<T> &a) {
+    a.fill_rows = a.vectors >= 128 ? 32 : kRowThreads;
+    a.fill_blocks = (a.capacity + a.fill_rows - 1) / a.fill_rows;
 }
 
 int status() { return cudaGetLastError() == cudaSuccess ? GSORT_OK : GSORT_ECUDA; }
 
+template <int J, int U, typename T, int MODE> int start_combine(const RowsLaunch &L, RowArgs<T> &a) {
+    const int64_t blocks = split_rows(a, U);
+    if (blocks > 0x7FFFFFFF) return GSORT_ETOOBIG;
+    k_combine<T, MODE, J, U><<<static_cast<uint32_t>(blocks), kRowThreads, 0, L.stream>>>(a);
+    return status();
+}
+
 }  // namespace
 
 int launch_dispatch(const RowsLaunch &L) {
-    return with_vector(L, [&](auto t, auto n) {
-        using T = decltype(t);
-        constexpr int N = decltype(n)::value;
-        RowArgs<T> a = row_args<T>(L);
-        a.vectors = static_cast<uint32_t>(L.width / N);
-        const int64_t blocks = (L.tokens * a.vectors + kRowThreads - 1) / kRowThreads;
-        if (blocks + zero_blocks(L, kRowThreads) > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
-        a.row_blocks = static_cast<uint32_t>(blocks);
-        k_dispatch<T, N><<<a.row_blocks + zero_blocks(L, kRowThreads), kRowThreads, 0, L.stream>>>(a);
+    return with_rows(L, [&](auto &a, auto m) {
+        constexpr int MODE = decltype(m)::value;
+        const int64_t blocks = split_rows(a, 1);
+        set_fill(a);
+        if (blocks + a.fill_blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
+        using T = std::decay_t<decltype(*a.out)>;
+        k_dispatch<T, MODE><<<a.fill_blocks + static_cast<uint32_t>(blocks), kRowThreads, 0, L.stream>>>(a);
         return status();
     });
 }
 
 int launch_combine(const RowsLaunch &L) {
-    return with_vector(L, [&](auto t, auto n) {
-        using T = decltype(t);
-        constexpr int N = decltype(n)::value;
-        RowArgs<T> a = row_args<T>(L);
-        a.vectors = static_cast<uint32_t>(L.width / N);
-        const int64_t blocks = (L.tokens * a.vectors + kRowThreads - 1) / kRowThreads;
-        if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
-        a.row_blocks = static_cast<uint32_t>(blocks);
-        k_combine<T, N><<<a.row_blocks, kRowThreads, 0, L.stream>>>(a);
-        return status();
+    return with_rows(L, [&](auto &a, auto m) {
+        constexpr int MODE = decltype(m)::value;
+        using T = std::decay_t<decltype(*a.out)>;
+        // four 16-byte loads in flight: 16384 x 8 rows of 8 KB take 200 us so, 255 with eight
+        if (MODE == kShifted) return start_combine<2, 2, T, MODE>(L, a);
+        if (L.chosen == 1) return start_combine<1, 4, T, MODE>(L, a);
+        if (L.chosen == 2) return start_combine<2, 2, T, MODE>(L, a);
+        return start_combine<4, 1, T, MODE>(L, a);
     });
 }
 
 int launch_combine_backward(const RowsLaunch &L) {
-    return with_vector(L, [&](auto t, auto n) {
-        using T = decltype(t);
-        constexpr int N = decltype(n)::value;
-        RowArgs<T> a = row_args<T>(L);
-        a.vectors = static_cast<uint32_t>(L.width / N);
-        if (L.tokens + zero_blocks(L, kDotThreads) > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
-        a.row_blocks = static_cast<uint32_t>(L.tokens);
-        k_combine_backward<T, N><<<a.row_blocks + zero_blocks(L, kDotThreads), kDotThreads, 0, L.stream>>>(a);
+    return with_rows(L, [&](auto &a, auto m) {
+        constexpr int MODE = decltype(m)::value;
+        using T = std::decay_t<decltype(*a.out)>;
+        const int64_t pairs = L.tokens * L.chosen;
+        // up to a warp to a pair where pairs fill the device, else up to a CTA
+        a.log_lanes = lanes_for(a.vectors, 2);
+        if (pairs >= 8 * 4 * L.sm_count) a.log_lanes = std::min(a.log_lanes, 5u);
+        const int64_t per = kRowThreads >> a.log_lanes, blocks = (pairs + per - 1) / per;
+        set_fill(a);
+        if (blocks + a.fill_blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
+        k_combine_backward<T, MODE><<<a.fill_blocks + static_cast<uint32_t>(blocks), kRowThreads, 0, L.stream>>>(a);
         return status();
     });
 }

@@ -12,6 +12,7 @@ library refuses raises GsortError.
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple
 
 import torch
@@ -167,11 +168,13 @@ def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, expert
 
 
 # ---------------------------------------------------- grouping and row moves
+@functools.lru_cache(maxsize=1024)
 def group_capacity(pairs: int, num_experts: int, align: int = 1) -> int:
     """Rows of the grouped layout that any choice of experts fits into."""
     return int(_entry("gsort_group_capacity")(pairs, num_experts, align))
 
 
+@functools.lru_cache(maxsize=1024)
 def group_workspace_bytes(pairs: int, num_experts: int) -> int:
     return int(_entry("gsort_group_workspace_bytes")(pairs, num_experts))
 

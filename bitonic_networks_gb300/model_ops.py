@@ -79,30 +79,31 @@ def _call(name: str, device: torch.device, *args):
         raise GsortError(rc, name)
 
 
-def _rows2d(t: torch.Tensor, name: str) -> int:
-    """Checks a 2-D float CUDA tensor with consecutive row elements; returns its dtype code."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _matrix(t: torch.Tensor, name: str):
+    """Checks a 2-D float CUDA tensor with consecutive row elements; returns
+    (pointer, dtype code, rows, width, row stride)."""
     code = _FLOATS.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA tensor of two dimensions, got {tuple(t.shape)} on {t.device}")
+    rows, width = t.shape
+    stride, step = t.stride()
+    if step != 1 and width > 1:
         raise ValueError(f"the elements of a row of {name} must be consecutive")
-    return code
+    # the stride of a tensor with one row (or none) means nothing
+    return t.data_ptr(), code, rows, width, stride if rows > 1 else width
 
 
-def _flat(t: torch.Tensor, name: str, dtype, shape, device):
-    """Checks a contiguous tensor of the given dtype and shape on the device."""
-    if t.dtype != dtype:
+def _flat(t: torch.Tensor, name: str, dtype, shape, device) -> int:
+    """Checks a contiguous tensor of the given dtype and shape on the device; returns its pointer."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {device}")
+    return t.data_ptr()
 
 
 def _choice(value, table, name):
@@ -110,11 +111,6 @@ def _choice(value, table, name):
     if code is None:
         raise ValueError(f"{name} must be one of {', '.join(table)}, got {value!r}")
     return code
-
-
-def _stride(t: torch.Tensor) -> int:
-    # the stride of a tensor with one row (or none) means nothing
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 # ----------------------------------------------------------------- routing
@@ -130,19 +126,17 @@ def route_experts(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = N
     of -inf or NaN are never chosen.  Returns (weights [tokens, k] float32,
     experts [tokens, k] int32), best first and ties to the lower index; a token
     with fewer candidates has experts -1 with weight 0."""
-    code = _rows2d(logits, "logits")
-    tokens, experts = logits.shape
+    ptr, code, tokens, experts, stride = _matrix(logits, "logits")
     dev = logits.device
-    if bias is not None:
-        _flat(bias, "bias", torch.float32, (experts,), dev)
+    bias_ptr = None if bias is None else _flat(bias, "bias", torch.float32, (experts,), dev)
     k = int(k)
     if k < 1:
         raise ValueError("k must be at least 1")
+    how, by = _choice(score, _SCORES, "score"), _choice(group_score, _GROUP_SCORES, "group_score")
     weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
     chosen = torch.empty((tokens, k), dtype=torch.int32, device=dev)
-    _call("gsort_route_experts", dev, logits.data_ptr(), code, tokens, experts, _stride(logits),
-          _ptr(bias), _choice(score, _SCORES, "score"), groups, groups if groups_kept is None else groups_kept,
-          _choice(group_score, _GROUP_SCORES, "group_score"), k, 1 if renormalise else 0, scale,
+    _call("gsort_route_experts", dev, ptr, code, tokens, experts, stride, bias_ptr, how, groups,
+          groups if groups_kept is None else groups_kept, by, k, 1 if renormalise else 0, scale,
           weights.data_ptr(), chosen.data_ptr())
     return weights, chosen
 
@@ -152,18 +146,17 @@ def route_experts_backward(d_weights: torch.Tensor, logits: torch.Tensor, expert
                            scale: float = 1.0) -> torch.Tensor:
     """Gradient of route_experts' weights by the logits, for the experts it
     chose; [tokens, experts] of the logits' dtype."""
-    code = _rows2d(logits, "logits")
-    tokens, number = logits.shape
+    ptr, code, tokens, number, stride = _matrix(logits, "logits")
     dev = logits.device
     if experts.dim() != 2:
         raise ValueError("experts must have two dimensions")
-    k = experts.shape[1]
-    _flat(experts, "experts", torch.int32, (tokens, k), dev)
-    _flat(d_weights, "d_weights", torch.float32, (tokens, k), dev)
+    shape = (tokens, experts.shape[1])
+    experts_ptr = _flat(experts, "experts", torch.int32, shape, dev)
+    d_ptr = _flat(d_weights, "d_weights", torch.float32, shape, dev)
+    how = _choice(score, _SCORES, "score")
     out = torch.empty((tokens, number), dtype=logits.dtype, device=dev)
-    _call("gsort_route_experts_backward", dev, d_weights.data_ptr(), logits.data_ptr(), code, tokens,
-          number, _stride(logits), experts.data_ptr(), k, _choice(score, _SCORES, "score"),
-          1 if renormalise else 0, scale, out.data_ptr())
+    _call("gsort_route_experts_backward", dev, d_ptr, ptr, code, tokens, number, stride, experts_ptr,
+          shape[1], how, 1 if renormalise else 0, scale, out.data_ptr())
     return out
 
 
@@ -189,7 +182,7 @@ def group_by_expert(experts: torch.Tensor, num_experts: int, *, align: int = 1,
     if experts.dim() != 2:
         raise ValueError("experts must have two dimensions")
     dev = experts.device
-    _flat(experts, "experts", torch.int32, experts.shape, dev)
+    ptr = _flat(experts, "experts", torch.int32, experts.shape, dev)
     pairs = experts.numel()
     capacity = group_capacity(pairs, num_experts, align)
     nbytes = group_workspace_bytes(pairs, num_experts)
@@ -198,31 +191,31 @@ def group_by_expert(experts: torch.Tensor, num_experts: int, *, align: int = 1,
     counts = torch.empty(max(num_experts, 0), dtype=torch.int32, device=dev)
     rows = torch.empty(capacity, dtype=torch.int32, device=dev)
     positions = torch.empty_like(experts)
-    _call("gsort_group_by_expert", dev, experts.data_ptr(), pairs, num_experts, align, offsets.data_ptr(),
-          counts.data_ptr(), rows.data_ptr(), capacity, positions.data_ptr(), _ptr(ws),
-          ws.numel() * ws.element_size() if ws is not None else 0)
+    _call("gsort_group_by_expert", dev, ptr, pairs, num_experts, align, offsets.data_ptr(),
+          counts.data_ptr(), rows.data_ptr(), capacity, positions.data_ptr(),
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
     return ExpertGroups(offsets, counts, rows, positions)
 
 
 def _layout(groups: ExpertGroups, device):
-    tokens, k = groups.positions.shape
-    capacity = groups.rows.shape[0]
-    _flat(groups.positions, "groups.positions", torch.int32, (tokens, k), device)
-    _flat(groups.rows, "groups.rows", torch.int32, (capacity,), device)
-    return tokens, k, capacity
+    """(pointer to positions, pointer to rows, tokens, slots, capacity)"""
+    positions, rows = groups.positions, groups.rows
+    tokens, k = positions.shape
+    return (_flat(positions, "groups.positions", torch.int32, positions.shape, device),
+            _flat(rows, "groups.rows", torch.int32, (rows.numel(),), device), tokens, k, rows.numel())
 
 
 def dispatch_rows(x: torch.Tensor, groups: ExpertGroups) -> torch.Tensor:
     """Copies each token's row of x [tokens, width] to its pairs' rows of the
     grouped layout; rows without a pair are zero.  Returns [capacity, width]."""
-    code = _rows2d(x, "x")
+    ptr, code, given, width, stride = _matrix(x, "x")
     dev = x.device
-    tokens, k, capacity = _layout(groups, dev)
-    if x.shape[0] != tokens:
-        raise ValueError(f"x must have {tokens} rows, got {x.shape[0]}")
-    out = torch.empty((capacity, x.shape[1]), dtype=x.dtype, device=dev)
-    _call("gsort_dispatch_rows", dev, x.data_ptr(), code, tokens, x.shape[1], _stride(x),
-          groups.positions.data_ptr(), k, groups.rows.data_ptr(), capacity, out.data_ptr())
+    positions, rows, tokens, k, capacity = _layout(groups, dev)
+    if given != tokens:
+        raise ValueError(f"x must have {tokens} rows, got {given}")
+    out = torch.empty((capacity, width), dtype=x.dtype, device=dev)
+    _call("gsort_dispatch_rows", dev, ptr, code, tokens, width, stride, positions, k, rows, capacity,
+          out.data_ptr())
     return out
 
 
@@ -230,35 +223,34 @@ def combine_rows(y: torch.Tensor, groups: ExpertGroups, weights: torch.Tensor | 
     """Sums each token's rows of y [capacity, width] in the grouped layout, with
     weights [tokens, slots] float32 (None: ones, dispatch_rows' gradient).
     Dropped pairs add nothing.  Returns [tokens, width]."""
-    code = _rows2d(y, "y")
+    ptr, code, given, width, stride = _matrix(y, "y")
     dev = y.device
-    tokens, k, capacity = _layout(groups, dev)
-    if y.shape[0] != capacity:
-        raise ValueError(f"y must have {capacity} rows, got {y.shape[0]}")
-    if weights is not None:
-        _flat(weights, "weights", torch.float32, (tokens, k), dev)
-    out = torch.empty((tokens, y.shape[1]), dtype=y.dtype, device=dev)
-    _call("gsort_combine_rows", dev, y.data_ptr(), code, capacity, y.shape[1], _stride(y), _ptr(weights),
-          groups.positions.data_ptr(), tokens, k, out.data_ptr())
+    positions, _, tokens, k, capacity = _layout(groups, dev)
+    if given != capacity:
+        raise ValueError(f"y must have {capacity} rows, got {given}")
+    w = None if weights is None else _flat(weights, "weights", torch.float32, (tokens, k), dev)
+    out = torch.empty((tokens, width), dtype=y.dtype, device=dev)
+    _call("gsort_combine_rows", dev, ptr, code, capacity, width, stride, w, positions, tokens, k,
+          out.data_ptr())
     return out
 
 
 def combine_rows_backward(d_out: torch.Tensor, y: torch.Tensor, groups: ExpertGroups, weights: torch.Tensor):
     """Gradients of combine_rows by y and by the weights: (d_y [capacity,
     width], zero where a row holds no pair; d_weights [tokens, slots])."""
-    code = _rows2d(d_out, "d_out")
-    dev = d_out.device
-    if _rows2d(y, "y") != code:
+    ptr, code, given, width, stride = _matrix(d_out, "d_out")
+    y_ptr, y_code, y_rows, y_width, y_stride = _matrix(y, "y")
+    if y_code != code:
         raise TypeError("d_out and y must have one dtype")
-    tokens, k, capacity = _layout(groups, dev)
-    if tuple(d_out.shape) != (tokens, y.shape[1]) or y.shape[0] != capacity or y.device != dev:
+    dev = d_out.device
+    positions, rows, tokens, k, capacity = _layout(groups, dev)
+    if given != tokens or y_rows != capacity or y_width != width or y.device != dev:
         raise ValueError("d_out must be [tokens, width] and y [capacity, width] on one device")
-    _flat(weights, "weights", torch.float32, (tokens, k), dev)
-    d_y = torch.empty((capacity, y.shape[1]), dtype=y.dtype, device=dev)
+    w = _flat(weights, "weights", torch.float32, (tokens, k), dev)
+    d_y = torch.empty((capacity, width), dtype=y.dtype, device=dev)
     d_weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
-    _call("gsort_combine_rows_backward", dev, d_out.data_ptr(), code, tokens, y.shape[1], _stride(d_out),
-          y.data_ptr(), capacity, _stride(y), weights.data_ptr(), groups.positions.data_ptr(), k,
-          groups.rows.data_ptr(), d_y.data_ptr(), d_weights.data_ptr())
+    _call("gsort_combine_rows_backward", dev, ptr, code, tokens, width, stride, y_ptr, capacity, y_stride, w,
+          positions, k, rows, d_y.data_ptr(), d_weights.data_ptr())
     return d_y, d_weights
 
 
@@ -278,8 +270,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, *,
     read of the logits.  Logits of -inf are masked.  A negative target gives 0,
     one beyond the vocabulary NaN; alternatives come best first, ties to the
     lower index, with -inf and -1 where a row has too few unmasked logits."""
-    code = _rows2d(logits, "logits")
-    rows, vocab = logits.shape
+    ptr, code, rows, vocab, stride = _matrix(logits, "logits")
     dev = logits.device
     at, size = _targets(targets, rows, dev)
     if top < 0:
@@ -289,8 +280,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, *,
     stats = torch.empty((rows, 2), dtype=torch.float32, device=dev)
     top_lp = torch.empty((rows, top), dtype=torch.float32, device=dev) if top else None
     top_ids = torch.empty((rows, top), dtype=torch.int32, device=dev) if top else None
-    _call("gsort_token_logprobs", dev, logits.data_ptr(), code, rows, vocab, _stride(logits), at, size, top,
-          _ptr(lp), entropy.data_ptr(), stats.data_ptr(), _ptr(top_lp), _ptr(top_ids))
+    _call("gsort_token_logprobs", dev, ptr, code, rows, vocab, stride, at, size, top, _ptr(lp),
+          entropy.data_ptr(), stats.data_ptr(), _ptr(top_lp), _ptr(top_ids))
     return TokenLogprobs(lp, entropy, top_lp, top_ids, stats)
 
 
@@ -300,24 +291,27 @@ def token_logprobs_backward(d_logprobs: torch.Tensor | None, d_entropy: torch.Te
     """Gradient by the logits of sum(d_logprobs * logprobs + d_entropy *
     entropy), [rows, vocab] of the logits' dtype; `result` is the forward
     call's.  `out` may be the logits themselves.  Without it the gradient's rows
-    are laid out as the logits' are."""
-    code = _rows2d(logits, "logits")
-    rows, vocab = logits.shape
+    lie up to 15 bytes apart where the logits' rows do not follow each other."""
+    ptr, code, rows, vocab, stride = _matrix(logits, "logits")
     dev = logits.device
     at, size = _targets(targets, rows, dev)
-    if d_logprobs is not None:
-        if targets is None:
-            raise ValueError("d_logprobs needs targets")
-        _flat(d_logprobs, "d_logprobs", torch.float32, (rows,), dev)
-    if d_entropy is not None:
-        _flat(d_entropy, "d_entropy", torch.float32, (rows,), dev)
-    _flat(result.entropy, "result.entropy", torch.float32, (rows,), dev)
-    _flat(result.stats, "result.stats", torch.float32, (rows, 2), dev)
+    if d_logprobs is not None and targets is None:
+        raise ValueError("d_logprobs needs targets")
+    dl = None if d_logprobs is None else _flat(d_logprobs, "d_logprobs", torch.float32, (rows,), dev)
+    dh = None if d_entropy is None else _flat(d_entropy, "d_entropy", torch.float32, (rows,), dev)
+    entropy = _flat(result.entropy, "result.entropy", torch.float32, (rows,), dev)
+    stats = _flat(result.stats, "result.stats", torch.float32, (rows, 2), dev)
     if out is None:
-        out = torch.empty((rows, _stride(logits)), dtype=logits.dtype, device=dev)[:, :vocab]
-    elif _rows2d(out, "out") != code or out.shape != logits.shape or out.device != dev:
-        raise ValueError("out must have the logits' dtype, shape and device")
-    _call("gsort_token_logprobs_backward", dev, _ptr(d_logprobs), _ptr(d_entropy), logits.data_ptr(), code,
-          rows, vocab, _stride(logits), at, size, result.entropy.data_ptr(), result.stats.data_ptr(),
-          out.data_ptr(), _stride(out))
+        # rows as far from a 16-byte boundary as the logits' move in whole vectors
+        out_stride = vocab + (stride - vocab) % (16 // logits.element_size())
+        out = torch.empty((rows, out_stride), dtype=logits.dtype, device=dev)
+        out_ptr = out.data_ptr()
+        if out_stride != vocab:
+            out = out[:, :vocab]
+    else:
+        out_ptr, out_code, _, _, out_stride = _matrix(out, "out")
+        if out_code != code or out.shape != logits.shape or out.device != dev:
+            raise ValueError("out must have the logits' dtype, shape and device")
+    _call("gsort_token_logprobs_backward", dev, dl, dh, ptr, code, rows, vocab, stride, at, size, entropy,
+          stats, out_ptr, out_stride)
     return out

@@ -225,6 +225,16 @@ def test_offsets_beyond_32_bits():
     check_gradient(x, t, r, out=torch.empty(2, vocab, dtype=torch.bfloat16, device="cuda"))
 
 
+def test_last_positions_of_a_batch():
+    """Rows far apart: the gradient takes no more room than its rows."""
+    x = logits_of(6 * 50, 1003, torch.bfloat16, 17).view(6, 50, 1003)[:, -1]
+    t = torch.arange(6).cuda()
+    r = check(x, t, 3)
+    check_gradient(x, t, r)
+    dx = gs.token_logprobs_backward(None, torch.ones(6).cuda(), x, t, r)
+    assert dx.untyped_storage().nbytes() <= 6 * (1003 + 7) * 2
+
+
 def test_no_rows():
     x = torch.empty(0, 10).cuda()
     r = gs.token_logprobs(x, torch.empty(0, dtype=torch.int64).cuda(), top=3)

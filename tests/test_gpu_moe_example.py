@@ -1,0 +1,47 @@
+"""The example model: its whole gradient against the same model in plain 64-bit
+torch, and that it learns."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+import bitonic_networks_gb300 as gs
+from conftest import ROOT
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def example():
+    spec = importlib.util.spec_from_file_location("moe_step", os.path.join(ROOT, "examples", "moe_step.py"))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_gradients_of_the_model(example):
+    torch.manual_seed(3)
+    model = example.Model(200, 64, 8, 2, align=16).cuda()
+    tokens, targets = torch.randint(200, (2, 97), device="cuda")
+    logprobs, entropy = example.TokenLogprobs.apply(model.logits(tokens), targets)
+    (-logprobs.mean() - 0.1 * entropy.mean()).backward()
+
+    p = {k: v.detach().double().requires_grad_() for k, v in model.named_parameters()}
+    x = p["embed"][tokens]
+    router = x @ p["router"]
+    _, chosen = gs.route_experts((x @ p["router"]).detach().float(), 2, score="sigmoid", bias=model.bias, renormalise=True)
+    s = torch.sigmoid(router).gather(1, chosen.long())
+    w = s / s.sum(1, keepdim=True)
+    y = torch.relu(torch.einsum("th,tkho->tko", x, p["expert"][chosen.long()]))
+    lp = torch.log_softmax((x + (w.unsqueeze(-1) * y).sum(1)) @ p["head"], -1)
+    h = -(lp.exp() * lp).sum(-1)
+    (-lp.gather(1, targets.unsqueeze(1)).mean() - 0.1 * h.mean()).backward()
+    for name, v in model.named_parameters():
+        far = (v.grad.double() - p[name].grad).norm() / p[name].grad.norm()
+        assert far < 1e-4, (name, float(far))     # 32-bit products of 64 and 200 terms, a few in a row
+
+
+def test_the_example_learns(example):
+    losses, best, given = example.main(["--steps", "40", "--tokens", "256", "--vocab", "300"])
+    assert losses[-1] < 0.25 * losses[0] and best == given

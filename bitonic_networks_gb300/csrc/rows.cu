@@ -27,10 +27,10 @@ namespace gsort {
 namespace {
 
 constexpr int kRowThreads = 256;
-// CTAs per SM that a kernel's registers leave room for where rows start
+// CTAs per SM that a kernel's registers leave room for where 16-bit rows start
 // anywhere: loads wait for memory, and more of them do with more CTAs (8191 x 6
-// rows of 1001 32-bit elements: combine 45 us with 4 CTAs of 2 x 2 loads per
-// thread, 67 with 3 of 4; backward 84 with 6 CTAs, 89 with 4).
+// rows of 1001: combine 29 us with 4 CTAs of 2 x 2 loads per thread, 37 with 3
+// of 4 x 1; backward 55 with 6 CTAs, 58 with 4).
 constexpr int kShiftedCombine = 4, kShiftedBackward = 6;
 
 // Addresses at which 32 bytes of an array can be read; none where last < first.
@@ -55,9 +55,21 @@ template <typename T> struct RowArgs {
     uint32_t fill_rows, fill_blocks;   // rows that a CTA looks over to zero them; such CTAs: the rest move rows
 };
 
-// How rows are read: every row starts and ends at 16 bytes; anywhere; or element
-// by element, for arrays that hold no two aligned vectors.
-enum RowMode { kAligned, kShifted, kElements };
+// How rows move: every row starts and ends at 16 bytes; anywhere, in 16-byte
+// vectors; anywhere, in single 32-bit elements that neighbouring threads hold
+// side by side (for the sums of 32-bit rows: fewer instructions than shifting,
+// 8191 x 6 rows of 1001: combine 39 us against 45, backward 81 against 84); or
+// element by element, for arrays that hold only a few.
+enum RowMode { kAligned, kShifted, kSingle, kElements };
+
+// Where a thread's N elements of vector v of a row are: e, e + kStep, ...
+// kSingle: a warp's threads are side by side, 32 apart.
+template <int MODE> constexpr int kStep = MODE == kSingle ? 32 : 1;
+
+template <typename T, int MODE> __device__ __forceinline__ int32_t element_of(uint32_t v, int32_t shift) {
+    if (MODE == kSingle) return static_cast<int32_t>((v & ~31u) * Wide<T>::kCount + (v & 31u));
+    return static_cast<int32_t>(v * Wide<T>::kCount) - shift;
+}
 
 // 16 bytes of a row from element e on, in two steps, so that several can be in
 // flight: the loads, which do not branch, and the shift.  Elements outside the
@@ -71,7 +83,7 @@ template <typename T> __device__ __forceinline__ uintptr_t address_of(const T *r
 }
 
 template <typename T, int MODE>
-__device__ __forceinline__ Loaded start_read(const T *row, int32_t e, const ReadSpan &span) {
+__device__ __forceinline__ Loaded start_read(const T *row, int32_t e, uint32_t width, const ReadSpan &span) {
     Loaded x;
     if (MODE == kAligned) {
         x.q = *reinterpret_cast<const uint4 *>(row + e);
@@ -80,6 +92,10 @@ __device__ __forceinline__ Loaded start_read(const T *row, int32_t e, const Read
         const uint4 *p = reinterpret_cast<const uint4 *>(min(max(low, span.first), span.last));
         x.q = p[0];
         x.r = p[1];
+    } else if (MODE == kSingle) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(row) + e;
+        const int32_t left = static_cast<int32_t>(width) - e;
+        x.q = make_uint4(left > 0 ? w[0] : 0u, left > 32 ? w[32] : 0u, left > 64 ? w[64] : 0u, left > 96 ? w[96] : 0u);
     }
     return x;
 }
@@ -87,7 +103,7 @@ __device__ __forceinline__ Loaded start_read(const T *row, int32_t e, const Read
 template <typename T, int MODE>
 __device__ __forceinline__ uint4 end_read(const Loaded &x, const T *row, int32_t e, uint32_t width, const ReadSpan &span) {
     constexpr int N = Wide<T>::kCount;
-    if (MODE == kAligned) return x.q;
+    if (MODE == kAligned || MODE == kSingle) return x.q;
     const uintptr_t at = address_of(row, e), low = at & ~static_cast<uintptr_t>(15);
     uint4 q;
     if (MODE == kShifted) {
@@ -119,22 +135,26 @@ __device__ __forceinline__ uint4 end_read(const Loaded &x, const T *row, int32_t
     return q;
 }
 
-// A row that is written: vector v holds its elements from first(v) on.
+// A row that is written.
 template <typename T, int MODE> struct OutRow {
     T *row;
     int32_t shift;           // elements between the boundary at or before the row and the row
 
     __device__ __forceinline__ explicit OutRow(T *r)
         : row(r), shift(MODE == kAligned ? 0 : static_cast<int32_t>((reinterpret_cast<uintptr_t>(r) & 15) / sizeof(T))) {}
-    __device__ __forceinline__ int32_t first(uint32_t v) const { return static_cast<int32_t>(v * Wide<T>::kCount) - shift; }
+    __device__ __forceinline__ int32_t at(uint32_t v) const { return element_of<T, MODE>(v, shift); }
+    // Whether the N elements from e on are all of the row.
+    static __device__ __forceinline__ bool whole(int32_t e, uint32_t width) {
+        return MODE == kAligned || (e >= 0 && e + (Wide<T>::kCount - 1) * kStep<MODE> < static_cast<int32_t>(width));
+    }
     __device__ __forceinline__ void write(int32_t e, uint32_t width, const uint4 &q) const {
         constexpr int N = Wide<T>::kCount;
-        if (MODE == kAligned || (e >= 0 && e + N <= static_cast<int32_t>(width))) {
+        if (MODE != kSingle && whole(e, width)) {
             *reinterpret_cast<uint4 *>(row + e) = q;
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (static_cast<uint32_t>(e + i) < width) row[e + i] = Wide<T>::element(q, i);
+                if (static_cast<uint32_t>(e + i * kStep<MODE>) < width) row[e + i * kStep<MODE>] = Wide<T>::element(q, i);
         }
     }
 };
@@ -152,7 +172,7 @@ template <typename T, int MODE> __device__ __forceinline__ void fill_rows(const 
     for (uint32_t n = 0; empty; ++n, empty &= empty - 1) {
         if (a.fill_rows == 32 && n % kWarps != warp) continue;
         const OutRow<T, MODE> o(a.out + static_cast<int64_t>(first + __ffs(empty) - 1) * a.width);
-        for (uint32_t v = lane; v < a.vectors; v += 32) o.write(o.first(v), a.width, make_uint4(0, 0, 0, 0));
+        for (uint32_t v = lane; v < a.vectors; v += 32) o.write(o.at(v), a.width, make_uint4(0, 0, 0, 0));
     }
 }
 
@@ -178,17 +198,17 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(const RowArgs<T> a) {
     if (at.token >= a.tokens || at.v >= a.vectors) return;
     const T *row = a.by_token + at.token * a.token_stride;
     uint4 q;
-    if (MODE == kAligned) q = start_read<T, MODE>(row, at.v * Wide<T>::kCount, a.token_span).q;
+    if (MODE == kAligned) q = start_read<T, MODE>(row, element_of<T, MODE>(at.v, 0), a.width, a.token_span).q;
     const int32_t *pos = a.positions + static_cast<int64_t>(at.token) * a.chosen;
 #pragma unroll 4
     for (uint32_t j = 0; j < a.chosen; ++j) {
         const uint32_t p = static_cast<uint32_t>(pos[j]);
         if (p >= a.capacity) continue;
         const OutRow<T, MODE> o(a.out + static_cast<int64_t>(p) * a.width);
-        const int32_t e = o.first(at.v);
-        // from L1: each place has its own boundaries
-        if (MODE != kAligned) q = end_read<T, MODE>(start_read<T, MODE>(row, e, a.token_span), row, e, a.width, a.token_span);
-        o.write(e, a.width, q);
+        const int32_t to = o.at(at.v);
+        // from L1: each row has its own boundaries
+        if (MODE != kAligned) q = end_read<T, MODE>(start_read<T, MODE>(row, to, a.width, a.token_span), row, to, a.width, a.token_span);
+        o.write(to, a.width, q);
     }
 }
 
@@ -220,7 +240,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedCombin
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t v = min(at.v + u * lanes, a.vectors - 1);     // no branch around the loads
-                y[j][u] = start_read<T, MODE>(row[j], out.first(v), a.row_span);
+                y[j][u] = start_read<T, MODE>(row[j], out.at(v), a.width, a.row_span);
             }
         }
 #pragma unroll
@@ -229,7 +249,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedCombin
             for (int u = 0; u < U; ++u) {
                 const uint32_t v = at.v + u * lanes;
                 if (!there[j] || v >= a.vectors) continue;
-                const uint4 q = end_read<T, MODE>(y[j][u], row[j], out.first(v), a.width, a.row_span);
+                const uint4 q = end_read<T, MODE>(y[j][u], row[j], out.at(v), a.width, a.row_span);
 #pragma unroll
                 for (int i = 0; i < N / 2; ++i) acc[u][i] = fma2(pair(w[j], w[j]), Wide<T>::pair_of(q, i), acc[u][i]);
             }
@@ -241,7 +261,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedCombin
         uint4 o;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(o, i, acc[u][i]);
-        out.write(out.first(v), a.width, o);
+        out.write(out.at(v), a.width, o);
     }
 }
 
@@ -271,17 +291,17 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedBackwa
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t v = min(v0 + u * lanes, a.vectors - 1);       // no branch around the loads
-                d[u] = start_read<T, MODE>(d_row, out.first(v), a.token_span);
-                y[u] = start_read<T, MODE>(y_row, out.first(v), a.row_span);
+                d[u] = start_read<T, MODE>(d_row, out.at(v), a.width, a.token_span);
+                y[u] = start_read<T, MODE>(y_row, out.at(v), a.width, a.row_span);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t v = v0 + u * lanes;
                 if (v >= a.vectors) continue;
-                const int32_t e = out.first(v);
+                const int32_t e = out.at(v);
                 const uint4 dq = end_read<T, MODE>(d[u], d_row, e, a.width, a.token_span);
                 const uint4 yq = end_read<T, MODE>(y[u], y_row, e, a.width, a.row_span);
-                const bool whole = MODE == kAligned || (e >= 0 && e + N <= static_cast<int32_t>(a.width));
+                const bool whole = MODE == kSingle || out.whole(e, a.width);    // kSingle reads 0 beside the row
                 uint4 g;
 #pragma unroll
                 for (int i = 0; i < N / 2; ++i) {
@@ -335,8 +355,8 @@ template <typename T> RowArgs<T> row_args(const RowsLaunch &L) {
     return a;
 }
 
-// Calls f(arguments, mode).
-template <typename F> int with_rows(const RowsLaunch &L, F &&f) {
+// Calls f(arguments, mode).  sums: the rows are summed, not only copied.
+template <typename F> int with_rows(const RowsLaunch &L, bool sums, F &&f) {
     using std::integral_constant;
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
@@ -350,6 +370,11 @@ template <typename F> int with_rows(const RowsLaunch &L, F &&f) {
             return f(a, integral_constant<int, kAligned>{});
         }
         a.vectors = (a.width + 2 * (N - 1)) / N;     // a row of `width` can touch so many
+        if constexpr (sizeof(T) == 4)
+            if (some && sums) {
+                a.vectors = (a.width + 127) / 128 * 32;
+                return f(a, integral_constant<int, kSingle>{});
+            }
         if (some && spans(L.by_token, a.token_span) && spans(L.by_row, a.row_span)) return f(a, integral_constant<int, kShifted>{});
         return f(a, integral_constant<int, kElements>{});
     });
@@ -388,7 +413,7 @@ template <int J, int U, typename T, int MODE> int start_combine(const RowsLaunch
 }  // namespace
 
 int launch_dispatch(const RowsLaunch &L) {
-    return with_rows(L, [&](auto &a, auto m) {
+    return with_rows(L, false, [&](auto &a, auto m) {
         constexpr int MODE = decltype(m)::value;
         const int64_t blocks = split_rows(a, 1);
         set_fill(a);
@@ -400,11 +425,11 @@ int launch_dispatch(const RowsLaunch &L) {
 }
 
 int launch_combine(const RowsLaunch &L) {
-    return with_rows(L, [&](auto &a, auto m) {
+    return with_rows(L, true, [&](auto &a, auto m) {
         constexpr int MODE = decltype(m)::value;
         using T = std::decay_t<decltype(*a.out)>;
         // four 16-byte loads in flight: 16384 x 8 rows of 8 KB take 200 us so, 255 with eight
-        if (MODE == kShifted) return start_combine<2, 2, T, MODE>(L, a);
+        if (MODE == kShifted || MODE == kSingle) return start_combine<2, 2, T, MODE>(L, a);
         if (L.chosen == 1) return start_combine<1, 4, T, MODE>(L, a);
         if (L.chosen == 2) return start_combine<2, 2, T, MODE>(L, a);
         return start_combine<4, 1, T, MODE>(L, a);
@@ -412,7 +437,7 @@ int launch_combine(const RowsLaunch &L) {
 }
 
 int launch_combine_backward(const RowsLaunch &L) {
-    return with_rows(L, [&](auto &a, auto m) {
+    return with_rows(L, true, [&](auto &a, auto m) {
         constexpr int MODE = decltype(m)::value;
         using T = std::decay_t<decltype(*a.out)>;
         const int64_t pairs = L.tokens * L.chosen;

@@ -13,6 +13,7 @@ library refuses raises GsortError.
 from __future__ import annotations
 
 import functools
+import operator
 from typing import NamedTuple
 
 import torch
@@ -70,7 +71,7 @@ def _call(name: str, device: torch.device, *args):
     making a stream object, and the device is switched only where it is another."""
     fn = _entry(name)
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
@@ -106,6 +107,14 @@ def _flat(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     return t.data_ptr()
 
 
+def _int(value, name: str) -> int:
+    """An integer that fits the C int it is passed as."""
+    value = operator.index(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} is out of range: {value}")
+    return value
+
+
 def _choice(value, table, name):
     code = table.get(value)
     if code is None:
@@ -129,14 +138,15 @@ def route_experts(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = N
     ptr, code, tokens, experts, stride = _matrix(logits, "logits")
     dev = logits.device
     bias_ptr = None if bias is None else _flat(bias, "bias", torch.float32, (experts,), dev)
-    k = int(k)
+    k, groups = _int(k, "k"), _int(groups, "groups")
+    kept = groups if groups_kept is None else _int(groups_kept, "groups_kept")
     if k < 1:
         raise ValueError("k must be at least 1")
     how, by = _choice(score, _SCORES, "score"), _choice(group_score, _GROUP_SCORES, "group_score")
     weights = torch.empty((tokens, k), dtype=torch.float32, device=dev)
     chosen = torch.empty((tokens, k), dtype=torch.int32, device=dev)
     _call("gsort_route_experts", dev, ptr, code, tokens, experts, stride, bias_ptr, how, groups,
-          groups if groups_kept is None else groups_kept, by, k, 1 if renormalise else 0, scale,
+          kept, by, k, 1 if renormalise else 0, scale,
           weights.data_ptr(), chosen.data_ptr())
     return weights, chosen
 
@@ -183,6 +193,7 @@ def group_by_expert(experts: torch.Tensor, num_experts: int, *, align: int = 1,
         raise ValueError("experts must have two dimensions")
     dev = experts.device
     ptr = _flat(experts, "experts", torch.int32, experts.shape, dev)
+    num_experts, align = _int(num_experts, "num_experts"), _int(align, "align")
     pairs = experts.numel()
     capacity = group_capacity(pairs, num_experts, align)
     nbytes = group_workspace_bytes(pairs, num_experts)
@@ -273,6 +284,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, *,
     ptr, code, rows, vocab, stride = _matrix(logits, "logits")
     dev = logits.device
     at, size = _targets(targets, rows, dev)
+    top = _int(top, "top")
     if top < 0:
         raise ValueError("top must not be negative")
     lp = None if targets is None else torch.empty(rows, dtype=torch.float32, device=dev)

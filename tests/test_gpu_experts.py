@@ -145,6 +145,27 @@ def test_masked_tokens_keep_their_contents_out():
     assert torch.isfinite(d_y).all() and (d_w[7] == 0).all() and torch.isfinite(d_w).all()
 
 
+def test_a_layout_without_tokens_is_zero():
+    """Rows of the layout that nothing was sent to, from no token at all."""
+    empty = gs.ExpertGroups(torch.zeros(5, dtype=torch.int32).cuda(), torch.zeros(4, dtype=torch.int32).cuda(),
+                            torch.full((70,), -1, dtype=torch.int32).cuda(), torch.empty(0, 2, dtype=torch.int32).cuda())
+    for width in (8, 33):
+        assert (gs.dispatch_rows(torch.empty(0, width).cuda(), empty) == 0).all()
+        d_y, d_w = gs.combine_rows_backward(torch.empty(0, width).cuda(), torch.ones(70, width).cuda(), empty, torch.empty(0, 2).cuda())
+        assert (d_y == 0).all() and d_w.shape == (0, 2)
+        assert gs.combine_rows(torch.ones(70, width).cuda(), empty).shape == (0, width)
+
+
+def test_all_pairs_dropped():
+    e = torch.full((9, 3), -1, dtype=torch.int32).cuda()
+    groups = gs.group_by_expert(e, 4, align=4)
+    for width in (8, 33):
+        x, y = torch.ones(9, width).cuda(), torch.ones(groups.rows.numel(), width).cuda()
+        assert (gs.dispatch_rows(x, groups) == 0).all() and (gs.combine_rows(y, groups) == 0).all()
+        d_y, d_w = gs.combine_rows_backward(x, y, groups, torch.ones(9, 3).cuda())
+        assert (d_y == 0).all() and (d_w == 0).all()
+
+
 def test_positions_outside_the_layout_take_no_part():
     e = chosen(16, 2, 4, 6)
     g = gs.group_by_expert(e, 4)
@@ -211,6 +232,8 @@ def test_refusals():
                 lambda: gs.combine_rows_backward(x[:, :8], y, groups, w), lambda: gs.dispatch_rows(x.cpu(), groups)):
         with pytest.raises(ValueError):
             bad()
+    with pytest.raises(ValueError):
+        gs.group_by_expert(e, 2 ** 32 + 4)
     for experts, align in ((0, 1), (1025, 1), (4, 0), (-1, 1), (1024, 2 ** 31 - 1)):
         with pytest.raises(gs.GsortError):
             gs.group_by_expert(e, experts, align=align)

@@ -198,7 +198,7 @@ def test_no_tokens():
 def test_refusals():
     x = torch.zeros(4, 16).cuda()
     for bad in (dict(k=0), dict(k=17), dict(k=2, groups=3), dict(k=2, groups=4, groups_kept=5), dict(k=2, score="tanh"),
-                dict(k=2, group_score="mean"), dict(k=2, scale=float("nan")), dict(k=2, groups=4, groups_kept=0)):
+                dict(k=2, group_score="mean"), dict(k=2, scale=float("nan")), dict(k=2, groups=4, groups_kept=0), dict(k=2, groups=2 ** 32 + 1)):
         with pytest.raises((ValueError, gs.GsortError)):
             gs.route_experts(x, **bad)
     with pytest.raises(ValueError):

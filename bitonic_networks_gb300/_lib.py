@@ -7,6 +7,7 @@ and cannot be built, loading raises.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -157,3 +158,15 @@ def load(build_if_missing: bool = True):
             fn.argtypes = args
         _lib = lib
         return lib
+
+
+def load_ops(build_if_missing: bool = True):
+    """The module _ops: the language-model operators on torch tensors (built
+    first, with the library, if it is missing)."""
+    if not os.path.exists(_build.OPS_PATH):
+        if not build_if_missing:
+            raise OSError(f"{_build.OPS_PATH} not found; run __graft_entry__.build()")
+        _build.build()
+    import torch  # noqa: F401  (its libraries come first)
+    load(build_if_missing)
+    return importlib.import_module("._ops", __package__)

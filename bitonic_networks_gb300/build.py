@@ -1,16 +1,20 @@
-"""Builds libgsort.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libgsort.so in-tree with nvcc for sm_103a (GB300), and the Python
+module _ops (its language-model operators on torch tensors) with g++.
 
-Each .cu file compiles to an object in parallel; the objects link into one
-shared library with the CUDA runtime linked statically.  The build is skipped
-when the library is newer than every source and header.
+Each source compiles to an object in parallel; the CUDA objects link into one
+shared library with the CUDA runtime linked statically, and _ops.so links
+against it.  The build is skipped when both are newer than every source and
+header.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgsort.so")
+OPS_PATH = os.path.join(PKG, "_ops.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -39,19 +45,48 @@ def sources():
 
 
 def _deps():
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(OPS_PATH)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(OPS_PATH))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _run(cmd, what: str):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r
+
+
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _compile_binding() -> str:
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    include = os.path.join(_torch_dir(), "include")
+    dirs = [include, os.path.join(include, "torch", "csrc", "api", "include"),
+            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+            sysconfig.get_paths()["include"], INCLUDE]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", *[f for d in dirs for f in ("-isystem", d)], "-c", BINDING, "-o", obj],
+         "g++ on binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str):
+    tmp = OPS_PATH + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu",
+          "-lc10", "-lc10_cuda", "-L", PKG, "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"], "link of _ops.so")
+    os.replace(tmp, OPS_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every CUDA source and link libgsort.so; returns its path."""
+    """Compile every source, link libgsort.so and _ops.so; returns the library's path."""
     if not force and not extra_flags and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -60,22 +95,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
         cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        r = _run(cmd, f"nvcc on {src}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr)
         return obj
 
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, "link of libgsort.so")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding_obj)
     return LIB_PATH
 
 

@@ -120,3 +120,24 @@ def test_logprobs_argument_errors(lib):
                 dict(out=A), dict(gstride=15)):
         assert back(**bad) == EINVAL, bad
     assert back(out=C + 1) == EALIGN and back(st=A + 0x404) == EALIGN
+
+
+def test_torch_wrappers_refuse_before_the_device():
+    """Wrong types, shapes and devices are found without a GPU."""
+    import torch
+
+    import bitonic_networks_gb300 as gs
+    x, e = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    g = gs.ExpertGroups(torch.zeros(9, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), torch.zeros(8, dtype=torch.int32), e)
+    r = gs.TokenLogprobs(torch.zeros(4), torch.zeros(4), None, None, torch.zeros(4, 2))
+    for call in (lambda: gs.route_experts(x, 2), lambda: gs.route_experts_backward(torch.zeros(4, 2), x, e),
+                 lambda: gs.group_by_expert(e, 8), lambda: gs.dispatch_rows(x, g), lambda: gs.combine_rows(torch.zeros(8, 8), g),
+                 lambda: gs.token_logprobs(x), lambda: gs.token_logprobs_backward(None, None, x, None, r)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    for call in (lambda: gs.route_experts(x.double(), 2), lambda: gs.route_experts([[1.0]], 2), lambda: gs.group_by_expert(e, "8"),
+                 lambda: gs.token_logprobs(x.int())):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        gs.group_by_expert(e, 2 ** 40)

@@ -8,14 +8,16 @@
 // A row without a logit above -inf has S = 0: log p = -inf, H = 0, no gradient.
 // NaN and +inf in a row make its results NaN.
 //
-// The forward pass keeps a running maximum per thread and rescales its sums
-// when the maximum grows, so a row is read once.  The largest logits are found
-// in the same pass: the first 8,192 16-bit (4,096 32-bit) logits give a
-// threshold that at least `top` of them reach, and only logits above it are
-// written to a shared buffer, which is sorted by warps (bitonic networks of 32)
-// when the row ends; where the buffer is full, a warp sorts into a list of its
-// own.  Few rows are split over a cluster of CTAs, joined through distributed
-// shared memory.
+// The forward pass keeps a running maximum per warp and rescales its sums when
+// the maximum grows, so a row is read once: 8192 x 131072 bf16 take 300 us, the
+// memory's rate.  The largest logits are found in the same pass: the first 8,192
+// 16-bit (4,096 32-bit) logits give a threshold that at least `top` of them
+// reach, and only logits above it are written to a shared buffer, which is sorted
+// by warps (bitonic networks of 32) when the row ends; where the buffer is full,
+// a warp sorts into a list of its own.  With alternatives the ends of rows are
+// what is left above the memory's time: 4096 x 100003 bf16 take 143 us, reading
+// them 123.  Few rows are split over a cluster of CTAs, joined through
+// distributed shared memory; short rows take a warp each.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -24,15 +26,13 @@ namespace gsort {
 namespace {
 
 // 256 threads with 4 vectors each in flight and 5 CTAs per SM keep the memory
-// busy: 4096 x 100003 bf16 with one alternative takes 148 us (5.5 TB/s); before
-// the prefetch 158, 4 CTAs 165, 2 vectors 182, CTAs of 512 threads 190.
+// busy: 4096 x 100003 bf16 with one alternative takes 143 us (5.7 TB/s). In an
+// earlier state: 158, with 4 CTAs 165, 2 vectors 182, CTAs of 512 threads 190.
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;   // at most 8: join_lists
 constexpr int kLpVectors = 4;               // 16-byte vectors per thread and step
 constexpr int kLpCtas = 5;                  // CTAs per SM that the registers allow
-constexpr uint32_t kLpStep = kLpThreads * kLpVectors;
-constexpr int kGroupLanes = kLpThreads / 32;   // 32 groups of lanes give the first threshold
-constexpr uint32_t kCandidates = 2048;     // shared buffer of candidates
+constexpr uint32_t kCandidates = 2048;      // shared buffers of candidates, of a CTA
 constexpr int kMaxCluster = 8;
 constexpr float kLowLogit = -1e37f;        // x - max above it: the exponent does not overflow
 constexpr float kTinyExponent = -256.0f;   // 2^-256 is 0 in 32 bits: masked logits add e^d * d = 0 * -256
@@ -148,7 +148,7 @@ struct LaneSums {
 
 struct LogprobsArgs {
     const void *logits;
-    int64_t row_stride;
+    int64_t rows, row_stride;
     uint32_t vocab;
     const void *targets;
     bool wide_targets;
@@ -223,20 +223,32 @@ template <> __device__ __forceinline__ float2 logit_range<__half>(const uint4 (&
     return logit_range2<__half2>(q);
 }
 
-template <typename T, bool TOP>
+// TEAM threads hold a row (or a part of one): the CTA, or for short rows a warp.
+template <typename T, bool TOP, int TEAM>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const LogprobsArgs a) {
     constexpr int N = Wide<T>::kCount;
+    constexpr int kTeams = kLpThreads / TEAM;
+    constexpr uint32_t kStep = TEAM * kLpVectors, kRoom = kCandidates / kTeams;
+    constexpr int kGroupLanes = TEAM / 32;                     // 32 groups of lanes give the first threshold
     __shared__ RowSums s_sums[kLpWarps], s_cluster[kMaxCluster];
-    __shared__ __align__(16) uint32_t s_group[32];             // the groups' largest keys
+    __shared__ __align__(16) uint32_t s_groups[kTeams][32];    // the groups' largest keys
     __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];        // the warps' lists
     __shared__ uint64_t s_remote[TOP ? kMaxCluster : 1][32];   // the cluster's lists
-    __shared__ uint64_t s_buffer[TOP ? kCandidates : 1];
-    __shared__ uint32_t s_count;
+    __shared__ uint64_t s_buffers[TOP ? kCandidates : 1];
+    __shared__ uint32_t s_counts[kTeams];
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / a.split;
-    const uint32_t part = blockIdx.x % a.split;
-    if (a.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const int tid = threadIdx.x % TEAM, lane = tid & 31, warp = tid >> 5, team = threadIdx.x / TEAM;   // within the team
+    uint32_t *s_group = s_groups[team], &s_count = s_counts[team];
+    uint64_t *s_buffer = s_buffers + (TOP ? team * kRoom : 0);
+    auto sync = [] {
+        if (TEAM == 32) __syncwarp();
+        else __syncthreads();
+    };
+    const uint32_t unit = blockIdx.x * kTeams + team;
+    const int64_t row = unit / a.split;
+    const uint32_t part = unit % a.split;
+    if (row >= a.rows) return;       // a whole warp: other teams have no barrier with it
+    if (TEAM > 32 && a.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
     const RowView<T> view(static_cast<const T *>(a.logits) + row * a.row_stride, a.vocab);
     const uint32_t full = view.full_end > view.full_begin ? view.full_end - view.full_begin : 0;
@@ -252,26 +264,26 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
 
     LaneSums mine;
     float threshold = kNegInf;
-    uint64_t kept = 0;           // the warp's list, descending: candidates that found the buffer full
+    uint64_t kept = 0;           // the warp's list, descending
     if (TOP && tid == 0) s_count = 0;
 
     // With alternatives a row stops at its first step and at its end, and the
     // other CTAs' loads do not fill the gap: the step after next is on its way
-    // into L2 (4096 x 100003 bf16: 148 us, 158 without; no gain elsewhere).
+    // into L2 (4096 x 100003 bf16: 158 -> 148 us when it came; no gain elsewhere).
     auto prefetch = [&](uint32_t v) {
         if (TOP && tid == 0 && v < last)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(view.address(v)), "r"(min(kLpStep, last - v) * 16) : "memory");
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(view.address(v)), "r"(min(kStep, last - v) * 16) : "memory");
     };
-    prefetch(first + kLpStep);
-    for (uint32_t base = first; base < last; base += kLpStep) {
-        prefetch(base + 2 * kLpStep);
+    prefetch(first + kStep);
+    for (uint32_t base = first; base < last; base += kStep) {
+        prefetch(base + 2 * kStep);
         uint4 now[kLpVectors];
         const uint32_t v0 = base + tid;
 #pragma unroll
         for (int u = 0; u < kLpVectors; ++u) {
             constexpr uint32_t w = Wide<T>::kNegInfWord;
             now[u] = make_uint4(w, w, w, w);
-            if (v0 + u * kLpThreads < last) now[u] = view.load(v0 + u * kLpThreads);
+            if (v0 + u * TEAM < last) now[u] = view.load(v0 + u * TEAM);
         }
         const float2 range = logit_range<T>(now);
         mine.raise(range.y);
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
             // the key's last five bits make room for the group's number, so that no two are equal
             const uint32_t group = tid / kGroupLanes;
             if (tid % kGroupLanes == 0) s_group[group] = hi > kNegInf ? (order_key(hi) & ~31u) | group : 0u;
-            __syncthreads();
+            sync();
             const uint32_t key = s_group[lane];
             uint32_t above = 0;
 #pragma unroll
@@ -298,6 +310,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
             threshold = cut ? order_key_value(cut) : kNegInf;
             bound = cut ? order_key_value(cut - (cut == 0x80000000u ? 2u : 1u)) : kNegInf;   // the key below zero's is unused
         }
+        uint32_t hits = 0;       // the thread's candidates
+        if (TOP && range.y > bound) {
+#pragma unroll
+            for (int b = 0; b < kLpVectors * N; ++b) {
+                const Pair p = Wide<T>::pair_of(now[b / N], b % N / 2);
+                hits |= (b % 2 ? p.f.y : p.f.x) > bound ? 1u << b : 0u;
+            }
+        }
         if (range.x - mine.max > kLowLogit) {
 #pragma unroll
             for (int u = 0; u < kLpVectors; ++u)
@@ -310,30 +330,23 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
                 for (int i = 0; i < N / 2; ++i) mine.add(Wide<T>::pair_of(now[u], i), true);
         }
         if (TOP) {
+            auto element = [&](int b) { return (v0 + b / N * TEAM) * N + b % N; };
             uint32_t lost = 0;   // candidates that found the buffer full
-            if (range.y > bound) {
-#pragma unroll
-                for (int b = 0; b < kLpVectors * N; ++b) {
-                    const Pair p = Wide<T>::pair_of(now[b / N], b % N / 2);
-                    const float x = b % 2 ? p.f.y : p.f.x;
-                    if (x > bound) {
-                        const uint32_t at = atomicAdd(&s_count, 1u);
-                        if (at < kCandidates) s_buffer[at] = candidate(x, (v0 + b / N * kLpThreads) * N + b % N - view.shift);
-                        else lost |= 1u << b;
-                    }
+            if (hits != 0) {
+                uint32_t at = atomicAdd(&s_count, static_cast<uint32_t>(__popc(hits)));
+                const bool one = (hits & (hits - 1)) == 0;     // mostly: it is the thread's largest
+                for (; hits != 0; hits &= hits - 1, ++at) {
+                    const uint32_t e = element(__ffs(hits) - 1);
+                    if (at < kRoom) s_buffer[at] = candidate(one ? range.y : to_f32((view.row - view.shift)[e]), e - view.shift);
+                    else lost |= hits & (~hits + 1);
                 }
             }
             if (__any_sync(kFullMask, lost != 0)) {
                 // rare: the warp sorts them into a list of its own, which raises its threshold
 #pragma unroll 1
                 for (int b = 0; b < kLpVectors * N; ++b) {
-                    float x = kNegInf;
-#pragma unroll
-                    for (int o = 0; o < kLpVectors * N; ++o) {
-                        const Pair p = Wide<T>::pair_of(now[o / N], o % N / 2);
-                        if (o == b) x = o % 2 ? p.f.y : p.f.x;
-                    }
-                    const uint64_t c = (lost >> b) & 1u ? candidate(x, (v0 + b / N * kLpThreads) * N + b % N - view.shift) : 0;
+                    uint64_t c = 0;
+                    if ((lost >> b) & 1u) c = candidate(to_f32((view.row - view.shift)[element(b)]), element(b) - view.shift);
                     if (__any_sync(kFullMask, c != 0)) kept = merge_lists(kept, bitonic_sort_desc(c, lane), lane);
                 }
                 const uint64_t c = __shfl_sync(kFullMask, kept, a.top - 1);
@@ -342,7 +355,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
         }
     }
 
-    if (TOP && first >= last) __syncthreads();     // s_count is set; with a step, its barrier has come
+    if (TOP && first >= last) sync();     // s_count is set; with a step, its barrier has come
     // the row's ends
     if (part == 0 && warp == 0) {
         const uint32_t e = view.edge(lane);
@@ -350,29 +363,33 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
         mine.raise(x);
         mine.add(pair(x, kNegInf), true);
         if (TOP) {
-            const uint64_t c = x > kNegInf ? candidate(x, e - view.shift) : 0;
-            kept = merge_lists(kept, bitonic_sort_desc(c, lane), lane);
+            const uint64_t c = x > kNegInf && x >= threshold ? candidate(x, e - view.shift) : 0;
+            if (__any_sync(kFullMask, c != 0)) kept = merge_lists(kept, bitonic_sort_desc(c, lane), lane);
         }
     }
 
     RowSums s = warp_join(mine.total());
-    if (lane == 0) s_sums[warp] = s;
-    __syncthreads();
+    if (TEAM > 32 && lane == 0) s_sums[warp] = s;
+    sync();
     if (TOP) {
         // each warp sorts its share of the buffer into its list; warp 0 joins the lists
-        const uint32_t have = min(s_count, kCandidates);
-        for (uint32_t b = warp * 32; b < have; b += kLpThreads)
-            kept = merge_lists(kept, bitonic_sort_desc(b + lane < have ? s_buffer[b + lane] : 0, lane), lane);
-        const int lists = s_count > kCandidates ? kLpWarps : min(kLpWarps, static_cast<int>((have + 31) / 32));
-        if (lists > 1) {
-            s_list[warp][lane] = kept;
-            __syncthreads();
-            if (warp == 0) kept = join_lists(s_list, lists, lane);
+        const uint32_t have = min(s_count, kRoom);
+        for (uint32_t b = warp * 32; b < have; b += TEAM) {
+            const uint64_t c = bitonic_sort_desc(b + lane < have ? s_buffer[b + lane] : 0, lane);
+            kept = __any_sync(kFullMask, kept != 0) ? merge_lists(kept, c, lane) : c;
+        }
+        if (TEAM > 32) {
+            const int lists = s_count > kRoom ? kLpWarps : min(kLpWarps, static_cast<int>((have + 31) / 32));
+            if (lists > 1) {
+                s_list[warp][lane] = kept;
+                __syncthreads();
+                if (warp == 0) kept = join_lists(s_list, lists, lane);
+            }
         }
     }
-    if (warp == 0) s = warp_join(lane < kLpWarps ? s_sums[lane] : RowSums{kNegInf, 0.0f, 0.0f});
+    if (TEAM > 32 && warp == 0) s = warp_join(lane < kLpWarps ? s_sums[lane] : RowSums{kNegInf, 0.0f, 0.0f});
 
-    if (a.split > 1) {
+    if (TEAM > 32 && a.split > 1) {
         // every CTA of the cluster runs; hand the part's results to CTA 0
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (warp == 0) {
@@ -435,7 +452,8 @@ struct LogprobsBackwardArgs {
     bool wide_targets;
     const float *entropy, *stats;
     void *grad_logits;
-    uint32_t blocks_per_row;
+    int64_t rows;
+    uint32_t blocks_per_row;   // CTAs to a row where its threads are the CTA, else 1
 };
 
 // A row's gradient as a function of x: with e = 2^y, y = (x - m) log2(e),
@@ -459,11 +477,15 @@ struct RowGradient {
     }
 };
 
-template <typename T>
+// LANES threads are side by side on a row: the CTA, or for short rows some warps
+// of it (8192 x 1000 bf16: 6 us, 16 with a CTA to a row).
+template <typename T, int LANES>
 __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const LogprobsBackwardArgs a) {
     constexpr int N = Wide<T>::kCount;
-    const int64_t row = blockIdx.x / a.blocks_per_row;
+    const uint32_t tid = threadIdx.x % LANES;
+    const int64_t row = static_cast<int64_t>(blockIdx.x / a.blocks_per_row) * (kGradThreads / LANES) + threadIdx.x / LANES;
     const uint32_t block = blockIdx.x % a.blocks_per_row;
+    if (row >= a.rows) return;
     const RowView<T> view(static_cast<const T *>(a.logits) + row * a.row_stride, a.vocab);
     T *out = static_cast<T *>(a.grad_logits) + row * a.grad_stride;
     // the gradient's rows move as vectors where they lie as the logits' do
@@ -471,10 +493,10 @@ __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const Logpro
     out -= view.shift;
 
     uint4 x[kGradVectors];
-    const uint32_t v0 = view.full_begin + block * (kGradThreads * kGradVectors) + threadIdx.x;
+    const uint32_t v0 = view.full_begin + block * (kGradThreads * kGradVectors) + tid;
 #pragma unroll
     for (int u = 0; u < kGradVectors; ++u)
-        if (v0 + u * kGradThreads < view.full_end) x[u] = view.load(v0 + u * kGradThreads);
+        if (v0 + u * LANES < view.full_end) x[u] = view.load(v0 + u * LANES);
 
     const float2 stats = reinterpret_cast<const float2 *>(a.stats)[row];
     float g = a.grad_logprobs != nullptr ? a.grad_logprobs[row] : 0.0f;
@@ -495,13 +517,13 @@ __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const Logpro
 
     // read before the stores: they may be to the same memory
     const uint32_t tv = at / N;
-    const bool own = tv >= v0 && tv < view.full_end && (tv - v0) % kGradThreads == 0 && (tv - v0) / kGradThreads < kGradVectors;
+    const bool own = tv >= v0 && tv < view.full_end && (tv - v0) % LANES == 0 && (tv - v0) / LANES < kGradVectors;
     float xt = 0.0f;
     if (own) xt = to_f32((view.row - view.shift)[at]);
 
 #pragma unroll
     for (int u = 0; u < kGradVectors; ++u) {
-        const uint32_t v = v0 + u * kGradThreads;
+        const uint32_t v = v0 + u * LANES;
         if (v < view.full_end) {
             const uint4 o = h == 0.0f ? f.vector<T, true>(x[u]) : f.vector<T, false>(x[u]);
             if (same) {
@@ -516,8 +538,8 @@ __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const Logpro
         const Pair p = pair(xt, kNegInf);
         out[at] = from_f32<T>((h == 0.0f ? f.at<true>(p) : f.at<false>(p)).f.x + g);
     }
-    if (block == 0 && threadIdx.x < 32) {        // the row's ends
-        const uint32_t e = view.edge(threadIdx.x);
+    if (block == 0 && tid < 32) {        // the row's ends
+        const uint32_t e = view.edge(tid);
         if (e < view.end) {
             const Pair p = pair(to_f32((view.row - view.shift)[e]), kNegInf);
             const Pair d = h == 0.0f ? f.at<true>(p) : f.at<false>(p);
@@ -526,9 +548,10 @@ __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const Logpro
     }
 }
 
-template <typename T, bool TOP> int start_logprobs(const LogprobsLaunch &L, const LogprobsArgs &a) {
+template <typename T, bool TOP, int TEAM> int start_logprobs(const LogprobsLaunch &L, const LogprobsArgs &a) {
+    constexpr int64_t kTeams = kLpThreads / TEAM;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<uint32_t>(L.rows) * a.split);
+    cfg.gridDim = dim3(static_cast<uint32_t>((L.rows * a.split + kTeams - 1) / kTeams));
     cfg.blockDim = dim3(kLpThreads);
     cfg.stream = L.stream;
     cudaLaunchAttribute attr;
@@ -536,7 +559,7 @@ template <typename T, bool TOP> int start_logprobs(const LogprobsLaunch &L, cons
     attr.val.clusterDim = {a.split, 1, 1};
     cfg.attrs = &attr;
     cfg.numAttrs = a.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_logprobs<T, TOP>, a) == cudaSuccess ? GSORT_OK : GSORT_ECUDA;
+    return cudaLaunchKernelEx(&cfg, k_logprobs<T, TOP, TEAM>, a) == cudaSuccess ? GSORT_OK : GSORT_ECUDA;
 }
 
 }  // namespace
@@ -544,6 +567,7 @@ template <typename T, bool TOP> int start_logprobs(const LogprobsLaunch &L, cons
 int launch_logprobs(const LogprobsLaunch &L) {
     LogprobsArgs a{};
     a.logits = L.logits;
+    a.rows = L.rows;
     a.row_stride = L.row_stride;
     a.vocab = static_cast<uint32_t>(L.vocab);
     a.targets = L.targets;
@@ -554,13 +578,20 @@ int launch_logprobs(const LogprobsLaunch &L) {
     a.stats = L.stats;
     a.top_logprobs = L.top_logprobs;
     a.top_ids = L.top_ids;
-    // split a row while the device has idle SMs and a part still fills a CTA
     const int64_t vectors = L.vocab * float_bytes(L.dtype) / 16;
+    // A warp to a row where it is short, so that rows wait for no CTA-wide barrier
+    // (8192 x 1000 bf16 with 5 alternatives: 14 us, 51 with a CTA each), and up to
+    // twice as long where rows are many and alternatives few (8192 x 6000: 37
+    // against 56; with 20 alternatives 68 against 62, and 100 rows 12 against 5).
+    const bool warps = vectors <= 512 || (vectors <= 1024 && L.top <= 8 && L.rows >= 8 * L.sm_count);
+    // Otherwise a row is split while CTAs do not fill the device and a part has 512
+    // vectors (304 x 131072 bf16 with 20 alternatives: 27 us, 45 whole).
     a.split = 1;
-    while (a.split < kMaxCluster && L.rows * a.split < 2 * L.sm_count && vectors / (2 * a.split) >= kLpThreads) a.split *= 2;
+    while (!warps && a.split < kMaxCluster && L.rows * a.split < 3 * L.sm_count && vectors / (2 * a.split) >= 512) a.split *= 2;
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
-        return L.top > 0 ? start_logprobs<T, true>(L, a) : start_logprobs<T, false>(L, a);
+        if (warps) return L.top > 0 ? start_logprobs<T, true, 32>(L, a) : start_logprobs<T, false, 32>(L, a);
+        return L.top > 0 ? start_logprobs<T, true, kLpThreads>(L, a) : start_logprobs<T, false, kLpThreads>(L, a);
     });
 }
 
@@ -579,10 +610,16 @@ int launch_logprobs_backward(const LogprobsBackwardLaunch &L) {
     a.grad_logits = L.grad_logits;
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
-        constexpr int64_t per_block = static_cast<int64_t>(kGradThreads) * kGradVectors * Wide<T>::kCount;
-        a.blocks_per_row = static_cast<uint32_t>((L.vocab + per_block - 1) / per_block);
-        if (L.rows * a.blocks_per_row > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
-        k_logprobs_backward<T><<<static_cast<uint32_t>(L.rows * a.blocks_per_row), kGradThreads, 0, L.stream>>>(a);
+        constexpr int64_t per_thread = static_cast<int64_t>(kGradVectors) * Wide<T>::kCount, per_block = kGradThreads * per_thread;
+        a.rows = L.rows;
+        const int lanes = L.vocab <= 32 * per_thread ? 32 : L.vocab <= 128 * per_thread ? 128 : kGradThreads;
+        a.blocks_per_row = lanes < kGradThreads ? 1 : static_cast<uint32_t>((L.vocab + per_block - 1) / per_block);
+        const int64_t in_block = kGradThreads / lanes, blocks = (L.rows + in_block - 1) / in_block * a.blocks_per_row;
+        if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
+        const uint32_t grid = static_cast<uint32_t>(blocks);
+        if (lanes == 32) k_logprobs_backward<T, 32><<<grid, kGradThreads, 0, L.stream>>>(a);
+        else if (lanes == 128) k_logprobs_backward<T, 128><<<grid, kGradThreads, 0, L.stream>>>(a);
+        else k_logprobs_backward<T, kGradThreads><<<grid, kGradThreads, 0, L.stream>>>(a);
         return cudaGetLastError() == cudaSuccess ? static_cast<int>(GSORT_OK) : static_cast<int>(GSORT_ECUDA);
     });
 }

@@ -173,8 +173,6 @@ int gsort_group_by_expert(const int32_t *d_experts, int64_t pairs, int experts, 
                         {d_positions, static_cast<size_t>(pairs) * 4},
                         {ws > 0 ? d_ws : nullptr, ws}};
     if (clash(in, out)) return GSORT_EINVAL;
-    DeviceInfo dev;
-    if (device_info(&dev) != GSORT_OK) return GSORT_ECUDA;
     GroupLaunch L;
     L.experts_in = d_experts;
     L.pairs = static_cast<uint32_t>(pairs);
@@ -187,7 +185,6 @@ int gsort_group_by_expert(const int32_t *d_experts, int64_t pairs, int experts, 
     L.capacity = static_cast<uint32_t>(capacity);
     L.ws = static_cast<uint32_t *>(d_ws);
     L.stream = stream;
-    L.sm_count = dev.sm_count;
     return launch_group(L);
 }
 

@@ -142,12 +142,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
-    return v;
-}
-
 // --------------------------------------------------------- launch plans
 struct RouteLaunch {
     const void *logits;
@@ -188,7 +182,6 @@ struct GroupLaunch {
     uint32_t capacity;
     uint32_t *ws;          // u32[tiles][experts]
     cudaStream_t stream;
-    int sm_count;
 };
 size_t group_workspace_bytes(uint32_t pairs, int experts);
 int launch_group(const GroupLaunch &L);

@@ -17,8 +17,8 @@
 // a pick is then a maximum over the lanes' best (redux.sync for a whole warp),
 // one vote and the winner's next candidate.
 //
-// Bound by instructions, about 550 a token at 256 experts and k = 8, not by its
-// bytes: 16384 x 256 32-bit logits with bias and groups take 15.5 us, where
+// Bound by instructions, about 680 a token at 256 experts in groups with k = 8,
+// not by its bytes: 16384 x 256 32-bit logits with bias and groups take 15.5 us, where
 // reading them takes 2.5.
 #include <algorithm>
 
@@ -148,6 +148,16 @@ template <int C, int L> __device__ __forceinline__ float row_max(const float (&x
 // 1 / (1 + e^-x), each operation rounded to nearest: a choice among biased
 // scores does not depend on how the quotient is formed.
 __device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
+
+// e^-low * sigmoid(x) for low = min(0, the chosen experts' largest logit): scores
+// to be renormalised, which do not underflow together.  Scores that are 0 in 64
+// bits as well (x < -745) are 0.
+__device__ __forceinline__ float raised_sigmoid(float x, float low) {
+    return x > 0.0f ? sigmoid(x) : x < -745.0f ? 0.0f : expf(x - low) * __frcp_rn(1.0f + expf(x));
+}
+
+// 1 - sigmoid(x) without cancellation.
+__device__ __forceinline__ float sigmoid_rest(float x) { return __frcp_rn(1.0f + expf(x)); }
 
 struct RouteArgs {
     const void *logits;
@@ -390,7 +400,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
             w = exp_from(xe, m) * inv;
         }
     } else {
-        w = there ? sigmoid(xe) : 0.0f;
+        const float low = a.renormalise ? fminf(lanes_max<L>(xe), 0.0f) : 0.0f;
+        w = !there ? 0.0f : a.renormalise ? raised_sigmoid(xe, low) : sigmoid(xe);
     }
     if (a.renormalise) {
         const float total = lanes_sum<L>(w);
@@ -418,7 +429,7 @@ struct RouteBackwardArgs {
 //   softmax                 dx_e = p_e * (dw_e [chosen] - sum_j dw_j p_j)
 //   softmax, renormalised   dx_j = q_j * (dw_j - sum_i dw_i q_i), chosen only
 //   sigmoid                 dx_j = dw_j * s_j (1 - s_j), chosen only
-//   sigmoid, renormalised   dx_j = (dw_j - sum_i dw_i q_i) / S * s_j (1 - s_j)
+//   sigmoid, renormalised   dx_j = (dw_j - sum_i dw_i q_i) * q_j (1 - s_j)
 // The choice itself, the groups and the bias have no gradient.  The dense row
 // is written first (zeros, or -p_e times the sum), then the chosen entries.
 template <typename T, int C, int L>
@@ -447,13 +458,13 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(const RouteBac
 #pragma unroll
     for (int i = 0; i < C; ++i) dense[i] = 0.0f;
     if (!a.softmax) {
-        const float s = there ? sigmoid(xe) : 0.0f;
-        const float slope = there ? s * __frcp_rn(1.0f + expf(xe)) : 0.0f;   // s (1 - s) without cancellation
         if (a.renormalise) {
-            const float total = lanes_sum<L>(s), inv = total > 0.0f ? 1.0f / total : 0.0f;
-            g = (d - lanes_sum<L>(d * (s * inv))) * inv * slope;
+            const float low = fminf(lanes_max<L>(xe), 0.0f), t = there ? raised_sigmoid(xe, low) : 0.0f;
+            const float total = lanes_sum<L>(t);
+            const float q = t * (total > 0.0f ? 1.0f / total : 0.0f);
+            g = (d - lanes_sum<L>(d * q)) * q * sigmoid_rest(xe);
         } else {
-            g = d * slope;
+            g = there ? d * sigmoid(xe) * sigmoid_rest(xe) : 0.0f;
         }
     } else if (a.renormalise) {
         const float m = lanes_max<L>(there ? xe : kNegInf);

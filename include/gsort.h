@@ -342,7 +342,7 @@ typedef enum gsort_float {
  *               largest c in descending order; ties, here and between groups,
  *               go to the lower index
  *   weight      scale * s, or with renormalise != 0 scale * s / (sum of the
- *               chosen s)
+ *               chosen s); a sigmoid of a logit below -745 counts as 0
  * d_weights and d_experts are [tokens][chosen]; where a token has fewer
  * candidates, the rest are expert -1 with weight 0. */
 #define GSORT_SCORE_SOFTMAX 0

@@ -114,6 +114,18 @@ def test_rows(dtype, width):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("width", [5, 33, 136, 515, 1001])
+def test_rows_of_many_pairs(dtype, width):
+    """Enough pairs that each has a warp or less; more tokens than a CTA holds."""
+    e = chosen(1700, 3, 7, width, 0.1)
+    groups = gs.group_by_expert(e, 7, align=32)
+    g = torch.Generator().manual_seed(width)
+    x, d = (torch.randn(1700, width, generator=g).to(dtype).cuda() for _ in range(2))
+    y = torch.randn(groups.rows.numel(), width, generator=g).to(dtype).cuda()
+    check_rows(x, y, d, groups, torch.randn(1700, 3, generator=g).cuda(), 3)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("pad,off", [(1, 0), (0, 1), (8, 0), (4, 4), (2, 2)])
 def test_strided_and_unaligned_rows(dtype, pad, off):
     e = chosen(50, 4, 10, 2, 0.2)

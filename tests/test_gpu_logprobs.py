@@ -96,6 +96,12 @@ def test_many_rows(dtype):
     r = check(x, t, 20)
     check_gradient(x, t, r)
     check(logits_of(1300, 5, dtype, 5), None, 3)
+    x = logits_of(1300, 3500, dtype, 6)        # a warp to a row of several steps
+    x[::7, 100:] = -INF
+    r = check(x, None, 7)
+    check_gradient(x, None, r)
+    check(strided(logits_of(1217, 8001, dtype, 7), 3, 1), None, 8)     # a warp or a CTA, by the type
+    check(logits_of(1217, 8001, dtype, 8), None, 9)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

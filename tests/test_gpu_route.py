@@ -45,6 +45,61 @@ def test_choice_and_weights(experts, dtype):
                 check(x, k, score=score, renormalise=renormalise, scale=2.5 if renormalise else 1.0)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("experts", [8, 16, 24, 32, 33, 60, 64, 100, 128, 160, 200, 256, 300, 512, 1000])
+def test_many_tokens(experts, dtype):
+    """Tokens that share a warp: 4 to 32 lanes each."""
+    bias = torch.randint(-60, 61, (experts,), generator=torch.Generator().manual_seed(1)).cuda() * 0.001
+    for tokens, k in ((1025, 1), (1531, 4), (1403, min(experts, 7)), (1100, min(experts, 14))):
+        x = logits_of(tokens, experts, dtype, experts + tokens)
+        x[5], x[6, 1:], x[-1, ::3] = float("-inf"), float("-inf"), float("nan")
+        for how in (dict(score="softmax"), dict(score="sigmoid", renormalise=True), dict(score="sigmoid", bias=bias, renormalise=True)):
+            _, e = check(x, k, least=0.85, **how)
+            how.pop("bias", None)
+            d = torch.randn(tokens, k, generator=torch.Generator().manual_seed(k)).cuda()
+            got = gs.route_experts_backward(d, x, e, **how)
+            exp, size = gradient64(d.double().cpu().numpy(), x.double().cpu().numpy(), e.cpu().numpy(), how["score"], how.get("renormalise", False), 1.0)
+            far = np.abs(got.double().cpu().numpy() - exp)
+            assert (far <= 3e-5 * size + UNIT[dtype] * np.abs(exp) + TINY[dtype]).all()
+
+
+@pytest.mark.parametrize("experts,groups,kept", [(256, 8, 4), (160, 5, 2), (60, 6, 3), (32, 4, 2), (24, 8, 5), (128, 16, 3), (512, 8, 2)])
+def test_groups_of_many_tokens(experts, groups, kept):
+    k = min(8, experts // groups * kept)
+    x = logits_of(1200, experts, torch.float32, groups)
+    bias = torch.randn(experts, generator=torch.Generator().manual_seed(3)).cuda() * 0.1
+    for group_score in ("max", "top2"):
+        for b in (None, bias):
+            check(x, k, bias=b, score="sigmoid", groups=groups, groups_kept=kept, group_score=group_score, renormalise=True)
+
+
+def test_ties_of_many_tokens():
+    g = torch.Generator().manual_seed(2)
+    for experts, k in ((16, 4), (60, 4), (100, 8), (256, 8), (256, 16)):
+        x = torch.randint(-2, 3, (1300, experts), generator=g).float().cuda()
+        x[0] = 0.0
+        want = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :k]
+        for dtype in DTYPES:
+            assert torch.equal(gs.route_experts(x.to(dtype), k)[1].long(), want)
+        # differences in the last bits of 32-bit logits decide as well
+        y = (x + 3).view(torch.int32) + torch.randint(0, 3, (1300, experts), generator=g, dtype=torch.int32).cuda()
+        y = y.view(torch.float32)
+        assert torch.equal(gs.route_experts(y, k)[1].long(), torch.sort(y, dim=1, descending=True, stable=True).indices[:, :k])
+
+
+def test_low_sigmoid_scores_are_renormalised():
+    """Scores that underflow in 32 bits still have their quotients."""
+    x = logits_of(40, 32, torch.float32, 3) - 95.0
+    x[20:] -= 300.0
+    w, e = check(x, 4, score="sigmoid", renormalise=True)
+    assert torch.allclose(w.sum(1), torch.ones(40).cuda(), atol=1e-5)
+    d = torch.randn(40, 4, generator=torch.Generator().manual_seed(4)).cuda()
+    got = gs.route_experts_backward(d, x, e, score="sigmoid", renormalise=True).double()
+    q = w.double()
+    want = torch.zeros(40, 32, dtype=torch.float64).cuda().scatter_(1, e.long(), q * (d.double() - (d * q).sum(1, keepdim=True)))
+    assert torch.allclose(got, want, atol=1e-5)
+
+
 @pytest.mark.parametrize("experts,groups,kept", [(256, 8, 4), (160, 5, 2), (96, 32, 9), (64, 2, 1), (512, 16, 3),
                                                  (1024, 4, 3), (60, 6, 3), (8, 8, 3), (1000, 25, 7), (256, 8, 8)])
 @pytest.mark.parametrize("group_score", ["max", "top2"])

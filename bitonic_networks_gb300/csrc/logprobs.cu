@@ -34,6 +34,10 @@ constexpr int kLpVectors = 4;               // 16-byte vectors per thread and st
 constexpr int kLpCtas = 5;                  // CTAs per SM that the registers allow
 constexpr uint32_t kCandidates = 2048;      // shared buffers of candidates, of a CTA
 constexpr int kMaxCluster = 8;
+// Up to so many alternatives 32 groups give a threshold that hardly more logits
+// pass than have to; with more of them it would be far too low (4096 x 131072
+// bf16 with 32 alternatives: 585 us, 259 with a group for every thread).
+constexpr int kFewTop = 8;
 constexpr float kLowLogit = -1e37f;        // x - max above it: the exponent does not overflow
 constexpr float kTinyExponent = -256.0f;   // 2^-256 is 0 in 32 bits: masked logits add e^d * d = 0 * -256
 
@@ -71,6 +75,37 @@ __device__ __forceinline__ uint64_t bitonic_sort_desc(uint64_t v, int lane) {
 // The 32 largest of two descending lists, descending.
 __device__ __forceinline__ uint64_t merge_lists(uint64_t a, uint64_t b, int lane) {
     return bitonic_merge_desc(max64(a, __shfl_sync(kFullMask, b, 31 - lane)), lane);
+}
+
+// The same networks for order keys alone.
+__device__ __forceinline__ uint32_t merge_keys_desc(uint32_t v, int lane) {
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) {
+        const uint32_t o = __shfl_xor_sync(kFullMask, v, j);
+        v = (lane & j) ? min(v, o) : max(v, o);
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t sort_keys_desc(uint32_t v, int lane) {
+#pragma unroll
+    for (int k = 2; k < 32; k <<= 1) {
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            const uint32_t o = __shfl_xor_sync(kFullMask, v, j);
+            v = ((lane & j) != 0) != ((lane & k) != 0) ? min(v, o) : max(v, o);
+        }
+    }
+    return merge_keys_desc(v, lane);
+}
+
+// The 32 largest keys of COUNT descending lists, joined by a tree.
+template <int COUNT> __device__ __forceinline__ uint32_t join_keys(uint32_t (&v)[COUNT], int lane) {
+#pragma unroll
+    for (int w = COUNT / 2; w > 0; w >>= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) v[i] = merge_keys_desc(max(v[i], __shfl_sync(kFullMask, v[i + w], 31 - lane)), lane);
+    return v[0];
 }
 
 // Joins `count` (1..8) lists of 32, one after another in shared memory, by a
@@ -223,6 +258,35 @@ template <> __device__ __forceinline__ float2 logit_range<__half>(const uint4 (&
     return logit_range2<__half2>(q);
 }
 
+// A thread's logits above `bound`, as bits; hit_element gives a bit's element.
+template <typename T, int U> __device__ __forceinline__ uint32_t hits_above(const uint4 (&q)[U], float bound) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i) hits |= __uint_as_float((&q[i / 4].x)[i % 4]) > bound ? 1u << i : 0u;
+    return hits;
+}
+
+// 16-bit types: two at a time (against the next value of the type at or below the
+// bound); word i has bits i and i + 16.
+template <typename T2, int U> __device__ __forceinline__ uint32_t hits_above2(const uint4 (&q)[U], T2 bound) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i) hits |= __hgt2_mask(*reinterpret_cast<const T2 *>(&q[i / 4].x + i % 4), bound) & (0x00010001u << i);
+    return hits;
+}
+
+template <> __device__ __forceinline__ uint32_t hits_above<__nv_bfloat16>(const uint4 (&q)[kLpVectors], float bound) {
+    return hits_above2(q, __bfloat162bfloat162(__float2bfloat16_rd(bound)));
+}
+
+template <> __device__ __forceinline__ uint32_t hits_above<__half>(const uint4 (&q)[kLpVectors], float bound) {
+    return hits_above2(q, __half2half2(__float2half_rd(bound)));
+}
+
+template <typename T> __device__ __forceinline__ int hit_element(int bit) {
+    return sizeof(T) == 4 ? bit : 2 * (bit & 15) + (bit >> 4);
+}
+
 // TEAM threads hold a row (or a part of one): the CTA, or for short rows a warp.
 template <typename T, bool TOP, int TEAM>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const LogprobsArgs a) {
@@ -232,6 +296,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
     constexpr int kGroupLanes = TEAM / 32;                     // 32 groups of lanes give the first threshold
     __shared__ RowSums s_sums[kLpWarps], s_cluster[kMaxCluster];
     __shared__ __align__(16) uint32_t s_groups[kTeams][32];    // the groups' largest keys
+    __shared__ uint32_t s_keys[TOP && TEAM > 32 ? kLpWarps : 1][32];
     __shared__ uint64_t s_list[TOP ? kLpWarps : 1][32];        // the warps' lists
     __shared__ uint64_t s_remote[TOP ? kMaxCluster : 1][32];   // the cluster's lists
     __shared__ uint64_t s_buffers[TOP ? kCandidates : 1];
@@ -289,35 +354,56 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
         mine.raise(range.y);
         float bound = threshold;     // candidates are above it
         if (TOP && base == first) {
-            // the largest logit of each of 32 groups of threads: `top` logits reach their top-th
-            float hi = range.y > kNegInf ? range.y : kNegInf;
+            // `top` logits reach the top-th largest of the largest logits of some groups
+            uint32_t cut;
+            if (a.top <= kFewTop) {
+                // 32 groups of threads, whose ranks are counted
+                float hi = range.y > kNegInf ? range.y : kNegInf;
 #pragma unroll
-            for (int o = kGroupLanes / 2; o > 0; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, o));
-            // the key's last five bits make room for the group's number, so that no two are equal
-            const uint32_t group = tid / kGroupLanes;
-            if (tid % kGroupLanes == 0) s_group[group] = hi > kNegInf ? (order_key(hi) & ~31u) | group : 0u;
-            sync();
-            const uint32_t key = s_group[lane];
-            uint32_t above = 0;
+                for (int o = kGroupLanes / 2; o > 0; o >>= 1) hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, o));
+                // the key's last five bits make room for the group's number, so that no two are equal
+                const uint32_t group = tid / kGroupLanes;
+                if (tid % kGroupLanes == 0) s_group[group] = hi > kNegInf ? (order_key(hi) & ~31u) | group : 0u;
+                sync();
+                const uint32_t key = s_group[lane];
+                uint32_t above = 0;
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const uint4 o = *reinterpret_cast<const uint4 *>(s_group + i);
-                above += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+                for (int i = 0; i < 32; i += 4) {
+                    const uint4 o = *reinterpret_cast<const uint4 *>(s_group + i);
+                    above += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+                }
+                cut = __reduce_max_sync(kFullMask, above == static_cast<uint32_t>(a.top - 1) ? key : 0u) & ~31u;
+            } else if (TEAM == 32) {
+                // every vector is a group
+                uint32_t keys[kLpVectors];
+#pragma unroll
+                for (int u = 0; u < kLpVectors; ++u) {
+                    float hi = kNegInf;
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) {
+                        const Pair p = Wide<T>::pair_of(now[u], i);
+                        hi = fmaxf(hi, fmaxf(p.f.x, p.f.y));
+                    }
+                    keys[u] = sort_keys_desc(hi > kNegInf ? order_key(hi) : 0u, lane);
+                }
+                sync();              // s_count is set
+                cut = __shfl_sync(kFullMask, join_keys(keys, lane), a.top - 1);
+            } else {
+                // every thread is a group: each warp sorts its own, then joins all
+                s_keys[warp][lane] = sort_keys_desc(range.y > kNegInf ? order_key(range.y) : 0u, lane);
+                sync();
+                uint32_t keys[kLpWarps];
+#pragma unroll
+                for (int w = 0; w < kLpWarps; ++w) keys[w] = s_keys[w][lane];
+                cut = __shfl_sync(kFullMask, join_keys(keys, lane), a.top - 1);
             }
-            const uint32_t cut = __reduce_max_sync(kFullMask, above == static_cast<uint32_t>(a.top - 1) ? key : 0u) & ~31u;
             // logits of this step that equal it may belong to the best; later ones have
             // higher indices: only a greater logit displaces one of this step
             threshold = cut ? order_key_value(cut) : kNegInf;
             bound = cut ? order_key_value(cut - (cut == 0x80000000u ? 2u : 1u)) : kNegInf;   // the key below zero's is unused
         }
         uint32_t hits = 0;       // the thread's candidates
-        if (TOP && range.y > bound) {
-#pragma unroll
-            for (int b = 0; b < kLpVectors * N; ++b) {
-                const Pair p = Wide<T>::pair_of(now[b / N], b % N / 2);
-                hits |= (b % 2 ? p.f.y : p.f.x) > bound ? 1u << b : 0u;
-            }
-        }
+        if (TOP && range.y > bound) hits = hits_above<T>(now, bound);
         if (range.x - mine.max > kLowLogit) {
 #pragma unroll
             for (int u = 0; u < kLpVectors; ++u)
@@ -330,7 +416,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
                 for (int i = 0; i < N / 2; ++i) mine.add(Wide<T>::pair_of(now[u], i), true);
         }
         if (TOP) {
-            auto element = [&](int b) { return (v0 + b / N * TEAM) * N + b % N; };
+            auto element = [&](int bit) {
+                const int b = hit_element<T>(bit);
+                return (v0 + b / N * TEAM) * N + b % N;
+            };
             uint32_t lost = 0;   // candidates that found the buffer full
             if (hits != 0) {
                 uint32_t at = atomicAdd(&s_count, static_cast<uint32_t>(__popc(hits)));

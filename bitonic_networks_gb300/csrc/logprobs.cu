@@ -670,9 +670,10 @@ int launch_logprobs(const LogprobsLaunch &L) {
     const int64_t vectors = L.vocab * float_bytes(L.dtype) / 16;
     // A warp to a row where it is short, so that rows wait for no CTA-wide barrier
     // (8192 x 1000 bf16 with 5 alternatives: 14 us, 51 with a CTA each), and up to
-    // twice as long where rows are many and alternatives few (8192 x 6000: 37
-    // against 56; with 20 alternatives 68 against 62, and 100 rows 12 against 5).
-    const bool warps = vectors <= 512 || (vectors <= 1024 && L.top <= 8 && L.rows >= 8 * L.sm_count);
+    // four times as long where rows fill the device and alternatives are few
+    // (8192 x 12000: 61 against 75; with 20 the candidates outgrow a warp's share
+    // of the buffer: 8192 x 5000 41 against 62, x 8000 77 against 66).
+    const bool warps = vectors <= 512 || (vectors <= (L.top <= kFewTop ? 2048 : 640) && L.rows >= 24 * L.sm_count);
     // Otherwise a row is split while CTAs do not fill the device and a part has 512
     // vectors (304 x 131072 bf16 with 20 alternatives: 27 us, 45 whole).
     a.split = 1;

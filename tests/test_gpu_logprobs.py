@@ -102,6 +102,8 @@ def test_many_rows(dtype):
     check_gradient(x, None, r)
     check(strided(logits_of(1217, 8001, dtype, 7), 3, 1), None, 8)     # a warp or a CTA, by the type
     check(logits_of(1217, 8001, dtype, 8), None, 9)
+    for vocab, top in ((6001, 5), (2400, 20), (4900, 32), (8100, 1)):  # rows that fill the device
+        check(logits_of(3700, vocab, dtype, vocab), None, top)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -30,18 +30,20 @@ constexpr int kRowThreads = 256;
 // CTAs per SM that a kernel's registers leave room for where 16-bit rows start
 // anywhere: loads wait for memory, and more of them do with more CTAs (8191 x 6
 // rows of 1001: combine 29 us with 4 CTAs of 2 x 2 loads per thread, 37 with 3
-// of 4 x 1; backward 55 with 6 CTAs, 58 with 4).
+// of 4 x 1; backward 55 with 6 CTAs, 58 with 4; since then 27 and 50).
 constexpr int kShiftedCombine = 4, kShiftedBackward = 6;
 
-// Addresses at which 32 bytes of an array can be read; none where last < first.
-struct ReadSpan {
-    uintptr_t first, last;
+// A row that is read.  inner: it is neither the first nor the last of its array,
+// so that 64 bytes before and after it are the array's.
+template <typename T> struct InRow {
+    const T *row;
+    bool inner;
 };
 
 template <typename T> struct RowArgs {
     const T *by_token;
     const T *by_row;
-    ReadSpan token_span, row_span;
+    const uint4 *token_safe, *row_safe;   // 32 bytes that can be read in place of others
     T *out;
     const int32_t *positions;
     const int32_t *rows;
@@ -55,11 +57,19 @@ template <typename T> struct RowArgs {
     uint32_t fill_rows, fill_blocks;   // rows that a CTA looks over to zero them; such CTAs: the rest move rows
 };
 
+template <typename T> __device__ __forceinline__ InRow<T> token_row(const RowArgs<T> &a, uint32_t t) {
+    return {a.by_token + static_cast<int64_t>(t) * a.token_stride, t > 0 && t + 1 < a.tokens};
+}
+
+template <typename T> __device__ __forceinline__ InRow<T> layout_row(const RowArgs<T> &a, uint32_t p) {
+    return {a.by_row + static_cast<int64_t>(p) * a.row_stride, p > 0 && p + 1 < a.capacity};
+}
+
 // How rows move: every row starts and ends at 16 bytes; anywhere, in 16-byte
 // vectors; anywhere, in single 32-bit elements that neighbouring threads hold
 // side by side (for the sums of 32-bit rows: fewer instructions than shifting,
 // 8191 x 6 rows of 1001: combine 39 us against 45, backward 81 against 84); or
-// element by element, for arrays that hold only a few.
+// element by element, for rows of less than 64 bytes.
 enum RowMode { kAligned, kShifted, kSingle, kElements };
 
 // Where a thread's N elements of vector v of a row are: e, e + kStep, ...
@@ -83,17 +93,16 @@ template <typename T> __device__ __forceinline__ uintptr_t address_of(const T *r
 }
 
 template <typename T, int MODE>
-__device__ __forceinline__ Loaded start_read(const T *row, int32_t e, uint32_t width, const ReadSpan &span) {
+__device__ __forceinline__ Loaded start_read(const InRow<T> &in, int32_t e, uint32_t width, const uint4 *safe) {
     Loaded x;
     if (MODE == kAligned) {
-        x.q = *reinterpret_cast<const uint4 *>(row + e);
+        x.q = *reinterpret_cast<const uint4 *>(in.row + e);
     } else if (MODE == kShifted) {
-        const uintptr_t low = address_of(row, e) & ~static_cast<uintptr_t>(15);
-        const uint4 *p = reinterpret_cast<const uint4 *>(min(max(low, span.first), span.last));
+        const uint4 *p = in.inner ? reinterpret_cast<const uint4 *>(address_of(in.row, e) & ~static_cast<uintptr_t>(15)) : safe;
         x.q = p[0];
         x.r = p[1];
     } else if (MODE == kSingle) {
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(row) + e;
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(in.row) + e;
         const int32_t left = static_cast<int32_t>(width) - e;
         x.q = make_uint4(left > 0 ? w[0] : 0u, left > 32 ? w[32] : 0u, left > 64 ? w[64] : 0u, left > 96 ? w[96] : 0u);
     }
@@ -101,12 +110,12 @@ __device__ __forceinline__ Loaded start_read(const T *row, int32_t e, uint32_t w
 }
 
 template <typename T, int MODE>
-__device__ __forceinline__ uint4 end_read(const Loaded &x, const T *row, int32_t e, uint32_t width, const ReadSpan &span) {
+__device__ __forceinline__ uint4 end_read(const Loaded &x, const InRow<T> &in, int32_t e, uint32_t width) {
     constexpr int N = Wide<T>::kCount;
     if (MODE == kAligned || MODE == kSingle) return x.q;
-    const uintptr_t at = address_of(row, e), low = at & ~static_cast<uintptr_t>(15);
     uint4 q;
     if (MODE == kShifted) {
+        const uint32_t at = static_cast<uint32_t>(address_of(in.row, e));
         uint32_t w[5] = {x.q.x, x.q.y, x.q.z, x.q.w, x.r.x};
         const bool two = at & 8, one = at & 4;
         w[0] = two ? x.q.z : x.q.x;
@@ -125,10 +134,10 @@ __device__ __forceinline__ uint4 end_read(const Loaded &x, const T *row, int32_t
         }
         q = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (MODE == kElements || low < span.first || low > span.last) {      // the array's ends
+    if (MODE == kElements || !in.inner) {
         float f[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = static_cast<uint32_t>(e + i) < width ? to_f32(row[e + i]) : 0.0f;
+        for (int i = 0; i < N; ++i) f[i] = static_cast<uint32_t>(e + i) < width ? to_f32(in.row[e + i]) : 0.0f;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, pair(f[2 * i], f[2 * i + 1]));
     }
@@ -196,9 +205,9 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(const RowArgs<T> a) {
     }
     const RowPlace at = row_place<1>(a);
     if (at.token >= a.tokens || at.v >= a.vectors) return;
-    const T *row = a.by_token + at.token * a.token_stride;
+    const InRow<T> in = token_row(a, at.token);
     uint4 q;
-    if (MODE == kAligned) q = start_read<T, MODE>(row, element_of<T, MODE>(at.v, 0), a.width, a.token_span).q;
+    if (MODE == kAligned) q = start_read<T, MODE>(in, element_of<T, MODE>(at.v, 0), a.width, a.token_safe).q;
     const int32_t *pos = a.positions + static_cast<int64_t>(at.token) * a.chosen;
 #pragma unroll 4
     for (uint32_t j = 0; j < a.chosen; ++j) {
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(const RowArgs<T> a) {
         const OutRow<T, MODE> o(a.out + static_cast<int64_t>(p) * a.width);
         const int32_t to = o.at(at.v);
         // from L1: each row has its own boundaries
-        if (MODE != kAligned) q = end_read<T, MODE>(start_read<T, MODE>(row, to, a.width, a.token_span), row, to, a.width, a.token_span);
+        if (MODE != kAligned) q = end_read<T, MODE>(start_read<T, MODE>(in, to, a.width, a.token_safe), in, to, a.width);
         o.write(to, a.width, q);
     }
 }
@@ -228,7 +237,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedCombin
         for (int i = 0; i < N / 2; ++i) acc[u][i] = pair(0.0f, 0.0f);
     for (uint32_t j0 = 0; j0 < a.chosen; j0 += J) {
         Loaded y[J][U];
-        const T *row[J];
+        InRow<T> row[J];
         float w[J];
         bool there[J];
 #pragma unroll
@@ -236,11 +245,11 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedCombin
             const uint32_t p = j0 + j < a.chosen ? static_cast<uint32_t>(a.positions[pair0 + j0 + j]) : a.capacity;
             there[j] = p < a.capacity;
             w[j] = !there[j] ? 0.0f : a.weights ? a.weights[pair0 + j0 + j] : 1.0f;
-            row[j] = a.by_row + static_cast<int64_t>(there[j] ? p : 0) * a.row_stride;
+            row[j] = layout_row(a, there[j] ? p : 0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t v = min(at.v + u * lanes, a.vectors - 1);     // no branch around the loads
-                y[j][u] = start_read<T, MODE>(row[j], out.at(v), a.width, a.row_span);
+                y[j][u] = start_read<T, MODE>(row[j], out.at(v), a.width, a.row_safe);
             }
         }
 #pragma unroll
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedCombin
             for (int u = 0; u < U; ++u) {
                 const uint32_t v = at.v + u * lanes;
                 if (!there[j] || v >= a.vectors) continue;
-                const uint4 q = end_read<T, MODE>(y[j][u], row[j], out.at(v), a.width, a.row_span);
+                const uint4 q = end_read<T, MODE>(y[j][u], row[j], out.at(v), a.width);
 #pragma unroll
                 for (int i = 0; i < N / 2; ++i) acc[u][i] = fma2(pair(w[j], w[j]), Wide<T>::pair_of(q, i), acc[u][i]);
             }
@@ -283,24 +292,23 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedBackwa
     Pair dots = pair(0.0f, 0.0f);
     if (p < a.capacity) {
         const float w = a.weights[pr];
-        const T *d_row = a.by_token + static_cast<int64_t>(pr / a.chosen) * a.token_stride;
-        const T *y_row = a.by_row + static_cast<int64_t>(p) * a.row_stride;
+        const InRow<T> d_row = token_row(a, pr / a.chosen), y_row = layout_row(a, p);
         const OutRow<T, MODE> out(a.out + static_cast<int64_t>(p) * a.width);
         for (uint32_t v0 = threadIdx.x & (lanes - 1); v0 < a.vectors; v0 += lanes * U) {
             Loaded d[U], y[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t v = min(v0 + u * lanes, a.vectors - 1);       // no branch around the loads
-                d[u] = start_read<T, MODE>(d_row, out.at(v), a.width, a.token_span);
-                y[u] = start_read<T, MODE>(y_row, out.at(v), a.width, a.row_span);
+                d[u] = start_read<T, MODE>(d_row, out.at(v), a.width, a.token_safe);
+                y[u] = start_read<T, MODE>(y_row, out.at(v), a.width, a.row_safe);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t v = v0 + u * lanes;
                 if (v >= a.vectors) continue;
                 const int32_t e = out.at(v);
-                const uint4 dq = end_read<T, MODE>(d[u], d_row, e, a.width, a.token_span);
-                const uint4 yq = end_read<T, MODE>(y[u], y_row, e, a.width, a.row_span);
+                const uint4 dq = end_read<T, MODE>(d[u], d_row, e, a.width);
+                const uint4 yq = end_read<T, MODE>(y[u], y_row, e, a.width);
                 const bool whole = MODE == kSingle || out.whole(e, a.width);    // kSingle reads 0 beside the row
                 uint4 g;
 #pragma unroll
@@ -328,11 +336,9 @@ __global__ void __launch_bounds__(kRowThreads, MODE == kShifted ? kShiftedBackwa
     if ((threadIdx.x & (lanes - 1)) == 0 && pr < pairs) a.grad_weights[pr] = dot;
 }
 
-template <typename T> ReadSpan span_of(const void *p, int64_t rows, int64_t stride, int64_t width) {
-    if (p == nullptr || rows == 0) return {1, 0};
-    const uintptr_t begin = reinterpret_cast<uintptr_t>(p), end = begin + ((rows - 1) * stride + width) * sizeof(T);
-    const uintptr_t first = (begin + 15) & ~static_cast<uintptr_t>(15), last = end & ~static_cast<uintptr_t>(15);
-    return last >= first + 32 ? ReadSpan{first, last - 32} : ReadSpan{1, 0};
+// 32 bytes at a 16-byte boundary of an array of at least 64 bytes.
+inline const uint4 *safe_in(const void *p) {
+    return reinterpret_cast<const uint4 *>((reinterpret_cast<uintptr_t>(p) + 15) & ~static_cast<uintptr_t>(15));
 }
 
 template <typename T> RowArgs<T> row_args(const RowsLaunch &L) {
@@ -350,32 +356,33 @@ template <typename T> RowArgs<T> row_args(const RowsLaunch &L) {
     a.chosen = L.chosen;
     a.capacity = static_cast<uint32_t>(L.capacity);
     a.width = static_cast<uint32_t>(L.width);
-    a.token_span = span_of<T>(L.by_token, L.tokens, L.token_stride, L.width);
-    a.row_span = span_of<T>(L.by_row, L.capacity, L.row_stride, L.width);
+    a.token_safe = safe_in(L.by_token);
+    a.row_safe = safe_in(L.by_row);
     return a;
 }
 
-// Calls f(arguments, mode).  sums: the rows are summed, not only copied.
-template <typename F> int with_rows(const RowsLaunch &L, bool sums, F &&f) {
+// Calls f(arguments, mode).  SUMS: the rows are summed, not only copied.
+template <bool SUMS, typename F> int with_rows(const RowsLaunch &L, F &&f) {
     using std::integral_constant;
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int N = Wide<T>::kCount;
         RowArgs<T> a = row_args<T>(L);
         auto fits = [&](const void *p, int64_t stride) { return p == nullptr || (aligned(p, 16) && stride % N == 0); };
-        auto spans = [&](const void *p, const ReadSpan &s) { return p == nullptr || s.first <= s.last; };
         const bool some = L.tokens > 0 && L.capacity > 0;
         if (some && L.width % N == 0 && fits(L.by_token, L.token_stride) && fits(L.by_row, L.row_stride) && fits(L.out, L.width)) {
             a.vectors = a.width / N;
             return f(a, integral_constant<int, kAligned>{});
         }
         a.vectors = (a.width + 2 * (N - 1)) / N;     // a row of `width` can touch so many
-        if constexpr (sizeof(T) == 4)
-            if (some && sums) {
+        if constexpr (SUMS && sizeof(T) == 4) {
+            if (some) {
                 a.vectors = (a.width + 127) / 128 * 32;
                 return f(a, integral_constant<int, kSingle>{});
             }
-        if (some && spans(L.by_token, a.token_span) && spans(L.by_row, a.row_span)) return f(a, integral_constant<int, kShifted>{});
+        } else {
+            if (some && L.width * sizeof(T) >= 64) return f(a, integral_constant<int, kShifted>{});
+        }
         return f(a, integral_constant<int, kElements>{});
     });
 }
@@ -413,7 +420,7 @@ template <int J, int U, typename T, int MODE> int start_combine(const RowsLaunch
 }  // namespace
 
 int launch_dispatch(const RowsLaunch &L) {
-    return with_rows(L, false, [&](auto &a, auto m) {
+    return with_rows<false>(L, [&](auto &a, auto m) {
         constexpr int MODE = decltype(m)::value;
         const int64_t blocks = split_rows(a, 1);
         set_fill(a);
@@ -425,7 +432,7 @@ int launch_dispatch(const RowsLaunch &L) {
 }
 
 int launch_combine(const RowsLaunch &L) {
-    return with_rows(L, true, [&](auto &a, auto m) {
+    return with_rows<true>(L, [&](auto &a, auto m) {
         constexpr int MODE = decltype(m)::value;
         using T = std::decay_t<decltype(*a.out)>;
         // four 16-byte loads in flight: 16384 x 8 rows of 8 KB take 200 us so, 255 with eight
@@ -437,7 +444,7 @@ int launch_combine(const RowsLaunch &L) {
 }
 
 int launch_combine_backward(const RowsLaunch &L) {
-    return with_rows(L, true, [&](auto &a, auto m) {
+    return with_rows<true>(L, [&](auto &a, auto m) {
         constexpr int MODE = decltype(m)::value;
         using T = std::decay_t<decltype(*a.out)>;
         const int64_t pairs = L.tokens * L.chosen;

@@ -54,7 +54,7 @@ template <typename T> struct RowArgs {
     uint32_t vectors;        // vectors that a written row touches, at most
     uint32_t log_lanes;      // 2^log_lanes threads side by side on a row
     uint32_t chunks;         // a row's pieces of lanes * U vectors
-    uint32_t fill_rows, fill_blocks;   // rows that a CTA looks over to zero them; such CTAs: the rest move rows
+    uint32_t fill_blocks;    // CTAs that fill rows with zeros; the rest move rows
 };
 
 template <typename T> __device__ __forceinline__ InRow<T> token_row(const RowArgs<T> &a, uint32_t t) {
@@ -168,20 +168,21 @@ template <typename T, int MODE> struct OutRow {
     }
 };
 
-// Zeros the rows that no pair holds.  A warp looks over 32 rows; of wide ones
-// (2 KB and more) the CTA's warps look over the same and take them in turn.
-// These CTAs come first, so that a long run of such rows (the end of the layout)
-// is under way while the others are moved (256 experts padded to 16, 16384 x 8
-// rows of 8 KB: 189 us, and 220 when they came last with 32 rows to a warp).
+// Zeros the rows that no pair holds.  Warp w of W looks over rows w, w + W, ...:
+// a run of such rows (the end of the layout) is shared among the warps.  These
+// CTAs come first, so that it is under way while the others are moved (256
+// experts padded to 16, 16384 x 8 rows of 8 KB: 185 us, and 220 when they came
+// last with 32 rows in a row to a warp).
 template <typename T, int MODE> __device__ __forceinline__ void fill_rows(const RowArgs<T> &a) {
     constexpr uint32_t kWarps = kRowThreads / 32;
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t first = a.fill_rows == 32 ? blockIdx.x * 32 : (blockIdx.x * kWarps + warp) * 32;
-    uint32_t empty = __ballot_sync(kFullMask, first + lane < a.capacity && a.rows[first + lane] < 0);
-    for (uint32_t n = 0; empty; ++n, empty &= empty - 1) {
-        if (a.fill_rows == 32 && n % kWarps != warp) continue;
-        const OutRow<T, MODE> o(a.out + static_cast<int64_t>(first + __ffs(empty) - 1) * a.width);
-        for (uint32_t v = lane; v < a.vectors; v += 32) o.write(o.at(v), a.width, make_uint4(0, 0, 0, 0));
+    const uint32_t lane = threadIdx.x & 31, warps = a.fill_blocks * kWarps;
+    for (uint32_t base = blockIdx.x * kWarps + (threadIdx.x >> 5); base < a.capacity; base += 32 * warps) {
+        const uint32_t r = base + lane * warps;
+        uint32_t empty = __ballot_sync(kFullMask, r < a.capacity && a.rows[r] < 0);
+        for (; empty; empty &= empty - 1) {
+            const OutRow<T, MODE> o(a.out + static_cast<int64_t>(base + (__ffs(empty) - 1) * warps) * a.width);
+            for (uint32_t v = lane; v < a.vectors; v += 32) o.write(o.at(v), a.width, make_uint4(0, 0, 0, 0));
+        }
     }
 }
 
@@ -404,8 +405,9 @@ template <typename T> int64_t split_rows(RowArgs<T> &a, int per_thread) {
 }
 
 template <typename T> void set_fill(RowArgs<T> &a) {
-    a.fill_rows = a.vectors >= 128 ? 32 : kRowThreads;
-    a.fill_blocks = (a.capacity + a.fill_rows - 1) / a.fill_rows;
+    // a row to a warp in a small layout, up to 32 in a large one
+    const uint32_t rows = std::min(32u, std::max(1u, a.capacity / 4096)) * (kRowThreads / 32);
+    a.fill_blocks = (a.capacity + rows - 1) / rows;
 }
 
 int status() { return cudaGetLastError() == cudaSuccess ? GSORT_OK : GSORT_ECUDA; }

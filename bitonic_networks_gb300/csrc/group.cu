@@ -172,8 +172,11 @@ __global__ void __launch_bounds__(kGroupThreads) k_group_place(const GroupArgs a
             if (n < end) {
                 int32_t p = -1;
                 if (key[i] < E) {
-                    p = static_cast<int32_t>(s_base[key[i]] + count[key[i]] + rank[i]);
-                    a.rows[p] = static_cast<int32_t>(n);
+                    const uint32_t to = s_base[key[i]] + count[key[i]] + rank[i];
+                    if (to < a.capacity) {     // always, unless the experts change meanwhile
+                        p = static_cast<int32_t>(to);
+                        a.rows[to] = static_cast<int32_t>(n);
+                    }
                 }
                 a.positions[n] = p;
             }

@@ -45,3 +45,38 @@ def test_gradients_of_the_model(example):
 def test_the_example_learns(example):
     losses, best, given = example.main(["--steps", "40", "--tokens", "256", "--vocab", "300"])
     assert losses[-1] < 0.25 * losses[0] and best == given
+
+
+def test_a_layer_in_a_cuda_graph():
+    """A decode step's calls captured on a side stream and replayed on new inputs
+    (small and large enough for the two kernels of the grouping)."""
+    for tokens in (16, 3000):
+        g = torch.Generator(device="cuda").manual_seed(tokens)
+        logits, x = torch.empty(tokens, 64).cuda(), torch.empty(tokens, 200, dtype=torch.bfloat16).cuda()
+        answers = torch.empty(tokens, 5000, dtype=torch.bfloat16).cuda()
+
+        def fill():
+            for t in (logits, x, answers):
+                t.normal_(generator=g)
+
+        def step():
+            w, e = gs.route_experts(logits, 4, renormalise=True)
+            groups = gs.group_by_expert(e, 64, align=8)
+            out = gs.combine_rows(gs.dispatch_rows(x, groups), groups, w)
+            r = gs.token_logprobs(answers, top=3)
+            return [w, e, *groups, out, r.entropy, r.top_logprobs, r.top_ids]
+
+        fill()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            held = step()
+        for _ in range(3):
+            fill()
+            graph.replay()
+            for got, want in zip(held, step()):
+                assert torch.equal(got, want)

@@ -15,7 +15,7 @@
 // reach, and only logits above it are written to a shared buffer, which is sorted
 // by warps (bitonic networks of 32) when the row ends; where the buffer is full,
 // a warp sorts into a list of its own.  With alternatives the ends of rows are
-// what is left above the memory's time: 4096 x 100003 bf16 take 143 us, reading
+// what is left above the memory's time: 4096 x 100003 bf16 take 134 us, reading
 // them 123.  Few rows are split over a cluster of CTAs, joined through
 // distributed shared memory; short rows take a warp each.
 #include <algorithm>
@@ -26,7 +26,7 @@ namespace gsort {
 namespace {
 
 // 256 threads with 4 vectors each in flight and 5 CTAs per SM keep the memory
-// busy: 4096 x 100003 bf16 with one alternative takes 143 us (5.7 TB/s). In an
+// busy: 4096 x 100003 bf16 with one alternative takes 134 us (6.1 TB/s). In an
 // earlier state: 158, with 4 CTAs 165, 2 vectors 182, CTAs of 512 threads 190.
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;   // at most 8: join_lists
@@ -36,7 +36,7 @@ constexpr uint32_t kCandidates = 2048;      // shared buffers of candidates, of 
 constexpr int kMaxCluster = 8;
 // Up to so many alternatives 32 groups give a threshold that hardly more logits
 // pass than have to; with more of them it would be far too low (4096 x 131072
-// bf16 with 32 alternatives: 585 us, 259 with a group for every thread).
+// bf16 with 32 alternatives: 585 us, 259 with a group for every thread, 217 now).
 constexpr int kFewTop = 8;
 constexpr float kLowLogit = -1e37f;        // x - max above it: the exponent does not overflow
 constexpr float kTinyExponent = -256.0f;   // 2^-256 is 0 in 32 bits: masked logits add e^d * d = 0 * -256

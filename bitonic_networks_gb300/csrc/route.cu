@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
     }
     if (a.renormalise) {
         const float total = lanes_sum<L>(w);
-        w *= total > 0.0f ? 1.0f / total : 0.0f;    // one quotient a token, none of zero
+        // a quotient, not a product with 1 / total: one expert alone has exactly 1
+        if (there) w = total > 0.0f ? w / total : 0.0f;
     }
     if (live && sub < a.chosen) {
         a.weights[token * a.chosen + sub] = w * a.scale;
@@ -461,7 +462,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(const RouteBac
         if (a.renormalise) {
             const float low = fminf(lanes_max<L>(xe), 0.0f), t = there ? raised_sigmoid(xe, low) : 0.0f;
             const float total = lanes_sum<L>(t);
-            const float q = t * (total > 0.0f ? 1.0f / total : 0.0f);
+            float q = 0.0f;          // a quotient: of one expert alone it is 1 and the gradient 0
+            if (there && total > 0.0f) q = t / total;
             g = (d - lanes_sum<L>(d * q)) * q * sigmoid_rest(xe);
         } else {
             g = there ? d * sigmoid(xe) * sigmoid_rest(xe) : 0.0f;
@@ -470,7 +472,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(const RouteBac
         const float m = lanes_max<L>(there ? xe : kNegInf);
         const float q0 = there ? exp_from(xe, m) : 0.0f;
         const float total = lanes_sum<L>(q0);
-        const float q = q0 * (total > 0.0f ? 1.0f / total : 0.0f);
+        float q = 0.0f;
+        if (there) q = q0 / total;       // the largest adds 1 to the total
         const float mean = lanes_sum<L>(d * q);
         g = q * (d - mean);
     } else {

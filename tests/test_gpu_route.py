@@ -87,6 +87,16 @@ def test_ties_of_many_tokens():
         assert torch.equal(gs.route_experts(y, k)[1].long(), torch.sort(y, dim=1, descending=True, stable=True).indices[:, :k])
 
 
+def test_one_renormalised_expert_has_weight_one_and_no_gradient():
+    for tokens in (50, 2000):
+        x = logits_of(tokens, 100, torch.float32, tokens)
+        for score in ("softmax", "sigmoid"):
+            w, e = gs.route_experts(x, 1, score=score, renormalise=True)
+            assert (w == 1).all()
+            d = torch.randn(tokens, 1, generator=torch.Generator().manual_seed(1)).cuda()
+            assert (gs.route_experts_backward(d, x, e, score=score, renormalise=True) == 0).all()
+
+
 def test_low_sigmoid_scores_are_renormalised():
     """Scores that underflow in 32 bits still have their quotients."""
     x = logits_of(40, 32, torch.float32, 3) - 95.0

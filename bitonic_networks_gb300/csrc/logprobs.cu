@@ -38,6 +38,7 @@ constexpr int kMaxCluster = 8;
 // pass than have to; with more of them it would be far too low (4096 x 131072
 // bf16 with 32 alternatives: 585 us, 259 with a group for every thread, 217 now).
 constexpr int kFewTop = 8;
+constexpr uint32_t kRefresh = 64;          // candidates of a warp's row that are sorted before its end
 constexpr float kLowLogit = -1e37f;        // x - max above it: the exponent does not overflow
 constexpr float kTinyExponent = -256.0f;   // 2^-256 is 0 in 32 bits: masked logits add e^d * d = 0 * -256
 
@@ -169,13 +170,27 @@ struct LaneSums {
         dot = pair(a.dot, b.dot);
     }
 
-    // low: some logit is so low that its exponent needs the bound
-    __device__ __forceinline__ void add(Pair x, bool low) {
-        Pair y = mul2(add2(x, minus), pair(kLog2e, kLog2e));
-        if (low) y = pair(max_nan(y.f.x, kTinyExponent), max_nan(y.f.y, kTinyExponent));
-        const Pair e = pair(exp2_approx(y.f.x), exp2_approx(y.f.y));
-        sum = add2(sum, e);
-        dot = fma2(e, y, dot);
+    // Adds COUNT pairs, summed on their own first: the sum is about 1 beside the
+    // largest logit and rounds at each addition to it.
+    // low: some logit is so low that its exponent needs the bound.
+    template <int COUNT> __device__ __forceinline__ void add(const Pair (&x)[COUNT], bool low) {
+        Pair part;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            Pair y = mul2(add2(x[i], minus), pair(kLog2e, kLog2e));
+            if (low) y = pair(max_nan(y.f.x, kTinyExponent), max_nan(y.f.y, kTinyExponent));
+            const Pair e = pair(exp2_approx(y.f.x), exp2_approx(y.f.y));
+            part = i == 0 ? e : add2(part, e);
+            dot = fma2(e, y, dot);
+        }
+        sum = add2(sum, part);
+    }
+
+    template <typename T> __device__ __forceinline__ void add_vector(const uint4 &q, bool low) {
+        Pair x[Wide<T>::kCount / 2];
+#pragma unroll
+        for (int i = 0; i < Wide<T>::kCount / 2; ++i) x[i] = Wide<T>::pair_of(q, i);
+        add(x, low);
     }
 
     __device__ __forceinline__ RowSums total() const { return {max, sum.f.x + sum.f.y, dot.f.x + dot.f.y}; }
@@ -332,6 +347,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
     uint64_t kept = 0;           // the warp's list, descending
     if (TOP && tid == 0) s_count = 0;
 
+    // sorts the warp's share of the buffer into its list
+    auto take = [&](uint32_t have) {
+        for (uint32_t b = warp * 32; b < have; b += TEAM) {
+            const uint64_t c = bitonic_sort_desc(b + lane < have ? s_buffer[b + lane] : 0, lane);
+            kept = __any_sync(kFullMask, kept != 0) ? merge_lists(kept, c, lane) : c;
+        }
+    };
+
     // With alternatives a row stops at its first step and at its end, and the
     // other CTAs' loads do not fill the gap: the step after next is on its way
     // into L2 (4096 x 100003 bf16: 158 -> 148 us when it came; no gain elsewhere).
@@ -406,14 +429,10 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
         if (TOP && range.y > bound) hits = hits_above<T>(now, bound);
         if (range.x - mine.max > kLowLogit) {
 #pragma unroll
-            for (int u = 0; u < kLpVectors; ++u)
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) mine.add(Wide<T>::pair_of(now[u], i), false);
+            for (int u = 0; u < kLpVectors; ++u) mine.template add_vector<T>(now[u], false);
         } else {
 #pragma unroll
-            for (int u = 0; u < kLpVectors; ++u)
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) mine.add(Wide<T>::pair_of(now[u], i), true);
+            for (int u = 0; u < kLpVectors; ++u) mine.template add_vector<T>(now[u], true);
         }
         if (TOP) {
             auto element = [&](int bit) {
@@ -442,6 +461,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
                 if (c) threshold = fmaxf(threshold, order_key_value(static_cast<uint32_t>(c >> 32)));
             }
         }
+        if (TOP && TEAM == 32) {
+            // a warp's buffer is small, and nobody else waits: sorting it now raises the
+            // threshold (8192 x 12000 bf16 with 20 alternatives: 149 us without, 71)
+            __syncwarp();
+            const uint32_t have = s_count;
+            if (have >= kRefresh) {
+                take(min(have, kRoom));
+                __syncwarp();
+                if (lane == 0) s_count = 0;
+                __syncwarp();
+                const uint64_t c = __shfl_sync(kFullMask, kept, a.top - 1);
+                if (c) threshold = fmaxf(threshold, order_key_value(static_cast<uint32_t>(c >> 32)));
+            }
+        }
     }
 
     if (TOP && first >= last) sync();     // s_count is set; with a step, its barrier has come
@@ -450,7 +483,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
         const uint32_t e = view.edge(lane);
         const float x = e < view.end ? to_f32((view.row - view.shift)[e]) : kNegInf;
         mine.raise(x);
-        mine.add(pair(x, kNegInf), true);
+        const Pair one[1] = {pair(x, kNegInf)};
+        mine.add(one, true);
         if (TOP) {
             const uint64_t c = x > kNegInf && x >= threshold ? candidate(x, e - view.shift) : 0;
             if (__any_sync(kFullMask, c != 0)) kept = merge_lists(kept, bitonic_sort_desc(c, lane), lane);
@@ -463,10 +497,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) k_logprobs(const Logprobs
     if (TOP) {
         // each warp sorts its share of the buffer into its list; warp 0 joins the lists
         const uint32_t have = min(s_count, kRoom);
-        for (uint32_t b = warp * 32; b < have; b += TEAM) {
-            const uint64_t c = bitonic_sort_desc(b + lane < have ? s_buffer[b + lane] : 0, lane);
-            kept = __any_sync(kFullMask, kept != 0) ? merge_lists(kept, c, lane) : c;
-        }
+        take(have);
         if (TEAM > 32) {
             const int lists = s_count > kRoom ? kLpWarps : min(kLpWarps, static_cast<int>((have + 31) / 32));
             if (lists > 1) {
@@ -670,10 +701,9 @@ int launch_logprobs(const LogprobsLaunch &L) {
     const int64_t vectors = L.vocab * float_bytes(L.dtype) / 16;
     // A warp to a row where it is short, so that rows wait for no CTA-wide barrier
     // (8192 x 1000 bf16 with 5 alternatives: 14 us, 51 with a CTA each), and up to
-    // four times as long where rows fill the device and alternatives are few
-    // (8192 x 12000: 61 against 75; with 20 the candidates outgrow a warp's share
-    // of the buffer: 8192 x 5000 41 against 62, x 8000 77 against 66).
-    const bool warps = vectors <= 512 || (vectors <= (L.top <= kFewTop ? 2048 : 640) && L.rows >= 24 * L.sm_count);
+    // four times as long where rows fill the device (8192 x 12000 with 5 61 against
+    // 75, with 20 71 against 87).
+    const bool warps = vectors <= 512 || (vectors <= 2048 && L.rows >= 24 * L.sm_count);
     // Otherwise a row is split while CTAs do not fill the device and a part has 512
     // vectors (304 x 131072 bf16 with 20 alternatives: 27 us, 45 whole).
     a.split = 1;

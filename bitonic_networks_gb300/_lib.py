@@ -150,7 +150,7 @@ def load(build_if_missing: bool = True):
         if not os.path.exists(path):
             if not build_if_missing:
                 raise OSError(f"{path} not found; run __graft_entry__.build()")
-            _build.build()
+            _build.build_library()
         lib = ctypes.CDLL(path)
         for name, (res, args) in SIGNATURES.items():
             fn = getattr(lib, name)

@@ -3,8 +3,9 @@ module _ops (its language-model operators on torch tensors) with g++.
 
 Each source compiles to an object in parallel; the CUDA objects link into one
 shared library with the CUDA runtime linked statically, and _ops.so links
-against it.  The build is skipped when both are newer than every source and
-header.
+against it.  The library needs nvcc alone: where torch or g++ is missing it is
+there all the same, and only _ops fails.  A build is skipped when its result is
+newer than every source and header.
 """
 from __future__ import annotations
 
@@ -44,16 +45,17 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return (sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__])
+def _newer_than(path: str, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer_than(LIB_PATH, sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+                       + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__])
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(OPS_PATH)):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(OPS_PATH))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and _newer_than(OPS_PATH, [BINDING, __file__] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def _run(cmd, what: str):
@@ -64,7 +66,10 @@ def _run(cmd, what: str):
 
 
 def _torch_dir() -> str:
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch is not installed: _ops, the language-model operators on torch tensors, needs it")
+    return spec.submodule_search_locations[0]
 
 
 def _compile_binding() -> str:
@@ -85,9 +90,9 @@ def _link_binding(obj: str):
     os.replace(tmp, OPS_PATH)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every source, link libgsort.so and _ops.so; returns the library's path."""
-    if not force and not extra_flags and up_to_date():
+def build_library(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Compile the CUDA sources and link libgsort.so; returns its path."""
+    if not force and not extra_flags and library_up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
@@ -101,15 +106,24 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
-        binding = ex.submit(_compile_binding)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, len(srcs))) as ex:
         objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    _run(cmd, "link of libgsort.so")
+    _run([cc, *ARCH, "-shared", "-o", tmp, *objs], "link of libgsort.so")
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding_obj)
+    return LIB_PATH
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Build libgsort.so and _ops.so; returns the library's path.  The library
+    is linked whatever becomes of _ops."""
+    if not force and not extra_flags and up_to_date():
+        return LIB_PATH
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_compile_binding)
+        build_library(force, verbose, extra_flags)
+        _link_binding(binding.result())
     return LIB_PATH
 
 

@@ -162,10 +162,10 @@ def load(build_if_missing: bool = True):
 
 def load_ops(build_if_missing: bool = True):
     """The module _ops: the language-model operators on torch tensors (built
-    first, with the library, if it is missing)."""
-    if not os.path.exists(_build.OPS_PATH):
+    first, with the library, if it is missing or for another torch)."""
+    if not _build.ops_match():
         if not build_if_missing:
-            raise OSError(f"{_build.OPS_PATH} not found; run __graft_entry__.build()")
+            raise OSError(f"{_build.OPS_PATH} not found, or for another torch; run __graft_entry__.build()")
         _build.build()
     import torch  # noqa: F401  (its libraries come first)
     load(build_if_missing)

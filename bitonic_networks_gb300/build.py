@@ -5,7 +5,8 @@ Each source compiles to an object in parallel; the CUDA objects link into one
 shared library with the CUDA runtime linked statically, and _ops.so links
 against it.  The library needs nvcc alone: where torch or g++ is missing it is
 there all the same, and only _ops fails.  A build is skipped when its result is
-newer than every source and header.
+newer than every source and header, and _ops is for the Python and the torch
+that are installed.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libgsort.so")
 OPS_PATH = os.path.join(PKG, "_ops.so")
+OPS_STAMP = os.path.join(BUILD_DIR, "ops.stamp")     # what _ops.so was built for
 BINDING = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -54,8 +56,21 @@ def library_up_to_date() -> bool:
                        + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__])
 
 
+def ops_match() -> bool:
+    """Whether _ops.so is there and for this Python and this torch."""
+    if not (os.path.exists(OPS_PATH) and os.path.exists(OPS_STAMP)):
+        return False
+    try:
+        want = _ops_stamp()
+    except RuntimeError:      # no torch
+        return False
+    with open(OPS_STAMP) as f:
+        return f.read() == want
+
+
 def up_to_date() -> bool:
-    return library_up_to_date() and _newer_than(OPS_PATH, [BINDING, __file__] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    return (library_up_to_date() and ops_match()
+            and _newer_than(OPS_PATH, [BINDING, __file__] + glob.glob(os.path.join(INCLUDE, "*.h"))))
 
 
 def _run(cmd, what: str):
@@ -70,6 +85,13 @@ def _torch_dir() -> str:
     if spec is None or not spec.submodule_search_locations:
         raise RuntimeError("torch is not installed: _ops, the language-model operators on torch tensors, needs it")
     return spec.submodule_search_locations[0]
+
+
+def _ops_stamp() -> str:
+    """The C++ module holds for one interpreter and one build of torch (its
+    version file names both the version and the sources' commit)."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{f.read()}"
 
 
 def _compile_binding() -> str:
@@ -88,6 +110,8 @@ def _link_binding(obj: str):
     _run(["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu",
           "-lc10", "-lc10_cuda", "-L", PKG, "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"], "link of _ops.so")
     os.replace(tmp, OPS_PATH)
+    with open(OPS_STAMP, "w") as f:
+        f.write(_ops_stamp())
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

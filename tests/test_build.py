@@ -68,3 +68,12 @@ def test_a_stale_library_is_linked_after_torch_has_gone(tree):
     with pytest.raises(RuntimeError, match="torch"):
         b.build()
     assert os.path.getmtime(b.LIB_PATH) > 0
+
+
+def test_a_module_for_another_torch_is_not_up_to_date(tree):
+    b.build()
+    assert b.up_to_date()
+    tree(11)
+    assert not b.up_to_date()
+    b.build()
+    assert b.up_to_date()

@@ -129,7 +129,11 @@ template <int C, int L> __device__ __forceinline__ float row_sum(const float (&v
 // The largest candidate has 1 even at +inf.
 __device__ __forceinline__ float exp_from(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
-// The same for a whole row, where only sums and a gradient's dense part are
+// A softmax's score, each operation rounded to nearest: the product is not fused
+// with what is added to it.
+__device__ __forceinline__ float softmax_score(float x, float m, float inv) { return __fmul_rn(exp_from(x, m), inv); }
+
+// e^(x - m) for a whole row, where only sums and a gradient's dense part are
 // formed from it: 2 ulp and (x - m) 2^-24, and a third of the instructions.
 template <int C>
 __device__ __forceinline__ void row_exp(const float (&x)[C], float m, float (&e)[C]) {
@@ -295,9 +299,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
     // order keys of the choice values; 0: no candidate
     uint32_t key[C];
     if (biased) {
+        // the scores that the weights are made of, to the last bit: near ties are theirs to decide
         if (a.softmax) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) c[i] *= inv;
+            for (int i = 0; i < C; ++i) c[i] = x[i] > kNegInf ? softmax_score(x[i], m, inv) : 0.0f;
         } else {
 #pragma unroll
             for (int i = 0; i < C; ++i) c[i] = sigmoid(x[i]);
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
                 gkey = first;
             } else {
                 float value = order_key_value(first), other = order_key_value(second);
-                if (!biased && a.softmax) value = exp_from(value, m) * inv, other = exp_from(other, m) * inv;
+                if (!biased && a.softmax) value = softmax_score(value, m, inv), other = softmax_score(other, m, inv);
                 if (!biased && !a.softmax) value = sigmoid(value), other = sigmoid(other);
                 gkey = order_key(second != 0u ? value + other : value);
             }
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
             const float mc = lanes_max<L>(xe);
             w = there ? exp_from(xe, mc) : 0.0f;
         } else if (there) {
-            w = exp_from(xe, m) * inv;
+            w = softmax_score(xe, m, inv);
         }
     } else {
         const float low = a.renormalise ? fminf(lanes_max<L>(xe), 0.0f) : 0.0f;

@@ -292,3 +292,52 @@ def test_another_stream():
         w2, e2 = gs.route_experts(x, 8)
     s.synchronize()
     assert torch.equal(w, w2) and torch.equal(e, e2)
+
+
+def all_scores(x, score):
+    """Every expert's score [tokens, experts], as the weights that the operator
+    returns where a bias makes it choose 32 experts at a time."""
+    s = torch.zeros(x.shape).cuda()
+    for first in range(0, x.shape[1], 32):
+        some = min(32, x.shape[1] - first)
+        bias = torch.zeros(x.shape[1]).cuda()
+        bias[first:first + some] = 100.0
+        w, e = gs.route_experts(x, some, bias=bias, score=score)
+        s.scatter_(1, e.long(), w)
+    return s
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts", [16, 60, 100, 256, 1000])
+def test_biased_choice_is_by_the_scores_that_are_returned(experts, score):
+    """Biases that bring all choice values together: what is left of their
+    differences is in the scores' last bits.  The order has to be that of the
+    32-bit sums of returned score and bias, bit for bit."""
+    k = min(32, experts)
+    for tokens in (1, 1100):
+        for seed in range(6):
+            x = logits_of(1, experts, torch.float32, seed).expand(tokens, -1).contiguous()
+            s = all_scores(x, score)[0].cpu().numpy()
+            bias = np.float32(2.0 ** -7) - s
+            value = s + bias
+            assert value.dtype == np.float32 and np.ptp(value) < 1e-6
+            want = np.argsort(-value, kind="stable")[:k]
+            _, e = gs.route_experts(x, k, bias=torch.from_numpy(bias).cuda(), score=score)
+            assert (e.cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups", [(64, 8), (60, 6), (256, 8)])
+def test_biased_groups_are_by_the_scores_that_are_returned(experts, groups, score):
+    for tokens in (1, 1100):
+        for seed in range(6):
+            x = logits_of(1, experts, torch.float32, 30 + seed).expand(tokens, -1).contiguous()
+            s = all_scores(x, score)[0].cpu().numpy()
+            bias = np.float32(2.0 ** -7) - s
+            value = s + bias
+            best = -np.sort(-value.reshape(groups, -1), axis=1)
+            kept = np.argsort(-(best[:, 0] + best[:, 1]), kind="stable")[:3]
+            inside = np.isin(np.arange(experts) // (experts // groups), kept)
+            want = np.argsort(-np.where(inside, value, -np.inf), kind="stable")[:8]
+            _, e = gs.route_experts(x, 8, bias=torch.from_numpy(bias).cuda(), score=score, groups=groups, groups_kept=3, group_score="top2")
+            assert (e.cpu().numpy() == want).all()

@@ -578,18 +578,27 @@ struct LogprobsBackwardArgs {
 
 // A row's gradient as a function of x: with e = 2^y, y = (x - m) log2(e),
 //   -p (g + h (ln p + H)) = e * (q1 y + q0),  q1 = -h ln2 / S,  q0 = -(g + h (H - ln S)) / S
-struct RowGradient {
+// A 16-bit gradient rounds to 2^-9 or 2^-12 of itself: there the product in y may
+// round too (up to (m - x) 2^-23 of e).  A 32-bit one keeps what it lost; the
+// memory bounds it all the same.
+template <typename T> struct RowGradient {
     Pair minus, q0, q1;
 
     // FLAT: q1 = 0, no entropy in the loss
     template <bool FLAT> __device__ __forceinline__ Pair at(Pair x) const {
-        Pair y = mul2(add2(x, minus), pair(kLog2e, kLog2e));
+        const Pair d = add2(x, minus);
+        Pair y;
+        if (sizeof(T) == 4) {
+            const Pair e = exp_exact2(d, y);
+            return mul2(e, FLAT ? q0 : fma2(q1, y, q0));
+        }
+        y = mul2(d, pair(kLog2e, kLog2e));
         if (FLAT) return mul2(pair(exp2_approx(y.f.x), exp2_approx(y.f.y)), q0);
         y = pair(max_nan(y.f.x, kTinyExponent), max_nan(y.f.y, kTinyExponent));
         return mul2(pair(exp2_approx(y.f.x), exp2_approx(y.f.y)), fma2(q1, y, q0));
     }
 
-    template <typename T, bool FLAT> __device__ __forceinline__ uint4 vector(const uint4 &x) const {
+    template <bool FLAT> __device__ __forceinline__ uint4 vector(const uint4 &x) const {
         uint4 o;
 #pragma unroll
         for (int i = 0; i < Wide<T>::kCount / 2; ++i) Wide<T>::set_pair(o, i, at<FLAT>(Wide<T>::pair_of(x, i)));
@@ -628,7 +637,7 @@ __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const Logpro
     const bool empty = stats.y == 0.0f;      // every logit is -inf: -inf - 0 stays -inf, and e = 0
     const float m = empty ? 0.0f : stats.x, inv = empty ? 0.0f : -1.0f / stats.y;
     const float q0 = empty ? 0.0f : (h == 0.0f ? g : g + h * (a.entropy[row] - logf(stats.y))) * inv, q1 = h * kLn2 * inv;
-    RowGradient f;
+    RowGradient<T> f;
     f.minus = pair(-m, -m);
     f.q0 = pair(q0, q0);
     f.q1 = pair(q1, q1);
@@ -645,7 +654,7 @@ __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const Logpro
     for (int u = 0; u < kGradVectors; ++u) {
         const uint32_t v = v0 + u * LANES;
         if (v < view.full_end) {
-            const uint4 o = h == 0.0f ? f.vector<T, true>(x[u]) : f.vector<T, false>(x[u]);
+            const uint4 o = h == 0.0f ? f.template vector<true>(x[u]) : f.template vector<false>(x[u]);
             if (same) {
                 __stcs(reinterpret_cast<uint4 *>(out) + v, o);
             } else {
@@ -656,13 +665,13 @@ __global__ void __launch_bounds__(kGradThreads) k_logprobs_backward(const Logpro
     }
     if (own) {                                   // over this thread's own vector, rounded once
         const Pair p = pair(xt, kNegInf);
-        out[at] = from_f32<T>((h == 0.0f ? f.at<true>(p) : f.at<false>(p)).f.x + g);
+        out[at] = from_f32<T>((h == 0.0f ? f.template at<true>(p) : f.template at<false>(p)).f.x + g);
     }
     if (block == 0 && tid < 32) {        // the row's ends
         const uint32_t e = view.edge(tid);
         if (e < view.end) {
             const Pair p = pair(to_f32((view.row - view.shift)[e]), kNegInf);
-            const Pair d = h == 0.0f ? f.at<true>(p) : f.at<false>(p);
+            const Pair d = h == 0.0f ? f.template at<true>(p) : f.template at<false>(p);
             out[e] = from_f32<T>(d.f.x + (e == at ? g : 0.0f));
         }
     }

@@ -16,6 +16,7 @@ inline int float_bytes(int dtype) {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eRest = static_cast<float>(1.4426950408889634 - kLog2e);
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -134,6 +135,20 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
+}
+
+// e^d for d <= 0 where results stay in 32 bits.  2^(d log2(e)) with the product
+// rounded would be off by |d| 2^-23 of itself (3 bits at d = -30); what the
+// product lost is put back: e^d = 2^y (1 + r ln2), y + r = d log2(e).  Within 2
+// ulp and 2^-24.  d is bounded where e^d is 0, so that r and y are numbers.
+__device__ __forceinline__ Pair exp_exact2(Pair d, Pair &y) {
+    constexpr float kZero = -178.0f;
+    d = pair(max_nan(d.f.x, kZero), max_nan(d.f.y, kZero));
+    y = mul2(d, pair(kLog2e, kLog2e));
+    Pair r = fma2(d, pair(kLog2e, kLog2e), pair(-y.f.x, -y.f.y));
+    r = fma2(d, pair(kLog2eRest, kLog2eRest), r);
+    const Pair e = pair(exp2_approx(y.f.x), exp2_approx(y.f.y));
+    return fma2(mul2(e, pair(kLn2, kLn2)), r, e);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

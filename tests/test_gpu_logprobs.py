@@ -273,3 +273,28 @@ def test_refusals():
     with pytest.raises(gs.GsortError):         # overlapping, but not in place
         a = buf[:64].view(4, 16)
         gs.token_logprobs_backward(r.logprobs, None, a, t, r, out=buf[4:68].view(4, 16))
+
+
+def test_float32_gradient_far_from_the_maximum():
+    """A float32 gradient keeps its relative accuracy where probabilities are
+    small: against 64 bits from the forward call's own stats and entropy, with
+    x - max exact.  In units of 2^-24: the exponential 2 ulp = 4 and its correction
+    1, three products and a quotient 4, together 8 (a 2^-21); with the entropy's term
+    the factor beside the exponential has 7 more of its terms' size: 16."""
+    for vocab, pad in ((37, 0), (4096, 0), (20_001, 1)):
+        g = torch.Generator().manual_seed(vocab)
+        x = torch.randint(-80 * 256, 1, (5, vocab), generator=g).float() / 256 + 16
+        x[:, 0] = 16.0
+        x = strided(x.cuda(), pad, 0)
+        t = torch.zeros(5, dtype=torch.int64).cuda()
+        r = gs.token_logprobs(x, t)
+        a = torch.randn(5, generator=g).cuda()
+        d, total, h = x.double() - 16.0, r.stats[:, 1:].double(), r.entropy.double().unsqueeze(1)
+        p, a64 = d.exp() / total, a.double().unsqueeze(1)
+        got = gs.token_logprobs_backward(a, None, x, t, r).double()
+        off = ((got + p * a64).abs() / (p * a64.abs()))[:, 1:]
+        assert off.max() <= 2.0 ** -21, float(off.max())
+        got = gs.token_logprobs_backward(None, a, x, t, r).double()
+        size = p * a64.abs() * (d.abs() + (h - total.log()).abs())
+        off = (got + p * a64 * (d - total.log() + h)).abs() / size
+        assert off.max() <= 2.0 ** -20, float(off.max())

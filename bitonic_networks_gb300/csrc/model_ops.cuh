@@ -151,6 +151,12 @@ __device__ __forceinline__ Pair exp_exact2(Pair d, Pair &y) {
     return fma2(mul2(e, pair(kLn2, kLn2)), r, e);
 }
 
+__device__ __forceinline__ float exp_exact(float d) {     // the same for one number, NaN apart
+    d = fmaxf(d, -178.0f);
+    const float y = d * kLog2e, r = fmaf(d, kLog2eRest, fmaf(d, kLog2e, -y)), e = exp2_approx(y);
+    return fmaf(e * kLn2, r, e);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);

@@ -134,11 +134,16 @@ __device__ __forceinline__ float exp_from(float x, float m) { return x == m ? 1.
 __device__ __forceinline__ float softmax_score(float x, float m, float inv) { return __fmul_rn(exp_from(x, m), inv); }
 
 // e^(x - m) for a whole row, where only sums and a gradient's dense part are
-// formed from it: 2 ulp and (x - m) 2^-24, and a third of the instructions.
-template <int C>
+// formed from it: 2 ulp and (m - x) 2^-23, and a third of the instructions.  What
+// a sum gets of that is (m - x) e^(x - m) 2^-23 at most, below its own rounding;
+// a dense part in 16 bits rounds to 2^-9 or 2^-12.  EXACT: a dense part in 32 bits.
+template <bool EXACT, int C>
 __device__ __forceinline__ void row_exp(const float (&x)[C], float m, float (&e)[C]) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) e[i] = x[i] > kNegInf ? (x[i] == m ? 1.0f : exp2_approx((x[i] - m) * kLog2e)) : 0.0f;
+    for (int i = 0; i < C; ++i) {
+        const float d = x[i] == m ? 0.0f : x[i] - m;      // +inf - +inf
+        e[i] = x[i] > kNegInf ? (EXACT ? exp_exact(d) : exp2_approx(d * kLog2e)) : 0.0f;
+    }
 }
 
 // Largest candidate of the row (NaN is none); -inf where there is no candidate.
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(const RouteArgs a) {
     float c[C];
     if (a.softmax && (biased || !a.renormalise || (a.groups > 1 && a.top2))) {
         m = row_max<C, L>(x);
-        row_exp<C>(x, m, c);
+        row_exp<false, C>(x, m, c);
         const float sum = row_sum<C, L>(c);
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_backward(const RouteBac
         float x[C];
         load_row<T, C>(row, a.experts, a.access, e0, x);
         const float m = row_max<C, L>(x);
-        row_exp<C>(x, m, dense);
+        row_exp<sizeof(T) == 4, C>(x, m, dense);
         const float sum = row_sum<C, L>(dense);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
         const float p = there ? exp_from(xe, m) * inv : 0.0f;

@@ -341,3 +341,22 @@ def test_biased_groups_are_by_the_scores_that_are_returned(experts, groups, scor
             want = np.argsort(-np.where(inside, value, -np.inf), kind="stable")[:8]
             _, e = gs.route_experts(x, 8, bias=torch.from_numpy(bias).cuda(), score=score, groups=groups, groups_kept=3, group_score="top2")
             assert (e.cpu().numpy() == want).all()
+
+
+@pytest.mark.parametrize("experts", [60, 256, 1000])
+def test_float32_gradient_of_far_experts(experts):
+    """Softmax gradients of experts that were not chosen are -p times one sum, so
+    their quotient with that of an expert at the maximum is e^(x - max).  In
+    units of 2^-24: the exponential 2 ulp = 4, its correction 1, and two
+    roundings of either gradient 4; x - max is exact here."""
+    for tokens in (3, 1100):
+        g = torch.Generator().manual_seed(experts)
+        x = torch.randint(-80 * 256, 0, (tokens, experts), generator=g).float() / 256 + 16
+        x[:, 0] = x[:, 7] = 16.0
+        x = x.cuda()
+        _, e = gs.route_experts(x, 1)
+        assert (e == 0).all()
+        dx = gs.route_experts_backward(torch.ones(tokens, 1).cuda(), x, e).double()
+        want = torch.exp(x.double() - 16.0)
+        far = (dx / dx[:, 7:8] / want - 1).abs()[:, 1:]
+        assert far.max() <= 10 * 2.0 ** -24, float(far.max())

@@ -42,25 +42,24 @@ class Route(torch.autograd.Function):
 class Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, groups):
-        ctx.groups = groups
+        ctx.save_for_backward(*groups)
         return gs.dispatch_rows(x, groups)
 
     @staticmethod
     def backward(ctx, d):
-        return gs.combine_rows(d.contiguous(), ctx.groups), None
+        return gs.combine_rows(d.contiguous(), gs.ExpertGroups(*ctx.saved_tensors)), None
 
 
 class Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, groups):
-        ctx.save_for_backward(y, weights)
-        ctx.groups = groups
+        ctx.save_for_backward(y, weights, *groups)
         return gs.combine_rows(y, groups, weights)
 
     @staticmethod
     def backward(ctx, d):
-        y, weights = ctx.saved_tensors
-        d_y, d_weights = gs.combine_rows_backward(d.contiguous(), y, ctx.groups, weights)
+        y, weights, *groups = ctx.saved_tensors
+        d_y, d_weights = gs.combine_rows_backward(d.contiguous(), y, gs.ExpertGroups(*groups), weights)
         return d_y, d_weights, None
 
 
@@ -68,14 +67,15 @@ class TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, targets):
         r = gs.token_logprobs(logits, targets)
-        ctx.save_for_backward(logits, targets)
-        ctx.result = r
+        # an output kept as an attribute would hold its own node, and all before it, for ever
+        ctx.save_for_backward(logits, targets, r.entropy, r.stats)
         return r.logprobs, r.entropy
 
     @staticmethod
     def backward(ctx, d_logprobs, d_entropy):
-        logits, targets = ctx.saved_tensors
-        return gs.token_logprobs_backward(d_logprobs.contiguous(), d_entropy.contiguous(), logits, targets, ctx.result), None
+        logits, targets, entropy, stats = ctx.saved_tensors
+        r = gs.TokenLogprobs(None, entropy, None, None, stats)
+        return gs.token_logprobs_backward(d_logprobs.contiguous(), d_entropy.contiguous(), logits, targets, r), None
 
 
 class Model(torch.nn.Module):

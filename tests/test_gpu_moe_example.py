@@ -1,5 +1,6 @@
 """The example model: its whole gradient against the same model in plain 64-bit
 torch, and that it learns."""
+import gc
 import importlib.util
 import os
 
@@ -80,3 +81,21 @@ def test_a_layer_in_a_cuda_graph():
             graph.replay()
             for got, want in zip(held, step()):
                 assert torch.equal(got, want)
+
+
+def test_training_leaves_no_tensors_behind(example):
+    """What a step holds on the device is free again after it."""
+    torch.manual_seed(4)
+    model = example.Model(200, 64, 8, 2).cuda()
+    tokens, targets = torch.randint(200, (2, 97), device="cuda")
+
+    def steps(count):
+        for _ in range(count):
+            logprobs, entropy = example.TokenLogprobs.apply(model.logits(tokens), targets)
+            (-logprobs.mean() - 0.1 * entropy.mean()).backward()
+            model.zero_grad()
+        del logprobs, entropy
+        gc.collect()
+        return torch.cuda.memory_allocated()
+
+    assert steps(3) == steps(20)

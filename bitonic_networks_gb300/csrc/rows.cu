@@ -168,17 +168,19 @@ template <typename T, int MODE> struct OutRow {
     }
 };
 
-// Zeros the rows that no pair holds.  Warp w of W looks over rows w, w + W, ...:
+// Zeros the rows that no pair holds: without a pair, or with one whose position
+// was taken away since.  Warp w of W looks over rows w, w + W, ...:
 // a run of such rows (the end of the layout) is shared among the warps.  These
 // CTAs come first, so that it is under way while the others are moved (256
 // experts padded to 16, 16384 x 8 rows of 8 KB: 185 us, and 220 when they came
 // last with 32 rows in a row to a warp).
 template <typename T, int MODE> __device__ __forceinline__ void fill_rows(const RowArgs<T> &a) {
     constexpr uint32_t kWarps = kRowThreads / 32;
-    const uint32_t lane = threadIdx.x & 31, warps = a.fill_blocks * kWarps;
+    const uint32_t lane = threadIdx.x & 31, warps = a.fill_blocks * kWarps, pairs = a.tokens * a.chosen;
     for (uint32_t base = blockIdx.x * kWarps + (threadIdx.x >> 5); base < a.capacity; base += 32 * warps) {
         const uint32_t r = base + lane * warps;
-        uint32_t empty = __ballot_sync(kFullMask, r < a.capacity && a.rows[r] < 0);
+        const uint32_t n = r < a.capacity ? static_cast<uint32_t>(a.rows[r]) : 0u;
+        uint32_t empty = __ballot_sync(kFullMask, r < a.capacity && (n >= pairs || static_cast<uint32_t>(a.positions[n]) != r));
         for (; empty; empty &= empty - 1) {
             const OutRow<T, MODE> o(a.out + static_cast<int64_t>(base + (__ffs(empty) - 1) * warps) * a.width);
             for (uint32_t v = lane; v < a.vectors; v += 32) o.write(o.at(v), a.width, make_uint4(0, 0, 0, 0));

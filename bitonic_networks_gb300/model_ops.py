@@ -31,7 +31,8 @@ class ExpertGroups(NamedTuple):
     offsets    [experts + 1] int32  first row of each expert's segment, a multiple of the alignment
     counts     [experts] int32      pairs of each expert
     rows       [capacity] int32     the pair in each row of the layout, -1 where there is none
-    positions  [tokens, slots] int32  each pair's row, -1 for a dropped pair
+    positions  [tokens, slots] int32  each pair's row, -1 for a dropped pair (set to -1 later, it
+               drops the pair from the row moves as well: its row counts as without a pair)
     """
     offsets: torch.Tensor
     counts: torch.Tensor

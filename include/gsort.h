@@ -386,10 +386,12 @@ int gsort_group_by_expert(const int32_t *d_experts, int64_t pairs, int experts, 
                           int32_t *d_positions, void *d_ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Rows to the experts and back.  `width` elements to a row, `chosen` slots to
- * a token, positions and rows as gsort_group_by_expert gives them (a position
- * outside 0..capacity-1 takes no part).  Outputs are contiguous.
+ * a token, positions and rows as gsort_group_by_expert gives them.  Positions
+ * may be taken away afterwards: a pair whose position is outside
+ * 0..capacity-1 takes no part, and the row that d_rows has for it counts as held
+ * by no pair.  Outputs are contiguous and written whole.
  *   dispatch          d_out[positions[t][j]] = d_x[t]; rows that no pair
- *                     holds (d_rows < 0) are zero
+ *                     holds are zero
  *   combine           d_out[t] = sum over j of weights[t][j] *
  *                     d_y[positions[t][j]]; d_weights NULL: ones.  With ones
  *                     it is dispatch's gradient.

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import bitonic_networks_gb300 as gs
+from bitonic_networks_gb300 import _lib
 from model_ref import DTYPES, TINY, UNIT, group_ref, strided
 
 pytestmark = pytest.mark.gpu
@@ -249,3 +250,34 @@ def test_refusals():
     for experts, align in ((0, 1), (1025, 1), (4, 0), (-1, 1), (1024, 2 ** 31 - 1)):
         with pytest.raises(gs.GsortError):
             gs.group_by_expert(e, experts, align=align)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("width", [1, 33, 136, 1001])
+def test_rows_of_dropped_positions_are_zero(dtype, width):
+    """A pair whose position was taken away (or moved outside the layout) holds no
+    row: its row of the layout is written as zeros, not left as it was."""
+    lib, code = _lib.load(), DTYPES.index(dtype)
+    tokens, k, experts = 300, 3, 8
+    groups = gs.group_by_expert(chosen(tokens, k, experts, width), experts, align=16)
+    positions = groups.positions.clone()
+    gone = torch.rand(tokens, k, generator=torch.Generator().manual_seed(5)).cuda() < 0.3
+    rows = positions[gone].long()
+    positions[gone] = -1
+    positions[0, 0] = groups.rows.numel()
+    rows = torch.cat([rows, groups.positions[0, :1].long()])
+    capacity = groups.rows.numel()
+    g = torch.Generator().manual_seed(3)
+    x, y = torch.randn(tokens, width, generator=g).to(dtype).cuda(), torch.randn(capacity, width, generator=g).to(dtype).cuda()
+    w = torch.randn(tokens, k, generator=g).cuda()
+    whole = gs.dispatch_rows(x, groups)
+    d_whole, _ = gs.combine_rows_backward(x, y, groups, w)
+    whole[rows], d_whole[rows] = 0.0, 0.0
+    stream = torch.cuda.current_stream().cuda_stream
+    out, d_y, d_w = torch.full_like(y, 7.0), torch.full_like(y, 7.0), torch.full_like(w, 7.0)
+    assert lib.gsort_dispatch_rows(x.data_ptr(), code, tokens, width, width, positions.data_ptr(), k, groups.rows.data_ptr(), capacity,
+                                   out.data_ptr(), stream) == 0
+    assert lib.gsort_combine_rows_backward(x.data_ptr(), code, tokens, width, width, y.data_ptr(), capacity, width, w.data_ptr(),
+                                           positions.data_ptr(), k, groups.rows.data_ptr(), d_y.data_ptr(), d_w.data_ptr(), stream) == 0
+    assert torch.equal(out, whole) and torch.equal(d_y, d_whole)
+    assert (d_w[gone] == 0).all() and d_w[0, 0] == 0

@@ -10,6 +10,11 @@ bfloat16 or float16; all arithmetic is in 32 bits.  Rows may be strided
 Arguments of a wrong type or shape raise TypeError or ValueError, what the
 library refuses raises GsortError.
 
+The forward calls take part in autograd: where gradients are recorded and an
+input requires one, their outputs carry it, computed by the backward calls
+(which can also be made directly, and record nothing).  There are no second
+derivatives, no forward-mode derivatives and no vmap.
+
 The checks, allocations and launches are in the compiled module _ops: a call for
 a few tokens takes as long as its host work.
 """
@@ -18,6 +23,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .gsort import GsortError
@@ -59,7 +65,30 @@ def _checked(result, name: str):
     return result
 
 
+def _wants_grad(t) -> bool:
+    return getattr(t, "requires_grad", False) and torch.is_grad_enabled()
+
+
 # ----------------------------------------------------------------- routing
+class _RouteExperts(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, bias, score, groups, groups_kept, group_score, renormalise, scale):
+        weights, experts = route_experts(logits, k, bias=bias, score=score, groups=groups, groups_kept=groups_kept,
+                                         group_score=group_score, renormalise=renormalise, scale=scale)
+        ctx.save_for_backward(logits, experts)
+        ctx.how = score, renormalise, scale
+        ctx.mark_non_differentiable(experts)
+        return weights, experts
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_weights, _):
+        logits, experts = ctx.saved_tensors
+        score, renormalise, scale = ctx.how
+        return (route_experts_backward(d_weights.contiguous(), logits, experts, score=score, renormalise=renormalise, scale=scale),
+                *[None] * 8)
+
+
 def route_experts(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None,
                   score: str = "softmax", groups: int = 1, groups_kept: int | None = None,
                   group_score: str = "max", renormalise: bool = False, scale: float = 1.0):
@@ -71,7 +100,10 @@ def route_experts(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = N
     the sum of their two largest scores) can be chosen.  Experts with a logit
     of -inf or NaN are never chosen.  Returns (weights [tokens, k] float32,
     experts [tokens, k] int32), best first and ties to the lower index; a token
-    with fewer candidates has experts -1 with weight 0."""
+    with fewer candidates has experts -1 with weight 0.  The weights have a
+    gradient by the logits; the choice, and so the bias, has none."""
+    if _wants_grad(logits):
+        return _RouteExperts.apply(logits, k, bias, score, groups, groups_kept, group_score, renormalise, scale)
     return _checked(_ops.route_experts(logits, k, bias, score, groups, groups_kept, group_score, renormalise, scale),
                     "gsort_route_experts")
 
@@ -104,9 +136,41 @@ def group_by_expert(experts: torch.Tensor, num_experts: int, *, align: int = 1,
                                   "gsort_group_by_expert"))
 
 
+class _DispatchRows(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, *groups):
+        ctx.save_for_backward(*groups)
+        return dispatch_rows(x, ExpertGroups(*groups))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_rows):
+        return combine_rows(d_rows.contiguous(), ExpertGroups(*ctx.saved_tensors)), *[None] * 4
+
+
+class _CombineRows(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weights, *groups):
+        ctx.save_for_backward(y, weights, *groups)
+        return combine_rows(y, ExpertGroups(*groups), weights)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        y, weights, *groups = ctx.saved_tensors
+        groups, d_weights, d_out = ExpertGroups(*groups), None, d_out.contiguous()
+        if weights is None:
+            d_y = dispatch_rows(d_out, groups)
+        else:
+            d_y, d_weights = combine_rows_backward(d_out, y, groups, weights)
+        return d_y, d_weights, *[None] * 4
+
+
 def dispatch_rows(x: torch.Tensor, groups: ExpertGroups) -> torch.Tensor:
     """Copies each token's row of x [tokens, width] to its pairs' rows of the
     grouped layout; rows without a pair are zero.  Returns [capacity, width]."""
+    if _wants_grad(x):
+        return _DispatchRows.apply(x, *groups)
     return _checked(_ops.dispatch_rows(x, groups.positions, groups.rows), "gsort_dispatch_rows")
 
 
@@ -114,6 +178,8 @@ def combine_rows(y: torch.Tensor, groups: ExpertGroups, weights: torch.Tensor | 
     """Sums each token's rows of y [capacity, width] in the grouped layout, with
     weights [tokens, slots] float32 (None: ones, dispatch_rows' gradient).
     Dropped pairs add nothing.  Returns [tokens, width]."""
+    if _wants_grad(y) or _wants_grad(weights):
+        return _CombineRows.apply(y, weights, *groups)
     return _checked(_ops.combine_rows(y, groups.positions, groups.rows, weights), "gsort_combine_rows")
 
 
@@ -125,12 +191,38 @@ def combine_rows_backward(d_out: torch.Tensor, y: torch.Tensor, groups: ExpertGr
 
 
 # ------------------------------------------------------- log probabilities
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, targets, top):
+        logprobs, entropy, top_logprobs, top_ids, stats = token_logprobs(logits, targets, top=top)
+        # outputs go the same way as inputs: as attributes they would hold their own node for ever
+        ctx.save_for_backward(logits, targets, entropy, stats)
+        ctx.mark_non_differentiable(stats, *([] if top_ids is None else [top_ids]))
+        ctx.set_materialize_grads(False)
+        return logprobs, entropy, top_logprobs, top_ids, stats
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_logprobs, d_entropy, d_top_logprobs, _ids, _stats):
+        if d_top_logprobs is not None:
+            raise RuntimeError("top_logprobs have no gradient: give the tokens as targets")
+        if d_logprobs is None and d_entropy is None:
+            return None, None, None
+        logits, targets, entropy, stats = ctx.saved_tensors
+        d_logprobs, d_entropy = (None if d is None else d.contiguous() for d in (d_logprobs, d_entropy))
+        return token_logprobs_backward(d_logprobs, d_entropy, logits, targets, TokenLogprobs(None, entropy, None, None, stats)), None, None
+
+
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, *, top: int = 0) -> TokenLogprobs:
     """Log probabilities of targets [rows] under softmax(logits [rows, vocab]),
     each row's entropy, and its `top` (at most 32) most likely tokens, from one
     read of the logits.  Logits of -inf are masked.  A negative target gives 0,
     one beyond the vocabulary NaN; alternatives come best first, ties to the
-    lower index, with -inf and -1 where a row has too few unmasked logits."""
+    lower index, with -inf and -1 where a row has too few unmasked logits.
+    logprobs and entropy have a gradient; going back through top_logprobs raises
+    RuntimeError."""
+    if _wants_grad(logits):
+        return TokenLogprobs(*_TokenLogprobs.apply(logits, targets, top))
     return TokenLogprobs(*_checked(_ops.token_logprobs(logits, targets, top), "gsort_token_logprobs"))
 
 

@@ -6,8 +6,8 @@ for some steps and then asked for likely next tokens.
 Each step routes the tokens' rows to experts (route_experts), groups them by
 expert (group_by_expert), moves them there (dispatch_rows), applies each
 expert's matrix to its segment of the grouped layout, moves the results back
-(combine_rows) and scores the given tokens (token_logprobs); the gradients go
-the same way back.  The matrix products are torch's.  Prints the loss before
+(combine_rows) and scores the given tokens (token_logprobs); autograd takes the
+gradients the same way back.  The matrix products are torch's.  Prints the loss before
 and after, and the alternatives to one answer with their log probabilities.
 """
 import argparse
@@ -21,61 +21,12 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import bitonic_networks_gb300 as gs
 
 
-class Route(torch.autograd.Function):
-    """Weights (with a gradient) and experts of the k best experts of each token."""
-
+class TokenLogprobs:
     @staticmethod
-    def forward(ctx, logits, k, how):
-        weights, experts = gs.route_experts(logits, k, **how)
-        ctx.save_for_backward(logits, experts)
-        ctx.how = how
-        ctx.mark_non_differentiable(experts)
-        return weights, experts
-
-    @staticmethod
-    def backward(ctx, d_weights, _):
-        logits, experts = ctx.saved_tensors
-        how = {k: v for k, v in ctx.how.items() if k in ("score", "renormalise", "scale")}
-        return gs.route_experts_backward(d_weights.contiguous(), logits, experts, **how), None, None
-
-
-class Dispatch(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, groups):
-        ctx.save_for_backward(*groups)
-        return gs.dispatch_rows(x, groups)
-
-    @staticmethod
-    def backward(ctx, d):
-        return gs.combine_rows(d.contiguous(), gs.ExpertGroups(*ctx.saved_tensors)), None
-
-
-class Combine(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, y, weights, groups):
-        ctx.save_for_backward(y, weights, *groups)
-        return gs.combine_rows(y, groups, weights)
-
-    @staticmethod
-    def backward(ctx, d):
-        y, weights, *groups = ctx.saved_tensors
-        d_y, d_weights = gs.combine_rows_backward(d.contiguous(), y, gs.ExpertGroups(*groups), weights)
-        return d_y, d_weights, None
-
-
-class TokenLogprobs(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, logits, targets):
+    def apply(logits, targets):
+        """Log probabilities of the targets and the rows' entropies, both with gradients."""
         r = gs.token_logprobs(logits, targets)
-        # an output kept as an attribute would hold its own node, and all before it, for ever
-        ctx.save_for_backward(logits, targets, r.entropy, r.stats)
         return r.logprobs, r.entropy
-
-    @staticmethod
-    def backward(ctx, d_logprobs, d_entropy):
-        logits, targets, entropy, stats = ctx.saved_tensors
-        r = gs.TokenLogprobs(None, entropy, None, None, stats)
-        return gs.token_logprobs_backward(d_logprobs.contiguous(), d_entropy.contiguous(), logits, targets, r), None
 
 
 class Model(torch.nn.Module):
@@ -90,15 +41,14 @@ class Model(torch.nn.Module):
 
     def logits(self, tokens):
         x = self.embed[tokens]
-        how = dict(score="sigmoid", bias=self.bias, renormalise=True)
-        weights, experts = Route.apply(x @ self.router, self.k, how)
+        weights, experts = gs.route_experts(x @ self.router, self.k, score="sigmoid", bias=self.bias, renormalise=True)
         groups = gs.group_by_expert(experts, self.experts, align=self.align)
         self.load = groups.counts
-        rows = Dispatch.apply(x, groups)
+        rows = gs.dispatch_rows(x, groups)
         starts = groups.offsets.tolist()
         out = [torch.relu(rows[a:b] @ w) for w, a, b in zip(self.expert, starts, starts[1:])]
         y = torch.cat(out + [rows.new_zeros(rows.shape[0] - starts[-1], rows.shape[1])])
-        return (x + Combine.apply(y, weights, groups)) @ self.head
+        return (x + gs.combine_rows(y, groups, weights)) @ self.head
 
     def balance(self, rate=0.01):
         """Raises the choice bias of experts with less than the mean load, lowers the others'."""

@@ -440,10 +440,13 @@ int launch_combine(const RowsLaunch &L) {
         constexpr int MODE = decltype(m)::value;
         using T = std::decay_t<decltype(*a.out)>;
         // four 16-byte loads in flight: 16384 x 8 rows of 8 KB take 200 us so, 255 with eight
-        if (MODE == kShifted || MODE == kSingle) return start_combine<2, 2, T, MODE>(L, a);
-        if (L.chosen == 1) return start_combine<1, 4, T, MODE>(L, a);
-        if (L.chosen == 2) return start_combine<2, 2, T, MODE>(L, a);
-        return start_combine<4, 1, T, MODE>(L, a);
+        if constexpr (MODE == kShifted || MODE == kSingle) {
+            return start_combine<2, 2, T, MODE>(L, a);
+        } else {
+            if (L.chosen == 1) return start_combine<1, 4, T, MODE>(L, a);
+            if (L.chosen == 2) return start_combine<2, 2, T, MODE>(L, a);
+            return start_combine<4, 1, T, MODE>(L, a);
+        }
     });
 }
 

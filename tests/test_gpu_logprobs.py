@@ -298,3 +298,23 @@ def test_float32_gradient_far_from_the_maximum():
         size = p * a64.abs() * (d.abs() + (h - total.log()).abs())
         off = (got + p * a64 * (d - total.log() + h)).abs() / size
         assert off.max() <= 2.0 ** -20, float(off.max())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [37, 5000, 70_001])
+def test_masked_logits_have_no_gradient(dtype, vocab):
+    """Exactly zero, but for a masked token that was itself given."""
+    x = logits_of(6, vocab, dtype, 21)
+    x[0, vocab // 3:] = -INF
+    x[1, ::2] = -INF
+    x[2] = -INF
+    x[3, 1:] = -INF
+    t = torch.tensor([0, 0, 0, 0, 2, -1]).cuda()
+    r = gs.token_logprobs(x, t)
+    ones = torch.ones(6).cuda()
+    masked = torch.isneginf(x)
+    masked[torch.arange(6), t] = False
+    assert masked.sum() > vocab
+    for dl, dh in ((ones, ones), (ones, None), (None, ones)):
+        dx = gs.token_logprobs_backward(dl, dh, x, t, r)
+        assert (dx[masked] == 0).all() and (dx[2] == 0).all() and torch.isfinite(dx).all()

@@ -99,3 +99,45 @@ def test_training_leaves_no_tensors_behind(example):
         return torch.cuda.memory_allocated()
 
     assert steps(3) == steps(20)
+
+
+def test_every_call_runs_on_the_current_stream():
+    """The inputs are filled on a side stream after work of some milliseconds: a
+    launch on another stream would find them empty."""
+    tokens, experts, width, vocab = 700, 64, 136, 5000
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    real = [torch.randn(tokens, n, generator=gen, device="cuda") for n in (experts, width, vocab, 4)]
+    late = [torch.zeros_like(t) for t in real]
+    given = torch.arange(tokens, device="cuda") % vocab
+
+    def calls(logits, x, answers, d):
+        w, e = gs.route_experts(logits, 4, renormalise=True)
+        yield [w, e]
+        yield [gs.route_experts_backward(d, logits, e, renormalise=True)]
+        g = gs.group_by_expert(e, experts, align=8)
+        yield list(g)
+        rows = gs.dispatch_rows(x, g)
+        yield [rows]
+        yield [gs.combine_rows(rows, g, w)]
+        yield list(gs.combine_rows_backward(x, rows, g, w))
+        r = gs.token_logprobs(answers, given, top=3)
+        yield list(r)
+        yield [gs.token_logprobs_backward(d[:, 0].contiguous(), None, answers, given, r)]
+
+    want = list(calls(*real))
+    list(calls(*late))                          # the kernels are loaded
+    big = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(60):
+            big.add_(1.0)
+        filled = torch.cuda.Event()
+        for to, t in zip(late, real):
+            to.copy_(t)
+        filled.record()
+        got = list(calls(*late))
+        early = not filled.query()              # every call was made before the inputs were there
+        same = [torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w)]
+    torch.cuda.synchronize()
+    assert early and all(same), (early, same)

@@ -26,7 +26,9 @@ constexpr int kGroupThreads = 1024;
 constexpr int kGroupWarps = kGroupThreads / 32;
 constexpr int kGroupItems = 4;                                   // pairs per thread and tile
 constexpr uint32_t kGroupTile = kGroupThreads * kGroupItems;
-constexpr uint32_t kGroupMaxTiles = 148;   // CTAs of one launch: all resident at once, and a bound on the counts each one reads
+// CTAs of one launch: each reads the counts of all of them, so there are no more than
+// run at once, and the workspace's size does not depend on the device (152 SMs here).
+constexpr uint32_t kGroupMaxTiles = 148;
 
 struct GroupArgs {
     const int32_t *experts_in;

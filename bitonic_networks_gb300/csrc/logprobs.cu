@@ -171,7 +171,10 @@ struct LaneSums {
     }
 
     // Adds COUNT pairs, summed on their own first: the sum is about 1 beside the
-    // largest logit and rounds at each addition to it.
+    // largest logit and rounds at each addition to it.  An exponential is off by up to
+    // 2^-22 + (max - x) 2^-23 of itself (ex2.approx, and the product rounded); in a sum
+    // that is (max - x) e^(x - max) 2^-23 a logit, and rows from 1000 to 131072
+    // logits are as near to 64 bits as with expf (3e-8 to 5e-8 on normal logits).
     // low: some logit is so low that its exponent needs the bound.
     template <int COUNT> __device__ __forceinline__ void add(const Pair (&x)[COUNT], bool low) {
         Pair part;
@@ -710,11 +713,18 @@ int launch_logprobs(const LogprobsLaunch &L) {
     const int64_t vectors = L.vocab * float_bytes(L.dtype) / 16;
     // A warp to a row where it is short, so that rows wait for no CTA-wide barrier
     // (8192 x 1000 bf16 with 5 alternatives: 14 us, 51 with a CTA each), and up to
-    // four times as long where rows fill the device (8192 x 12000 with 5 61 against
-    // 75, with 20 71 against 87).
+    // four times as long where rows fill the device, 24 to an SM.  bf16, a warp / a
+    // CTA to a row in us:
+    //   8192 x 6000 22 / 35, with 20 alternatives 46 / 64; x 12000 36 / 50, 70 / 86
+    //   3660 x 6000 with 20 alternatives 28 / 31; x 12000 42 / 41; x 16000 52 / 44
+    //   1824 x 6000 with 20 alternatives 19 / 18; x 12000 29 / 23; x 16000 36 / 25
+    // One limit for all: by length and alternatives the two cross between 1824 rows
+    // (x 6000 without alternatives 9.2 / 10.2) and 4864 (x 16000 with 20 53 / 56).
     const bool warps = vectors <= 512 || (vectors <= 2048 && L.rows >= 24 * L.sm_count);
     // Otherwise a row is split while CTAs do not fill the device and a part has 512
-    // vectors (304 x 131072 bf16 with 20 alternatives: 27 us, 45 whole).
+    // vectors: up to 3 CTAs to an SM before the last halving.  131072 bf16 with 20
+    // alternatives, with 1 / 3 / 12 to an SM: 76 rows 13.8 / 12.4 / 12.4 us, 152 21.7 /
+    // 17.6 / 20.6, 304 26 / 24 / 35, 380 32 / 28 / 42, 450 32 / 36 / 48.
     a.split = 1;
     while (!warps && a.split < kMaxCluster && L.rows * a.split < 3 * L.sm_count && vectors / (2 * a.split) >= 512) a.split *= 2;
     return with_float_type(L.dtype, [&](auto t) {

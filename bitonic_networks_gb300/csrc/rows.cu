@@ -30,7 +30,8 @@ constexpr int kRowThreads = 256;
 // CTAs per SM that a kernel's registers leave room for where 16-bit rows start
 // anywhere: loads wait for memory, and more of them do with more CTAs (8191 x 6
 // rows of 1001: combine 29 us with 4 CTAs of 2 x 2 loads per thread, 37 with 3
-// of 4 x 1; backward 55 with 6 CTAs, 58 with 4; since then 27 and 50).
+// of 4 x 1; backward 55 with 6 CTAs, 58 with 4; since then 26 and 49).  The
+// combine spills 20 to 24 bytes under its bound.
 constexpr int kShiftedCombine = 4, kShiftedBackward = 6;
 
 // A row that is read.  inner: it is neither the first nor the last of its array,
@@ -407,7 +408,8 @@ template <typename T> int64_t split_rows(RowArgs<T> &a, int per_thread) {
 }
 
 template <typename T> void set_fill(RowArgs<T> &a) {
-    // a row to a warp in a small layout, up to 32 in a large one
+    // a row to a warp in a small layout, up to 32 in a large one (8 KB rows of 256 experts
+    // padded to 16: 512 pairs 6.9 us, 32 with 32 rows to a warp; 131072 pairs 187, 200 with one)
     const uint32_t rows = std::min(32u, std::max(1u, a.capacity / 4096)) * (kRowThreads / 32);
     a.fill_blocks = (a.capacity + rows - 1) / rows;
 }
@@ -455,7 +457,9 @@ int launch_combine_backward(const RowsLaunch &L) {
         constexpr int MODE = decltype(m)::value;
         using T = std::decay_t<decltype(*a.out)>;
         const int64_t pairs = L.tokens * L.chosen;
-        // up to a warp to a pair where pairs fill the device, else up to a CTA
+        // up to a warp to a pair where pairs fill the device, else up to a CTA (4096 bf16, a
+        // warp / a CTA to a pair: 1024 pairs 6.5 / 4.9 us, 2432 9.7 / 11.3, 4928 18.9 / 21.7, 16384
+        // 50 / 72; 1001 bf16: 1024 4.7 / 3.5, 4928 9.5 / 8.2, 16384 18.9 / 20.7)
         a.log_lanes = lanes_for(a.vectors, 2);
         if (pairs >= 8 * 4 * L.sm_count) a.log_lanes = std::min(a.log_lanes, 5u);
         const int64_t per = kRowThreads >> a.log_lanes, blocks = (pairs + per - 1) / per;

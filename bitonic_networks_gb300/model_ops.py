@@ -5,7 +5,8 @@ of given tokens, with their gradients.
 Every call takes CUDA tensors (there is no CPU fallback), runs on the current
 stream of their device without synchronising, and returns newly allocated
 tensors unless an output is given.  Activations and logits are float32,
-bfloat16 or float16; all arithmetic is in 32 bits.  Rows may be strided
+bfloat16 or float16; all arithmetic is in 32 bits (include/gsort.h says how
+far exponentials are off).  Rows may be strided
 (tensor[:, :n] of a wider tensor); the elements of a row are consecutive.
 Arguments of a wrong type or shape raise TypeError or ValueError, what the
 library refuses raises GsortError.

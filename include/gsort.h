@@ -311,7 +311,10 @@ int gsort_segmented_sort(const void *d_keys_in, void *d_keys_out,
  * layer of experts, and the selection over a model's output.
  *
  * Element types of activations and logits; arithmetic and sums are in 32
- * bits whatever the type, rounded once when stored.  Pointers are aligned to
+ * bits whatever the type, rounded once when stored.  Exponentials that enter
+ * a sum over a row, or a 16-bit gradient, carry a relative error of up to 2^-22 +
+ * (max - x) 2^-23; those of weights, choices and float32 gradients are within
+ * 2^-21 of e^(x - max), the difference rounded to 32 bits.  Pointers are aligned to
  * their element (else GSORT_EALIGN); rows and bases that are also 16-byte
  * aligned move as 16-byte vectors.  Strides count elements, from one row to
  * the next; elements of a row are consecutive.  A count of zero rows is a

@@ -25,6 +25,7 @@ from typing import NamedTuple
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from .gsort import GsortError
@@ -139,39 +140,39 @@ def group_by_expert(experts: torch.Tensor, num_experts: int, *, align: int = 1,
 
 class _DispatchRows(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, *groups):
-        ctx.save_for_backward(*groups)
-        return dispatch_rows(x, ExpertGroups(*groups))
+    def forward(ctx, x, rows, positions):
+        ctx.save_for_backward(rows, positions)
+        return dispatch_rows(x, ExpertGroups(None, None, rows, positions))
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_rows):
-        return combine_rows(d_rows.contiguous(), ExpertGroups(*ctx.saved_tensors)), *[None] * 4
+        return combine_rows(d_rows.contiguous(), ExpertGroups(None, None, *ctx.saved_tensors)), None, None
 
 
 class _CombineRows(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, y, weights, *groups):
-        ctx.save_for_backward(y, weights, *groups)
-        return combine_rows(y, ExpertGroups(*groups), weights)
+    def forward(ctx, y, weights, rows, positions):
+        ctx.save_for_backward(y, weights, rows, positions)
+        return combine_rows(y, ExpertGroups(None, None, rows, positions), weights)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_out):
-        y, weights, *groups = ctx.saved_tensors
-        groups, d_weights, d_out = ExpertGroups(*groups), None, d_out.contiguous()
+        y, weights, rows, positions = ctx.saved_tensors
+        groups, d_weights, d_out = ExpertGroups(None, None, rows, positions), None, d_out.contiguous()
         if weights is None:
             d_y = dispatch_rows(d_out, groups)
         else:
             d_y, d_weights = combine_rows_backward(d_out, y, groups, weights)
-        return d_y, d_weights, *[None] * 4
+        return d_y, d_weights, None, None
 
 
 def dispatch_rows(x: torch.Tensor, groups: ExpertGroups) -> torch.Tensor:
     """Copies each token's row of x [tokens, width] to its pairs' rows of the
     grouped layout; rows without a pair are zero.  Returns [capacity, width]."""
     if _wants_grad(x):
-        return _DispatchRows.apply(x, *groups)
+        return _DispatchRows.apply(x, groups.rows, groups.positions)
     return _checked(_ops.dispatch_rows(x, groups.positions, groups.rows), "gsort_dispatch_rows")
 
 
@@ -180,7 +181,7 @@ def combine_rows(y: torch.Tensor, groups: ExpertGroups, weights: torch.Tensor | 
     weights [tokens, slots] float32 (None: ones, dispatch_rows' gradient).
     Dropped pairs add nothing.  Returns [tokens, width]."""
     if _wants_grad(y) or _wants_grad(weights):
-        return _CombineRows.apply(y, weights, *groups)
+        return _CombineRows.apply(y, weights, groups.rows, groups.positions)
     return _checked(_ops.combine_rows(y, groups.positions, groups.rows, weights), "gsort_combine_rows")
 
 
@@ -234,5 +235,8 @@ def token_logprobs_backward(d_logprobs: torch.Tensor | None, d_entropy: torch.Te
     entropy), [rows, vocab] of the logits' dtype; `result` is the forward
     call's.  `out` may be the logits themselves.  Without it the gradient's rows
     lie up to 15 bytes apart where the logits' rows do not follow each other."""
-    return _checked(_ops.token_logprobs_backward(d_logprobs, d_entropy, logits, targets, result.entropy, result.stats, out),
+    grad = _checked(_ops.token_logprobs_backward(d_logprobs, d_entropy, logits, targets, result.entropy, result.stats, out),
                     "gsort_token_logprobs_backward")
+    if out is not None and not out.is_inference():
+        increment_version(out)      # autograd refuses what it had saved of it
+    return grad

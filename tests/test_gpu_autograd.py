@@ -113,3 +113,17 @@ def test_other_kinds_of_derivatives_are_refused():
         torch.vmap(lambda a: gs.token_logprobs(a).entropy)(x)
     with pytest.raises(RuntimeError):
         torch.vmap(lambda a: gs.route_experts(a, 2)[0])(x.requires_grad_())
+
+
+def test_a_gradient_over_saved_logits_is_noticed():
+    """Written over the logits, the gradient is no longer what the graph saved."""
+    x, d = leaf(9, 300), torch.ones(9).cuda()
+    y = x * 1.0
+    r = gs.token_logprobs(y)
+    with torch.inference_mode():
+        z = x.clone()
+        gs.token_logprobs_backward(None, d, z, None, gs.token_logprobs(z), out=z)
+    with torch.no_grad():
+        gs.token_logprobs_backward(None, d, y, None, r, out=y)
+    with pytest.raises(RuntimeError, match="modified"):
+        r.entropy.sum().backward()

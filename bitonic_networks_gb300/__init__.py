@@ -20,6 +20,8 @@ _MODEL_OPS = [
     "route_experts", "route_experts_backward", "group_by_expert", "group_capacity",
     "group_workspace_bytes", "dispatch_rows", "combine_rows", "combine_rows_backward",
     "token_logprobs", "token_logprobs_backward", "ExpertGroups", "TokenLogprobs",
+    "embed_tokens", "embed_tokens_backward", "embed_workspace_bytes", "adjust_logits", "adjust_logits_backward",
+    "gradient_norm", "clip_gradients", "ClippedGradients",
 ]
 __all__ += _MODEL_OPS
 

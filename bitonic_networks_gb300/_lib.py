@@ -31,6 +31,27 @@ class Options(ctypes.Structure):
     ]
 
 
+class Adjustments(ctypes.Structure):
+    """struct gsort_adjustments."""
+    _fields_ = [
+        ("d_history", ctypes.c_void_p),
+        ("length", ctypes.c_int64),
+        ("history_stride", ctypes.c_int64),
+        ("history_bytes", ctypes.c_int),
+        ("d_prompt", ctypes.c_void_p),
+        ("d_repetition", ctypes.c_void_p),
+        ("d_presence", ctypes.c_void_p),
+        ("d_frequency", ctypes.c_void_p),
+        ("d_bias_tokens", ctypes.c_void_p),
+        ("d_bias", ctypes.c_void_p),
+        ("biases", ctypes.c_int64),
+        ("bias_stride", ctypes.c_int64),
+        ("bias_bytes", ctypes.c_int),
+        ("d_allowed", ctypes.c_void_p),
+        ("allowed_stride", ctypes.c_int64),
+    ]
+
+
 # name -> (restype, argtypes); every symbol that include/gsort.h declares
 SIGNATURES = {
     "gsort_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -128,6 +149,28 @@ SIGNATURES = {
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
         ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
         ctypes.c_int64, ctypes.c_void_p]),
+    "gsort_embed_tokens": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
+    "gsort_embed_tokens_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "gsort_embed_tokens_backward": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,
+        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "gsort_adjust_logits": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+        ctypes.POINTER(Adjustments), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "gsort_adjust_logits_backward": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_int64, ctypes.POINTER(Adjustments), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "gsort_gradient_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64]),
+    "gsort_gradient_norm": (ctypes.c_int, [
+        ctypes.POINTER(ctypes.c_void_p), c_i64p, ctypes.POINTER(ctypes.c_int), ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "gsort_clip_gradients": (ctypes.c_int, [
+        ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), c_i64p, ctypes.POINTER(ctypes.c_int),
+        ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+        ctypes.c_void_p]),
     "gsort_check": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "gsort_radix_num_variants": (ctypes.c_int, []),
     "gsort_radix_variant_name": (ctypes.c_char_p, [ctypes.c_int]),

@@ -2,6 +2,8 @@
 // argument checks before any CUDA call, then one launcher.
 #include <algorithm>
 #include <cmath>
+#include <new>
+#include <vector>
 
 #include "model_ops.cuh"
 
@@ -59,6 +61,151 @@ int layout_args(int dtype, int64_t tokens, int64_t width, int chosen, int64_t ca
     if (tokens > GSORT_MAX_N || width > GSORT_MAX_N || capacity > GSORT_MAX_N) return GSORT_ETOOBIG;
     if (tokens * chosen > GSORT_MAX_N) return GSORT_ETOOBIG;
     return GSORT_OK;
+}
+
+int embed_args(int dtype, int64_t vocab, int64_t width, int64_t tokens, int token_bytes, float scale) {
+    if (float_bytes(dtype) == 0 || vocab < 1 || width < 1 || tokens < 0) return GSORT_EINVAL;
+    if (token_bytes != 4 && token_bytes != 8) return GSORT_EINVAL;
+    if (tokens > GSORT_MAX_N || vocab > GSORT_MAX_N || width > GSORT_MAX_N) return GSORT_ETOOBIG;
+    return std::isfinite(scale) ? GSORT_OK : GSORT_EINVAL;
+}
+
+// Rows that are only read may all be one (stride 0).
+int list_args(int64_t rows, int64_t width, int64_t stride) {
+    return stride == 0 ? rows_args(1, width, width) : rows_args(rows, width, stride);
+}
+
+// The logits' adjustment (in: the logits) or its gradient (in: the gradient by the adjusted logits).
+int adjust(bool backward, const void *logits, int64_t logits_stride, const void *in, int64_t in_stride, int dtype, int64_t rows,
+           int64_t vocab, const gsort_adjustments *how, void *out, int64_t out_stride, cudaStream_t stream) {
+    if (float_bytes(dtype) == 0 || how == nullptr) return GSORT_EINVAL;
+    const gsort_adjustments &h = *how;
+    int rc = rows_args(rows, vocab, in_stride);
+    if (rc == GSORT_OK) rc = rows_args(rows, vocab, out_stride);
+    const bool history = h.d_history != nullptr && h.length > 0 && (!backward || h.d_repetition != nullptr);
+    if (rc == GSORT_OK && backward && history) rc = rows_args(rows, vocab, logits_stride);
+    if (rc != GSORT_OK) return rc;
+    if (h.length < 0 || h.biases < 0) return GSORT_EINVAL;
+    const int64_t words = (vocab + 31) / 32;
+    if (h.d_history != nullptr && h.history_bytes != 4 && h.history_bytes != 8) return GSORT_EINVAL;
+    if (h.d_history == nullptr && (h.length > 0 || h.d_prompt || h.d_repetition || h.d_presence || h.d_frequency)) return GSORT_EINVAL;
+    if (h.biases > 0 && (h.d_bias_tokens == nullptr || h.d_bias == nullptr)) return GSORT_EINVAL;
+    if (h.biases > 0 && h.bias_bytes != 4 && h.bias_bytes != 8) return GSORT_EINVAL;
+    if (history) rc = list_args(rows, h.length, h.history_stride);
+    if (rc == GSORT_OK && h.biases > 0) rc = list_args(rows, h.biases, h.bias_stride);
+    if (rc == GSORT_OK && h.d_allowed != nullptr) rc = list_args(rows, words, h.allowed_stride);
+    if (rc != GSORT_OK || rows == 0) return rc;
+    if (in == nullptr || out == nullptr || (backward && history && logits == nullptr)) return GSORT_EINVAL;
+    const size_t size = float_bytes(dtype), n = static_cast<size_t>(rows);
+    if (!aligned(in, size) || !aligned(out, size) || !aligned(logits, size) || !aligned(h.d_prompt, 4) || !aligned(h.d_repetition, 4) ||
+        !aligned(h.d_presence, 4) || !aligned(h.d_frequency, 4) || !aligned(h.d_bias, 4) || !aligned(h.d_allowed, 4) ||
+        (history && !aligned(h.d_history, h.history_bytes)) || (h.biases > 0 && !aligned(h.d_bias_tokens, h.bias_bytes)))
+        return GSORT_EALIGN;
+    const bool in_place = in == out && (in_stride == out_stride || rows == 1);
+    const Span ins[] = {in_place ? Span{nullptr, 0} : rows_span(in, rows, vocab, in_stride, size),
+                        backward && history ? rows_span(logits, rows, vocab, logits_stride, size) : Span{nullptr, 0},
+                        history ? rows_span(h.d_history, rows, h.length, h.history_stride, h.history_bytes) : Span{nullptr, 0},
+                        {h.d_prompt, n * 4}, {h.d_repetition, n * 4}, {h.d_presence, n * 4}, {h.d_frequency, n * 4},
+                        h.biases > 0 ? rows_span(h.d_bias_tokens, rows, h.biases, h.bias_stride, h.bias_bytes) : Span{nullptr, 0},
+                        h.biases > 0 ? rows_span(h.d_bias, rows, h.biases, h.bias_stride, 4) : Span{nullptr, 0},
+                        h.d_allowed ? rows_span(h.d_allowed, rows, words, h.allowed_stride, 4) : Span{nullptr, 0}};
+    const Span outs[] = {rows_span(out, rows, vocab, out_stride, size)};
+    if (clash(ins, outs)) return GSORT_EINVAL;
+    AdjustLaunch L;
+    L.backward = backward;
+    L.logits = logits;
+    L.in = in;
+    L.out = out;
+    L.dtype = dtype;
+    L.rows = rows;
+    L.vocab = vocab;
+    L.logits_stride = logits_stride;
+    L.in_stride = in_stride;
+    L.out_stride = out_stride;
+    L.history = history ? h.d_history : nullptr;
+    L.history_stride = h.history_stride;
+    L.length = h.length;
+    L.history_bytes = h.history_bytes;
+    L.prompt = h.d_prompt;
+    L.repetition = h.d_repetition;
+    L.presence = h.d_presence;
+    L.frequency = h.d_frequency;
+    L.bias_tokens = h.d_bias_tokens;
+    L.bias = h.d_bias;
+    L.bias_stride = h.bias_stride;
+    L.biases = h.biases;
+    L.bias_bytes = h.bias_bytes;
+    L.allowed = h.d_allowed;
+    L.allowed_stride = h.allowed_stride;
+    L.stream = stream;
+    return launch_adjust(L);
+}
+
+// Whether an output overlaps another output, the workspace, the norm or another tensor than the one
+// it is the clipped form of (or that one in part).
+bool tensors_clash(const void *const *in, void *const *out, const int64_t *elements, const int *dtypes, int64_t tensors, const Span &norm,
+                   const Span &ws) {
+    struct Range {
+        uintptr_t begin, end;
+        bool written;
+    };
+    std::vector<Range> ranges;
+    ranges.reserve(2 * tensors + 2);
+    for (const Span &s : {norm, ws})
+        if (s.bytes > 0) ranges.push_back({reinterpret_cast<uintptr_t>(s.p), reinterpret_cast<uintptr_t>(s.p) + s.bytes, true});
+    for (int64_t i = 0; i < tensors; ++i) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]), n = static_cast<uintptr_t>(elements[i]) * float_bytes(dtypes[i]);
+        if (n == 0) continue;
+        const bool same = out != nullptr && in[i] == out[i];
+        ranges.push_back({a, a + n, same});
+        if (out != nullptr && !same) ranges.push_back({reinterpret_cast<uintptr_t>(out[i]), reinterpret_cast<uintptr_t>(out[i]) + n, true});
+    }
+    auto before = [](const Range &x, const Range &y) { return x.begin < y.begin; };
+    if (!std::is_sorted(ranges.begin(), ranges.end(), before)) std::sort(ranges.begin(), ranges.end(), before);
+    uintptr_t end = 0, written = 0;      // the furthest end of any range so far, and of a written one
+    for (const Range &r : ranges) {
+        if (r.begin < written || (r.written && r.begin < end)) return true;
+        end = std::max(end, r.end);
+        if (r.written) written = std::max(written, r.end);
+    }
+    return false;
+}
+
+int norm(const void *const *in, void *const *out, const int64_t *elements, const int *dtypes, int64_t tensors, float max_norm,
+         float scale, float *d_norm, void *ws, size_t ws_bytes, cudaStream_t stream) {
+    if (tensors < 0 || !std::isfinite(scale) || !(max_norm >= 0.0f)) return GSORT_EINVAL;
+    if (tensors > GSORT_MAX_N) return GSORT_ETOOBIG;
+    if (d_norm == nullptr || (tensors > 0 && (in == nullptr || elements == nullptr || dtypes == nullptr))) return GSORT_EINVAL;
+    if (!aligned(d_norm, 4)) return GSORT_EALIGN;
+    for (int64_t i = 0; i < tensors; ++i) {
+        const int size = float_bytes(dtypes[i]);
+        if (size == 0 || elements[i] < 0) return GSORT_EINVAL;
+        if (elements[i] > static_cast<int64_t>(1) << 44) return GSORT_ETOOBIG;
+        if (elements[i] > 0 && (in[i] == nullptr || (out != nullptr && out[i] == nullptr))) return GSORT_EINVAL;
+        if (!aligned(in[i], size) || (out != nullptr && !aligned(out[i], size))) return GSORT_EALIGN;
+    }
+    const size_t need = norm_workspace_bytes(tensors);
+    if (need > 0) {
+        if (ws == nullptr || ws_bytes < need) return GSORT_EWORKSPACE;
+        if (!aligned(ws, kWsAlign)) return GSORT_EALIGN;
+    }
+    try {
+        if (tensors_clash(in, out, elements, dtypes, tensors, {d_norm, 4}, {ws, need})) return GSORT_EINVAL;
+    } catch (const std::bad_alloc &) {
+        return GSORT_ETOOBIG;
+    }
+    NormLaunch L;
+    L.in = in;
+    L.out = out;
+    L.sizes = elements;
+    L.dtypes = dtypes;
+    L.tensors = tensors;
+    L.scale = scale;
+    L.max_norm = max_norm;
+    L.norm = d_norm;
+    L.ws = static_cast<unsigned char *>(ws);
+    L.stream = stream;
+    return launch_norm(L);
 }
 
 }  // namespace
@@ -366,6 +513,110 @@ int gsort_token_logprobs_backward(const float *d_grad_logprobs, const float *d_g
     L.grad_stride = grad_stride;
     L.stream = stream;
     return launch_logprobs_backward(L);
+}
+
+int gsort_embed_tokens(const void *d_table, int dtype, int64_t vocab, int64_t width,
+                       int64_t row_stride, const void *d_tokens, int token_bytes, int64_t tokens,
+                       float scale, void *d_out, cudaStream_t stream) {
+    int rc = embed_args(dtype, vocab, width, tokens, token_bytes, scale);
+    if (rc == GSORT_OK) rc = rows_args(vocab, width, row_stride);
+    if (rc != GSORT_OK || tokens == 0) return rc;
+    if (d_table == nullptr || d_tokens == nullptr || d_out == nullptr) return GSORT_EINVAL;
+    const size_t size = float_bytes(dtype);
+    if (!aligned(d_table, size) || !aligned(d_out, size) || !aligned(d_tokens, token_bytes)) return GSORT_EALIGN;
+    const Span in[] = {rows_span(d_table, vocab, width, row_stride, size), {d_tokens, static_cast<size_t>(tokens) * token_bytes}};
+    const Span out[] = {rows_span(d_out, tokens, width, width, size)};
+    if (clash(in, out)) return GSORT_EINVAL;
+    EmbedLaunch L;
+    L.in = d_table;
+    L.dtype = dtype;
+    L.vocab = vocab;
+    L.width = width;
+    L.in_stride = row_stride;
+    L.tokens = d_tokens;
+    L.token_bytes = token_bytes;
+    L.n = tokens;
+    L.scale = scale;
+    L.out = d_out;
+    L.stream = stream;
+    return launch_embed(L);
+}
+
+size_t gsort_embed_tokens_backward_workspace_bytes(int64_t tokens, int64_t width, int dtype) {
+    if (tokens < 1 || tokens > GSORT_MAX_N || width < 1 || width > GSORT_MAX_N || float_bytes(dtype) == 0) return 0;
+    return embed_workspace_bytes(tokens, width, dtype);
+}
+
+int gsort_embed_tokens_backward(const void *d_grad_out, int dtype, int64_t tokens, int64_t width,
+                                int64_t grad_stride, const void *d_tokens, int token_bytes,
+                                int64_t vocab, float scale, int accumulate, void *d_grad_table,
+                                int64_t table_stride, void *d_ws, size_t ws_bytes,
+                                cudaStream_t stream) {
+    int rc = embed_args(dtype, vocab, width, tokens, token_bytes, scale);
+    if (rc == GSORT_OK) rc = rows_args(tokens, width, grad_stride);
+    if (rc == GSORT_OK) rc = rows_args(vocab, width, table_stride);
+    if (rc != GSORT_OK) return rc;
+    if (tokens == 0 && accumulate != 0) return GSORT_OK;
+    if (d_grad_table == nullptr || (tokens > 0 && (d_grad_out == nullptr || d_tokens == nullptr))) return GSORT_EINVAL;
+    const size_t size = float_bytes(dtype);
+    if (!aligned(d_grad_out, size) || !aligned(d_grad_table, size) || !aligned(d_tokens, token_bytes)) return GSORT_EALIGN;
+    const size_t ws = gsort_embed_tokens_backward_workspace_bytes(tokens, width, dtype);
+    if (ws > 0) {
+        if (d_ws == nullptr || ws_bytes < ws) return GSORT_EWORKSPACE;
+        if (!aligned(d_ws, kWsAlign)) return GSORT_EALIGN;
+    }
+    const Span in[] = {rows_span(d_grad_out, tokens, width, grad_stride, size), {d_tokens, static_cast<size_t>(tokens) * token_bytes}};
+    const Span out[] = {rows_span(d_grad_table, vocab, width, table_stride, size), {ws > 0 ? d_ws : nullptr, ws}};
+    if (clash(in, out)) return GSORT_EINVAL;
+    DeviceInfo dev;
+    if (device_info(&dev) != GSORT_OK) return GSORT_ECUDA;
+    EmbedBackwardLaunch L;
+    L.d_out = d_grad_out;
+    L.dtype = dtype;
+    L.n = tokens;
+    L.width = width;
+    L.d_stride = grad_stride;
+    L.tokens = d_tokens;
+    L.token_bytes = token_bytes;
+    L.vocab = vocab;
+    L.scale = scale;
+    L.accumulate = accumulate != 0;
+    L.d_table = d_grad_table;
+    L.table_stride = table_stride;
+    L.ws = static_cast<unsigned char *>(d_ws);
+    L.stream = stream;
+    L.sm_count = dev.sm_count;
+    return launch_embed_backward(L);
+}
+
+int gsort_adjust_logits(const void *d_logits, int dtype, int64_t rows, int64_t vocab,
+                        int64_t row_stride, const gsort_adjustments *how, void *d_out,
+                        int64_t out_stride, cudaStream_t stream) {
+    return adjust(false, nullptr, 0, d_logits, row_stride, dtype, rows, vocab, how, d_out, out_stride, stream);
+}
+
+int gsort_adjust_logits_backward(const void *d_grad_out, int dtype, int64_t rows, int64_t vocab,
+                                 int64_t grad_stride, const void *d_logits, int64_t row_stride,
+                                 const gsort_adjustments *how, void *d_grad_logits,
+                                 int64_t grad_logits_stride, cudaStream_t stream) {
+    return adjust(true, d_logits, row_stride, d_grad_out, grad_stride, dtype, rows, vocab, how, d_grad_logits, grad_logits_stride, stream);
+}
+
+size_t gsort_gradient_norm_workspace_bytes(int64_t tensors) {
+    return tensors < 1 || tensors > GSORT_MAX_N ? 0 : norm_workspace_bytes(tensors);
+}
+
+int gsort_gradient_norm(const void *const *d_gradients, const int64_t *elements, const int *dtypes,
+                        int64_t tensors, float *d_norm, void *d_ws, size_t ws_bytes,
+                        cudaStream_t stream) {
+    return norm(d_gradients, nullptr, elements, dtypes, tensors, INFINITY, 1.0f, d_norm, d_ws, ws_bytes, stream);
+}
+
+int gsort_clip_gradients(const void *const *d_gradients, void *const *d_out, const int64_t *elements,
+                         const int *dtypes, int64_t tensors, float max_norm, float scale,
+                         float *d_norm, void *d_ws, size_t ws_bytes, cudaStream_t stream) {
+    if (tensors > 0 && d_out == nullptr) return GSORT_EINVAL;
+    return norm(d_gradients, d_out, elements, dtypes, tensors, max_norm, scale, d_norm, d_ws, ws_bytes, stream);
 }
 
 }  // extern "C"

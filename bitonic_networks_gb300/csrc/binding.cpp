@@ -12,6 +12,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_like.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -20,6 +22,7 @@
 #include <climits>
 #include <optional>
 #include <string>
+#include <vector>
 
 #include "gsort.h"
 
@@ -433,10 +436,345 @@ PyObject *token_logprobs_backward(PyObject *, PyObject *const *a, Py_ssize_t n) 
     });
 }
 
+// ---------------------------------------------------------------- embedding
+// Token ids of any shape, one behind another.
+Targets tokens_of(const Tensor &t, at::Device device) {
+    if (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong)
+        refuse(PyExc_TypeError, "tokens must be int32 or int64, got %s", text(t).c_str());
+    return {flat(t, "tokens", t.scalar_type(), t.sizes(), device), static_cast<int>(t.element_size())};
+}
+
+PyObject *embed_tokens(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry("embed_tokens", n, 3, [&] {
+        const Tensor &table = tensor(a[0], "table"), &tokens = tensor(a[1], "tokens");
+        const Matrix x = matrix(table, "table");
+        const Targets t = tokens_of(tokens, x.device);
+        const float scale = real(a[2]);
+        Tensor out;
+        int rc;
+        {
+            WithoutGil released;
+            const c10::cuda::CUDAGuard guard(x.device);
+            std::vector<int64_t> shape(tokens.sizes().begin(), tokens.sizes().end());
+            shape.push_back(x.width);
+            out = make(shape, table.scalar_type(), x.device);
+            rc = gsort_embed_tokens(x.p, x.code, x.rows, x.width, x.stride, t.p, t.bytes, tokens.numel(), scale, out.data_ptr(),
+                                    stream_of(x.device));
+        }
+        return result(rc, out);
+    });
+}
+
+PyObject *embed_tokens_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry("embed_tokens_backward", n, 7, [&] {
+        const Tensor &d = tensor(a[0], "d_out"), &tokens = tensor(a[1], "tokens");
+        const int vocab = integer(a[2], "vocab");
+        const float scale = real(a[3]);
+        const auto given = optional_tensor(a[4], "out"), space = optional_tensor(a[6], "workspace");
+        const bool accumulate = truth(a[5]);
+        const int code = float_code(d, "d_out");
+        if (!d.is_cuda() || d.dim() != tokens.dim() + 1 || d.sizes().slice(0, tokens.dim()) != tokens.sizes())
+            refuse(PyExc_ValueError, "d_out must be a CUDA tensor with a row for each token, got %s for tokens %s", text(d).c_str(), text(tokens).c_str());
+        const at::Device device = d.device();
+        const Targets t = tokens_of(tokens, device);
+        const int64_t width = d.size(-1), rows = tokens.numel();
+        int64_t stride = width;
+        if (d.dim() == 2) stride = matrix(d, "d_out").stride;
+        else if (!d.is_contiguous()) refuse(PyExc_ValueError, "d_out must be contiguous, or have two dimensions, got %s", text(d).c_str());
+        if (vocab < 1) refuse(PyExc_ValueError, "vocab must be at least 1");
+        if (accumulate && !given.has_value()) refuse(PyExc_ValueError, "accumulate needs out");
+        if (space.has_value() && (space->device() != device || !space->is_contiguous()))
+            refuse(PyExc_ValueError, "workspace must be contiguous and on %s", device.str().c_str());
+        int64_t table_stride = width;
+        if (given.has_value()) {
+            const Matrix o = matrix(*given, "out");
+            if (o.code != code || o.rows != vocab || o.width != width || o.device != device)
+                refuse(PyExc_ValueError, "out must have d_out's dtype and device and shape [%d, %lld], got %s", vocab,
+                       static_cast<long long>(width), text(*given).c_str());
+            table_stride = o.stride;
+        }
+        Tensor out;
+        int rc;
+        {
+            WithoutGil released;
+            const c10::cuda::CUDAGuard guard(device);
+            const int64_t bytes = static_cast<int64_t>(gsort_embed_tokens_backward_workspace_bytes(rows, width, code));
+            Tensor ws = space.value_or(Tensor());
+            if (!ws.defined() && bytes > 0) ws = make({bytes}, at::kByte, device);
+            out = given.has_value() ? *given : make({vocab, width}, d.scalar_type(), device);
+            rc = gsort_embed_tokens_backward(d.data_ptr(), code, rows, width, stride, t.p, t.bytes, vocab, scale, accumulate, out.data_ptr(),
+                                             table_stride, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0,
+                                             stream_of(device));
+        }
+        return result(rc, out);
+    });
+}
+
+// ---------------------------------------------------------- adjusted logits
+// [rows, any] on the device, the elements of a row consecutive; the rows may be one (expanded).
+struct Lists {
+    void *p;
+    int64_t length, stride;
+    int bytes;
+};
+
+Lists lists(const std::optional<Tensor> &t, const char *name, int64_t rows, at::Device device, std::initializer_list<at::ScalarType> types) {
+    if (!t.has_value()) return {nullptr, 0, 0, 0};
+    bool fits = false;
+    std::string names;
+    for (const at::ScalarType type : types) {
+        fits = fits || t->scalar_type() == type;
+        names += (names.empty() ? "" : " or ") + std::string(at::toString(type));
+    }
+    if (!fits) refuse(PyExc_TypeError, "%s must be %s, got %s", name, names.c_str(), text(*t).c_str());
+    if (t->device() != device || t->dim() != 2 || t->size(0) != rows)
+        refuse(PyExc_ValueError, "%s must have %lld rows on %s, got %s", name, static_cast<long long>(rows), device.str().c_str(), text(*t).c_str());
+    if (t->size(1) > 1 && t->stride(1) != 1) refuse(PyExc_ValueError, "the elements of a row of %s must be consecutive", name);
+    return {t->data_ptr(), t->size(1), rows > 1 ? t->stride(0) : t->size(1), static_cast<int>(t->element_size())};
+}
+
+// The fields of the adjustments, in the order of the arguments from a[0] on.
+gsort_adjustments adjustments(const std::optional<Tensor> (&t)[8], const Matrix &x) {
+    gsort_adjustments h = {};
+    const Lists history = lists(t[0], "history", x.rows, x.device, {at::kInt, at::kLong});
+    const Lists tokens = lists(t[5], "bias_tokens", x.rows, x.device, {at::kInt, at::kLong});
+    const Lists bias = lists(t[6], "bias", x.rows, x.device, {at::kFloat});
+    const Lists allowed = lists(t[7], "allowed", x.rows, x.device, {at::kInt});
+    h.d_prompt = flat<int32_t>(t[1], "prompt", at::kInt, {x.rows}, x.device);
+    h.d_repetition = flat<float>(t[2], "repetition", at::kFloat, {x.rows}, x.device);
+    h.d_presence = flat<float>(t[3], "presence", at::kFloat, {x.rows}, x.device);
+    h.d_frequency = flat<float>(t[4], "frequency", at::kFloat, {x.rows}, x.device);
+    if (!t[0].has_value() && (t[1].has_value() || t[2].has_value() || t[3].has_value() || t[4].has_value()))
+        refuse(PyExc_ValueError, "penalties need a history");
+    if (t[5].has_value() != t[6].has_value()) refuse(PyExc_ValueError, "bias_tokens and bias come together");
+    if (tokens.length != bias.length || (tokens.length > 0 && tokens.stride != bias.stride))
+        refuse(PyExc_ValueError, "bias_tokens and bias must have one shape and one distance between rows");
+    const int64_t words = (x.width + 31) / 32;
+    if (t[7].has_value() && allowed.length != words)
+        refuse(PyExc_ValueError, "allowed must have %lld words to a row, got %s", static_cast<long long>(words), text(*t[7]).c_str());
+    // an empty history has no address, but its penalties are no mistake
+    if (history.length > 0) {
+        h.d_history = history.p;
+        h.length = history.length;
+        h.history_stride = history.stride;
+        h.history_bytes = history.bytes;
+    } else {
+        h.d_prompt = nullptr;
+        h.d_repetition = h.d_presence = h.d_frequency = nullptr;
+    }
+    h.d_bias_tokens = tokens.p;
+    h.d_bias = static_cast<float *>(bias.p);
+    h.biases = tokens.length;
+    h.bias_stride = tokens.stride;
+    h.bias_bytes = tokens.bytes;
+    h.d_allowed = static_cast<uint32_t *>(allowed.p);
+    h.allowed_stride = allowed.stride;
+    return h;
+}
+
+// The output's row stride: of the tensor given, or one with which rows lie to 16
+// bytes as the input's do, so that both move in whole vectors.
+int64_t adjusted_stride(const std::optional<Tensor> &given, const Matrix &x, int64_t element) {
+    if (!given.has_value()) {
+        const int64_t vector = 16 / element, between = (x.stride - x.width) % vector;
+        return x.width + (between < 0 ? 0 : between);
+    }
+    const Matrix o = matrix(*given, "out");
+    if (o.code != x.code || o.rows != x.rows || o.width != x.width || o.device != x.device)
+        refuse(PyExc_ValueError, "out must have the input's dtype, shape and device, got %s", text(*given).c_str());
+    return o.stride;
+}
+
+Tensor adjusted_out(const std::optional<Tensor> &given, const Matrix &x, at::ScalarType type, int64_t stride) {
+    if (given.has_value()) return *given;
+    const Tensor whole = make({x.rows, stride}, type, x.device);
+    return stride == x.width ? whole : whole.narrow(1, 0, x.width);
+}
+
+PyObject *adjust_logits(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry("adjust_logits", n, 10, [&] {
+        const Tensor &logits = tensor(a[0], "logits");
+        const Matrix x = matrix(logits, "logits");
+        const std::optional<Tensor> given = optional_tensor(a[9], "out");
+        const std::optional<Tensor> how[8] = {optional_tensor(a[1], "history"),     optional_tensor(a[2], "prompt"),
+                                              optional_tensor(a[3], "repetition"),  optional_tensor(a[4], "presence"),
+                                              optional_tensor(a[5], "frequency"),   optional_tensor(a[6], "bias_tokens"),
+                                              optional_tensor(a[7], "bias"),        optional_tensor(a[8], "allowed")};
+        const gsort_adjustments h = adjustments(how, x);
+        const int64_t stride = adjusted_stride(given, x, logits.element_size());
+        Tensor out;
+        int rc;
+        {
+            WithoutGil released;
+            const c10::cuda::CUDAGuard guard(x.device);
+            out = adjusted_out(given, x, logits.scalar_type(), stride);
+            rc = gsort_adjust_logits(x.p, x.code, x.rows, x.width, x.stride, &h, out.data_ptr(), stride, stream_of(x.device));
+        }
+        return result(rc, out);
+    });
+}
+
+PyObject *adjust_logits_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry("adjust_logits_backward", n, 6, [&] {
+        const Tensor &dt = tensor(a[0], "d_out");
+        const Matrix d = matrix(dt, "d_out");
+        const auto logits = optional_tensor(a[1], "logits"), given = optional_tensor(a[5], "out");
+        const std::optional<Tensor> how[8] = {optional_tensor(a[2], "history"), std::nullopt, optional_tensor(a[3], "repetition"), std::nullopt,
+                                              std::nullopt, std::nullopt, std::nullopt, optional_tensor(a[4], "allowed")};
+        const gsort_adjustments h = adjustments(how, d);
+        void *lp = nullptr;
+        int64_t logits_stride = 0;
+        if (logits.has_value()) {
+            const Matrix x = matrix(*logits, "logits");
+            if (x.code != d.code || x.rows != d.rows || x.width != d.width || x.device != d.device)
+                refuse(PyExc_ValueError, "logits must have d_out's dtype, shape and device, got %s and %s", text(*logits).c_str(), text(dt).c_str());
+            lp = x.p;
+            logits_stride = x.stride;
+        } else if (h.d_repetition != nullptr) {
+            refuse(PyExc_ValueError, "repetition needs the logits");
+        }
+        const int64_t stride = adjusted_stride(given, d, dt.element_size());
+        Tensor out;
+        int rc;
+        {
+            WithoutGil released;
+            const c10::cuda::CUDAGuard guard(d.device);
+            out = adjusted_out(given, d, dt.scalar_type(), stride);
+            rc = gsort_adjust_logits_backward(d.p, d.code, d.rows, d.width, d.stride, lp, logits_stride, &h, out.data_ptr(), stride,
+                                              stream_of(d.device));
+        }
+        return result(rc, out);
+    });
+}
+
+// ------------------------------------------------------------ gradient norm
+// The tensors of a list: dense, on one device.
+struct TensorList {
+    PyObject *fast = nullptr;       // keeps the items
+    std::vector<const void *> data;
+    std::vector<int64_t> sizes;
+    std::vector<int> codes;
+    std::optional<at::Device> device;
+
+    ~TensorList() { Py_XDECREF(fast); }
+    int64_t count() const { return static_cast<int64_t>(sizes.size()); }
+    const Tensor &at(int64_t i) const { return THPVariable_Unpack(PySequence_Fast_GET_ITEM(fast, i)); }
+
+    void read(PyObject *o, const char *name, const char *what) {
+        fast = PySequence_Fast(o, what);
+        if (fast == nullptr) throw Refused{};
+        const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
+        data.reserve(n);
+        sizes.reserve(n);
+        codes.reserve(n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            const Tensor &t = tensor(PySequence_Fast_GET_ITEM(fast, i), name);
+            codes.push_back(float_code(t, name));
+            if (!t.is_cuda() || (device.has_value() && t.device() != *device))
+                refuse(PyExc_ValueError, "%s must be CUDA tensors of one device, got %s", name, text(t).c_str());
+            if (!t.is_non_overlapping_and_dense()) refuse(PyExc_ValueError, "%s must be dense, got %s with gaps or overlaps", name, text(t).c_str());
+            if (t.requires_grad() && c10::GradMode::is_enabled())
+                refuse(PyExc_RuntimeError, "norm and clipping have no gradient: call them under torch.no_grad() or on detached tensors");
+            device = t.device();
+            data.push_back(t.data_ptr());
+            sizes.push_back(t.numel());
+        }
+    }
+};
+
+at::Device norm_device(const TensorList &list) {
+    if (!list.device.has_value()) refuse(PyExc_ValueError, "there are no gradients");
+    return *list.device;
+}
+
+Tensor norm_workspace(const TensorList &list, at::Device device) {
+    return make({static_cast<int64_t>(gsort_gradient_norm_workspace_bytes(list.count()))}, at::kByte, device);
+}
+
+PyObject *gradient_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry("gradient_norm", n, 1, [&] {
+        TensorList g;
+        g.read(a[0], "gradients", "gradients must be a list of tensors");
+        const at::Device device = norm_device(g);
+        Tensor out;
+        int rc;
+        {
+            WithoutGil released;
+            const c10::cuda::CUDAGuard guard(device);
+            const Tensor ws = norm_workspace(g, device);
+            out = make({}, at::kFloat, device);
+            rc = gsort_gradient_norm(g.data.data(), g.sizes.data(), g.codes.data(), g.count(), floats(out), ws.data_ptr(), ws.nbytes(),
+                                     stream_of(device));
+        }
+        return result(rc, out);
+    });
+}
+
+// (list of the clipped tensors, norm)
+PyObject *clip_gradients(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return entry("clip_gradients", n, 4, [&]() -> PyObject * {
+        TensorList g, o;
+        g.read(a[0], "gradients", "gradients must be a list of tensors");
+        const float max_norm = real(a[1]), scale = real(a[2]);
+        const at::Device device = norm_device(g);
+        std::vector<Tensor> made;
+        std::vector<void *> out;
+        out.reserve(g.count());
+        if (a[3] != Py_None) {
+            o.read(a[3], "out", "out must be a list of tensors");
+            if (o.count() != g.count()) refuse(PyExc_ValueError, "out must have as many tensors as the gradients");
+            for (int64_t i = 0; i < g.count(); ++i) {
+                const Tensor &x = g.at(i), &y = o.at(i);
+                bool same = x.scalar_type() == y.scalar_type() && x.sizes() == y.sizes() && x.device() == y.device();
+                for (int64_t k = 0; same && k < x.dim(); ++k) same = x.size(k) < 2 || x.stride(k) == y.stride(k);
+                if (!same) refuse(PyExc_ValueError, "out[%lld] must have its gradient's dtype, shape, strides and device, got %s and %s",
+                                  static_cast<long long>(i), text(y).c_str(), text(x).c_str());
+                out.push_back(y.data_ptr());
+            }
+        }
+        Tensor norm;
+        int rc;
+        {
+            WithoutGil released;
+            const c10::cuda::CUDAGuard guard(device);
+            if (out.empty()) {
+                made.reserve(g.count());
+                for (int64_t i = 0; i < g.count(); ++i) {
+                    made.push_back(at::empty_like(g.at(i)));
+                    out.push_back(made.back().data_ptr());
+                }
+            }
+            const Tensor ws = norm_workspace(g, device);
+            norm = make({}, at::kFloat, device);
+            rc = gsort_clip_gradients(g.data.data(), out.data(), g.sizes.data(), g.codes.data(), g.count(), max_norm, scale, floats(norm),
+                                      ws.data_ptr(), ws.nbytes(), stream_of(device));
+        }
+        if (rc != GSORT_OK) return PyLong_FromLong(rc);
+        PyObject *list = PyList_New(static_cast<Py_ssize_t>(g.count()));
+        if (list == nullptr) return nullptr;
+        for (int64_t i = 0; i < g.count(); ++i) {
+            PyObject *item = made.empty() ? PySequence_Fast_GET_ITEM(o.fast, i) : wrap(made[i]);
+            if (made.empty()) Py_INCREF(item);
+            if (item == nullptr) {
+                Py_DECREF(list);
+                return nullptr;
+            }
+            PyList_SET_ITEM(list, i, item);
+        }
+        PyObject *last = wrap(norm);
+        PyObject *both = last ? PyTuple_Pack(2, list, last) : nullptr;
+        Py_XDECREF(last);
+        Py_DECREF(list);
+        return both;
+    });
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(route_experts),   METHOD(route_experts_backward), METHOD(group_by_expert),
                          METHOD(dispatch_rows),   METHOD(combine_rows),           METHOD(combine_rows_backward),
-                         METHOD(token_logprobs),  METHOD(token_logprobs_backward), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(token_logprobs),  METHOD(token_logprobs_backward), METHOD(embed_tokens),
+                         METHOD(embed_tokens_backward), METHOD(adjust_logits),     METHOD(adjust_logits_backward),
+                         METHOD(gradient_norm),   METHOD(clip_gradients),          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,548 @@
+// embed.cu -- rows of an embedding table by token, and the table's gradient.
+//
+//   lookup     out[t] = scale * table[tokens[t]], zeros for a token that is not
+//              in 0 .. vocab - 1
+//   gradient   d_table[v] = scale * sum over t with tokens[t] = v of d_out[t],
+//              zeros for a token that does not occur; or, accumulated,
+//              d_table[v] += scale * sum, other rows left as they are
+//
+// The gradient sorts the positions by token (stable, so that the order of every
+// sum is given by the input) and sums runs of equal tokens.  The sorted positions
+// are cut into equal pieces whatever the tokens are: frequent tokens make long
+// runs (in a text one of 65536 positions in ten may hold the same token), rare
+// ones a run of one position, and a piece costs the same either way.  Within a
+// piece a group of lanes walks its positions with several rows' loads in flight;
+// runs that cross its ends leave partial sums, which are joined in shared memory
+// within a CTA and through the workspace between CTAs, always in the order of the
+// positions.  Every row of d_out is read once and every row of d_table written
+// once, so the memory bounds it.  Sums are 32-bit, rounded once.
+#include <algorithm>
+
+#include "row_access.cuh"
+
+namespace gsort {
+namespace {
+
+constexpr uint32_t kNoKey = 0xFFFFFFFFu;
+constexpr int kEmbedThreads = kRowThreads;
+constexpr int kMinLogLanes = 3, kMaxLogLanes = 5;   // lanes side by side on a row
+constexpr uint32_t kMaxUnits = kEmbedThreads >> kMinLogLanes;
+constexpr uint32_t kMaxPer = 32;                    // positions of a group of lanes
+constexpr uint32_t kFillCtas = 608;                 // CTAs that keep a GB300 busy: 4 to an SM
+
+// Rows in flight per thread; a shifted one takes two vectors of registers.
+template <int MODE> constexpr int kLoads = MODE == kShifted ? 4 : 8;
+
+__device__ __forceinline__ int64_t token_at(const void *tokens, int bytes, int64_t i) {
+    return bytes == 8 ? static_cast<const int64_t *>(tokens)[i] : static_cast<const int32_t *>(tokens)[i];
+}
+
+// A token as a sort key: what is no token comes last.
+__device__ __forceinline__ uint32_t token_key(int64_t token, uint32_t vocab) {
+    return static_cast<uint64_t>(token) < vocab ? static_cast<uint32_t>(token) : vocab;
+}
+
+// ------------------------------------------------------------------ lookup
+template <typename T> struct EmbedArgs {
+    const T *table;
+    const uint4 *safe;       // 32 bytes that can be read in place of others
+    T *out;
+    const void *tokens;
+    int64_t row_stride;
+    float scale;
+    int token_bytes;
+    uint32_t n, vocab, width, vectors, log_lanes, chunks;
+};
+
+template <typename T, int MODE, bool SCALED, int U>
+__global__ void __launch_bounds__(kEmbedThreads) k_embed(const EmbedArgs<T> a) {
+    constexpr int N = Wide<T>::kCount;
+    const uint32_t lanes = 1u << a.log_lanes;
+    const uint32_t group = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
+    const uint32_t t = group * (kEmbedThreads >> a.log_lanes) + (threadIdx.x >> a.log_lanes);
+    if (t >= a.n) return;
+    const uint32_t v0 = chunk * lanes * U + (threadIdx.x & (lanes - 1));
+    const uint32_t key = token_key(token_at(a.tokens, a.token_bytes, t), a.vocab);
+    const bool there = key < a.vocab;
+    const uint32_t k = there ? key : 0;
+    const InRow<T> in{a.table + static_cast<int64_t>(k) * a.row_stride, k > 0 && k + 1 < a.vocab};
+    const OutRow<T, MODE> out(a.out + static_cast<int64_t>(t) * a.width);
+    Loaded x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)     // no branch around the loads
+        x[u] = start_read<T, MODE>(in, out.at(min(v0 + u * lanes, a.vectors - 1)), a.width, a.safe);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t v = v0 + u * lanes;
+        if (v >= a.vectors) continue;
+        const int32_t e = out.at(v);
+        uint4 q = end_read<T, MODE>(x[u], in, e, a.width);
+        if (!there) {
+            q = make_uint4(0, 0, 0, 0);
+        } else if (SCALED) {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, mul2(pair(a.scale, a.scale), Wide<T>::pair_of(q, i)));
+        }
+        out.write(e, a.width, q);
+    }
+}
+
+// ------------------------------------------------------------ order by token
+// Every token as a key, with its position.
+__global__ void __launch_bounds__(256) k_token_keys(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys,
+                                                    uint32_t *positions) {
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    keys[i] = token_key(token_at(tokens, bytes, i), vocab);
+    positions[i] = i;
+}
+
+// Few tokens are sorted by counting: a token's place is the number of tokens that
+// are smaller, or equal and before it.  A lane holds a token, a warp compares
+// its 32 tokens with an eighth of all (a broadcast from shared memory each).
+constexpr uint32_t kRankMax = 8192;
+
+__global__ void __launch_bounds__(256) k_token_rank(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys,
+                                                    uint32_t *order) {
+    extern __shared__ __align__(16) uint32_t s_keys[];   // n rounded up to 32
+    __shared__ uint32_t s_rank[8][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = (n + 31) / 32;
+    for (uint32_t i = threadIdx.x; i < groups * 32; i += 256)
+        s_keys[i] = i < n ? token_key(token_at(tokens, bytes, i), vocab) : kNoKey;   // behind every token
+    __syncthreads();
+    const uint32_t i = blockIdx.x * 32 + lane, mine = s_keys[i];
+    uint32_t rank = 0;
+    for (uint32_t g = warp; g < groups; g += 8) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(s_keys + g * 32);
+        if (g < blockIdx.x) {              // equal ones are before
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint4 k = q[j];
+                rank += (k.x <= mine) + (k.y <= mine) + (k.z <= mine) + (k.w <= mine);
+            }
+        } else if (g > blockIdx.x) {       // equal ones are behind
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint4 k = q[j];
+                rank += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+            }
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 32; ++j) {
+                const uint32_t k = s_keys[g * 32 + j];
+                rank += k < mine || (k == mine && j < lane);
+            }
+        }
+    }
+    s_rank[warp][lane] = rank;
+    __syncthreads();
+    if (warp == 0 && i < n) {
+        rank = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) rank += s_rank[w][lane];
+        keys[rank] = mine;
+        order[rank] = i;
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+template <typename T> struct EmbedSumArgs {
+    const T *d;
+    const uint4 *safe;
+    T *out;
+    const uint32_t *keys, *order;    // sorted
+    const uint32_t *status;          // of the sort; null: it cannot fail
+    float *partials;                 // [chunks][2][slabs * lanes][N]: sums up to a chunk's end and from its start
+    int64_t d_stride, out_stride;
+    float scale;
+    bool accumulate;
+    uint32_t n, vocab, width, vectors;
+    uint32_t log_lanes, slabs;       // 2^log_lanes lanes hold a vector each; slabs of them make a row
+    uint32_t per;                    // positions of a group of lanes
+    uint32_t chunks;                 // of (256 >> log_lanes) * per positions
+    uint32_t fill_blocks, fill_rows; // CTAs that write zeros; rows that a warp of them looks over
+};
+
+template <typename T, int MODE> struct RowSum {
+    static constexpr int N = Wide<T>::kCount;
+    Pair p[N / 2];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) p[i] = pair(0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void add(const uint4 &q) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) p[i] = add2(p[i], Wide<T>::pair_of(q, i));
+    }
+    __device__ __forceinline__ void add(const float *f) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 x = reinterpret_cast<const float4 *>(f)[i];
+            p[2 * i] = add2(p[2 * i], pair(x.x, x.y));
+            p[2 * i + 1] = add2(p[2 * i + 1], pair(x.z, x.w));
+        }
+    }
+    __device__ __forceinline__ void store(float *f) const {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            reinterpret_cast<float4 *>(f)[i] = make_float4(p[2 * i].f.x, p[2 * i].f.y, p[2 * i + 1].f.x, p[2 * i + 1].f.y);
+    }
+    // The run's sum to its row of the table.
+    __device__ __forceinline__ void write(const EmbedSumArgs<T> &a, uint32_t key, uint32_t v, float scale) const {
+        const OutRow<T, MODE> out(a.out + static_cast<int64_t>(key) * a.out_stride);
+        const int32_t e = out.at(v);
+        uint4 q;
+        if (a.accumulate) {
+            if (MODE != kSingle && out.whole(e, a.width)) {
+                q = *reinterpret_cast<const uint4 *>(out.row + e);
+            } else {
+                float f[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    f[i] = static_cast<uint32_t>(e + i * kStep<MODE>) < a.width ? to_f32(out.row[e + i * kStep<MODE>]) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, pair(f[2 * i], f[2 * i + 1]));
+            }
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, fma2(p[i], pair(scale, scale), Wide<T>::pair_of(q, i)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, mul2(p[i], pair(scale, scale)));
+        }
+        out.write(e, a.width, q);
+    }
+};
+
+// Rows of the table whose token does not occur are zero: a lane looks one token
+// up in the sorted ones, a warp writes the rows that its lanes have found.
+template <typename T, int MODE> __device__ __forceinline__ void fill_absent(const EmbedSumArgs<T> &a, bool failed) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t base = (blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5)) * a.fill_rows, r = base + lane;
+    bool absent = false;
+    if (lane < a.fill_rows && r < a.vocab) {
+        uint32_t low = 0, high = a.n;      // the first key that is not below r
+        while (low < high) {
+            const uint32_t mid = low + (high - low) / 2;
+            if (a.keys[mid] < r) low = mid + 1;
+            else high = mid;
+        }
+        absent = failed || low >= a.n || a.keys[low] != r;
+    }
+    uint32_t q = 0;
+    if (failed) q = sizeof(T) == 4 ? 0x7FC00000u : 0x7FFF7FFFu;     // NaN
+    for (uint32_t rows = __ballot_sync(kFullMask, absent); rows; rows &= rows - 1) {
+        const OutRow<T, MODE> o(a.out + static_cast<int64_t>(base + (__ffs(rows) - 1)) * a.out_stride);
+        for (uint32_t v = lane; v < a.vectors; v += 32) o.write(o.at(v), a.width, make_uint4(q, q, q, q));
+    }
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kEmbedThreads) k_embed_sum(const EmbedSumArgs<T> a) {
+    constexpr int N = Wide<T>::kCount, U = kLoads<MODE>;
+    const bool failed = a.status != nullptr && *a.status != 0;     // of the sort: its results are void
+    if (blockIdx.x < a.fill_blocks) {
+        fill_absent<T, MODE>(a, failed);
+        return;
+    }
+    if (failed && !a.accumulate) return;
+    const float scale = failed ? __uint_as_float(0x7FC00000u) : a.scale;
+    __shared__ uint32_t s_key[kMaxUnits * kMaxPer + 2], s_order[kMaxUnits * kMaxPer];   // s_key[0]: the key before the chunk
+    __shared__ __align__(16) float s_head[kEmbedThreads][N];
+    const uint32_t block = blockIdx.x - a.fill_blocks, chunk = block / a.slabs, slab = block % a.slabs;
+    const uint32_t lanes = 1u << a.log_lanes, units = kEmbedThreads >> a.log_lanes, size = units * a.per;
+    const uint32_t base = chunk * size, count = min(size, a.n - base), tid = threadIdx.x;
+    for (uint32_t i = tid; i < count + 2; i += kEmbedThreads) {
+        const uint32_t p = base + i - 1;
+        s_key[i] = p < a.n ? a.keys[p] : kNoKey;
+    }
+    for (uint32_t i = tid; i < count; i += kEmbedThreads) s_order[i] = a.order[base + i];
+    __syncthreads();
+    const uint32_t unit = tid >> a.log_lanes, v = slab * lanes + (tid & (lanes - 1)), vv = min(v, a.vectors - 1);
+    const uint32_t begin = unit * a.per, end = min(begin + a.per, count);
+    const bool any = begin < end && s_key[begin + 1] < a.vocab;
+    uint32_t key = any ? s_key[begin + 1] : kNoKey;
+    const bool head = any && s_key[begin] == key;      // the run began before this unit
+    bool first = head;
+    RowSum<T, MODE> sum;
+    sum.clear();
+    if (any) {
+        for (uint32_t p0 = begin; p0 < end; p0 += U) {
+            Loaded x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t p = min(p0 + u, end - 1), k = s_key[p + 1], o = s_order[p];
+                const uint32_t row = o < a.n ? o : 0;
+                const OutRow<T, MODE> out(a.out + static_cast<int64_t>(k < a.vocab ? k : 0) * a.out_stride);
+                x[u] = start_read<T, MODE>(InRow<T>{a.d + static_cast<int64_t>(row) * a.d_stride, row > 0 && row + 1 < a.n}, out.at(vv),
+                                           a.width, a.safe);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint32_t p = p0 + u;
+                if (p >= end) continue;
+                const uint32_t k = s_key[p + 1], o = s_order[p];
+                if (k != key) {
+                    if (key < a.vocab) {
+                        if (first) sum.store(s_head[tid]);
+                        else if (v < a.vectors) sum.write(a, key, v, scale);
+                    }
+                    first = false;
+                    key = k;
+                    sum.clear();
+                }
+                if (k >= a.vocab) continue;
+                const uint32_t row = o < a.n ? o : 0;
+                const OutRow<T, MODE> out(a.out + static_cast<int64_t>(k) * a.out_stride);
+                sum.add(end_read<T, MODE>(x[u], InRow<T>{a.d + static_cast<int64_t>(row) * a.d_stride, row > 0 && row + 1 < a.n}, out.at(vv),
+                                          a.width));
+            }
+        }
+        if (key >= a.vocab) key = kNoKey;
+        if (key != kNoKey && first) sum.store(s_head[tid]);    // the whole unit is a part of one run
+    }
+    __syncthreads();
+    if (!any) return;
+    // Runs that go on behind the unit they began in: that unit joins their parts.
+    // The chunk's first unit does so for a run that began before the chunk.
+    const bool onward = key != kNoKey && s_key[end + 1] == key;
+    uint32_t i;
+    if (unit == 0 && head) {
+        const uint32_t k0 = s_key[1];
+        RowSum<T, MODE> part;
+        part.clear();
+        part.add(s_head[tid]);
+        if (first && onward) {             // the run covers this unit
+            for (i = 1; i < units && i * a.per < count && s_key[i * a.per + 1] == k0; ++i) {
+                part.add(s_head[(i << a.log_lanes) + (tid & (lanes - 1))]);
+                if (s_key[min((i + 1) * a.per, count)] != k0) break;
+            }
+        }
+        part.store(a.partials + ((static_cast<size_t>(chunk) * 2 + 1) * a.slabs * lanes + v) * N);
+    }
+    if (key == kNoKey || first) return;    // nothing that began here goes on
+    if (onward) {
+        bool leaves = true;                // the chunk
+        for (i = unit + 1; i < units && i * a.per < count; ++i) {
+            sum.add(s_head[(i << a.log_lanes) + (tid & (lanes - 1))]);
+            const uint32_t stop = min((i + 1) * a.per, count);
+            if (s_key[stop] != key || s_key[stop + 1] != key) {
+                leaves = false;
+                break;
+            }
+        }
+        if (leaves) {
+            sum.store(a.partials + (static_cast<size_t>(chunk) * 2 * a.slabs * lanes + v) * N);
+            return;
+        }
+    }
+    if (v < a.vectors) sum.write(a, key, v, scale);
+}
+
+// Joins the runs that cross ends of chunks: the CTA of the chunk in which a run
+// began adds the parts of those behind it, each group of lanes some of them.
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kEmbedThreads) k_embed_join(const EmbedSumArgs<T> a) {
+    constexpr int N = Wide<T>::kCount;
+    const uint32_t chunk = blockIdx.x / a.slabs, slab = blockIdx.x % a.slabs;
+    const uint32_t lanes = 1u << a.log_lanes, units = kEmbedThreads >> a.log_lanes, size = units * a.per;
+    const uint32_t base = chunk * size, end = base + size;
+    if (end >= a.n) return;
+    const uint32_t key = a.keys[end - 1];
+    if (key >= a.vocab || a.keys[end] != key || (base > 0 && a.keys[base - 1] == key && a.keys[base] == key)) return;
+    const bool failed = a.status != nullptr && *a.status != 0;
+    if (failed && !a.accumulate) return;
+    uint32_t low = end, high = a.n;        // the first key above this one
+    while (low < high) {
+        const uint32_t mid = low + (high - low) / 2;
+        if (a.keys[mid] <= key) low = mid + 1;
+        else high = mid;
+    }
+    const uint32_t last = (low - 1) / size;             // the chunk that the run ends in
+    __shared__ __align__(16) float s_part[kEmbedThreads][N];
+    const uint32_t tid = threadIdx.x, unit = tid >> a.log_lanes, v = slab * lanes + (tid & (lanes - 1));
+    const size_t row = static_cast<size_t>(a.slabs) * lanes * N;
+    RowSum<T, MODE> sum;
+    sum.clear();
+    if (unit == 0) sum.add(a.partials + static_cast<size_t>(chunk) * 2 * row + static_cast<size_t>(v) * N);
+#pragma unroll 4
+    for (uint32_t c = chunk + 1 + unit; c <= last; c += units) sum.add(a.partials + (static_cast<size_t>(c) * 2 + 1) * row + static_cast<size_t>(v) * N);
+    if (last - chunk > 1) {
+        sum.store(s_part[tid]);
+        __syncthreads();
+        if (unit != 0) return;
+        for (uint32_t i = 1; i < min(units, last - chunk); ++i) sum.add(s_part[(i << a.log_lanes) + tid]);
+    } else if (unit != 0) {
+        return;
+    }
+    if (v < a.vectors) sum.write(a, key, v, failed ? __uint_as_float(0x7FC00000u) : a.scale);
+}
+
+// ------------------------------------------------------------------- plans
+// How the gradient's work is cut: by sizes alone, so that the order of every sum
+// depends on nothing else.
+struct EmbedPlan {
+    uint32_t vectors_max, log_lanes, slabs, per, chunks;
+    size_t keys, order, keys_in, order_in, radix, partials, total;
+};
+
+EmbedPlan embed_plan(uint32_t n, uint32_t width, int size) {
+    EmbedPlan p{};
+    const uint32_t count = 16 / size;
+    // a row touches so many vectors at most, however it lies
+    p.vectors_max = size == 4 ? (width + 127) / 128 * 32 : (width + 2 * (count - 1)) / count;
+    p.log_lanes = kMinLogLanes;
+    while (p.log_lanes < kMaxLogLanes && (1u << p.log_lanes) < p.vectors_max) ++p.log_lanes;
+    const uint32_t lanes = 1u << p.log_lanes, units = kEmbedThreads / lanes;
+    p.slabs = (p.vectors_max + lanes - 1) / lanes;
+    // longer pieces leave fewer partial sums, shorter ones fill the device
+    p.per = kMaxPer;
+    while (p.per > 8 && static_cast<uint64_t>((n + units * p.per - 1) / (units * p.per)) * p.slabs < kFillCtas) p.per /= 2;
+    p.chunks = (n + units * p.per - 1) / (units * p.per);
+    const size_t bytes = align_up(static_cast<size_t>(n) * 4, kWsAlign);
+    size_t at = 0;
+    if (n > kRankMax) {          // the sort's header comes first: its status is the call's
+        p.radix = at;
+        at += align_up(radix_layout(n, true, 4).total, kWsAlign);
+        p.keys_in = at;
+        at += bytes;
+        p.order_in = at;
+        at += bytes;
+    } else {
+        at += kWsAlign;          // a status that is always GSORT_OK
+    }
+    p.keys = at;
+    at += bytes;
+    p.order = at;
+    at += bytes;
+    p.partials = at;
+    if (p.chunks > 1) at += static_cast<size_t>(p.chunks) * 2 * p.slabs * lanes * (16 / size) * 4;
+    p.total = align_up(at, kWsAlign);
+    return p;
+}
+
+}  // namespace
+
+size_t embed_workspace_bytes(int64_t tokens, int64_t width, int dtype) {
+    return embed_plan(static_cast<uint32_t>(tokens), static_cast<uint32_t>(width), float_bytes(dtype)).total;
+}
+
+int launch_embed(const EmbedLaunch &L) {
+    using std::integral_constant;
+    return with_float_type(L.dtype, [&](auto t) {
+        using T = decltype(t);
+        constexpr int N = Wide<T>::kCount;
+        EmbedArgs<T> a{};
+        a.table = static_cast<const T *>(L.in);
+        a.safe = safe_in(L.in);
+        a.out = static_cast<T *>(L.out);
+        a.tokens = L.tokens;
+        a.token_bytes = L.token_bytes;
+        a.row_stride = L.in_stride;
+        a.scale = L.scale;
+        a.n = static_cast<uint32_t>(L.n);
+        a.vocab = static_cast<uint32_t>(L.vocab);
+        a.width = static_cast<uint32_t>(L.width);
+        auto start = [&](auto m) {
+            constexpr int MODE = decltype(m)::value, U = 2;
+            a.log_lanes = lanes_for(a.vectors, U);
+            const uint32_t step = U << a.log_lanes, rows = kEmbedThreads >> a.log_lanes;
+            a.chunks = (a.vectors + step - 1) / step;
+            const int64_t blocks = static_cast<int64_t>((a.n + rows - 1) / rows) * a.chunks;
+            if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
+            const dim3 grid(static_cast<uint32_t>(blocks));
+            if (L.scale == 1.0f) k_embed<T, MODE, false, U><<<grid, kEmbedThreads, 0, L.stream>>>(a);
+            else k_embed<T, MODE, true, U><<<grid, kEmbedThreads, 0, L.stream>>>(a);
+            return launch_status();
+        };
+        if (L.width % N == 0 && aligned(L.in, 16) && aligned(L.out, 16) && L.in_stride % N == 0) {
+            a.vectors = a.width / N;
+            return start(integral_constant<int, kAligned>{});
+        }
+        a.vectors = (a.width + 2 * (N - 1)) / N;
+        if (L.width * sizeof(T) >= 64) return start(integral_constant<int, kShifted>{});
+        return start(integral_constant<int, kElements>{});
+    });
+}
+
+int launch_embed_backward(const EmbedBackwardLaunch &L) {
+    using std::integral_constant;
+    const uint32_t n = static_cast<uint32_t>(L.n), vocab = static_cast<uint32_t>(L.vocab);
+    const EmbedPlan plan = embed_plan(n, static_cast<uint32_t>(L.width), float_bytes(L.dtype));
+    uint32_t *keys = reinterpret_cast<uint32_t *>(L.ws + plan.keys), *order = reinterpret_cast<uint32_t *>(L.ws + plan.order);
+    if (n > 0 && n <= kRankMax) {
+        const uint32_t groups = (n + 31) / 32;
+        k_token_rank<<<groups, 256, groups * 32 * 4, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys, order);
+        if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
+    } else if (n > 0) {
+        uint32_t *keys_in = reinterpret_cast<uint32_t *>(L.ws + plan.keys_in);
+        uint32_t *order_in = reinterpret_cast<uint32_t *>(L.ws + plan.order_in);
+        k_token_keys<<<(n + 255) / 256, 256, 0, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys_in, order_in);
+        if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
+        RadixLaunch R{};
+        R.keys_in = keys_in;
+        R.keys_out = keys;
+        R.vals_in = order_in;
+        R.vals_out = order;
+        R.n = n;
+        R.kind = GSORT_KEY_U32;
+        R.end_bit = 32 - __builtin_clz(vocab);       // what is no token has the key `vocab`
+        R.ws = L.ws + plan.radix;
+        R.spin_limit = kDefaultSpinLimit;
+        R.stall_tile = kNoStall;
+        R.stream = L.stream;
+        R.sm_count = L.sm_count;
+        const int rc = launch_radix(R);
+        if (rc != GSORT_OK) return rc;
+    }
+    return with_float_type(L.dtype, [&](auto t) {
+        using T = decltype(t);
+        constexpr int N = Wide<T>::kCount;
+        EmbedSumArgs<T> a{};
+        a.d = static_cast<const T *>(L.d_out);
+        a.safe = safe_in(L.d_out);
+        a.out = static_cast<T *>(L.d_table);
+        a.keys = keys;
+        a.order = order;
+        a.status = n > kRankMax ? reinterpret_cast<const uint32_t *>(L.ws + plan.radix + kHdrStatus) : nullptr;
+        a.partials = reinterpret_cast<float *>(L.ws + plan.partials);
+        a.d_stride = L.d_stride;
+        a.out_stride = L.table_stride;
+        a.scale = L.scale;
+        a.accumulate = L.accumulate;
+        a.n = n;
+        a.vocab = vocab;
+        a.width = static_cast<uint32_t>(L.width);
+        a.log_lanes = plan.log_lanes;
+        a.slabs = plan.slabs;
+        a.per = plan.per;
+        a.chunks = plan.chunks;
+        if (!L.accumulate) {
+            a.fill_rows = std::min(32u, std::max(1u, vocab / 4096));
+            const uint32_t rows = a.fill_rows * (kEmbedThreads / 32);
+            a.fill_blocks = (vocab + rows - 1) / rows;
+        }
+        auto start = [&](auto m) {
+            constexpr int MODE = decltype(m)::value;
+            const int64_t blocks = static_cast<int64_t>(a.chunks) * a.slabs + a.fill_blocks;
+            if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
+            if (blocks == 0) return static_cast<int>(GSORT_OK);
+            k_embed_sum<T, MODE><<<static_cast<uint32_t>(blocks), kEmbedThreads, 0, L.stream>>>(a);
+            if (a.chunks > 1) k_embed_join<T, MODE><<<(a.chunks - 1) * a.slabs, kEmbedThreads, 0, L.stream>>>(a);
+            return launch_status();
+        };
+        if (L.width % N == 0 && aligned(L.d_out, 16) && aligned(L.d_table, 16) && L.d_stride % N == 0 && L.table_stride % N == 0) {
+            a.vectors = a.width / N;
+            return start(integral_constant<int, kAligned>{});
+        }
+        a.vectors = plan.vectors_max;
+        if constexpr (sizeof(T) == 4) {
+            return start(integral_constant<int, kSingle>{});
+        } else {
+            if (L.width * sizeof(T) >= 64) return start(integral_constant<int, kShifted>{});
+            return start(integral_constant<int, kElements>{});
+        }
+    });
+}
+
+}  // namespace gsort

@@ -1,5 +1,6 @@
 // Shared pieces of the language-model operators (expert routing, grouping,
-// row movement, token log probabilities): element types, 16-byte vectors,
+// row movement, token log probabilities, embedding, adjusted logits, gradient
+// norm): element types, 16-byte vectors,
 // order keys and the launch descriptions.
 #pragma once
 
@@ -256,6 +257,73 @@ struct LogprobsBackwardLaunch {
     cudaStream_t stream;
 };
 int launch_logprobs_backward(const LogprobsBackwardLaunch &L);
+
+struct EmbedLaunch {
+    const void *in;          // the table
+    int dtype;
+    int64_t vocab, width, in_stride;
+    const void *tokens;
+    int token_bytes;         // 4 or 8
+    int64_t n;
+    float scale;
+    void *out;               // [n][width], contiguous
+    cudaStream_t stream;
+};
+int launch_embed(const EmbedLaunch &L);
+
+struct EmbedBackwardLaunch {
+    const void *d_out;
+    int dtype;
+    int64_t n, width, d_stride;
+    const void *tokens;
+    int token_bytes;
+    int64_t vocab;
+    float scale;
+    bool accumulate;
+    void *d_table;
+    int64_t table_stride;
+    unsigned char *ws;
+    cudaStream_t stream;
+    int sm_count;
+};
+size_t embed_workspace_bytes(int64_t tokens, int64_t width, int dtype);
+int launch_embed_backward(const EmbedBackwardLaunch &L);
+
+struct AdjustLaunch {
+    bool backward;
+    const void *logits;      // read by the gradient, where a history is given
+    const void *in;
+    void *out;
+    int dtype;
+    int64_t rows, vocab, logits_stride, in_stride, out_stride;
+    const void *history;     // null: none
+    int64_t history_stride, length;
+    int history_bytes;
+    const int32_t *prompt;   // each null: none
+    const float *repetition, *presence, *frequency;
+    const void *bias_tokens;
+    const float *bias;
+    int64_t bias_stride, biases;
+    int bias_bytes;
+    const uint32_t *allowed; // null: none
+    int64_t allowed_stride;
+    cudaStream_t stream;
+};
+int launch_adjust(const AdjustLaunch &L);
+
+struct NormLaunch {
+    const void *const *in;
+    void *const *out;        // null: the norm alone
+    const int64_t *sizes;
+    const int *dtypes;
+    int64_t tensors;
+    float scale, max_norm;
+    float *norm;
+    unsigned char *ws;
+    cudaStream_t stream;
+};
+size_t norm_workspace_bytes(int64_t tensors);
+int launch_norm(const NormLaunch &L);
 
 // Calls f with a value of the element type that `dtype` names.
 template <typename F> int with_float_type(int dtype, F &&f) {

@@ -1,6 +1,7 @@
 """The library's language-model operators on torch tensors: routing to experts,
-grouping by expert, moving rows to the experts and back, and log probabilities
-of given tokens, with their gradients.
+grouping by expert, moving rows to the experts and back, log probabilities
+of given tokens, embedding lookup and adjusted logits, with their gradients; and
+the norm of many gradients, with clipping.
 
 Every call takes CUDA tensors (there is no CPU fallback), runs on the current
 stream of their device without synchronising, and returns newly allocated
@@ -60,6 +61,12 @@ class TokenLogprobs(NamedTuple):
     stats: torch.Tensor
 
 
+class ClippedGradients(NamedTuple):
+    """gradients: the clipped tensors, a list; norm: float32 scalar tensor, their norm before."""
+    gradients: list[torch.Tensor]
+    norm: torch.Tensor
+
+
 def _checked(result, name: str):
     """A call's tensors; an int in their place is the status of a refusal."""
     if result.__class__ is int:
@@ -69,6 +76,11 @@ def _checked(result, name: str):
 
 def _wants_grad(t) -> bool:
     return getattr(t, "requires_grad", False) and torch.is_grad_enabled()
+
+
+def _written(*tensors):
+    """Tensors that a call has written: autograd refuses what it had saved of them."""
+    increment_version([t for t in tensors if not t.is_inference()])
 
 
 # ----------------------------------------------------------------- routing
@@ -237,6 +249,142 @@ def token_logprobs_backward(d_logprobs: torch.Tensor | None, d_entropy: torch.Te
     lie up to 15 bytes apart where the logits' rows do not follow each other."""
     grad = _checked(_ops.token_logprobs_backward(d_logprobs, d_entropy, logits, targets, result.entropy, result.stats, out),
                     "gsort_token_logprobs_backward")
-    if out is not None and not out.is_inference():
-        increment_version(out)      # autograd refuses what it had saved of it
+    if out is not None:
+        _written(out)
     return grad
+
+
+# --------------------------------------------------------------- embedding
+class _EmbedTokens(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, tokens, scale):
+        ctx.save_for_backward(tokens)
+        ctx.vocab, ctx.scale = table.shape[0], scale
+        return embed_tokens(table, tokens, scale=scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        tokens, = ctx.saved_tensors
+        return embed_tokens_backward(d_out.contiguous(), tokens, ctx.vocab, scale=ctx.scale), None, None
+
+
+def embed_tokens(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0) -> torch.Tensor:
+    """scale * table[tokens] for a table [vocab, width] and int32 or int64 tokens
+    of any shape, contiguous; [*tokens.shape, width] of the table's dtype.  A token
+    that is not in 0..vocab-1 has a row of zeros and no gradient.  The table's
+    gradient is dense."""
+    if _wants_grad(table):
+        return _EmbedTokens.apply(table, tokens, scale)
+    return _checked(_ops.embed_tokens(table, tokens, scale), "gsort_embed_tokens")
+
+
+def embed_workspace_bytes(tokens: int, width: int, dtype: torch.dtype) -> int:
+    """Workspace of embed_tokens_backward for so many tokens."""
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
+    return int(_lib.load().gsort_embed_tokens_backward_workspace_bytes(tokens, width, code))
+
+
+def embed_tokens_backward(d_out: torch.Tensor, tokens: torch.Tensor, vocab: int, *, scale: float = 1.0,
+                          out: torch.Tensor | None = None, accumulate: bool = False,
+                          workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of embed_tokens by its table of `vocab` rows, for d_out
+    [*tokens.shape, width] (contiguous; with tokens of one dimension its rows may
+    be strided): each token's rows summed in 32 bits in their order, times scale.
+    Rows of tokens that do not occur are zero.  With accumulate the sums are added
+    to `out` [vocab, width], whose other rows stay as they are."""
+    grad = _checked(_ops.embed_tokens_backward(d_out, tokens, vocab, scale, out, accumulate, workspace),
+                    "gsort_embed_tokens_backward")
+    if out is not None:
+        _written(out)
+    return grad
+
+
+# --------------------------------------------------------- adjusted logits
+class _AdjustLogits(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, history, prompt, repetition, presence, frequency, bias_tokens, bias, allowed):
+        signs = repetition is not None      # what the gradient asks of logits and history
+        ctx.save_for_backward(logits if signs else None, history if signs else None, repetition, allowed)
+        return adjust_logits(logits, history=history, prompt=prompt, repetition=repetition, presence=presence,
+                             frequency=frequency, bias_tokens=bias_tokens, bias=bias, allowed=allowed)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        logits, history, repetition, allowed = ctx.saved_tensors
+        d_logits = adjust_logits_backward(d_out.contiguous(), logits, history=history, repetition=repetition, allowed=allowed)
+        return d_logits, *[None] * 8
+
+
+def adjust_logits(logits: torch.Tensor, *, history: torch.Tensor | None = None, prompt: torch.Tensor | None = None,
+                  repetition: torch.Tensor | None = None, presence: torch.Tensor | None = None,
+                  frequency: torch.Tensor | None = None, bias_tokens: torch.Tensor | None = None,
+                  bias: torch.Tensor | None = None, allowed: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Logits [rows, vocab] with penalties, biases and a mask, in this order:
+
+    history [rows, length] int32 or int64 holds the tokens before (entries outside
+    the vocabulary are padding), the first prompt [rows] int32 of them given, the
+    others generated.  A token of the history has its logit divided by repetition
+    [rows] float32 where it is positive and multiplied where not; a token
+    generated c > 0 times loses frequency * c + presence ([rows] float32 each).
+    bias [rows, entries] float32 is added to the tokens bias_tokens names (int32
+    or int64, of the same shape; of several entries for a token the last one holds, entries
+    outside the vocabulary are padding).  allowed [rows, ceil(vocab / 32)] int32
+    has bit v % 32 of word v // 32 set where token v may follow; the others become
+    -inf, which token_logprobs takes as masked.
+
+    history, biases and allowed may be expanded from one row.  `out` may be the
+    logits themselves, which are then written only where they change; it takes
+    part in no gradient.  The result has a gradient by the logits; the adjustments
+    have none.  Without `out`, result rows lie up to 15 bytes apart where the
+    logits' rows do not follow each other."""
+    if any(_wants_grad(t) for t in (repetition, presence, frequency, bias)):
+        raise RuntimeError("penalties and biases have no gradient: detach them")
+    if _wants_grad(logits):
+        if out is not None:
+            raise RuntimeError("adjust_logits with out takes part in no gradient: call it under torch.no_grad()")
+        return _AdjustLogits.apply(logits, history, prompt, repetition, presence, frequency, bias_tokens, bias, allowed)
+    adjusted = _checked(_ops.adjust_logits(logits, history, prompt, repetition, presence, frequency, bias_tokens, bias, allowed, out),
+                        "gsort_adjust_logits")
+    if out is not None:
+        _written(out)
+    return adjusted
+
+
+def adjust_logits_backward(d_out: torch.Tensor, logits: torch.Tensor | None, *, history: torch.Tensor | None = None,
+                           repetition: torch.Tensor | None = None, allowed: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of adjust_logits by its logits, from that by its result.  `out`
+    may be d_out itself.  The logits are needed with a repetition only, for
+    their signs."""
+    grad = _checked(_ops.adjust_logits_backward(d_out, logits, history, repetition, allowed, out),
+                    "gsort_adjust_logits_backward")
+    if out is not None:
+        _written(out)
+    return grad
+
+
+# ----------------------------------------------------------- gradient norm
+def gradient_norm(gradients) -> torch.Tensor:
+    """Euclidean norm of all elements of a list of tensors (dense, of one device,
+    any mix of float32, bfloat16 and float16); a float32 scalar tensor.  It takes
+    part in no gradient: tensors that require one raise RuntimeError where
+    gradients are recorded."""
+    return _checked(_ops.gradient_norm(gradients), "gsort_gradient_norm")
+
+
+def clip_gradients(gradients, max_norm: float, *, scale: float = 1.0, out=None) -> ClippedGradients:
+    """The gradients times scale, and times max_norm / norm where the norm of all
+    of them (times scale) is above max_norm; with that norm.  `out` is a list of
+    tensors like the gradients, or the gradients themselves (which are then not
+    written where nothing changes).  Nothing waits for the device: a norm that is
+    NaN makes every gradient NaN, an infinite one the finite gradients 0."""
+    gradients = list(gradients)
+    if out is not None:
+        out = list(out)
+    clipped = ClippedGradients(*_checked(_ops.clip_gradients(gradients, max_norm, scale, out), "gsort_clip_gradients"))
+    if out is not None:
+        _written(*out)
+    return clipped

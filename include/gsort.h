@@ -451,6 +451,92 @@ int gsort_token_logprobs_backward(const float *d_grad_logprobs, const float *d_g
                                   const float *d_entropy, const float *d_stats, void *d_grad_logits,
                                   int64_t grad_stride, cudaStream_t stream);
 
+/* Rows of an embedding table by token, and the table's gradient.  Tokens are 4-
+ * or 8-byte signed integers (token_bytes); one that is not in 0 .. vocab - 1
+ * stands for no row: its output is zero and it adds to no gradient.
+ *   embed      d_out[t] = scale * d_table[tokens[t]], contiguous
+ *   backward   d_grad_table[v] = scale * sum over t with tokens[t] = v of
+ *              d_grad_out[t], zeros for a token that does not occur; with
+ *              accumulate != 0 the sum is added to the row that is there, and
+ *              rows of tokens that do not occur are left as they are
+ * The gradient sums in 32 bits in an order that the tokens and the sizes give
+ * (results are the same from run to run) and rounds once.  With more than 8192
+ * tokens it uses the radix sort; where a wait of that gave up, gsort_check() of
+ * the workspace says so and the rows written are NaN.  The workspace may be NULL
+ * where gsort_embed_tokens_backward_workspace_bytes() is 0 (no tokens). */
+int gsort_embed_tokens(const void *d_table, int dtype, int64_t vocab, int64_t width,
+                       int64_t row_stride, const void *d_tokens, int token_bytes, int64_t tokens,
+                       float scale, void *d_out, cudaStream_t stream);
+
+size_t gsort_embed_tokens_backward_workspace_bytes(int64_t tokens, int64_t width, int dtype);
+
+int gsort_embed_tokens_backward(const void *d_grad_out, int dtype, int64_t tokens, int64_t width,
+                                int64_t grad_stride, const void *d_tokens, int token_bytes,
+                                int64_t vocab, float scale, int accumulate, void *d_grad_table,
+                                int64_t table_stride, void *d_ws, size_t ws_bytes,
+                                cudaStream_t stream);
+
+/* Logits before an answer is chosen.  Per row of `vocab` logits x, with a
+ * history of tokens (entries outside 0 .. vocab - 1 are padding), c the times
+ * that a token comes up in it behind its first d_prompt[r] entries, and "seen"
+ * where the token comes up in it at all:
+ *   y = x > 0 ? x / repetition[r] : x * repetition[r]   where seen, else x
+ *   y = y - (frequency[r] * c + presence[r])            where c > 0
+ *   y = y + bias                                        the last entry of the row's
+ *                                                       list that names the token
+ *   out = y where bit v % 32 of d_allowed[r][v / 32] is set, else -inf
+ * NULL pointers: no such step (no prompt: all of the history is generated).  A
+ * stride of 0 gives every row the same history, biases or mask.
+ * Values follow IEEE arithmetic in 32 bits, rounded once; a masked token is
+ * -inf whatever its logit was (NaN too).  d_out may be the logits themselves (same
+ * pointer and stride): rows are then read and written only where they change.
+ * The backward call takes the gradient by the adjusted logits to that by the
+ * logits: 0 where masked, else 1 / repetition or repetition times it where seen
+ * (by the sign of d_logits, which may be NULL without a history).  It reads the
+ * history, the repetition and the mask; the other fields take no part. */
+typedef struct gsort_adjustments {
+    const void *d_history;      /* [rows][length], history_stride entries apart */
+    int64_t length, history_stride;
+    int history_bytes;          /* 4 or 8 */
+    const int32_t *d_prompt;    /* [rows] */
+    const float *d_repetition, *d_presence, *d_frequency;   /* [rows] */
+    const void *d_bias_tokens;  /* [rows][biases], bias_stride entries apart */
+    const float *d_bias;        /* the same */
+    int64_t biases, bias_stride;
+    int bias_bytes;             /* of d_bias_tokens: 4 or 8 */
+    const uint32_t *d_allowed;  /* [rows][(vocab + 31) / 32], allowed_stride words apart */
+    int64_t allowed_stride;
+} gsort_adjustments;
+
+int gsort_adjust_logits(const void *d_logits, int dtype, int64_t rows, int64_t vocab,
+                        int64_t row_stride, const gsort_adjustments *how, void *d_out,
+                        int64_t out_stride, cudaStream_t stream);
+
+int gsort_adjust_logits_backward(const void *d_grad_out, int dtype, int64_t rows, int64_t vocab,
+                                 int64_t grad_stride, const void *d_logits, int64_t row_stride,
+                                 const gsort_adjustments *how, void *d_grad_logits,
+                                 int64_t grad_logits_stride, cudaStream_t stream);
+
+/* Norm of many tensors together, and clipping by it.  d_gradients, d_out,
+ * elements and dtypes are HOST arrays of `tensors` entries, read before the
+ * call returns; tensors are dense and of any mix of types.
+ *   norm           d_norm = sqrt(sum of the squares of all elements)
+ *   clip           d_norm = |scale| * that, and every element times
+ *                  scale * min(1, max_norm / norm), rounded once
+ * Squares that leave the 32-bit range are summed in 64 bits.  A NaN makes the norm
+ * and every output NaN; with an infinite one, and max_norm finite, finite elements
+ * become 0 and infinite ones NaN.  max_norm >= 0 (infinity: scaling alone).  An output may be
+ * its own input; other overlaps between outputs and inputs are refused. */
+size_t gsort_gradient_norm_workspace_bytes(int64_t tensors);
+
+int gsort_gradient_norm(const void *const *d_gradients, const int64_t *elements, const int *dtypes,
+                        int64_t tensors, float *d_norm, void *d_ws, size_t ws_bytes,
+                        cudaStream_t stream);
+
+int gsort_clip_gradients(const void *const *d_gradients, void *const *d_out, const int64_t *elements,
+                         const int *dtypes, int64_t tensors, float max_norm, float scale,
+                         float *d_norm, void *d_ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------------
  * Device-side status: synchronises `stream`, then returns GSORT_OK or the
  * error a kernel recorded in this workspace during the last call that used

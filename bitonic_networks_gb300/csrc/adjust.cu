@@ -10,12 +10,15 @@
 // and the gradient by x: 0 where the mask's bit is clear, else d * (seen ? (x > 0 ? 1 / r
 // : r) : 1).
 //
-// A CTA holds a piece of a row: counts of its tokens in shared memory, made by
-// one look over the row's whole history (which the caches hold for the row's
-// other CTAs), then one pass over its logits.  A bit for every token says
-// whether history or biases name it, so that the others cost no more than a copy.  The
-// memory bounds it: logits in, logits out.  In place, vectors in which nothing
-// changes are neither read nor written.
+// A CTA holds a piece of a row, a whole one where rows are many.  The tokens that
+// history or biases name in it are a set in shared memory: a bit for every token of
+// the piece, and the named ones before each word of bits, so that a named token has a
+// slot and the slots are no more than the history is long.  Counts are made in the slots by a
+// second look over the history.  The mask's words are laid beside the set's, so that a
+// vector's bits are all at one place.  Then the logits pass by once: a vector without a
+// bit costs a look at its bits and no more than a copy.  The memory bounds it: logits in,
+// logits out.  In place, vectors in which nothing changes are neither read nor
+// written.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -23,10 +26,13 @@
 namespace gsort {
 namespace {
 
-constexpr int kAdjustThreads = 256;
-constexpr int kAdjustVectors = 4;                 // 16-byte vectors per thread and step
-constexpr size_t kAdjustMaxSmem = 128 * 1024;     // of a CTA
+constexpr int kAdjustThreads = 512;
+constexpr int kAdjustVectors = 4;                 // 16-byte vectors in flight per thread, and as many of the next step
+constexpr int kHistoryLoads = 8;                  // tokens of the history in flight per thread
+constexpr size_t kAdjustMaxSmem = 112 * 1024;     // two CTAs to an SM
+constexpr int64_t kAdjustCtas = 304;              // that rows are cut into, where they are fewer
 constexpr uint32_t kSeenBefore = 0x80000000u;     // of a count: the token is in the prompt
+constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 
 template <typename T> struct AdjustArgs {
     const T *logits;         // the gradient's: null where no history is given
@@ -47,7 +53,8 @@ template <typename T> struct AdjustArgs {
     int bias_bytes;
     const uint32_t *allowed;
     int64_t allowed_stride;
-    uint32_t pieces, steps;  // pieces of a row, of `steps` * 1024 vectors each
+    uint32_t pieces, tokens; // pieces of a row, of so many tokens (a multiple of 256) each
+    uint32_t slots, bias_slots;      // words of the sets' slots
     bool vectors;            // rows of in and out lie the same way to 16 bytes
     bool in_place;
 };
@@ -56,162 +63,258 @@ __device__ __forceinline__ int64_t int_at(const void *p, int bytes, int64_t i) {
     return bytes == 8 ? static_cast<const int64_t *>(p)[i] : static_cast<const int32_t *>(p)[i];
 }
 
-// What a CTA knows of its piece of a row.
-struct Piece {
-    const uint32_t *named;     // a bit for every token: history or biases name it
-    const uint32_t *counts;    // null: no history
-    const uint32_t *biased;    // entry + 1 of the token's bias, 0: none; null: no biases
-    const float *bias;
-    const uint32_t *allowed;   // the row's mask; null: none
-    float repetition, presence, frequency;
-    int32_t first;             // the piece's first token (a vector may begin before the row)
-    uint32_t vocab;
+// n bits of a string of words from bit `at` on, all of one word.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t *words, uint32_t at, int n) {
+    return words[at >> 5] >> (at & 31) & ((1u << n) - 1);
+}
 
-    __device__ __forceinline__ uint32_t bits(const uint32_t *words, int32_t at, int n) const {   // n <= 8 bits from `at` on
-        const uint32_t w = static_cast<uint32_t>(at) >> 5, s = at & 31;
-        uint32_t b = words[w] >> s;
-        if (s + n > 32) b |= words[w + 1] << (32 - s);
-        return b & ((1u << n) - 1);
+// Tokens of a piece, by their distance from its first one, in shared memory.
+struct TokenSet {
+    uint32_t *bits;      // null: no set
+    uint32_t *before;    // members before each word of bits
+    uint32_t *slots;     // a word for each member
+
+    __device__ __forceinline__ bool has(uint32_t at) const { return bits != nullptr && (bits[at >> 5] >> (at & 31) & 1); }
+    __device__ __forceinline__ uint32_t &slot(uint32_t at) const {
+        return slots[before[at >> 5] + __popc(bits[at >> 5] & ((1u << (at & 31)) - 1))];
+    }
+    __device__ __forceinline__ void add(uint32_t at) const {
+        const uint32_t bit = 1u << (at & 31);
+        if (at != kNowhere && !(*const_cast<const volatile uint32_t *>(bits + (at >> 5)) & bit)) atomicOr(bits + (at >> 5), bit);
     }
 };
 
-__device__ __forceinline__ float adjusted(const Piece &p, float x, int32_t e) {
-    const uint32_t at = static_cast<uint32_t>(e - p.first);
-    if (p.counts != nullptr) {
-        const uint32_t c = p.counts[at];
-        if (c != 0) {
-            x = x > 0.0f ? x / p.repetition : x * p.repetition;
-            const uint32_t n = c & ~kSeenBefore;
-            if (n != 0) x -= fmaf(p.frequency, static_cast<float>(n), p.presence);
-        }
+// Counts the members before each word, and clears their slots.  Called by the whole CTA.
+__device__ __forceinline__ void number_members(const TokenSet &set, uint32_t words) {
+    __shared__ uint32_t s_sum[kAdjustThreads / 32];
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t per = (words + kAdjustThreads - 1) / kAdjustThreads, begin = min(tid * per, words), end = min(begin + per, words);
+    uint32_t mine = 0;
+    for (uint32_t w = begin; w < end; ++w) mine += __popc(set.bits[w]);
+    const uint32_t upto = warp_inclusive_scan(mine, lane);
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    uint32_t sum = upto - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < kAdjustThreads / 32; ++i) {
+        const uint32_t n = s_sum[i];
+        if (i < static_cast<int>(warp)) sum += n;
+        total += n;
     }
-    if (p.biased != nullptr) {
-        const uint32_t b = p.biased[at];
-        if (b != 0) x += p.bias[b - 1];
+    for (uint32_t w = begin; w < end; ++w) {
+        set.before[w] = sum;
+        sum += __popc(set.bits[w]);
     }
+    for (uint32_t i = tid; i < total; i += kAdjustThreads) set.slots[i] = 0;
+    __syncthreads();
+}
+
+// The tokens `base` + thread, + threads, ... of a list, as distances from the piece's first one.
+__device__ __forceinline__ void load_tokens(const void *list, int bytes, int64_t row, uint32_t length, uint32_t base, int64_t begin,
+                                            int64_t end, int64_t first, uint32_t (&at)[kHistoryLoads]) {
+    int64_t t[kHistoryLoads];
+#pragma unroll
+    for (int k = 0; k < kHistoryLoads; ++k) {
+        const uint32_t i = base + k * kAdjustThreads + threadIdx.x;
+        t[k] = i < length ? int_at(list, bytes, row + i) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kHistoryLoads; ++k) at[k] = t[k] >= begin && t[k] < end ? static_cast<uint32_t>(t[k] - first) : kNowhere;
+}
+
+// What a CTA knows of its piece of a row.
+struct Piece {
+    TokenSet seen, biased;
+    const float *bias;
+    uint32_t *allowed;         // bits of the piece's tokens, in shared memory; null: no mask
+    float repetition, presence, frequency;
+    int32_t first, begin, end; // the piece's first token (a vector may begin before the row), and its tokens
+};
+
+__device__ __forceinline__ float adjusted(const Piece &p, float x, uint32_t at) {
+    if (p.seen.has(at)) {
+        const uint32_t c = p.seen.slot(at), n = c & ~kSeenBefore;
+        x = x > 0.0f ? x / p.repetition : x * p.repetition;
+        if (n != 0) x -= fmaf(p.frequency, static_cast<float>(n), p.presence);
+    }
+    if (p.biased.has(at)) x += p.bias[p.biased.slot(at) - 1];
     return x;
 }
 
+// Elements whose bit is clear become -inf (or 0).
+template <typename T, bool ZERO> __device__ __forceinline__ void mask_vector(uint4 &q, uint32_t bits) {
+    uint32_t *w = &q.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t keep;
+        if (sizeof(T) == 4) keep = bits >> i & 1 ? 0xFFFFFFFFu : 0u;
+        else keep = (bits >> (2 * i) & 1) * 0xFFFFu | (bits >> (2 * i + 1) & 1) * 0xFFFF0000u;
+        w[i] = ZERO ? w[i] & keep : (w[i] & keep) | (Wide<T>::kNegInfWord & ~keep);
+    }
+}
+
 template <typename T, bool BACK>
-__global__ void __launch_bounds__(kAdjustThreads) k_adjust(const AdjustArgs<T> a) {
-    constexpr int N = Wide<T>::kCount;
+__global__ void __launch_bounds__(kAdjustThreads, 2) k_adjust(const AdjustArgs<T> a) {
+    constexpr int N = Wide<T>::kCount, U = kAdjustVectors;
+    constexpr uint32_t kAll = (1u << N) - 1;
     extern __shared__ __align__(16) uint32_t s_words[];
     const uint32_t row = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces, tid = threadIdx.x;
-    const uint32_t tokens = a.steps * (kAdjustThreads * kAdjustVectors * N);       // of a piece
     const T *in = a.in + static_cast<int64_t>(row) * a.in_stride;
     T *out = a.out + static_cast<int64_t>(row) * a.out_stride;
     // elements between the 16-byte boundary at or before the row and the row
     const int32_t shift = a.vectors ? static_cast<int32_t>((reinterpret_cast<uintptr_t>(in) & 15) / sizeof(T)) : 0;
-    const int64_t low = static_cast<int64_t>(piece) * tokens - shift;
+    const int64_t low = static_cast<int64_t>(piece) * a.tokens - shift;
     if (low >= a.vocab) return;
-    const int32_t first = static_cast<int32_t>(low);
-    const int32_t begin = max(first, 0), end = static_cast<int32_t>(min(low + tokens, static_cast<int64_t>(a.vocab)));
-    const bool history = a.history != nullptr, biases = !BACK && a.biases > 0;
+    Piece p{};
+    p.first = static_cast<int32_t>(low);
+    p.begin = max(p.first, 0);
+    p.end = static_cast<int32_t>(min(low + a.tokens, static_cast<int64_t>(a.vocab)));
+    const uint32_t vectors = (p.end - p.first + N - 1) / N;
 
-    // shared memory: a bit for each token, then counts and biases where there are any
-    uint32_t *named = s_words, *counts = named + tokens / 32, *biased = counts + (history && !BACK ? tokens : 0);
-    if (history || biases) {
-        const uint32_t words = tokens / 32 + (history && !BACK ? tokens : 0) + (biases ? tokens : 0);
-        for (uint32_t i = tid * 4; i < words; i += kAdjustThreads * 4) *reinterpret_cast<uint4 *>(s_words + i) = make_uint4(0, 0, 0, 0);
+    // the first vectors are on their way while the sets are made
+    uint4 q[U];
+    auto load = [&](uint32_t v0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t v = v0 + u * kAdjustThreads;
+            const int32_t e = p.first + static_cast<int32_t>(v * N);
+            if (v < vectors && e >= 0 && e + N <= p.end) q[u] = *reinterpret_cast<const uint4 *>(in + e);
+        }
+    };
+    const bool ahead = a.vectors && !a.in_place;
+    if (ahead) load(tid);
+
+    const uint32_t words = a.tokens / 32;
+    uint32_t *space = s_words;
+    if (a.history != nullptr) {
+        p.seen.bits = space;
+        p.seen.before = space + words;
+        p.seen.slots = space + 2 * words;
+        space += BACK ? words : 2 * words + a.slots;
+    }
+    if (!BACK && a.biases > 0) {
+        p.biased.bits = space;
+        p.biased.before = space + words;
+        p.biased.slots = space + 2 * words;
+        p.bias = a.bias + static_cast<int64_t>(row) * a.bias_stride;
+        space += 2 * words + a.bias_slots;
+    }
+    if (a.allowed != nullptr) {      // word w: the bits of the piece's tokens 32 w ..
+        const uint32_t *mask = a.allowed + static_cast<int64_t>(row) * a.allowed_stride;
+        const int32_t last = static_cast<int32_t>((a.vocab - 1) / 32);
+        p.allowed = space;
+#pragma unroll 4
+        for (uint32_t w = tid; w < words; w += kAdjustThreads) {
+            const int32_t at = p.first + static_cast<int32_t>(w * 32), k = at >> 5;      // -8 < at
+            const uint32_t here = k >= 0 && k <= last ? mask[k] : 0, next = (at & 31) != 0 && k < last ? mask[k + 1] : 0;
+            space[w] = __funnelshift_r(here, next, at & 31);
+        }
+        if (!p.seen.bits && !p.biased.bits) __syncthreads();
+    }
+    if (p.seen.bits || p.biased.bits) {
+        for (uint32_t w = tid; w < words; w += kAdjustThreads) {
+            if (p.seen.bits) p.seen.bits[w] = 0;
+            if (p.biased.bits) p.biased.bits[w] = 0;
+        }
         __syncthreads();
-        if (history) {
-            const uint32_t prompt = a.prompt ? static_cast<uint32_t>(max(a.prompt[row], 0)) : 0;
-            const int64_t base = static_cast<int64_t>(row) * a.history_stride;
-#pragma unroll 8
-            for (uint32_t i = tid; i < a.length; i += kAdjustThreads) {
-                const int64_t t = int_at(a.history, a.history_bytes, base + i);
-                if (t >= begin && t < end) {
-                    const uint32_t at = static_cast<uint32_t>(static_cast<int32_t>(t) - first);
-                    atomicOr(named + at / 32, 1u << (at & 31));
-                    if (!BACK) {
-                        if (i < prompt) atomicOr(counts + at, kSeenBefore);
-                        else atomicAdd(counts + at, 1u);
+        const int64_t history_row = static_cast<int64_t>(row) * a.history_stride, bias_row = static_cast<int64_t>(row) * a.bias_stride;
+        uint32_t at[kHistoryLoads];
+        constexpr uint32_t kStep = kAdjustThreads * kHistoryLoads;
+        if (p.seen.bits) {
+            for (uint32_t base = 0; base < a.length; base += kStep) {
+                load_tokens(a.history, a.history_bytes, history_row, a.length, base, p.begin, p.end, p.first, at);
+#pragma unroll
+                for (int k = 0; k < kHistoryLoads; ++k) p.seen.add(at[k]);
+            }
+        }
+        if (p.biased.bits) {
+            for (uint32_t i = tid; i < a.biases; i += kAdjustThreads) {
+                const int64_t t = int_at(a.bias_tokens, a.bias_bytes, bias_row + i);
+                if (t >= p.begin && t < p.end) p.biased.add(static_cast<uint32_t>(t - p.first));
+            }
+        }
+        __syncthreads();
+        if (!BACK) {
+            if (p.seen.bits) {
+                number_members(p.seen, words);
+                const uint32_t prompt = a.prompt ? static_cast<uint32_t>(max(a.prompt[row], 0)) : 0;
+                for (uint32_t base = 0; base < a.length; base += kStep) {
+                    // a history of one step is still there
+                    if (a.length > kStep) load_tokens(a.history, a.history_bytes, history_row, a.length, base, p.begin, p.end, p.first, at);
+#pragma unroll
+                    for (int k = 0; k < kHistoryLoads; ++k) {
+                        if (at[k] == kNowhere) continue;
+                        uint32_t *slot = &p.seen.slot(at[k]);
+                        if (base + k * kAdjustThreads + tid < prompt) atomicOr(slot, kSeenBefore);
+                        else atomicAdd(slot, 1u);
                     }
                 }
             }
-        }
-        if (biases) {
-            const int64_t base = static_cast<int64_t>(row) * a.bias_stride;
-            for (uint32_t i = tid; i < a.biases; i += kAdjustThreads) {
-                const int64_t t = int_at(a.bias_tokens, a.bias_bytes, base + i);
-                if (t >= begin && t < end) {
-                    const uint32_t at = static_cast<uint32_t>(static_cast<int32_t>(t) - first);
-                    atomicOr(named + at / 32, 1u << (at & 31));
-                    atomicMax(biased + at, i + 1);
+            if (p.biased.bits) {
+                number_members(p.biased, words);
+                for (uint32_t i = tid; i < a.biases; i += kAdjustThreads) {
+                    const int64_t t = int_at(a.bias_tokens, a.bias_bytes, bias_row + i);
+                    if (t >= p.begin && t < p.end) atomicMax(&p.biased.slot(static_cast<uint32_t>(t - p.first)), i + 1);
                 }
             }
+            __syncthreads();
         }
-        __syncthreads();
     }
-    Piece p;
-    p.named = history || biases ? named : nullptr;
-    p.counts = history ? counts : nullptr;
-    p.biased = biases ? biased : nullptr;
-    p.bias = biases ? a.bias + static_cast<int64_t>(row) * a.bias_stride : nullptr;
-    p.allowed = a.allowed ? a.allowed + static_cast<int64_t>(row) * a.allowed_stride : nullptr;
     p.repetition = a.repetition ? a.repetition[row] : 1.0f;
     p.presence = a.presence ? a.presence[row] : 0.0f;
     p.frequency = a.frequency ? a.frequency[row] : 0.0f;
-    p.first = first;
-    p.vocab = a.vocab;
-    const T *logits = BACK && history ? a.logits + static_cast<int64_t>(row) * a.logits_stride : nullptr;
+    const T *logits = BACK && p.seen.bits ? a.logits + static_cast<int64_t>(row) * a.logits_stride : nullptr;
 
-    auto one = [&](float x, int32_t e, bool name, bool allow) {
-        if (BACK) {
-            if (!allow) return 0.0f;
-            if (!name) return x;
-            return to_f32(logits[e]) > 0.0f ? x * (1.0f / p.repetition) : x * p.repetition;
-        }
-        return !allow ? kNegInf : name ? adjusted(p, x, e) : x;
+    // the value of a token that history or biases name
+    auto named = [&](float x, int32_t e) {
+        if (!BACK) return adjusted(p, x, static_cast<uint32_t>(e - p.first));
+        return to_f32(logits[e]) > 0.0f ? x * (1.0f / p.repetition) : x * p.repetition;
     };
     if (!a.vectors) {          // rows that lie differently: element by element
-        for (int32_t e = begin + static_cast<int32_t>(tid); e < end; e += kAdjustThreads) {
-            const bool name = p.named && p.bits(p.named, e - first, 1), allow = !p.allowed || p.bits(p.allowed, e, 1);
-            out[e] = from_f32<T>(one(to_f32(in[e]), e, name, allow));
+        for (int32_t e = p.begin + static_cast<int32_t>(tid); e < p.end; e += kAdjustThreads) {
+            const uint32_t at = static_cast<uint32_t>(e - p.first);
+            const float x = to_f32(in[e]);
+            const bool allow = !p.allowed || bits_at(p.allowed, at, 1);
+            out[e] = from_f32<T>(!allow ? (BACK ? 0.0f : kNegInf) : p.seen.has(at) || p.biased.has(at) ? named(x, e) : x);
         }
         return;
     }
-    for (uint32_t step = 0; step < a.steps; ++step) {
-        uint4 q[kAdjustVectors];
-        uint32_t name[kAdjustVectors], allow[kAdjustVectors];
-        int32_t at[kAdjustVectors];
+    for (uint32_t v0 = tid; v0 < vectors; v0 += kAdjustThreads * U) {
+        uint4 x[U];
 #pragma unroll
-        for (int u = 0; u < kAdjustVectors; ++u) {
-            const uint32_t v = (step * kAdjustVectors + u) * kAdjustThreads + tid;
-            const int32_t e = first + static_cast<int32_t>(v * N);
-            at[u] = e;
-            name[u] = 0;
-            allow[u] = (1u << N) - 1;
-            if (e < 0 || e + N > end) continue;
-            if (p.named) name[u] = p.bits(p.named, e - first, N);
-            if (p.allowed) allow[u] = p.bits(p.allowed, e, N);
-            if (a.in_place && name[u] == 0 && allow[u] == (1u << N) - 1) continue;
-            q[u] = *reinterpret_cast<const uint4 *>(in + e);
+        for (int u = 0; u < U; ++u) x[u] = q[u];
+        if (ahead) load(v0 + kAdjustThreads * U);
+        // Vectors are masked and written as a whole; the few named tokens are gathered
+        // and written after them (their code stands here once: in the unrolled part, 32
+        // times, it did not fit the instruction cache, 2048 x 131072 490 us).
+        uint32_t names = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t v = v0 + u * kAdjustThreads;
+            const int32_t e = p.first + static_cast<int32_t>(v * N);
+            if (v >= vectors) continue;
+            uint32_t name = 0, allow = kAll;
+            if (p.seen.bits) name = bits_at(p.seen.bits, v * N, N);
+            if (p.biased.bits) name |= bits_at(p.biased.bits, v * N, N);
+            if (p.allowed) allow = bits_at(p.allowed, v * N, N);
+            names |= (name & allow) << (u * N);
+            if (e < 0 || e + N > p.end) {        // the row's first and last elements
+                for (int32_t k = max(e, p.begin); k < min(e + N, p.end); ++k)
+                    out[k] = allow >> (k - e) & 1 ? in[k] : from_f32<T>(BACK ? 0.0f : kNegInf);
+                continue;
+            }
+            if (a.in_place) {
+                if (allow == kAll) continue;
+                x[u] = *reinterpret_cast<const uint4 *>(in + e);
+            }
+            if (allow != kAll) mask_vector<T, BACK>(x[u], allow);
+            *reinterpret_cast<uint4 *>(out + e) = x[u];
         }
-#pragma unroll
-        for (int u = 0; u < kAdjustVectors; ++u) {
-            const int32_t e = at[u];
-            if (e < 0 || e + N > end) {        // the row's first and last elements
-                for (int i = 0; i < N; ++i) {
-                    const int32_t k = e + i;
-                    if (k < begin || k >= end) continue;
-                    const bool n1 = p.named && p.bits(p.named, k - first, 1), a1 = !p.allowed || p.bits(p.allowed, k, 1);
-                    if (a.in_place && !n1 && a1) continue;
-                    out[k] = from_f32<T>(one(to_f32(in[k]), k, n1, a1));
-                }
-                continue;
-            }
-            if (name[u] == 0 && allow[u] == (1u << N) - 1) {
-                if (!a.in_place) *reinterpret_cast<uint4 *>(out + e) = q[u];
-                continue;
-            }
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                const Pair x = Wide<T>::pair_of(q[u], i);
-                Wide<T>::set_pair(q[u], i, pair(one(x.f.x, e + 2 * i, name[u] >> (2 * i) & 1, allow[u] >> (2 * i) & 1),
-                                                one(x.f.y, e + 2 * i + 1, name[u] >> (2 * i + 1) & 1, allow[u] >> (2 * i + 1) & 1)));
-            }
-            *reinterpret_cast<uint4 *>(out + e) = q[u];
+        while (names != 0) {
+            const uint32_t b = __ffs(names) - 1;
+            names &= names - 1;
+            const int32_t e = p.first + static_cast<int32_t>((v0 + b / N * kAdjustThreads) * N + b % N);
+            out[e] = from_f32<T>(named(to_f32(in[e]), e));     // in place, it holds its value still
         }
     }
 }
@@ -222,7 +325,7 @@ int launch_adjust(const AdjustLaunch &L) {
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int N = Wide<T>::kCount;
-        constexpr uint32_t kStep = kAdjustThreads * kAdjustVectors * N;     // tokens of a step
+        constexpr int64_t kLeast = kAdjustThreads * N;      // tokens of a piece: a vector for every thread
         AdjustArgs<T> a{};
         a.logits = static_cast<const T *>(L.logits);
         a.in = static_cast<const T *>(L.in);
@@ -251,14 +354,26 @@ int launch_adjust(const AdjustLaunch &L) {
         // a row has the distance from the boundary of its array and `row` strides
         a.vectors = ((reinterpret_cast<uintptr_t>(L.in) ^ reinterpret_cast<uintptr_t>(L.out)) & 15) == 0 &&
                     (L.rows == 1 || (L.in_stride - L.out_stride) % N == 0);
-        a.steps = 1;
-        const uint32_t tokens = a.steps * kStep;
-        a.pieces = static_cast<uint32_t>((L.vocab + (a.vectors ? N - 1 : 0) + tokens - 1) / tokens);
+        // pieces that fill the device, smaller ones where their sets would take too much room
+        const int64_t want = std::max<int64_t>(kAdjustCtas / L.rows, 1), most = (L.vocab + kLeast - 1) / kLeast;
+        const int64_t pieces = std::min(want, most), span = L.vocab + (a.vectors ? N - 1 : 0);
+        int64_t tokens = std::max<int64_t>(256, (std::min<int64_t>(span / pieces + 1, 1 << 18) + 255) / 256 * 256);
+        auto set_words = [&](int64_t members) { return L.backward ? tokens / 32 : 2 * (tokens / 32) + std::min(tokens, members); };
+        auto smem_bytes = [&] {
+            int64_t words = 0;
+            if (a.history != nullptr) words += set_words(L.length);
+            if (!L.backward && L.biases > 0) words += set_words(L.biases);
+            if (L.allowed != nullptr) words += tokens / 32;
+            return static_cast<size_t>(words) * 4;
+        };
+        while (smem_bytes() > kAdjustMaxSmem) tokens = (tokens / 2 + 255) / 256 * 256;
+        a.tokens = static_cast<uint32_t>(tokens);
+        a.slots = static_cast<uint32_t>(std::min(tokens, L.length));
+        a.bias_slots = static_cast<uint32_t>(std::min(tokens, L.biases));
+        a.pieces = static_cast<uint32_t>((span + tokens - 1) / tokens);
         const int64_t blocks = L.rows * a.pieces;
         if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
-        const bool history = a.history != nullptr, biases = !L.backward && a.biases > 0;
-        size_t smem = 0;
-        if (history || biases) smem = (tokens / 32 + (history && !L.backward ? tokens : 0) + (biases ? tokens : 0)) * 4;
+        const size_t smem = smem_bytes();
         const void *kernel = L.backward ? reinterpret_cast<const void *>(k_adjust<T, true>) : reinterpret_cast<const void *>(k_adjust<T, false>);
         if (smem > 48 * 1024 && set_smem_limit(kernel, kAdjustMaxSmem) != cudaSuccess) return static_cast<int>(GSORT_ECUDA);
         if (L.backward) k_adjust<T, true><<<static_cast<uint32_t>(blocks), kAdjustThreads, smem, L.stream>>>(a);

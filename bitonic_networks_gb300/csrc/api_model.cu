@@ -149,19 +149,24 @@ bool tensors_clash(const void *const *in, void *const *out, const int64_t *eleme
         uintptr_t begin, end;
         bool written;
     };
-    std::vector<Range> ranges;
-    ranges.reserve(2 * tensors + 2);
-    for (const Span &s : {norm, ws})
-        if (s.bytes > 0) ranges.push_back({reinterpret_cast<uintptr_t>(s.p), reinterpret_cast<uintptr_t>(s.p) + s.bytes, true});
+    auto before = [](const Range &x, const Range &y) { return x.begin < y.begin; };
+    // each of the two lists is mostly in order already
+    std::vector<Range> read, wrote, ranges;
+    read.reserve(tensors);
+    wrote.reserve(out != nullptr ? tensors + 2 : 2);
     for (int64_t i = 0; i < tensors; ++i) {
         const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]), n = static_cast<uintptr_t>(elements[i]) * float_bytes(dtypes[i]);
         if (n == 0) continue;
         const bool same = out != nullptr && in[i] == out[i];
-        ranges.push_back({a, a + n, same});
-        if (out != nullptr && !same) ranges.push_back({reinterpret_cast<uintptr_t>(out[i]), reinterpret_cast<uintptr_t>(out[i]) + n, true});
+        read.push_back({a, a + n, same});
+        if (out != nullptr && !same) wrote.push_back({reinterpret_cast<uintptr_t>(out[i]), reinterpret_cast<uintptr_t>(out[i]) + n, true});
     }
-    auto before = [](const Range &x, const Range &y) { return x.begin < y.begin; };
-    if (!std::is_sorted(ranges.begin(), ranges.end(), before)) std::sort(ranges.begin(), ranges.end(), before);
+    for (const Span &s : {norm, ws})
+        if (s.bytes > 0) wrote.push_back({reinterpret_cast<uintptr_t>(s.p), reinterpret_cast<uintptr_t>(s.p) + s.bytes, true});
+    for (std::vector<Range> *list : {&read, &wrote})
+        if (!std::is_sorted(list->begin(), list->end(), before)) std::sort(list->begin(), list->end(), before);
+    ranges.resize(read.size() + wrote.size());
+    std::merge(read.begin(), read.end(), wrote.begin(), wrote.end(), ranges.begin(), before);
     uintptr_t end = 0, written = 0;      // the furthest end of any range so far, and of a written one
     for (const Range &r : ranges) {
         if (r.begin < written || (r.written && r.begin < end)) return true;

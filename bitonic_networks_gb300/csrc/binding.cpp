@@ -750,17 +750,21 @@ PyObject *clip_gradients(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                       ws.data_ptr(), ws.nbytes(), stream_of(device));
         }
         if (rc != GSORT_OK) return PyLong_FromLong(rc);
-        PyObject *list = PyList_New(static_cast<Py_ssize_t>(g.count()));
-        if (list == nullptr) return nullptr;
-        for (int64_t i = 0; i < g.count(); ++i) {
-            PyObject *item = made.empty() ? PySequence_Fast_GET_ITEM(o.fast, i) : wrap(made[i]);
-            if (made.empty()) Py_INCREF(item);
-            if (item == nullptr) {
-                Py_DECREF(list);
-                return nullptr;
+        PyObject *list;
+        if (o.fast != nullptr) {
+            // autograd refuses what it had saved of them
+            for (int64_t i = 0; i < g.count(); ++i)
+                if (!o.at(i).is_inference()) o.at(i).unsafeGetTensorImpl()->bump_version();
+            list = PySequence_List(o.fast);
+        } else {
+            list = PyList_New(static_cast<Py_ssize_t>(g.count()));
+            for (int64_t i = 0; list != nullptr && i < g.count(); ++i) {
+                PyObject *item = wrap(made[i]);
+                if (item == nullptr) Py_CLEAR(list);
+                else PyList_SET_ITEM(list, i, item);
             }
-            PyList_SET_ITEM(list, i, item);
         }
+        if (list == nullptr) return nullptr;
         PyObject *last = wrap(norm);
         PyObject *both = last ? PyTuple_Pack(2, list, last) : nullptr;
         Py_XDECREF(last);

@@ -78,9 +78,10 @@ def _wants_grad(t) -> bool:
     return getattr(t, "requires_grad", False) and torch.is_grad_enabled()
 
 
-def _written(*tensors):
-    """Tensors that a call has written: autograd refuses what it had saved of them."""
-    increment_version([t for t in tensors if not t.is_inference()])
+def _written(out):
+    """A tensor that a call has written: autograd refuses what it had saved of it."""
+    if not out.is_inference():
+        increment_version(out)
 
 
 # ----------------------------------------------------------------- routing
@@ -381,10 +382,4 @@ def clip_gradients(gradients, max_norm: float, *, scale: float = 1.0, out=None) 
     tensors like the gradients, or the gradients themselves (which are then not
     written where nothing changes).  Nothing waits for the device: a norm that is
     NaN makes every gradient NaN, an infinite one the finite gradients 0."""
-    gradients = list(gradients)
-    if out is not None:
-        out = list(out)
-    clipped = ClippedGradients(*_checked(_ops.clip_gradients(gradients, max_norm, scale, out), "gsort_clip_gradients"))
-    if out is not None:
-        _written(*out)
-    return clipped
+    return ClippedGradients(*_checked(_ops.clip_gradients(gradients, max_norm, scale, out), "gsort_clip_gradients"))

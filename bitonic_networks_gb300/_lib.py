@@ -152,7 +152,8 @@ SIGNATURES = {
     "gsort_embed_tokens": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
         ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
-    "gsort_embed_tokens_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "gsort_embed_tokens_backward_workspace_bytes": (ctypes.c_size_t, [
+        ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
     "gsort_embed_tokens_backward": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
         ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,

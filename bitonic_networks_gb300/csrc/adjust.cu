@@ -68,24 +68,41 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t *words, uint32_t at, 
     return words[at >> 5] >> (at & 31) & ((1u << n) - 1);
 }
 
-// Tokens of a piece, by their distance from its first one, in shared memory.
+// Tokens of a piece, by their distance from its first one, in shared memory.  With
+// less than 32768 members the words `before` and the counts in the slots take 16 bits.
 struct TokenSet {
     uint32_t *bits;      // null: no set
     uint32_t *before;    // members before each word of bits
-    uint32_t *slots;     // a word for each member
+    uint32_t *slots;     // one for each member
+    bool narrow;
 
     __device__ __forceinline__ bool has(uint32_t at) const { return bits != nullptr && (bits[at >> 5] >> (at & 31) & 1); }
-    __device__ __forceinline__ uint32_t &slot(uint32_t at) const {
-        return slots[before[at >> 5] + __popc(bits[at >> 5] & ((1u << (at & 31)) - 1))];
+    __device__ __forceinline__ uint32_t member(uint32_t at) const {      // its number
+        const uint32_t w = at >> 5;
+        return (narrow ? reinterpret_cast<const uint16_t *>(before)[w] : before[w]) + __popc(bits[w] & ((1u << (at & 31)) - 1));
     }
     __device__ __forceinline__ void add(uint32_t at) const {
         const uint32_t bit = 1u << (at & 31);
         if (at != kNowhere && !(*const_cast<const volatile uint32_t *>(bits + (at >> 5)) & bit)) atomicOr(bits + (at >> 5), bit);
     }
+    // A token once more, in the prompt or behind it.
+    __device__ __forceinline__ void count(uint32_t at, bool prompt) const {
+        const uint32_t m = member(at), half = narrow ? 16 * (m & 1) : 0;
+        uint32_t *word = slots + (narrow ? m / 2 : m);
+        if (prompt) atomicOr(word, (narrow ? 0x8000u : kSeenBefore) << half);
+        else atomicAdd(word, 1u << half);
+    }
+    __device__ __forceinline__ uint32_t counted(uint32_t at) const {     // how often behind the prompt
+        const uint32_t m = member(at);
+        return narrow ? reinterpret_cast<const uint16_t *>(slots)[m] & 0x7FFFu : slots[m] & ~kSeenBefore;
+    }
 };
 
-// Counts the members before each word, and clears their slots.  Called by the whole CTA.
-__device__ __forceinline__ void number_members(const TokenSet &set, uint32_t words) {
+__host__ __device__ constexpr bool is_narrow(int64_t members) { return members < 32768; }
+
+// Counts the members before each word, and clears their slots (words of 1 or 2 to a
+// slot word).  Called by the whole CTA.
+__device__ __forceinline__ void number_members(const TokenSet &set, uint32_t words, uint32_t per_slot_word) {
     __shared__ uint32_t s_sum[kAdjustThreads / 32];
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t per = (words + kAdjustThreads - 1) / kAdjustThreads, begin = min(tid * per, words), end = min(begin + per, words);
@@ -102,24 +119,34 @@ __device__ __forceinline__ void number_members(const TokenSet &set, uint32_t wor
         total += n;
     }
     for (uint32_t w = begin; w < end; ++w) {
-        set.before[w] = sum;
+        if (set.narrow) reinterpret_cast<uint16_t *>(set.before)[w] = static_cast<uint16_t>(sum);
+        else set.before[w] = sum;
         sum += __popc(set.bits[w]);
     }
-    for (uint32_t i = tid; i < total; i += kAdjustThreads) set.slots[i] = 0;
+    for (uint32_t i = tid; i * per_slot_word < total; i += kAdjustThreads) set.slots[i] = 0;
     __syncthreads();
 }
 
 // The tokens `base` + thread, + threads, ... of a list, as distances from the piece's first one.
-__device__ __forceinline__ void load_tokens(const void *list, int bytes, int64_t row, uint32_t length, uint32_t base, int64_t begin,
-                                            int64_t end, int64_t first, uint32_t (&at)[kHistoryLoads]) {
-    int64_t t[kHistoryLoads];
+__device__ __forceinline__ void load_tokens(const void *list, int bytes, int64_t row, uint32_t length, uint32_t base, int32_t begin,
+                                            int32_t end, int32_t first, uint32_t (&at)[kHistoryLoads]) {
+    uint32_t t[kHistoryLoads];       // what is no 32-bit number is no token
+    const uint32_t i0 = base + threadIdx.x;
+    if (bytes == 4) {
+        const uint32_t *p = static_cast<const uint32_t *>(list) + row + i0;
 #pragma unroll
-    for (int k = 0; k < kHistoryLoads; ++k) {
-        const uint32_t i = base + k * kAdjustThreads + threadIdx.x;
-        t[k] = i < length ? int_at(list, bytes, row + i) : -1;
+        for (int k = 0; k < kHistoryLoads; ++k) t[k] = i0 + k * kAdjustThreads < length ? p[k * kAdjustThreads] : kNowhere;
+    } else {
+        const uint64_t *p = static_cast<const uint64_t *>(list) + row + i0;
+#pragma unroll
+        for (int k = 0; k < kHistoryLoads; ++k) {
+            const uint64_t x = i0 + k * kAdjustThreads < length ? p[k * kAdjustThreads] : ~0ull;
+            t[k] = x >> 32 ? kNowhere : static_cast<uint32_t>(x);
+        }
     }
+    const uint32_t span = static_cast<uint32_t>(end - begin);        // end <= 2^30: kNowhere is outside
 #pragma unroll
-    for (int k = 0; k < kHistoryLoads; ++k) at[k] = t[k] >= begin && t[k] < end ? static_cast<uint32_t>(t[k] - first) : kNowhere;
+    for (int k = 0; k < kHistoryLoads; ++k) at[k] = t[k] - static_cast<uint32_t>(begin) < span ? t[k] - static_cast<uint32_t>(first) : kNowhere;
 }
 
 // What a CTA knows of its piece of a row.
@@ -133,11 +160,11 @@ struct Piece {
 
 __device__ __forceinline__ float adjusted(const Piece &p, float x, uint32_t at) {
     if (p.seen.has(at)) {
-        const uint32_t c = p.seen.slot(at), n = c & ~kSeenBefore;
+        const uint32_t n = p.seen.counted(at);
         x = x > 0.0f ? x / p.repetition : x * p.repetition;
         if (n != 0) x -= fmaf(p.frequency, static_cast<float>(n), p.presence);
     }
-    if (p.biased.has(at)) x += p.bias[p.biased.slot(at) - 1];
+    if (p.biased.has(at)) x += p.bias[p.biased.slots[p.biased.member(at)] - 1];
     return x;
 }
 
@@ -148,7 +175,7 @@ template <typename T, bool ZERO> __device__ __forceinline__ void mask_vector(uin
     for (int i = 0; i < 4; ++i) {
         uint32_t keep;
         if (sizeof(T) == 4) keep = bits >> i & 1 ? 0xFFFFFFFFu : 0u;
-        else keep = (bits >> (2 * i) & 1) * 0xFFFFu | (bits >> (2 * i + 1) & 1) * 0xFFFF0000u;
+        else keep = ((bits >> (2 * i) | bits << 15 >> (2 * i)) & 0x00010001u) * 0xFFFFu;
         w[i] = ZERO ? w[i] & keep : (w[i] & keep) | (Wide<T>::kNegInfWord & ~keep);
     }
 }
@@ -169,7 +196,8 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) k_adjust(const AdjustArgs<T
     p.first = static_cast<int32_t>(low);
     p.begin = max(p.first, 0);
     p.end = static_cast<int32_t>(min(low + a.tokens, static_cast<int64_t>(a.vocab)));
-    const uint32_t vectors = (p.end - p.first + N - 1) / N;
+    // vectors of the piece that are whole: not those that the row's start or end cuts
+    const uint32_t low_v = p.first < 0 ? 1 : 0, high_v = static_cast<uint32_t>(p.end - p.first) / N;
 
     // the first vectors are on their way while the sets are made
     uint4 q[U];
@@ -177,8 +205,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) k_adjust(const AdjustArgs<T
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t v = v0 + u * kAdjustThreads;
-            const int32_t e = p.first + static_cast<int32_t>(v * N);
-            if (v < vectors && e >= 0 && e + N <= p.end) q[u] = *reinterpret_cast<const uint4 *>(in + e);
+            if (v >= low_v && v < high_v) q[u] = reinterpret_cast<const uint4 *>(in + p.first)[v];
         }
     };
     const bool ahead = a.vectors && !a.in_place;
@@ -187,17 +214,19 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) k_adjust(const AdjustArgs<T
     const uint32_t words = a.tokens / 32;
     uint32_t *space = s_words;
     if (a.history != nullptr) {
+        p.seen.narrow = is_narrow(a.length);
         p.seen.bits = space;
         p.seen.before = space + words;
-        p.seen.slots = space + 2 * words;
-        space += BACK ? words : 2 * words + a.slots;
+        p.seen.slots = p.seen.before + (p.seen.narrow ? words / 2 : words);
+        space = BACK ? p.seen.before : p.seen.slots + a.slots;
     }
     if (!BACK && a.biases > 0) {
+        p.biased.narrow = is_narrow(a.biases);
         p.biased.bits = space;
         p.biased.before = space + words;
-        p.biased.slots = space + 2 * words;
+        p.biased.slots = p.biased.before + (p.biased.narrow ? words / 2 : words);
         p.bias = a.bias + static_cast<int64_t>(row) * a.bias_stride;
-        space += 2 * words + a.bias_slots;
+        space = p.biased.slots + a.bias_slots;
     }
     if (a.allowed != nullptr) {      // word w: the bits of the piece's tokens 32 w ..
         const uint32_t *mask = a.allowed + static_cast<int64_t>(row) * a.allowed_stride;
@@ -236,25 +265,22 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) k_adjust(const AdjustArgs<T
         __syncthreads();
         if (!BACK) {
             if (p.seen.bits) {
-                number_members(p.seen, words);
+                number_members(p.seen, words, p.seen.narrow ? 2 : 1);
                 const uint32_t prompt = a.prompt ? static_cast<uint32_t>(max(a.prompt[row], 0)) : 0;
                 for (uint32_t base = 0; base < a.length; base += kStep) {
                     // a history of one step is still there
                     if (a.length > kStep) load_tokens(a.history, a.history_bytes, history_row, a.length, base, p.begin, p.end, p.first, at);
 #pragma unroll
                     for (int k = 0; k < kHistoryLoads; ++k) {
-                        if (at[k] == kNowhere) continue;
-                        uint32_t *slot = &p.seen.slot(at[k]);
-                        if (base + k * kAdjustThreads + tid < prompt) atomicOr(slot, kSeenBefore);
-                        else atomicAdd(slot, 1u);
+                        if (at[k] != kNowhere) p.seen.count(at[k], base + k * kAdjustThreads + tid < prompt);
                     }
                 }
             }
             if (p.biased.bits) {
-                number_members(p.biased, words);
+                number_members(p.biased, words, 1);
                 for (uint32_t i = tid; i < a.biases; i += kAdjustThreads) {
                     const int64_t t = int_at(a.bias_tokens, a.bias_bytes, bias_row + i);
-                    if (t >= p.begin && t < p.end) atomicMax(&p.biased.slot(static_cast<uint32_t>(t - p.first)), i + 1);
+                    if (t >= p.begin && t < p.end) atomicMax(p.biased.slots + p.biased.member(static_cast<uint32_t>(t - p.first)), i + 1);
                 }
             }
             __syncthreads();
@@ -270,16 +296,20 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) k_adjust(const AdjustArgs<T
         if (!BACK) return adjusted(p, x, static_cast<uint32_t>(e - p.first));
         return to_f32(logits[e]) > 0.0f ? x * (1.0f / p.repetition) : x * p.repetition;
     };
-    if (!a.vectors) {          // rows that lie differently: element by element
-        for (int32_t e = p.begin + static_cast<int32_t>(tid); e < p.end; e += kAdjustThreads) {
-            const uint32_t at = static_cast<uint32_t>(e - p.first);
-            const float x = to_f32(in[e]);
-            const bool allow = !p.allowed || bits_at(p.allowed, at, 1);
-            out[e] = from_f32<T>(!allow ? (BACK ? 0.0f : kNegInf) : p.seen.has(at) || p.biased.has(at) ? named(x, e) : x);
-        }
-        return;
-    }
-    for (uint32_t v0 = tid; v0 < vectors; v0 += kAdjustThreads * U) {
+    auto single = [&](int32_t e) {
+        const uint32_t at = static_cast<uint32_t>(e - p.first);
+        const float x = to_f32(in[e]);
+        const bool allow = !p.allowed || bits_at(p.allowed, at, 1);
+        out[e] = from_f32<T>(!allow ? (BACK ? 0.0f : kNegInf) : p.seen.has(at) || p.biased.has(at) ? named(x, e) : x);
+    };
+    // Single elements: the whole piece where rows lie differently, else those of the two
+    // vectors that the row's start and end cut.
+    const int32_t whole = a.vectors ? p.first + static_cast<int32_t>(low_v) * N : p.end;
+    for (int32_t e = p.begin + static_cast<int32_t>(tid); e < min(whole, p.end); e += kAdjustThreads) single(e);
+    if (!a.vectors) return;
+    const int32_t rest = max(p.first + static_cast<int32_t>(high_v) * N, whole);
+    if (rest + static_cast<int32_t>(tid) < p.end) single(rest + static_cast<int32_t>(tid));
+    for (uint32_t v0 = tid; v0 < high_v; v0 += kAdjustThreads * U) {
         uint4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) x[u] = q[u];
@@ -291,24 +321,18 @@ __global__ void __launch_bounds__(kAdjustThreads, 2) k_adjust(const AdjustArgs<T
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t v = v0 + u * kAdjustThreads;
-            const int32_t e = p.first + static_cast<int32_t>(v * N);
-            if (v >= vectors) continue;
+            if (v < low_v || v >= high_v) continue;
             uint32_t name = 0, allow = kAll;
             if (p.seen.bits) name = bits_at(p.seen.bits, v * N, N);
             if (p.biased.bits) name |= bits_at(p.biased.bits, v * N, N);
             if (p.allowed) allow = bits_at(p.allowed, v * N, N);
             names |= (name & allow) << (u * N);
-            if (e < 0 || e + N > p.end) {        // the row's first and last elements
-                for (int32_t k = max(e, p.begin); k < min(e + N, p.end); ++k)
-                    out[k] = allow >> (k - e) & 1 ? in[k] : from_f32<T>(BACK ? 0.0f : kNegInf);
-                continue;
-            }
             if (a.in_place) {
                 if (allow == kAll) continue;
-                x[u] = *reinterpret_cast<const uint4 *>(in + e);
+                x[u] = reinterpret_cast<const uint4 *>(in + p.first)[v];
             }
-            if (allow != kAll) mask_vector<T, BACK>(x[u], allow);
-            *reinterpret_cast<uint4 *>(out + e) = x[u];
+            if (p.allowed) mask_vector<T, BACK>(x[u], allow);
+            reinterpret_cast<uint4 *>(out + p.first)[v] = x[u];
         }
         while (names != 0) {
             const uint32_t b = __ffs(names) - 1;
@@ -358,18 +382,17 @@ int launch_adjust(const AdjustLaunch &L) {
         const int64_t want = std::max<int64_t>(kAdjustCtas / L.rows, 1), most = (L.vocab + kLeast - 1) / kLeast;
         const int64_t pieces = std::min(want, most), span = L.vocab + (a.vectors ? N - 1 : 0);
         int64_t tokens = std::max<int64_t>(256, (std::min<int64_t>(span / pieces + 1, 1 << 18) + 255) / 256 * 256);
-        auto set_words = [&](int64_t members) { return L.backward ? tokens / 32 : 2 * (tokens / 32) + std::min(tokens, members); };
         auto smem_bytes = [&] {
-            int64_t words = 0;
-            if (a.history != nullptr) words += set_words(L.length);
-            if (!L.backward && L.biases > 0) words += set_words(L.biases);
-            if (L.allowed != nullptr) words += tokens / 32;
-            return static_cast<size_t>(words) * 4;
+            const int64_t words = tokens / 32;
+            a.tokens = static_cast<uint32_t>(tokens);
+            a.slots = static_cast<uint32_t>((std::min(tokens, L.length) + 1) / (is_narrow(L.length) ? 2 : 1));
+            a.bias_slots = static_cast<uint32_t>(std::min(tokens, L.biases));
+            int64_t all = L.allowed != nullptr ? words : 0;
+            if (a.history != nullptr) all += words + (L.backward ? 0 : (is_narrow(L.length) ? words / 2 : words) + a.slots);
+            if (!L.backward && L.biases > 0) all += words + (is_narrow(L.biases) ? words / 2 : words) + a.bias_slots;
+            return static_cast<size_t>(all) * 4;
         };
         while (smem_bytes() > kAdjustMaxSmem) tokens = (tokens / 2 + 255) / 256 * 256;
-        a.tokens = static_cast<uint32_t>(tokens);
-        a.slots = static_cast<uint32_t>(std::min(tokens, L.length));
-        a.bias_slots = static_cast<uint32_t>(std::min(tokens, L.biases));
         a.pieces = static_cast<uint32_t>((span + tokens - 1) / tokens);
         const int64_t blocks = L.rows * a.pieces;
         if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);

@@ -547,9 +547,9 @@ int gsort_embed_tokens(const void *d_table, int dtype, int64_t vocab, int64_t wi
     return launch_embed(L);
 }
 
-size_t gsort_embed_tokens_backward_workspace_bytes(int64_t tokens, int64_t width, int dtype) {
-    if (tokens < 1 || tokens > GSORT_MAX_N || width < 1 || width > GSORT_MAX_N || float_bytes(dtype) == 0) return 0;
-    return embed_workspace_bytes(tokens, width, dtype);
+size_t gsort_embed_tokens_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int dtype) {
+    if (tokens < 1 || embed_args(dtype, vocab, width, tokens, 4, 1.0f) != GSORT_OK) return 0;
+    return embed_workspace_bytes(tokens, vocab, width, dtype);
 }
 
 int gsort_embed_tokens_backward(const void *d_grad_out, int dtype, int64_t tokens, int64_t width,
@@ -565,7 +565,7 @@ int gsort_embed_tokens_backward(const void *d_grad_out, int dtype, int64_t token
     if (d_grad_table == nullptr || (tokens > 0 && (d_grad_out == nullptr || d_tokens == nullptr))) return GSORT_EINVAL;
     const size_t size = float_bytes(dtype);
     if (!aligned(d_grad_out, size) || !aligned(d_grad_table, size) || !aligned(d_tokens, token_bytes)) return GSORT_EALIGN;
-    const size_t ws = gsort_embed_tokens_backward_workspace_bytes(tokens, width, dtype);
+    const size_t ws = gsort_embed_tokens_backward_workspace_bytes(tokens, vocab, width, dtype);
     if (ws > 0) {
         if (d_ws == nullptr || ws_bytes < ws) return GSORT_EWORKSPACE;
         if (!aligned(d_ws, kWsAlign)) return GSORT_EALIGN;

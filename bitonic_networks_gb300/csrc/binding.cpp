@@ -498,7 +498,7 @@ PyObject *embed_tokens_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         {
             WithoutGil released;
             const c10::cuda::CUDAGuard guard(device);
-            const int64_t bytes = static_cast<int64_t>(gsort_embed_tokens_backward_workspace_bytes(rows, width, code));
+            const int64_t bytes = static_cast<int64_t>(gsort_embed_tokens_backward_workspace_bytes(rows, vocab, width, code));
             Tensor ws = space.value_or(Tensor());
             if (!ws.defined() && bytes > 0) ws = make({bytes}, at::kByte, device);
             out = given.has_value() ? *given : make({vocab, width}, d.scalar_type(), device);

@@ -47,6 +47,7 @@ struct ClusterSortArgs {
     uint32_t fmask, flip;
     int alias;                 // keys or values sorted in place
     uint32_t *status, *abort_flag;
+    int next_early;            // the next kernel of the stream may start meanwhile, if it asks for that
 };
 
 template <int IPT, bool PAIRS>
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) k_cluster_sort(const Clust
     uint32_t *const s_tc = s_cnt + WARPS * kRow;           // [256] this CTA's digit counts (read by all)
     uint32_t *const s_goff = s_tc + 256;                   // [256] global index - tile slot
     uint32_t *const s_misc = s_goff + 256;                 // [32]
+    if (a.next_early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t rank = cluster.block_rank(), csize = cluster.num_blocks();
@@ -342,6 +344,7 @@ int launch_cluster_sort(const SmallSortLaunch &L) {
     a.alias = L.alias ? 1 : 0;
     a.status = L.status;
     a.abort_flag = L.abort_flag;
+    a.next_early = L.next_early ? 1 : 0;
     const bool pairs = L.vals_in != nullptr;
     constexpr uint32_t kTc = kClusterThreads * kClusterIpt;
     int csize = 1;

@@ -15,11 +15,15 @@
 // runs that cross its ends leave partial sums, which are joined in shared memory
 // within a CTA and through the workspace between CTAs, always in the order of the
 // positions.  Every row of d_out is read once and every row of d_table written
-// once, so the memory bounds it.  Sums are 32-bit, rounded once.
+// once, so the memory bounds it.  Sums are 32-bit, rounded once.  Rows of tokens that
+// do not occur are filled with zeros while the tokens are sorted, which takes few SMs.
 #include <algorithm>
 
 #include "row_access.cuh"
 
+#ifndef EMBED_U
+#define EMBED_U 2
+#endif
 namespace gsort {
 namespace {
 
@@ -88,25 +92,92 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed(const EmbedArgs<T> a) {
 }
 
 // ------------------------------------------------------------ order by token
-// Every token as a key, with its position.
+// Every token as a key, with its position; and its bit, where they are asked for.
 __global__ void __launch_bounds__(256) k_token_keys(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys,
-                                                    uint32_t *positions) {
+                                                    uint32_t *positions, uint32_t *bits) {
     const uint32_t i = blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
-    keys[i] = token_key(token_at(tokens, bytes, i), vocab);
+    const uint32_t key = token_key(token_at(tokens, bytes, i), vocab);
+    keys[i] = key;
     positions[i] = i;
+    // frequent tokens find their bit set
+    if (bits != nullptr && key < vocab && !(ld_relaxed(bits + key / 32) >> (key & 31) & 1)) atomicOr(bits + key / 32, 1u << (key & 31));
+}
+
+// --------------------------------------------- rows of tokens that do not occur
+struct FillArgs {
+    char *table;
+    int64_t stride, row_bytes;     // in bytes, even
+    uint32_t vocab;
+    uint32_t rows;                 // of a CTA, a multiple of 8, at most 256
+    const uint32_t *bits;          // a bit for each token that occurs; null: the CTA looks at the tokens itself
+};
+
+// A warp writes zeros (or what `word` has twice).
+__device__ __forceinline__ void fill_span(char *p, int64_t bytes, uint32_t word) {
+    const uint32_t lane = threadIdx.x & 31;
+    const int64_t head = min(static_cast<int64_t>(-reinterpret_cast<intptr_t>(p) & 15), bytes);
+    const int64_t vectors = (bytes - head) / 16, tail = head + vectors * 16;
+    if (lane < head / 2) reinterpret_cast<uint16_t *>(p)[lane] = static_cast<uint16_t>(word);
+    uint4 *v = reinterpret_cast<uint4 *>(p + head);
+#pragma unroll 4
+    for (int64_t i = lane; i < vectors; i += 32) v[i] = make_uint4(word, word, word, word);
+    if (lane < (bytes - tail) / 2) reinterpret_cast<uint16_t *>(p + tail)[lane] = static_cast<uint16_t>(word);
+}
+
+// Fills the rows of CTA `block` that are absent; s_bits: 8 words of shared memory.
+__device__ __forceinline__ void fill_absent(const FillArgs &a, uint32_t block, const void *tokens, int bytes, uint32_t n, uint32_t *s_bits) {
+    const uint32_t base = block * a.rows, tid = threadIdx.x;
+    if (tid < 8) s_bits[tid] = a.bits != nullptr && base / 32 + tid < (a.vocab + 31) / 32 ? a.bits[base / 32 + tid] : 0;
+    __syncthreads();
+    uint32_t from = base;              // the token of s_bits' first bit
+    if (a.bits != nullptr) {
+        from = base / 32 * 32;
+    } else {
+#pragma unroll 8
+        for (uint32_t i = tid; i < n; i += 256) {
+            const int64_t t = token_at(tokens, bytes, i) - base;
+            if (t >= 0 && t < a.rows) atomicOr(s_bits + t / 32, 1u << (t & 31));
+        }
+        __syncthreads();
+    }
+    const uint32_t per = a.rows / 8, first = base + (tid >> 5) * per;        // this warp's rows
+    if (first >= a.vocab) return;
+    const uint32_t rows = min(per, a.vocab - first), at = first - from;
+    uint32_t present = s_bits[at / 32] >> (at & 31);
+    if ((at & 31) != 0 && at / 32 < 7) present |= s_bits[at / 32 + 1] << (32 - (at & 31));
+    uint32_t absent = ~present & (rows == 32 ? 0xFFFFFFFFu : (1u << rows) - 1);
+    while (absent != 0) {              // runs of rows, which lie one behind another where the table has no gaps
+        const uint32_t start = __ffs(absent) - 1, more = ~(absent >> start), length = more == 0 ? 32 : __ffs(more) - 1;
+        const uint32_t run = a.stride == a.row_bytes ? length : 1;
+        fill_span(a.table + static_cast<int64_t>(first + start) * a.stride, run * a.row_bytes, 0);
+        absent &= ~((run == 32 ? 0xFFFFFFFFu : (1u << run) - 1) << start);
+    }
+}
+
+// Beside the sort that precedes it in the stream: neither needs the other.  What follows
+// waits for both.
+__global__ void __launch_bounds__(256) k_fill_absent(const FillArgs a) {
+    __shared__ uint32_t s_bits[8];
+    fill_absent(a, blockIdx.x, nullptr, 0, 0, s_bits);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Few tokens are sorted by counting: a token's place is the number of tokens that
 // are smaller, or equal and before it.  A lane holds a token, a warp compares
-// its 32 tokens with an eighth of all (a broadcast from shared memory each).
+// its 32 tokens with an eighth of all (a broadcast from shared memory each).  The
+// CTAs behind those of the tokens fill absent rows.
 constexpr uint32_t kRankMax = 8192;
 
 __global__ void __launch_bounds__(256) k_token_rank(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys,
-                                                    uint32_t *order) {
+                                                    uint32_t *order, const FillArgs fill) {
     extern __shared__ __align__(16) uint32_t s_keys[];   // n rounded up to 32
     __shared__ uint32_t s_rank[8][32];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = (n + 31) / 32;
+    if (blockIdx.x >= groups) {
+        fill_absent(fill, blockIdx.x - groups, tokens, bytes, n, s_rank[0]);
+        return;
+    }
     for (uint32_t i = threadIdx.x; i < groups * 32; i += 256)
         s_keys[i] = i < n ? token_key(token_at(tokens, bytes, i), vocab) : kNoKey;   // behind every token
     __syncthreads();
@@ -160,7 +231,6 @@ template <typename T> struct EmbedSumArgs {
     uint32_t log_lanes, slabs;       // 2^log_lanes lanes hold a vector each; slabs of them make a row
     uint32_t per;                    // positions of a group of lanes
     uint32_t chunks;                 // of (256 >> log_lanes) * per positions
-    uint32_t fill_blocks, fill_rows; // CTAs that write zeros; rows that a warp of them looks over
 };
 
 template <typename T, int MODE> struct RowSum {
@@ -189,7 +259,7 @@ template <typename T, int MODE> struct RowSum {
             reinterpret_cast<float4 *>(f)[i] = make_float4(p[2 * i].f.x, p[2 * i].f.y, p[2 * i + 1].f.x, p[2 * i + 1].f.y);
     }
     // The run's sum to its row of the table.
-    __device__ __forceinline__ void write(const EmbedSumArgs<T> &a, uint32_t key, uint32_t v, float scale) const {
+    __device__ __forceinline__ void write(const EmbedSumArgs<T> &a, uint32_t key, uint32_t v) const {
         const OutRow<T, MODE> out(a.out + static_cast<int64_t>(key) * a.out_stride);
         const int32_t e = out.at(v);
         uint4 q;
@@ -205,51 +275,27 @@ template <typename T, int MODE> struct RowSum {
                 for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, pair(f[2 * i], f[2 * i + 1]));
             }
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, fma2(p[i], pair(scale, scale), Wide<T>::pair_of(q, i)));
+            for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, fma2(p[i], pair(a.scale, a.scale), Wide<T>::pair_of(q, i)));
         } else {
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, mul2(p[i], pair(scale, scale)));
+            for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, mul2(p[i], pair(a.scale, a.scale)));
         }
         out.write(e, a.width, q);
     }
 };
 
-// Rows of the table whose token does not occur are zero: a lane looks one token
-// up in the sorted ones, a warp writes the rows that its lanes have found.
-template <typename T, int MODE> __device__ __forceinline__ void fill_absent(const EmbedSumArgs<T> &a, bool failed) {
-    const uint32_t lane = threadIdx.x & 31;
-    const uint32_t base = (blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5)) * a.fill_rows, r = base + lane;
-    bool absent = false;
-    if (lane < a.fill_rows && r < a.vocab) {
-        uint32_t low = 0, high = a.n;      // the first key that is not below r
-        while (low < high) {
-            const uint32_t mid = low + (high - low) / 2;
-            if (a.keys[mid] < r) low = mid + 1;
-            else high = mid;
-        }
-        absent = failed || low >= a.n || a.keys[low] != r;
-    }
-    uint32_t q = 0;
-    if (failed) q = sizeof(T) == 4 ? 0x7FC00000u : 0x7FFF7FFFu;     // NaN
-    for (uint32_t rows = __ballot_sync(kFullMask, absent); rows; rows &= rows - 1) {
-        const OutRow<T, MODE> o(a.out + static_cast<int64_t>(base + (__ffs(rows) - 1)) * a.out_stride);
-        for (uint32_t v = lane; v < a.vectors; v += 32) o.write(o.at(v), a.width, make_uint4(q, q, q, q));
-    }
-}
-
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kEmbedThreads) k_embed_sum(const EmbedSumArgs<T> a) {
     constexpr int N = Wide<T>::kCount, U = kLoads<MODE>;
-    const bool failed = a.status != nullptr && *a.status != 0;     // of the sort: its results are void
-    if (blockIdx.x < a.fill_blocks) {
-        fill_absent<T, MODE>(a, failed);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // the join looks at the keys meanwhile
+    if (a.status != nullptr && *a.status != 0) {       // the sort gave up, its results are void: all rows are NaN
+        for (uint32_t r = blockIdx.x * 8 + (threadIdx.x >> 5); r < a.vocab; r += gridDim.x * 8)
+            fill_span(reinterpret_cast<char *>(a.out + static_cast<int64_t>(r) * a.out_stride), static_cast<int64_t>(a.width) * sizeof(T), 0x7FFF7FFFu);
         return;
     }
-    if (failed && !a.accumulate) return;
-    const float scale = failed ? __uint_as_float(0x7FC00000u) : a.scale;
     __shared__ uint32_t s_key[kMaxUnits * kMaxPer + 2], s_order[kMaxUnits * kMaxPer];   // s_key[0]: the key before the chunk
     __shared__ __align__(16) float s_head[kEmbedThreads][N];
-    const uint32_t block = blockIdx.x - a.fill_blocks, chunk = block / a.slabs, slab = block % a.slabs;
+    const uint32_t chunk = blockIdx.x / a.slabs, slab = blockIdx.x % a.slabs;
     const uint32_t lanes = 1u << a.log_lanes, units = kEmbedThreads >> a.log_lanes, size = units * a.per;
     const uint32_t base = chunk * size, count = min(size, a.n - base), tid = threadIdx.x;
     for (uint32_t i = tid; i < count + 2; i += kEmbedThreads) {
@@ -285,7 +331,7 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed_sum(const EmbedSumArgs<
                 if (k != key) {
                     if (key < a.vocab) {
                         if (first) sum.store(s_head[tid]);
-                        else if (v < a.vectors) sum.write(a, key, v, scale);
+                        else if (v < a.vectors) sum.write(a, key, v);
                     }
                     first = false;
                     key = k;
@@ -336,7 +382,7 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed_sum(const EmbedSumArgs<
             return;
         }
     }
-    if (v < a.vectors) sum.write(a, key, v, scale);
+    if (v < a.vectors) sum.write(a, key, v);
 }
 
 // Joins the runs that cross ends of chunks: the CTA of the chunk in which a run
@@ -347,18 +393,21 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed_join(const EmbedSumArgs
     const uint32_t chunk = blockIdx.x / a.slabs, slab = blockIdx.x % a.slabs;
     const uint32_t lanes = 1u << a.log_lanes, units = kEmbedThreads >> a.log_lanes, size = units * a.per;
     const uint32_t base = chunk * size, end = base + size;
-    if (end >= a.n) return;
-    const uint32_t key = a.keys[end - 1];
-    if (key >= a.vocab || a.keys[end] != key || (base > 0 && a.keys[base - 1] == key && a.keys[base] == key)) return;
+    // the keys were there before the sums began: who has nothing to join is known without them
+    const uint32_t key = a.keys[end - 1], next = a.keys[end], first = a.keys[base], before = base > 0 ? a.keys[base - 1] : kNoKey;
     const bool failed = a.status != nullptr && *a.status != 0;
-    if (failed && !a.accumulate) return;
-    uint32_t low = end, high = a.n;        // the first key above this one
-    while (low < high) {
-        const uint32_t mid = low + (high - low) / 2;
-        if (a.keys[mid] <= key) low = mid + 1;
-        else high = mid;
+    const bool mine = !failed && key < a.vocab && next == key && !(first == key && before == key);
+    uint32_t last = chunk;                 // the chunk that the run ends in
+    if (mine) {
+        for (uint32_t c0 = chunk + 1;; c0 += kEmbedThreads) {
+            const uint64_t p = static_cast<uint64_t>(c0 + threadIdx.x) * size;
+            const uint32_t held = __syncthreads_count(p < a.n && a.keys[p] == key);
+            last += held;
+            if (held < kEmbedThreads) break;
+        }
     }
-    const uint32_t last = (low - 1) / size;             // the chunk that the run ends in
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!mine) return;
     __shared__ __align__(16) float s_part[kEmbedThreads][N];
     const uint32_t tid = threadIdx.x, unit = tid >> a.log_lanes, v = slab * lanes + (tid & (lanes - 1));
     const size_t row = static_cast<size_t>(a.slabs) * lanes * N;
@@ -375,7 +424,21 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed_join(const EmbedSumArgs
     } else if (unit != 0) {
         return;
     }
-    if (v < a.vectors) sum.write(a, key, v, failed ? __uint_as_float(0x7FC00000u) : a.scale);
+    if (v < a.vectors) sum.write(a, key, v);
+}
+
+// A launch that may start while the kernel before it in the stream runs, as soon as that allows it.
+template <typename A> int launch_early(void (*kernel)(const A), uint32_t ctas, cudaStream_t stream, const A &a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kEmbedThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? GSORT_OK : GSORT_ECUDA;
 }
 
 // ------------------------------------------------------------------- plans
@@ -383,10 +446,10 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed_join(const EmbedSumArgs
 // depends on nothing else.
 struct EmbedPlan {
     uint32_t vectors_max, log_lanes, slabs, per, chunks;
-    size_t keys, order, keys_in, order_in, radix, partials, total;
+    size_t keys, order, keys_in, order_in, radix, bits, partials, total;
 };
 
-EmbedPlan embed_plan(uint32_t n, uint32_t width, int size) {
+EmbedPlan embed_plan(uint32_t n, uint32_t vocab, uint32_t width, int size) {
     EmbedPlan p{};
     const uint32_t count = 16 / size;
     // a row touches so many vectors at most, however it lies
@@ -408,6 +471,8 @@ EmbedPlan embed_plan(uint32_t n, uint32_t width, int size) {
         at += bytes;
         p.order_in = at;
         at += bytes;
+        p.bits = at;
+        at += align_up((static_cast<size_t>(vocab) + 31) / 32 * 4, kWsAlign);
     } else {
         at += kWsAlign;          // a status that is always GSORT_OK
     }
@@ -423,8 +488,8 @@ EmbedPlan embed_plan(uint32_t n, uint32_t width, int size) {
 
 }  // namespace
 
-size_t embed_workspace_bytes(int64_t tokens, int64_t width, int dtype) {
-    return embed_plan(static_cast<uint32_t>(tokens), static_cast<uint32_t>(width), float_bytes(dtype)).total;
+size_t embed_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int dtype) {
+    return embed_plan(static_cast<uint32_t>(tokens), static_cast<uint32_t>(vocab), static_cast<uint32_t>(width), float_bytes(dtype)).total;
 }
 
 int launch_embed(const EmbedLaunch &L) {
@@ -444,7 +509,7 @@ int launch_embed(const EmbedLaunch &L) {
         a.vocab = static_cast<uint32_t>(L.vocab);
         a.width = static_cast<uint32_t>(L.width);
         auto start = [&](auto m) {
-            constexpr int MODE = decltype(m)::value, U = 2;
+            constexpr int MODE = decltype(m)::value, U = EMBED_U;
             a.log_lanes = lanes_for(a.vectors, U);
             const uint32_t step = U << a.log_lanes, rows = kEmbedThreads >> a.log_lanes;
             a.chunks = (a.vectors + step - 1) / step;
@@ -468,16 +533,26 @@ int launch_embed(const EmbedLaunch &L) {
 int launch_embed_backward(const EmbedBackwardLaunch &L) {
     using std::integral_constant;
     const uint32_t n = static_cast<uint32_t>(L.n), vocab = static_cast<uint32_t>(L.vocab);
-    const EmbedPlan plan = embed_plan(n, static_cast<uint32_t>(L.width), float_bytes(L.dtype));
+    const EmbedPlan plan = embed_plan(n, vocab, static_cast<uint32_t>(L.width), float_bytes(L.dtype));
     uint32_t *keys = reinterpret_cast<uint32_t *>(L.ws + plan.keys), *order = reinterpret_cast<uint32_t *>(L.ws + plan.order);
-    if (n > 0 && n <= kRankMax) {
+    FillArgs fill{};
+    fill.table = static_cast<char *>(L.d_table);
+    fill.row_bytes = L.width * float_bytes(L.dtype);
+    fill.stride = L.table_stride * float_bytes(L.dtype);
+    fill.vocab = vocab;
+    fill.rows = std::min(256u, std::max(8u, (vocab / kFillCtas + 7) / 8 * 8));
+    const uint32_t fill_ctas = L.accumulate ? 0 : (vocab + fill.rows - 1) / fill.rows;
+    if (n <= kRankMax) {
         const uint32_t groups = (n + 31) / 32;
-        k_token_rank<<<groups, 256, groups * 32 * 4, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys, order);
+        if (groups + fill_ctas == 0) return GSORT_OK;
+        k_token_rank<<<groups + fill_ctas, 256, groups * 32 * 4, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys, order, fill);
         if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
-    } else if (n > 0) {
+    } else {
         uint32_t *keys_in = reinterpret_cast<uint32_t *>(L.ws + plan.keys_in);
         uint32_t *order_in = reinterpret_cast<uint32_t *>(L.ws + plan.order_in);
-        k_token_keys<<<(n + 255) / 256, 256, 0, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys_in, order_in);
+        uint32_t *bits = L.accumulate ? nullptr : reinterpret_cast<uint32_t *>(L.ws + plan.bits);
+        if (bits && cudaMemsetAsync(bits, 0, (static_cast<size_t>(vocab) + 31) / 32 * 4, L.stream) != cudaSuccess) return GSORT_ECUDA;
+        k_token_keys<<<(n + 255) / 256, 256, 0, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys_in, order_in, bits);
         if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
         RadixLaunch R{};
         R.keys_in = keys_in;
@@ -492,8 +567,13 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
         R.stall_tile = kNoStall;
         R.stream = L.stream;
         R.sm_count = L.sm_count;
+        R.next_early = fill_ctas > 0;
         const int rc = launch_radix(R);
         if (rc != GSORT_OK) return rc;
+        if (fill_ctas > 0) {
+            fill.bits = bits;
+            if (launch_early(k_fill_absent, fill_ctas, L.stream, fill) != GSORT_OK) return GSORT_ECUDA;
+        }
     }
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
@@ -517,19 +597,12 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
         a.slabs = plan.slabs;
         a.per = plan.per;
         a.chunks = plan.chunks;
-        if (!L.accumulate) {
-            a.fill_rows = std::min(32u, std::max(1u, vocab / 4096));
-            const uint32_t rows = a.fill_rows * (kEmbedThreads / 32);
-            a.fill_blocks = (vocab + rows - 1) / rows;
-        }
         auto start = [&](auto m) {
             constexpr int MODE = decltype(m)::value;
-            const int64_t blocks = static_cast<int64_t>(a.chunks) * a.slabs + a.fill_blocks;
-            if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
-            if (blocks == 0) return static_cast<int>(GSORT_OK);
-            k_embed_sum<T, MODE><<<static_cast<uint32_t>(blocks), kEmbedThreads, 0, L.stream>>>(a);
-            if (a.chunks > 1) k_embed_join<T, MODE><<<(a.chunks - 1) * a.slabs, kEmbedThreads, 0, L.stream>>>(a);
-            return launch_status();
+            if (a.chunks == 0) return static_cast<int>(GSORT_OK);
+            k_embed_sum<T, MODE><<<a.chunks * a.slabs, kEmbedThreads, 0, L.stream>>>(a);
+            if (cudaGetLastError() != cudaSuccess) return static_cast<int>(GSORT_ECUDA);
+            return a.chunks > 1 ? launch_early(k_embed_join<T, MODE>, (a.chunks - 1) * a.slabs, L.stream, a) : static_cast<int>(GSORT_OK);
         };
         if (L.width % N == 0 && aligned(L.d_out, 16) && aligned(L.d_table, 16) && L.d_stride % N == 0 && L.table_stride % N == 0) {
             a.vectors = a.width / N;

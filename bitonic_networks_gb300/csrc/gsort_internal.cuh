@@ -206,6 +206,7 @@ struct RadixLaunch {
     int variant;
     cudaStream_t stream;
     int sm_count;
+    bool next_early = false;   // a launch after the sort with programmatic serialization may start while a one-cluster sort runs
 };
 
 // Layout of the radix workspace after the header.
@@ -273,6 +274,7 @@ struct SmallSortLaunch {
     uint32_t spin_limit, stall_tile;
     cudaStream_t stream;
     int sm_count;
+    bool next_early = false;     // see RadixLaunch (one-cluster sort)
 };
 bool small_sort_applies(uint32_t n, int key_bytes, int variant);
 uint32_t small_sort_tile();

@@ -286,7 +286,7 @@ struct EmbedBackwardLaunch {
     cudaStream_t stream;
     int sm_count;
 };
-size_t embed_workspace_bytes(int64_t tokens, int64_t width, int dtype);
+size_t embed_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int dtype);
 int launch_embed_backward(const EmbedBackwardLaunch &L);
 
 struct AdjustLaunch {

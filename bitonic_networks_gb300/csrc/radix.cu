@@ -342,6 +342,7 @@ int launch_radix(const RadixLaunch &L) {
         S.abort_flag = abort_flag;
         S.stream = s;
         S.sm_count = L.sm_count;
+        S.next_early = L.next_early;
         record(L.events, L.num_events, 1, s);
         const int rc = launch_cluster_sort(S);
         if (rc != 1) {

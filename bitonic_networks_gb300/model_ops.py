@@ -280,10 +280,10 @@ def embed_tokens(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.
     return _checked(_ops.embed_tokens(table, tokens, scale), "gsort_embed_tokens")
 
 
-def embed_workspace_bytes(tokens: int, width: int, dtype: torch.dtype) -> int:
-    """Workspace of embed_tokens_backward for so many tokens."""
+def embed_workspace_bytes(tokens: int, vocab: int, width: int, dtype: torch.dtype) -> int:
+    """Workspace of embed_tokens_backward for so many tokens and a table of this shape."""
     code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
-    return int(_lib.load().gsort_embed_tokens_backward_workspace_bytes(tokens, width, code))
+    return int(_lib.load().gsort_embed_tokens_backward_workspace_bytes(tokens, vocab, width, code))
 
 
 def embed_tokens_backward(d_out: torch.Tensor, tokens: torch.Tensor, vocab: int, *, scale: float = 1.0,

@@ -134,7 +134,7 @@ def test_rows_of_the_last_sequence_only():
 
 def test_given_workspace():
     d, tokens = normal(9000, 64), tokens_of(9000, 500)
-    need = gs.embed_workspace_bytes(9000, 64, torch.float32)
+    need = gs.embed_workspace_bytes(9000, 500, 64, torch.float32)
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     want = gs.embed_tokens_backward(d, tokens, 500)
     for _ in range(2):

@@ -23,12 +23,13 @@ def test_package_exports():
 
 def test_workspace_sizes(lib):
     ws = lib.gsort_embed_tokens_backward_workspace_bytes
-    assert ws(0, 64, 0) == ws(-1, 64, 0) == ws(1 << 30, 64, 0) == ws(5, 0, 0) == ws(5, 64, 3) == ws(5, 1 << 30, 0) == 0
+    assert ws(0, 9, 64, 0) == ws(-1, 9, 64, 0) == ws(1 << 30, 9, 64, 0) == ws(5, 9, 0, 0) == ws(5, 9, 64, 3) == ws(5, 9, 1 << 30, 0) == 0
+    assert ws(5, 0, 64, 0) == ws(5, 1 << 30, 64, 0) == 0
     for n in (1, 8192, 8193, 1 << 20, (1 << 30) - 1):
         for width, dtype in ((1, 1), (64, 0), (1001, 2), (8192, 1)):
-            assert ws(n, width, dtype) >= 8 * n and ws(n, width, dtype) % 256 == 0
+            assert ws(n, 9, width, dtype) >= 8 * n and ws(n, 9, width, dtype) % 256 == 0
     # the partial sums take an eighth of what the gradient itself takes, at most, where it is large
-    assert ws(65536, 4096, 1) < 65536 * 4096 * 2 / 8 + 65536 * 64 + (8 << 20)
+    assert ws(65536, 131072, 4096, 1) < 65536 * 4096 * 2 / 8 + 65536 * 64 + (8 << 20)
     norm = lib.gsort_gradient_norm_workspace_bytes
     assert norm(0) == norm(-1) == norm(1 << 30) == 0 and 0 < norm(1) == norm(1000) < norm(1001) == norm(2000)
 

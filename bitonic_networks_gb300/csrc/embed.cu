@@ -21,18 +21,23 @@
 
 #include "row_access.cuh"
 
-#ifndef EMBED_U
-#define EMBED_U 2
-#endif
 namespace gsort {
 namespace {
 
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;
 constexpr int kEmbedThreads = kRowThreads;
 constexpr int kMinLogLanes = 3, kMaxLogLanes = 5;   // lanes side by side on a row
-constexpr uint32_t kMaxUnits = kEmbedThreads >> kMinLogLanes;
-constexpr uint32_t kMaxPer = 32;                    // positions of a group of lanes
+constexpr uint32_t kMaxPer = 128;                   // positions of a group of lanes
+constexpr uint32_t kMaxChunk = 1024;                // positions of a CTA
 constexpr uint32_t kFillCtas = 608;                 // CTAs that keep a GB300 busy: 4 to an SM
+
+// A CTA that fills rows takes so many bytes: a table of 1 GB of 8 KB rows takes 146 us, 144 with
+// half, 151 with twice as many; with 65536 tokens, which make runs of absent rows short, the gradient
+// takes 384 us with its lookup, 393 with half.
+constexpr int64_t kFillBytes = 128 << 10;
+// Bytes that are filled while the tokens are sorted, by counting or in a cluster; what
+// is left is filled beside the sums.
+constexpr int64_t kBesideFew = 32 << 20, kBesideCounting = 64 << 20, kBesideCluster = 128 << 20;
 
 // Rows in flight per thread; a shifted one takes two vectors of registers.
 template <int MODE> constexpr int kLoads = MODE == kShifted ? 4 : 8;
@@ -94,12 +99,13 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed(const EmbedArgs<T> a) {
 // ------------------------------------------------------------ order by token
 // Every token as a key, with its position; and its bit, where they are asked for.
 __global__ void __launch_bounds__(256) k_token_keys(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys,
-                                                    uint32_t *positions, uint32_t *bits) {
+                                                    uint32_t *positions, uint32_t *bits, uint32_t *counters, uint32_t count) {
     const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+    for (uint32_t c = i; c < count; c += gridDim.x * 256) counters[c] = 0;
     if (i >= n) return;
     const uint32_t key = token_key(token_at(tokens, bytes, i), vocab);
     keys[i] = key;
-    positions[i] = i;
+    if (positions != nullptr) positions[i] = i;
     // frequent tokens find their bit set
     if (bits != nullptr && key < vocab && !(ld_relaxed(bits + key / 32) >> (key & 31) & 1)) atomicOr(bits + key / 32, 1u << (key & 31));
 }
@@ -109,57 +115,63 @@ struct FillArgs {
     char *table;
     int64_t stride, row_bytes;     // in bytes, even
     uint32_t vocab;
-    uint32_t rows;                 // of a CTA, a multiple of 8, at most 256
+    uint32_t rows;                 // of a CTA, at most 256
+    uint32_t first;                // CTA's number of the grid's first one
     const uint32_t *bits;          // a bit for each token that occurs; null: the CTA looks at the tokens itself
+    const void *tokens;
+    int token_bytes;
+    uint32_t n;
 };
 
-// A warp writes zeros (or what `word` has twice).
+// A CTA writes a span of bytes with what `word` has twice.
 __device__ __forceinline__ void fill_span(char *p, int64_t bytes, uint32_t word) {
-    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t tid = threadIdx.x;
     const int64_t head = min(static_cast<int64_t>(-reinterpret_cast<intptr_t>(p) & 15), bytes);
     const int64_t vectors = (bytes - head) / 16, tail = head + vectors * 16;
-    if (lane < head / 2) reinterpret_cast<uint16_t *>(p)[lane] = static_cast<uint16_t>(word);
+    if (tid < head / 2) reinterpret_cast<uint16_t *>(p)[tid] = static_cast<uint16_t>(word);
     uint4 *v = reinterpret_cast<uint4 *>(p + head);
 #pragma unroll 4
-    for (int64_t i = lane; i < vectors; i += 32) v[i] = make_uint4(word, word, word, word);
-    if (lane < (bytes - tail) / 2) reinterpret_cast<uint16_t *>(p + tail)[lane] = static_cast<uint16_t>(word);
+    for (int64_t i = tid; i < vectors; i += kEmbedThreads) v[i] = make_uint4(word, word, word, word);
+    if (tid < (bytes - tail) / 2) reinterpret_cast<uint16_t *>(p + tail)[tid] = static_cast<uint16_t>(word);
 }
 
-// Fills the rows of CTA `block` that are absent; s_bits: 8 words of shared memory.
-__device__ __forceinline__ void fill_absent(const FillArgs &a, uint32_t block, const void *tokens, int bytes, uint32_t n, uint32_t *s_bits) {
-    const uint32_t base = block * a.rows, tid = threadIdx.x;
-    if (tid < 8) s_bits[tid] = a.bits != nullptr && base / 32 + tid < (a.vocab + 31) / 32 ? a.bits[base / 32 + tid] : 0;
+// Fills the absent rows of CTA number `block`.  The CTA writes a run of them as a whole:
+// 400 MB of rows of 4004 bytes take 57 us so (7.0 TB/s), 63 with a run to each warp.
+__device__ __forceinline__ void fill_absent(const FillArgs &a, uint32_t block) {
+    __shared__ uint32_t s_bits[9];     // of 256 tokens, from any bit of the first word on
+    const uint32_t base = block * a.rows, rows = min(a.rows, a.vocab - base), tid = threadIdx.x;
+    const uint32_t shift = a.bits != nullptr ? base & 31 : 0;      // the bit of token `base`
+    if (tid < 9) s_bits[tid] = a.bits != nullptr && base / 32 + tid < (a.vocab + 31) / 32 ? a.bits[base / 32 + tid] : 0;
     __syncthreads();
-    uint32_t from = base;              // the token of s_bits' first bit
-    if (a.bits != nullptr) {
-        from = base / 32 * 32;
-    } else {
+    if (a.bits == nullptr) {
 #pragma unroll 8
-        for (uint32_t i = tid; i < n; i += 256) {
-            const int64_t t = token_at(tokens, bytes, i) - base;
-            if (t >= 0 && t < a.rows) atomicOr(s_bits + t / 32, 1u << (t & 31));
+        for (uint32_t i = tid; i < a.n; i += kEmbedThreads) {
+            const int64_t t = token_at(a.tokens, a.token_bytes, i) - base;
+            if (t >= 0 && t < rows) atomicOr(s_bits + t / 32, 1u << (t & 31));
         }
         __syncthreads();
     }
-    const uint32_t per = a.rows / 8, first = base + (tid >> 5) * per;        // this warp's rows
-    if (first >= a.vocab) return;
-    const uint32_t rows = min(per, a.vocab - first), at = first - from;
-    uint32_t present = s_bits[at / 32] >> (at & 31);
-    if ((at & 31) != 0 && at / 32 < 7) present |= s_bits[at / 32 + 1] << (32 - (at & 31));
-    uint32_t absent = ~present & (rows == 32 ? 0xFFFFFFFFu : (1u << rows) - 1);
-    while (absent != 0) {              // runs of rows, which lie one behind another where the table has no gaps
-        const uint32_t start = __ffs(absent) - 1, more = ~(absent >> start), length = more == 0 ? 32 : __ffs(more) - 1;
-        const uint32_t run = a.stride == a.row_bytes ? length : 1;
-        fill_span(a.table + static_cast<int64_t>(first + start) * a.stride, run * a.row_bytes, 0);
-        absent &= ~((run == 32 ? 0xFFFFFFFFu : (1u << run) - 1) << start);
+    // the first row from r on that is present (or absent), `rows` at most
+    auto find = [&](uint32_t r, bool present) {
+        while (r < rows) {
+            const uint32_t at = shift + r, left = 32 - (at & 31);
+            const uint32_t w = (present ? s_bits[at / 32] : ~s_bits[at / 32]) >> (at & 31);
+            if (w != 0) return min(r + __ffs(w) - 1, rows);        // zeros are shifted in
+            r += left;
+        }
+        return rows;
+    };
+    for (uint32_t r = find(0, false); r < rows;) {
+        const uint32_t end = find(r, true), run = a.stride == a.row_bytes ? end - r : 1;   // without gaps, rows are one span
+        for (; r < end; r += run) fill_span(a.table + (base + static_cast<int64_t>(r)) * a.stride, run * a.row_bytes, 0);
+        r = find(end, false);
     }
 }
 
-// Beside the sort that precedes it in the stream: neither needs the other.  What follows
+// Beside the kernel that precedes it in the stream: neither needs the other.  What follows
 // waits for both.
 __global__ void __launch_bounds__(256) k_fill_absent(const FillArgs a) {
-    __shared__ uint32_t s_bits[8];
-    fill_absent(a, blockIdx.x, nullptr, 0, 0, s_bits);
+    fill_absent(a, a.first + blockIdx.x);
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
@@ -168,16 +180,21 @@ __global__ void __launch_bounds__(256) k_fill_absent(const FillArgs a) {
 // its 32 tokens with an eighth of all (a broadcast from shared memory each).  The
 // CTAs behind those of the tokens fill absent rows.
 constexpr uint32_t kRankMax = 8192;
+constexpr uint32_t kFewTokens = 2048;      // every CTA that fills looks at them itself
 
 __global__ void __launch_bounds__(256) k_token_rank(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys,
-                                                    uint32_t *order, const FillArgs fill) {
+                                                    uint32_t *order, uint32_t *status, uint32_t *counters, uint32_t count,
+                                                    const FillArgs fill) {
     extern __shared__ __align__(16) uint32_t s_keys[];   // n rounded up to 32
     __shared__ uint32_t s_rank[8][32];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = (n + 31) / 32;
     if (blockIdx.x >= groups) {
-        fill_absent(fill, blockIdx.x - groups, tokens, bytes, n, s_rank[0]);
+        fill_absent(fill, blockIdx.x - groups);
         return;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // rows are filled meanwhile
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;              // of the call: this sort cannot fail
+    for (uint32_t c = blockIdx.x * 256 + threadIdx.x; c < count; c += groups * 256) counters[c] = 0;
     for (uint32_t i = threadIdx.x; i < groups * 32; i += 256)
         s_keys[i] = i < n ? token_key(token_at(tokens, bytes, i), vocab) : kNoKey;   // behind every token
     __syncthreads();
@@ -224,6 +241,7 @@ template <typename T> struct EmbedSumArgs {
     const uint32_t *keys, *order;    // sorted
     const uint32_t *status;          // of the sort; null: it cannot fail
     float *partials;                 // [chunks][2][slabs * lanes][N]: sums up to a chunk's end and from its start
+    uint32_t *counters;              // [chunks][slabs], zeros: parts of a run that began in the chunk
     int64_t d_stride, out_stride;
     float scale;
     bool accumulate;
@@ -247,8 +265,14 @@ template <typename T, int MODE> struct RowSum {
     }
     __device__ __forceinline__ void add(const float *f) {
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const float4 x = reinterpret_cast<const float4 *>(f)[i];
+        for (int i = 0; i < N / 4; ++i) add4(i, reinterpret_cast<const float4 *>(f)[i]);
+    }
+    __device__ __forceinline__ void add_other(const float *f) {       // of another CTA: from L2
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) add4(i, __ldcg(reinterpret_cast<const float4 *>(f) + i));
+    }
+    __device__ __forceinline__ void add4(int i, const float4 &x) {
+        {
             p[2 * i] = add2(p[2 * i], pair(x.x, x.y));
             p[2 * i + 1] = add2(p[2 * i + 1], pair(x.z, x.w));
         }
@@ -285,19 +309,24 @@ template <typename T, int MODE> struct RowSum {
 };
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kEmbedThreads) k_embed_sum(const EmbedSumArgs<T> a) {
+__global__ void __launch_bounds__(kEmbedThreads, 4) k_embed_sum(const EmbedSumArgs<T> a) {
     constexpr int N = Wide<T>::kCount, U = kLoads<MODE>;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // the join looks at the keys meanwhile
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // rows are filled meanwhile
     if (a.status != nullptr && *a.status != 0) {       // the sort gave up, its results are void: all rows are NaN
-        for (uint32_t r = blockIdx.x * 8 + (threadIdx.x >> 5); r < a.vocab; r += gridDim.x * 8)
+        for (uint32_t r = blockIdx.x; r < a.vocab; r += gridDim.x)
             fill_span(reinterpret_cast<char *>(a.out + static_cast<int64_t>(r) * a.out_stride), static_cast<int64_t>(a.width) * sizeof(T), 0x7FFF7FFFu);
         return;
     }
-    __shared__ uint32_t s_key[kMaxUnits * kMaxPer + 2], s_order[kMaxUnits * kMaxPer];   // s_key[0]: the key before the chunk
+    __shared__ uint32_t s_key[kMaxChunk + 2], s_order[kMaxChunk];   // s_key[0]: the key before the chunk
     __shared__ __align__(16) float s_head[kEmbedThreads][N];
+    __shared__ uint32_t s_last;
     const uint32_t chunk = blockIdx.x / a.slabs, slab = blockIdx.x % a.slabs;
     const uint32_t lanes = 1u << a.log_lanes, units = kEmbedThreads >> a.log_lanes, size = units * a.per;
     const uint32_t base = chunk * size, count = min(size, a.n - base), tid = threadIdx.x;
+    // keys at the ends of the chunks before and behind, to find where runs begin and end
+    const uint64_t behind_at = (static_cast<uint64_t>(chunk) + 1 + tid) * size;
+    const uint32_t key_before = tid + 1 < chunk ? a.keys[static_cast<size_t>(chunk - 1 - tid) * size - 1] : kNoKey;
+    const uint32_t key_behind = behind_at < a.n ? a.keys[behind_at] : kNoKey;
     for (uint32_t i = tid; i < count + 2; i += kEmbedThreads) {
         const uint32_t p = base + i - 1;
         s_key[i] = p < a.n ? a.keys[p] : kNoKey;
@@ -348,83 +377,83 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed_sum(const EmbedSumArgs<
         if (key != kNoKey && first) sum.store(s_head[tid]);    // the whole unit is a part of one run
     }
     __syncthreads();
-    if (!any) return;
     // Runs that go on behind the unit they began in: that unit joins their parts.
     // The chunk's first unit does so for a run that began before the chunk.
-    const bool onward = key != kNoKey && s_key[end + 1] == key;
-    uint32_t i;
-    if (unit == 0 && head) {
+    const bool onward = any && key != kNoKey && s_key[end + 1] == key;
+    const size_t row = static_cast<size_t>(a.slabs) * lanes * N;           // of partial sums
+    float *const mine = a.partials + static_cast<size_t>(chunk) * 2 * row + static_cast<size_t>(v) * N;
+    if (any && unit == 0 && head) {
         const uint32_t k0 = s_key[1];
         RowSum<T, MODE> part;
         part.clear();
         part.add(s_head[tid]);
         if (first && onward) {             // the run covers this unit
-            for (i = 1; i < units && i * a.per < count && s_key[i * a.per + 1] == k0; ++i) {
+            for (uint32_t i = 1; i < units && i * a.per < count && s_key[i * a.per + 1] == k0; ++i) {
                 part.add(s_head[(i << a.log_lanes) + (tid & (lanes - 1))]);
                 if (s_key[min((i + 1) * a.per, count)] != k0) break;
             }
         }
-        part.store(a.partials + ((static_cast<size_t>(chunk) * 2 + 1) * a.slabs * lanes + v) * N);
+        part.store(mine + row);
     }
-    if (key == kNoKey || first) return;    // nothing that began here goes on
-    if (onward) {
-        bool leaves = true;                // the chunk
-        for (i = unit + 1; i < units && i * a.per < count; ++i) {
+    if (any && key != kNoKey && !first) {  // a run that began here
+        bool leaves = onward;              // the chunk
+        for (uint32_t i = unit + 1; leaves && i < units && i * a.per < count; ++i) {
             sum.add(s_head[(i << a.log_lanes) + (tid & (lanes - 1))]);
             const uint32_t stop = min((i + 1) * a.per, count);
-            if (s_key[stop] != key || s_key[stop + 1] != key) {
-                leaves = false;
-                break;
+            leaves = s_key[stop] == key && s_key[stop + 1] == key;
+        }
+        if (leaves) sum.store(mine);
+        else if (v < a.vectors) sum.write(a, key, v);
+    }
+    // A run that crosses ends of chunks has a part in each of them.  The CTA that
+    // writes the last of these joins them, in their order.
+    const uint32_t front = s_key[1], back = s_key[count], next = s_key[count + 1];
+    const bool before = s_key[0] == front && front < a.vocab;
+    const bool behind = next == back && back < a.vocab;
+    for (int r = 0; r < 2; ++r) {          // the run at the chunk's start, and another one at its end
+        if (r == 0 ? !before : !(behind && !(before && front == back))) continue;
+        const uint32_t k = r == 0 ? front : back;
+        uint32_t from = chunk, to = chunk;
+        if (r == 0) {                      // the chunk it began in
+            for (from = chunk - 1;; from -= kEmbedThreads) {
+                const uint32_t c = from - tid;
+                const uint32_t held = __syncthreads_count(from == chunk - 1 ? key_before == k
+                                                                           : tid < from && a.keys[static_cast<size_t>(c) * size - 1] == k);
+                if (held < kEmbedThreads) {
+                    from -= held;
+                    break;
+                }
             }
         }
-        if (leaves) {
-            sum.store(a.partials + (static_cast<size_t>(chunk) * 2 * a.slabs * lanes + v) * N);
-            return;
+        if (r == 1 || (behind && front == back)) {       // the chunk it ends in
+            for (;; to += kEmbedThreads) {
+                const uint64_t p = static_cast<uint64_t>(to + 1 + tid) * size;
+                const uint32_t held = __syncthreads_count(to == chunk ? key_behind == k : p < a.n && a.keys[p] == k);
+                if (held < kEmbedThreads) {
+                    to += held;
+                    break;
+                }
+            }
         }
-    }
-    if (v < a.vectors) sum.write(a, key, v);
-}
-
-// Joins the runs that cross ends of chunks: the CTA of the chunk in which a run
-// began adds the parts of those behind it, each group of lanes some of them.
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kEmbedThreads) k_embed_join(const EmbedSumArgs<T> a) {
-    constexpr int N = Wide<T>::kCount;
-    const uint32_t chunk = blockIdx.x / a.slabs, slab = blockIdx.x % a.slabs;
-    const uint32_t lanes = 1u << a.log_lanes, units = kEmbedThreads >> a.log_lanes, size = units * a.per;
-    const uint32_t base = chunk * size, end = base + size;
-    // the keys were there before the sums began: who has nothing to join is known without them
-    const uint32_t key = a.keys[end - 1], next = a.keys[end], first = a.keys[base], before = base > 0 ? a.keys[base - 1] : kNoKey;
-    const bool failed = a.status != nullptr && *a.status != 0;
-    const bool mine = !failed && key < a.vocab && next == key && !(first == key && before == key);
-    uint32_t last = chunk;                 // the chunk that the run ends in
-    if (mine) {
-        for (uint32_t c0 = chunk + 1;; c0 += kEmbedThreads) {
-            const uint64_t p = static_cast<uint64_t>(c0 + threadIdx.x) * size;
-            const uint32_t held = __syncthreads_count(p < a.n && a.keys[p] == key);
-            last += held;
-            if (held < kEmbedThreads) break;
-        }
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!mine) return;
-    __shared__ __align__(16) float s_part[kEmbedThreads][N];
-    const uint32_t tid = threadIdx.x, unit = tid >> a.log_lanes, v = slab * lanes + (tid & (lanes - 1));
-    const size_t row = static_cast<size_t>(a.slabs) * lanes * N;
-    RowSum<T, MODE> sum;
-    sum.clear();
-    if (unit == 0) sum.add(a.partials + static_cast<size_t>(chunk) * 2 * row + static_cast<size_t>(v) * N);
-#pragma unroll 4
-    for (uint32_t c = chunk + 1 + unit; c <= last; c += units) sum.add(a.partials + (static_cast<size_t>(c) * 2 + 1) * row + static_cast<size_t>(v) * N);
-    if (last - chunk > 1) {
-        sum.store(s_part[tid]);
+        __threadfence();                   // this thread's part, before the count
         __syncthreads();
-        if (unit != 0) return;
-        for (uint32_t i = 1; i < min(units, last - chunk); ++i) sum.add(s_part[(i << a.log_lanes) + tid]);
-    } else if (unit != 0) {
-        return;
+        if (tid == 0) s_last = atomicAdd(a.counters + static_cast<size_t>(from) * a.slabs + slab, 1u) == to - from;
+        __syncthreads();
+        if (!s_last) continue;
+        __threadfence();
+        sum.clear();
+        const float *parts = a.partials + static_cast<size_t>(v) * N;
+        if (unit == 0) sum.add_other(parts + static_cast<size_t>(from) * 2 * row);
+#pragma unroll 4
+        for (uint32_t c = from + 1 + unit; c <= to; c += units) sum.add_other(parts + (static_cast<size_t>(c) * 2 + 1) * row);
+        sum.store(s_head[tid]);
+        __syncthreads();
+        if (unit == 0) {
+            for (uint32_t i = 1; i < min(units, to - from); ++i) sum.add(s_head[(i << a.log_lanes) + tid]);
+            if (v < a.vectors) sum.write(a, k, v);
+        }
+        __syncthreads();
     }
-    if (v < a.vectors) sum.write(a, key, v);
 }
 
 // A launch that may start while the kernel before it in the stream runs, as soon as that allows it.
@@ -446,7 +475,7 @@ template <typename A> int launch_early(void (*kernel)(const A), uint32_t ctas, c
 // depends on nothing else.
 struct EmbedPlan {
     uint32_t vectors_max, log_lanes, slabs, per, chunks;
-    size_t keys, order, keys_in, order_in, radix, bits, partials, total;
+    size_t keys, order, keys_in, order_in, radix, bits, partials, counters, total;
 };
 
 EmbedPlan embed_plan(uint32_t n, uint32_t vocab, uint32_t width, int size) {
@@ -459,7 +488,7 @@ EmbedPlan embed_plan(uint32_t n, uint32_t vocab, uint32_t width, int size) {
     const uint32_t lanes = 1u << p.log_lanes, units = kEmbedThreads / lanes;
     p.slabs = (p.vectors_max + lanes - 1) / lanes;
     // longer pieces leave fewer partial sums, shorter ones fill the device
-    p.per = kMaxPer;
+    p.per = std::min(kMaxPer, kMaxChunk / units);
     while (p.per > 8 && static_cast<uint64_t>((n + units * p.per - 1) / (units * p.per)) * p.slabs < kFillCtas) p.per /= 2;
     p.chunks = (n + units * p.per - 1) / (units * p.per);
     const size_t bytes = align_up(static_cast<size_t>(n) * 4, kWsAlign);
@@ -467,14 +496,16 @@ EmbedPlan embed_plan(uint32_t n, uint32_t vocab, uint32_t width, int size) {
     if (n > kRankMax) {          // the sort's header comes first: its status is the call's
         p.radix = at;
         at += align_up(radix_layout(n, true, 4).total, kWsAlign);
-        p.keys_in = at;
-        at += bytes;
         p.order_in = at;
+        at += bytes;
+    } else {
+        at += kWsAlign;          // the status alone
+    }
+    if (n > kFewTokens) {
+        p.keys_in = at;
         at += bytes;
         p.bits = at;
         at += align_up((static_cast<size_t>(vocab) + 31) / 32 * 4, kWsAlign);
-    } else {
-        at += kWsAlign;          // a status that is always GSORT_OK
     }
     p.keys = at;
     at += bytes;
@@ -482,6 +513,8 @@ EmbedPlan embed_plan(uint32_t n, uint32_t vocab, uint32_t width, int size) {
     at += bytes;
     p.partials = at;
     if (p.chunks > 1) at += static_cast<size_t>(p.chunks) * 2 * p.slabs * lanes * (16 / size) * 4;
+    p.counters = at;
+    if (p.chunks > 1) at += static_cast<size_t>(p.chunks) * p.slabs * 4;
     p.total = align_up(at, kWsAlign);
     return p;
 }
@@ -509,7 +542,7 @@ int launch_embed(const EmbedLaunch &L) {
         a.vocab = static_cast<uint32_t>(L.vocab);
         a.width = static_cast<uint32_t>(L.width);
         auto start = [&](auto m) {
-            constexpr int MODE = decltype(m)::value, U = EMBED_U;
+            constexpr int MODE = decltype(m)::value, U = 4;
             a.log_lanes = lanes_for(a.vectors, U);
             const uint32_t step = U << a.log_lanes, rows = kEmbedThreads >> a.log_lanes;
             a.chunks = (a.vectors + step - 1) / step;
@@ -540,40 +573,57 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
     fill.row_bytes = L.width * float_bytes(L.dtype);
     fill.stride = L.table_stride * float_bytes(L.dtype);
     fill.vocab = vocab;
-    fill.rows = std::min(256u, std::max(8u, (vocab / kFillCtas + 7) / 8 * 8));
+    fill.tokens = L.tokens;
+    fill.token_bytes = L.token_bytes;
+    fill.n = n;
+    fill.rows = static_cast<uint32_t>(std::min<int64_t>(256, std::max<int64_t>(1, kFillBytes / fill.row_bytes)));
     const uint32_t fill_ctas = L.accumulate ? 0 : (vocab + fill.rows - 1) / fill.rows;
-    if (n <= kRankMax) {
-        const uint32_t groups = (n + 31) / 32;
-        if (groups + fill_ctas == 0) return GSORT_OK;
-        k_token_rank<<<groups + fill_ctas, 256, groups * 32 * 4, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys, order, fill);
+    uint32_t *counters = reinterpret_cast<uint32_t *>(L.ws + plan.counters), *status = reinterpret_cast<uint32_t *>(L.ws + kHdrStatus);
+    const uint64_t sums = static_cast<uint64_t>(plan.chunks) * plan.slabs;
+    const uint32_t count = plan.chunks > 1 ? static_cast<uint32_t>(sums) : 0;
+    if (sums > 0x7FFFFFFF) return GSORT_ETOOBIG;
+    const uint32_t groups = (n + 31) / 32;
+    auto start_fill = [&](uint32_t from, uint32_t to) {
+        fill.first = from;
+        return from < to ? launch_early(k_fill_absent, to - from, L.stream, fill) : static_cast<int>(GSORT_OK);
+    };
+    // of the CTAs that fill, those before the sums
+    const int64_t beside = n <= kFewTokens ? kBesideFew : n <= kRankMax ? kBesideCounting : cluster_sort_applies(n, 4, 0, kNoStall, 1) ? kBesideCluster : 0;
+    const uint32_t filled = n == 0 ? fill_ctas : static_cast<uint32_t>(std::min<int64_t>(fill_ctas, beside / (fill.row_bytes * fill.rows)));
+    if (n <= kFewTokens) {
+        if (groups == 0 && fill_ctas == 0) return GSORT_OK;
+        k_token_rank<<<groups + filled, 256, groups * 32 * 4, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys, order, status, counters, count, fill);
         if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
     } else {
         uint32_t *keys_in = reinterpret_cast<uint32_t *>(L.ws + plan.keys_in);
-        uint32_t *order_in = reinterpret_cast<uint32_t *>(L.ws + plan.order_in);
+        uint32_t *order_in = n > kRankMax ? reinterpret_cast<uint32_t *>(L.ws + plan.order_in) : nullptr;
         uint32_t *bits = L.accumulate ? nullptr : reinterpret_cast<uint32_t *>(L.ws + plan.bits);
         if (bits && cudaMemsetAsync(bits, 0, (static_cast<size_t>(vocab) + 31) / 32 * 4, L.stream) != cudaSuccess) return GSORT_ECUDA;
-        k_token_keys<<<(n + 255) / 256, 256, 0, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys_in, order_in, bits);
+        k_token_keys<<<(n + 255) / 256, 256, 0, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys_in, order_in, bits, counters, count);
         if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
-        RadixLaunch R{};
-        R.keys_in = keys_in;
-        R.keys_out = keys;
-        R.vals_in = order_in;
-        R.vals_out = order;
-        R.n = n;
-        R.kind = GSORT_KEY_U32;
-        R.end_bit = 32 - __builtin_clz(vocab);       // what is no token has the key `vocab`
-        R.ws = L.ws + plan.radix;
-        R.spin_limit = kDefaultSpinLimit;
-        R.stall_tile = kNoStall;
-        R.stream = L.stream;
-        R.sm_count = L.sm_count;
-        R.next_early = fill_ctas > 0;
-        const int rc = launch_radix(R);
-        if (rc != GSORT_OK) return rc;
-        if (fill_ctas > 0) {
-            fill.bits = bits;
-            if (launch_early(k_fill_absent, fill_ctas, L.stream, fill) != GSORT_OK) return GSORT_ECUDA;
+        if (n <= kRankMax) {
+            k_token_rank<<<groups, 256, groups * 32 * 4, L.stream>>>(keys_in, 4, n, vocab, keys, order, status, nullptr, 0, fill);
+            if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
+        } else {
+            RadixLaunch R{};
+            R.keys_in = keys_in;
+            R.keys_out = keys;
+            R.vals_in = order_in;
+            R.vals_out = order;
+            R.n = n;
+            R.kind = GSORT_KEY_U32;
+            R.end_bit = 32 - __builtin_clz(vocab);       // what is no token has the key `vocab`
+            R.ws = L.ws + plan.radix;
+            R.spin_limit = kDefaultSpinLimit;
+            R.stall_tile = kNoStall;
+            R.stream = L.stream;
+            R.sm_count = L.sm_count;
+            R.next_early = fill_ctas > 0;
+            const int rc = launch_radix(R);
+            if (rc != GSORT_OK) return rc;
         }
+        fill.bits = bits;
+        if (start_fill(0, filled) != GSORT_OK) return GSORT_ECUDA;
     }
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
@@ -584,8 +634,9 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
         a.out = static_cast<T *>(L.d_table);
         a.keys = keys;
         a.order = order;
-        a.status = n > kRankMax ? reinterpret_cast<const uint32_t *>(L.ws + plan.radix + kHdrStatus) : nullptr;
+        a.status = n > kRankMax ? status : nullptr;
         a.partials = reinterpret_cast<float *>(L.ws + plan.partials);
+        a.counters = counters;
         a.d_stride = L.d_stride;
         a.out_stride = L.table_stride;
         a.scale = L.scale;
@@ -602,7 +653,7 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
             if (a.chunks == 0) return static_cast<int>(GSORT_OK);
             k_embed_sum<T, MODE><<<a.chunks * a.slabs, kEmbedThreads, 0, L.stream>>>(a);
             if (cudaGetLastError() != cudaSuccess) return static_cast<int>(GSORT_ECUDA);
-            return a.chunks > 1 ? launch_early(k_embed_join<T, MODE>, (a.chunks - 1) * a.slabs, L.stream, a) : static_cast<int>(GSORT_OK);
+            return start_fill(filled, fill_ctas);
         };
         if (L.width % N == 0 && aligned(L.d_out, 16) && aligned(L.d_table, 16) && L.d_stride % N == 0 && L.table_stride % N == 0) {
             a.vectors = a.width / N;

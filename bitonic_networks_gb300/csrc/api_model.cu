@@ -149,26 +149,31 @@ bool tensors_clash(const void *const *in, void *const *out, const int64_t *eleme
         uintptr_t begin, end;
         bool written;
     };
-    auto before = [](const Range &x, const Range &y) { return x.begin < y.begin; };
-    // each of the two lists is mostly in order already
-    std::vector<Range> read, wrote, ranges;
-    read.reserve(tensors);
-    wrote.reserve(out != nullptr ? tensors + 2 : 2);
+    // each of the two lists is mostly in order already, and taken as it comes
+    std::vector<Range> lists[2];             // read (and written over, where the output is the input), written
+    lists[0].reserve(tensors);
+    lists[1].reserve(out != nullptr ? tensors + 2 : 2);
+    bool sorted[2] = {true, true};
+    auto add = [&](int l, const void *p, uintptr_t n, bool written) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (n == 0) return;
+        sorted[l] = sorted[l] && (lists[l].empty() || lists[l].back().begin <= a);
+        lists[l].push_back({a, a + n, written});
+    };
     for (int64_t i = 0; i < tensors; ++i) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]), n = static_cast<uintptr_t>(elements[i]) * float_bytes(dtypes[i]);
-        if (n == 0) continue;
+        const uintptr_t n = static_cast<uintptr_t>(elements[i]) * float_bytes(dtypes[i]);
         const bool same = out != nullptr && in[i] == out[i];
-        read.push_back({a, a + n, same});
-        if (out != nullptr && !same) wrote.push_back({reinterpret_cast<uintptr_t>(out[i]), reinterpret_cast<uintptr_t>(out[i]) + n, true});
+        add(0, in[i], n, same);
+        if (out != nullptr && !same) add(1, out[i], n, true);
     }
-    for (const Span &s : {norm, ws})
-        if (s.bytes > 0) wrote.push_back({reinterpret_cast<uintptr_t>(s.p), reinterpret_cast<uintptr_t>(s.p) + s.bytes, true});
-    for (std::vector<Range> *list : {&read, &wrote})
-        if (!std::is_sorted(list->begin(), list->end(), before)) std::sort(list->begin(), list->end(), before);
-    ranges.resize(read.size() + wrote.size());
-    std::merge(read.begin(), read.end(), wrote.begin(), wrote.end(), ranges.begin(), before);
+    add(1, norm.p, norm.bytes, true);
+    add(1, ws.p, ws.bytes, true);
+    for (int l = 0; l < 2; ++l)
+        if (!sorted[l]) std::sort(lists[l].begin(), lists[l].end(), [](const Range &x, const Range &y) { return x.begin < y.begin; });
     uintptr_t end = 0, written = 0;      // the furthest end of any range so far, and of a written one
-    for (const Range &r : ranges) {
+    for (size_t i = 0, k = 0; i < lists[0].size() || k < lists[1].size();) {
+        const bool first = k == lists[1].size() || (i < lists[0].size() && lists[0][i].begin < lists[1][k].begin);
+        const Range &r = first ? lists[0][i++] : lists[1][k++];
         if (r.begin < written || (r.written && r.begin < end)) return true;
         end = std::max(end, r.end);
         if (r.written) written = std::max(written, r.end);

@@ -55,7 +55,7 @@ class WithoutGil {
 
 // ---------------------------------------------------------------- arguments
 const Tensor &tensor(PyObject *o, const char *name) {
-    if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a tensor", name);
+    if (!THPVariable_CheckExact(o) && !THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a tensor", name);
     return THPVariable_Unpack(o);
 }
 

@@ -5,11 +5,14 @@
 //
 // The tensors' addresses and sizes travel as a kernel parameter (up to 1000 of
 // them in a launch), so that a call needs no copy to the device and can be captured
-// in a graph.  Tensors are cut into chunks of 16-byte vectors at 16-byte boundaries, and
-// resident CTAs take them in turn, in steps of 16 KB of which the next one is loaded
-// before the last is worked on.  A thread's squares of a step are summed in 32 bits, all else
-// in 64; each CTA's sum goes to a slot of its own, so that the order is given by the
-// sizes.  A step whose squares leave the 32-bit range is summed in 64 bits.
+// in a graph.  What a tensor has between its first and last 16-byte boundary is cut into
+// chunks, which resident CTAs take in turn, in steps of 16 KB: bulk copies bring the next
+// two steps to shared memory while one is worked on, so that 4 CTAs keep up to 192 KB of an
+// SM's loads under way.  The few elements before the first and behind the last boundary of
+// each tensor are taken by a thread each, while the first copies run.
+// A thread's squares of a step are summed in 32 bits, all else in 64; each CTA's sum goes
+// to a slot of its own, so that the order is given by the sizes.  A step whose squares leave
+// the 32-bit range is summed in 64 bits.
 //
 // The memory bounds both kernels.  Clipping reads everything twice, as the norm has to be
 // known before the first product; it takes the chunks backwards, so that what was
@@ -26,10 +29,13 @@ constexpr int kNormThreads = 256;
 constexpr int kNormVectors = 4;                   // vectors of a thread in a step
 constexpr uint32_t kStep = kNormThreads * kNormVectors;     // vectors of a step
 constexpr int kFewTensors = 32, kManyTensors = 1000;
+constexpr int kStages = 3;
 constexpr uint32_t kNormCtas = 608;               // 4 to an SM of a GB300
+constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier
 constexpr uint64_t kSizeMask = (1ull << 56) - 1;
 // below it a thread's sum of squares may have lost what is under the 32-bit range
 constexpr float kTinySum = 1.2621774483536189e-29f;         // 2^-96
+constexpr size_t kNormSmem = kStages * kStep * 16;
 
 template <int M> struct TensorTable {
     const void *in[M];
@@ -40,27 +46,54 @@ template <int M> struct TensorTable {
     uint32_t steps;          // of a chunk
 };
 
-__host__ __device__ __forceinline__ int type_bytes(uint32_t type) { return type == GSORT_F32 ? 4 : 2; }
+__host__ __device__ __forceinline__ uint32_t type_bytes(uint32_t type) { return type == GSORT_F32 ? 4 : 2; }
 
-// A step: vectors [low, high) from `from` on are whole; the tensor's first and last
-// vector may be cut by its start or end.
-struct Step {
-    const char *from;        // at a 16-byte boundary, at most 15 bytes before the tensor
-    uint32_t tensor, type;
-    uint32_t low, high, vectors;
-    int64_t begin, size;     // bytes from the tensor's start to `from`, and of the tensor
+// How a tensor lies: bytes before its first 16-byte boundary, whole vectors from there on,
+// bytes behind its last boundary.
+struct Span {
+    uint32_t type, head, tail;
+    uint64_t vectors;
 };
 
-// The steps of a CTA, one after another.
-template <int M, bool BACKWARDS> struct Steps {
+__host__ __device__ __forceinline__ Span span_of(const void *p, uint64_t word) {
+    Span s;
+    s.type = static_cast<uint32_t>(word >> 56);
+    const uint64_t bytes = (word & kSizeMask) * type_bytes(s.type), before = -reinterpret_cast<uintptr_t>(p) & 15;
+    s.head = static_cast<uint32_t>(before < bytes ? before : bytes);
+    s.vectors = (bytes - s.head) / 16;
+    s.tail = static_cast<uint32_t>(bytes - s.head - s.vectors * 16);
+    return s;
+}
+
+// A step: `vectors` (0: the last one is behind) from a tensor's byte `begin` on.
+struct Step {
+    uint32_t tensor, type, vectors;
+    int64_t begin;
+};
+
+// The steps of a CTA, brought to shared memory in turn.
+template <int M, bool BACKWARDS> struct Ring {
     const TensorTable<M> &t;
-    uint32_t chunk, step;
+    uint4 (*data)[kStep];
+    Step *steps;             // [kStages]
+    uint64_t *full;          // [kStages], a barrier for each stage
+    uint32_t chunk, step;    // of the next copy; thread 0
 
-    __device__ __forceinline__ explicit Steps(const TensorTable<M> &table) : t(table), chunk(blockIdx.x), step(0) {}
-
-    __device__ __forceinline__ bool next(Step &s) {
+    __device__ __forceinline__ void start() {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+            chunk = blockIdx.x;
+            step = 0;
+            for (int i = 0; i < kStages; ++i) copy(i);
+        }
+        __syncthreads();     // the barriers are there
+    }
+    // Thread 0: the next step's copy into a stage.
+    __device__ __forceinline__ void copy(int stage) {
         const uint32_t chunks = t.first[t.tensors];
-        while (chunk < chunks) {
+        Step s{};
+        const char *from = nullptr;
+        while (s.vectors == 0 && chunk < chunks) {
             const uint32_t c = BACKWARDS ? chunks - 1 - chunk : chunk;
             uint32_t i = 0, high = t.tensors - 1;
             while (i < high) {
@@ -68,96 +101,97 @@ template <int M, bool BACKWARDS> struct Steps {
                 if (t.first[mid] <= c) i = mid;
                 else high = mid - 1;
             }
-            const uint64_t word = t.size[i];
-            s.tensor = i;
-            s.type = static_cast<uint32_t>(word >> 56);
-            s.size = static_cast<int64_t>(word & kSizeMask) * type_bytes(s.type);
-            const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(t.in[i])) & 15;
-            const int64_t v = (static_cast<int64_t>(c - t.first[i]) * t.steps + step) * kStep;
-            const int64_t left = (s.size + shift + 15) / 16 - v;
-            if (left > 0) {
-                s.begin = v * 16 - shift;
-                s.from = static_cast<const char *>(t.in[i]) + s.begin;
-                s.vectors = static_cast<uint32_t>(min(left, static_cast<int64_t>(kStep)));
-                s.low = s.begin < 0 ? 1 : 0;
-                s.high = s.begin + static_cast<int64_t>(s.vectors) * 16 > s.size ? s.vectors - 1 : s.vectors;
-                if (++step == t.steps) {
-                    step = 0;
-                    chunk += gridDim.x;
-                }
-                return true;
+            const Span span = span_of(t.in[i], t.size[i]);
+            const uint64_t v = (static_cast<uint64_t>(c - t.first[i]) * t.steps + step) * kStep;
+            if (v < span.vectors) {
+                s.tensor = i;
+                s.type = span.type;
+                s.vectors = static_cast<uint32_t>(min(span.vectors - v, static_cast<uint64_t>(kStep)));
+                s.begin = static_cast<int64_t>(span.head + v * 16);
+                from = static_cast<const char *>(t.in[i]) + s.begin;
             }
-            step = 0;
-            chunk += gridDim.x;
+            if (++step == t.steps || v + kStep >= span.vectors) {
+                step = 0;
+                chunk += gridDim.x;
+            }
         }
-        return false;
+        steps[stage] = s;
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&full[stage], s.vectors * 16);
+        if (s.vectors > 0) bulk_load(data[stage], from, s.vectors * 16, &full[stage]);
+    }
+    // Calls f(step, vectors) for every step; false if a copy did not come.
+    template <typename F> __device__ __forceinline__ bool run(F &&f) {
+        for (uint32_t k = 0;; ++k) {
+            const int stage = k % kStages;
+            const bool there = mbar_wait_bounded(&full[stage], (k / kStages) & 1, kWaitLimit);
+            if (there && steps[stage].vectors == 0) return true;
+            if (there) f(steps[stage], data[stage]);
+            if (__syncthreads_or(!there)) {        // leave once no copy can be under way any more
+                for (uint32_t i = k; i < k + kStages; ++i) mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1, kWaitLimit);
+                return false;
+            }
+            if (threadIdx.x == 0) copy(stage);
+        }
     }
 };
 
-__device__ __forceinline__ void load_step(const Step &s, uint4 (&q)[kNormVectors]) {
-#pragma unroll
-    for (int u = 0; u < kNormVectors; ++u) {
-        const uint32_t v = threadIdx.x + u * kNormThreads;
-        q[u] = v >= s.low && v < s.high ? reinterpret_cast<const uint4 *>(s.from)[v] : make_uint4(0, 0, 0, 0);
+template <int M, bool BACKWARDS> __device__ __forceinline__ Ring<M, BACKWARDS> make_ring(const TensorTable<M> &t) {
+    extern __shared__ __align__(128) uint4 s_data[];
+    __shared__ Step s_steps[kStages];
+    __shared__ __align__(8) uint64_t s_full[kStages];
+    return Ring<M, BACKWARDS>{t, reinterpret_cast<uint4 (*)[kStep]>(s_data), s_steps, s_full, 0, 0};
+}
+
+// Calls f(tensor, type, first element, elements) for the ends of tensors that this thread takes.
+template <int M, typename F> __device__ __forceinline__ void for_ends(const TensorTable<M> &t, F &&f) {
+    for (uint32_t i = blockIdx.x + gridDim.x * threadIdx.x; i < 2 * t.tensors; i += gridDim.x * kNormThreads) {
+        const uint32_t tensor = i / 2;
+        const Span s = span_of(t.in[tensor], t.size[tensor]);
+        const uint32_t size = type_bytes(s.type);
+        if (i % 2 == 0 && s.head > 0) f(tensor, s.type, static_cast<uint64_t>(0), s.head / size);
+        if (i % 2 == 1 && s.tail > 0) f(tensor, s.type, (s.head + s.vectors * 16) / size, s.tail / size);
     }
 }
 
-// The cut vector that this thread takes: threads 0 and 1 take the first and the last one.
-__device__ __forceinline__ bool takes_cut(const Step &s, uint32_t &v) {
-    v = threadIdx.x == 0 ? 0 : s.vectors - 1;
-    return threadIdx.x == 0 ? s.low > 0 : threadIdx.x == 1 && s.high < s.vectors && (s.low == 0 || s.vectors > 1);
-}
-
-// The elements of a cut vector, zeros beside the tensor.
-template <typename T> __device__ __forceinline__ uint4 cut_vector(const Step &s, uint32_t v) {
-    constexpr int N = Wide<T>::kCount;
-    const int64_t b = s.begin + static_cast<int64_t>(v) * 16;        // in bytes from the tensor's start
-    const T *p = reinterpret_cast<const T *>(s.from) + v * N;
-    float f[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t k = b + i * static_cast<int64_t>(sizeof(T));
-        f[i] = k >= 0 && k < s.size ? to_f32(p[i]) : 0.0f;
+// Calls f with a null pointer to the element type.
+template <typename F> __device__ __forceinline__ void with_type(uint32_t type, F &&f) {
+    switch (type) {
+        case GSORT_F32: f(static_cast<float *>(nullptr)); break;
+        case GSORT_BF16: f(static_cast<__nv_bfloat16 *>(nullptr)); break;
+        default: f(static_cast<__half *>(nullptr)); break;
     }
-    uint4 q;
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, pair(f[2 * i], f[2 * i + 1]));
-    return q;
 }
 
 // The sum of this thread's squares of a step.
-template <typename T> __device__ __forceinline__ double square_sum(const Step &s, const uint4 (&q)[kNormVectors]) {
+template <typename T> __device__ __forceinline__ double square_sum(uint32_t vectors, const uint4 *data) {
     constexpr int N = Wide<T>::kCount;
-    uint32_t cut, any = 0;
-    uint4 edge = make_uint4(0, 0, 0, 0);
-    if (takes_cut(s, cut)) edge = cut_vector<T>(s, cut);
+    uint32_t any = 0;
     Pair sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
-    auto add = [&](const uint4 &x) {
-        any |= x.x | x.y | x.z | x.w;
+#pragma unroll
+    for (int u = 0; u < kNormVectors; ++u) {
+        const uint32_t v = threadIdx.x + u * kNormThreads;
+        const uint4 q = v < vectors ? data[v] : make_uint4(0, 0, 0, 0);
+        any |= q.x | q.y | q.z | q.w;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            const Pair y = Wide<T>::pair_of(x, i);
+            const Pair y = Wide<T>::pair_of(q, i);
             sum[i % 2] = fma2(y, y, sum[i % 2]);
         }
-    };
-#pragma unroll
-    for (int u = 0; u < kNormVectors; ++u) add(q[u]);
-    add(edge);
+    }
     const Pair both = add2(sum[0], sum[1]);
     const float total = both.f.x + both.f.y;
     if (total >= kTinySum && total < -kNegInf) return total;
     if ((any & (sizeof(T) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) return 0.0;
     double d = 0.0;          // squares beyond the 32-bit range, infinities and NaN
-    auto add_wide = [&](const uint4 &x) {
+    for (uint32_t v = threadIdx.x; v < vectors; v += kNormThreads) {
+        const uint4 q = data[v];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const double y = to_f32(Wide<T>::element(x, i));
+            const double y = to_f32(Wide<T>::element(q, i));
             d = fma(y, y, d);
         }
-    };
-#pragma unroll
-    for (int u = 0; u < kNormVectors; ++u) add_wide(q[u]);
-    add_wide(edge);
+    }
     return d;
 }
 
@@ -181,25 +215,22 @@ __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.w
 template <int M>
 __global__ void __launch_bounds__(kNormThreads, 4) k_square_sums(const __grid_constant__ TensorTable<M> t, double *slots) {
     let_next_start();
+    Ring<M, false> ring = make_ring<M, false>(t);
+    ring.start();
     double d = 0.0;
-    Steps<M, false> steps(t);
-    Step now, then;
-    uint4 q[kNormVectors];
-    bool more = steps.next(now);
-    if (more) load_step(now, q);
-    while (more) {
-        uint4 x[kNormVectors];
-#pragma unroll
-        for (int u = 0; u < kNormVectors; ++u) x[u] = q[u];
-        more = steps.next(then);
-        if (more) load_step(then, q);
-        switch (now.type) {
-            case GSORT_F32: d += square_sum<float>(now, x); break;
-            case GSORT_BF16: d += square_sum<__nv_bfloat16>(now, x); break;
-            default: d += square_sum<__half>(now, x); break;
-        }
-        now = then;
-    }
+    for_ends(t, [&](uint32_t tensor, uint32_t type, uint64_t first, uint32_t count) {
+        with_type(type, [&](auto *p) {
+            using T = std::remove_pointer_t<decltype(p)>;
+            for (uint32_t k = 0; k < count; ++k) {
+                const double x = to_f32(static_cast<const T *>(t.in[tensor])[first + k]);
+                d = fma(x, x, d);
+            }
+        });
+    });
+    const bool whole = ring.run([&](const Step &s, const uint4 *data) {
+        with_type(s.type, [&](auto *p) { d += square_sum<std::remove_pointer_t<decltype(p)>>(s.vectors, data); });
+    });
+    if (!whole) d = __longlong_as_double(0x7FF8000000000000ll);      // a norm without all of its parts is none
     d = cta_sum(d);
     wait_for_last();         // so that who waits for this kernel has waited for those before it
     if (threadIdx.x == 0) slots[blockIdx.x] = d;
@@ -217,64 +248,50 @@ __global__ void __launch_bounds__(kNormThreads) k_norm(const double *slots, uint
     if (threadIdx.x == 0) *out = static_cast<float>(norm);
 }
 
-template <typename T> __device__ __forceinline__ void scale_step(const Step &s, uint4 (&q)[kNormVectors], void *tensor, float by) {
+template <typename T> __device__ __forceinline__ void scale_step(const Step &s, const uint4 *data, void *tensor, float by) {
     constexpr int N = Wide<T>::kCount;
     char *to = static_cast<char *>(tensor) + s.begin;
-    const bool same = (reinterpret_cast<uintptr_t>(to) & 15) == 0;
-    auto elements = [&](uint32_t v) {          // a vector's elements that are the tensor's, one by one
-        const int64_t b = s.begin + static_cast<int64_t>(v) * 16;
-        for (int i = 0; i < N; ++i) {
-            const int64_t k = b + i * static_cast<int64_t>(sizeof(T));
-            if (k >= 0 && k < s.size) reinterpret_cast<T *>(to)[v * N + i] = from_f32<T>(to_f32(reinterpret_cast<const T *>(s.from)[v * N + i]) * by);
-        }
-    };
-    if (!same) {             // the output lies differently
-        for (uint32_t v = threadIdx.x; v < s.vectors; v += kNormThreads) elements(v);
+    if ((reinterpret_cast<uintptr_t>(to) & 15) != 0) {         // the output lies differently
+        const T *from = reinterpret_cast<const T *>(data);
+        for (uint32_t i = threadIdx.x; i < s.vectors * N; i += kNormThreads) reinterpret_cast<T *>(to)[i] = from_f32<T>(to_f32(from[i]) * by);
         return;
     }
 #pragma unroll
     for (int u = 0; u < kNormVectors; ++u) {
         const uint32_t v = threadIdx.x + u * kNormThreads;
+        if (v >= s.vectors) break;
+        uint4 q = data[v];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q[u], i, mul2(Wide<T>::pair_of(q[u], i), pair(by, by)));
-        if (v >= s.low && v < s.high) reinterpret_cast<uint4 *>(to)[v] = q[u];
+        for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, mul2(Wide<T>::pair_of(q, i), pair(by, by)));
+        reinterpret_cast<uint4 *>(to)[v] = q;
     }
-    uint32_t cut;
-    if (takes_cut(s, cut)) elements(cut);
 }
 
 template <int M>
 __global__ void __launch_bounds__(kNormThreads, 4)
 k_clip(const __grid_constant__ TensorTable<M> t, const double *slots, uint32_t count, float scale, float max_norm, float *norm_out) {
     let_next_start();
+    Ring<M, true> ring = make_ring<M, true>(t);
+    ring.start();            // the gradients were there before the sums
     wait_for_last();
     const double norm = norm_of(slots, count, scale);
     if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
     // NaN stays: a gradient that is no number must not look like one
     const double part = norm > max_norm ? max_norm / norm : norm == norm ? 1.0 : norm;
     const float by = static_cast<float>(scale * part);
-    Steps<M, true> steps(t);
-    auto changes = [&](const Step &s) { return by != 1.0f || t.in[s.tensor] != t.out[s.tensor]; };     // else it is as it has to be
-    Step now, then;
-    uint4 q[kNormVectors];
-    bool more = steps.next(now);
-    if (more && changes(now)) load_step(now, q);
-    while (more) {
-        uint4 x[kNormVectors];
-#pragma unroll
-        for (int u = 0; u < kNormVectors; ++u) x[u] = q[u];
-        more = steps.next(then);
-        if (more && changes(then)) load_step(then, q);
-        if (changes(now)) {
-            void *out = t.out[now.tensor];
-            switch (now.type) {
-                case GSORT_F32: scale_step<float>(now, x, out, by); break;
-                case GSORT_BF16: scale_step<__nv_bfloat16>(now, x, out, by); break;
-                default: scale_step<__half>(now, x, out, by); break;
-            }
-        }
-        now = then;
-    }
+    auto changes = [&](uint32_t tensor) { return by != 1.0f || t.in[tensor] != t.out[tensor]; };     // else it is as it has to be
+    for_ends(t, [&](uint32_t tensor, uint32_t type, uint64_t first, uint32_t n) {
+        with_type(type, [&](auto *p) {
+            using T = std::remove_pointer_t<decltype(p)>;
+            for (uint32_t k = 0; changes(tensor) && k < n; ++k)
+                static_cast<T *>(t.out[tensor])[first + k] = from_f32<T>(to_f32(static_cast<const T *>(t.in[tensor])[first + k]) * by);
+        });
+    });
+    const bool whole = ring.run([&](const Step &s, const uint4 *data) {
+        if (changes(s.tensor))
+            with_type(s.type, [&](auto *p) { scale_step<std::remove_pointer_t<decltype(p)>>(s, data, t.out[s.tensor], by); });
+    });
+    if (!whole && norm_out != nullptr && threadIdx.x == 0) *norm_out = __uint_as_float(0x7FC00000u);
 }
 
 // The tensors from `at` on, as many as fit, and how many of the list they are.
@@ -295,20 +312,22 @@ template <int M> int64_t fill_table(const NormLaunch &L, int64_t at, TensorTable
     uint64_t chunks = 0;
     for (uint32_t i = 0; i < t.tensors; ++i) {
         t.first[i] = static_cast<uint32_t>(chunks);
-        const uint64_t span = (reinterpret_cast<uintptr_t>(t.in[i]) & 15) + (t.size[i] & kSizeMask) * type_bytes(static_cast<uint32_t>(t.size[i] >> 56));
-        chunks += (span + chunk_bytes - 1) / chunk_bytes;
+        chunks += (span_of(t.in[i], t.size[i]).vectors * 16 + chunk_bytes - 1) / chunk_bytes;
     }
     if (chunks > 0x7FFFFFFF) return -1;
     t.first[t.tensors] = static_cast<uint32_t>(chunks);
     return end - at;
 }
 
-template <int M> uint32_t ctas_of(const TensorTable<M> &t) { return std::min(t.first[t.tensors], kNormCtas); }
+// Ends alone have no chunks.
+template <int M> uint32_t ctas_of(const TensorTable<M> &t) { return std::max(1u, std::min(t.first[t.tensors], kNormCtas)); }
 
-template <typename K, typename... A> int launch(K kernel, uint32_t ctas, bool early, cudaStream_t stream, const A &...args) {
+template <typename K, typename... A> int launch(K kernel, uint32_t ctas, size_t smem, bool early, cudaStream_t stream, const A &...args) {
+    if (smem > 0 && set_smem_limit(reinterpret_cast<const void *>(kernel), smem) != cudaSuccess) return GSORT_ECUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kNormThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -331,17 +350,17 @@ template <int M> int launch_tables(const NormLaunch &L) {
         at += taken;
         if (t.tensors == 0) continue;
         const uint32_t ctas = ctas_of(t);
-        if ((rc = launch(k_square_sums<M>, ctas, used > 0, L.stream, t, slots + used)) != GSORT_OK) return rc;
+        if ((rc = launch(k_square_sums<M>, ctas, kNormSmem, used > 0, L.stream, t, slots + used)) != GSORT_OK) return rc;
         used += ctas;
     }
     if (L.out == nullptr || used == 0)
-        return launch(k_norm, 1, used > 0, L.stream, static_cast<const double *>(slots), used, L.scale, L.norm);
+        return launch(k_norm, 1, 0, used > 0, L.stream, static_cast<const double *>(slots), used, L.scale, L.norm);
     float *norm = L.norm;
     const bool one = L.tensors <= M;       // its table is still there
     for (at = 0; at < L.tensors;) {
         at += one ? L.tensors : fill_table(L, at, t);
         if (t.tensors == 0) continue;
-        rc = launch(k_clip<M>, ctas_of(t), true, L.stream, t, static_cast<const double *>(slots), used, L.scale,
+        rc = launch(k_clip<M>, ctas_of(t), kNormSmem, true, L.stream, t, static_cast<const double *>(slots), used, L.scale,
                     L.max_norm, norm);
         if (rc != GSORT_OK) return rc;
         norm = nullptr;

@@ -141,10 +141,46 @@ int adjust(bool backward, const void *logits, int64_t logits_stride, const void 
     return launch_adjust(L);
 }
 
+// Whether the outputs lie one behind another, upwards or downwards, on one side of the inputs
+// that are not outputs too, and nothing overlaps the norm and the workspace.  One look at lists as
+// they mostly are (1500 tensors: 10 us, 50 with the lists below).
+bool tensors_apart(const void *const *in, void *const *out, const int64_t *elements, const int *dtypes, int64_t tensors, const Span &norm,
+                   const Span &ws) {
+    bool up = true, down = true;
+    uintptr_t last = 0, last_end = 0, low = UINTPTR_MAX, high = 0, read_low = UINTPTR_MAX, read_high = 0;
+    auto outside = [&](uintptr_t a, uintptr_t n) {
+        return !ranges_overlap(norm.p, norm.bytes, reinterpret_cast<const void *>(a), n) &&
+               !(ws.bytes > 0 && ranges_overlap(ws.p, ws.bytes, reinterpret_cast<const void *>(a), n));
+    };
+    bool clear = ws.bytes == 0 || !ranges_overlap(norm.p, norm.bytes, ws.p, ws.bytes);
+    for (int64_t i = 0; i < tensors; ++i) {
+        const uintptr_t n = static_cast<uintptr_t>(elements[i]) * float_bytes(dtypes[i]);
+        if (n == 0) continue;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]), o = out != nullptr ? reinterpret_cast<uintptr_t>(out[i]) : a;
+        clear &= outside(a, n);
+        if (out == nullptr) continue;
+        if (o != a) {
+            clear &= outside(o, n);
+            read_low = std::min(read_low, a);
+            read_high = std::max(read_high, a + n);
+        }
+        if (high > 0) {
+            up &= o >= last_end;
+            down &= o + n <= last;
+        }
+        last = o;
+        last_end = o + n;
+        low = std::min(low, o);
+        high = std::max(high, o + n);
+    }
+    return clear && (up || down) && (read_high <= low || high <= read_low || read_high == 0);
+}
+
 // Whether an output overlaps another output, the workspace, the norm or another tensor than the one
 // it is the clipped form of (or that one in part).
 bool tensors_clash(const void *const *in, void *const *out, const int64_t *elements, const int *dtypes, int64_t tensors, const Span &norm,
                    const Span &ws) {
+    if (tensors_apart(in, out, elements, dtypes, tensors, norm, ws)) return false;
     struct Range {
         uintptr_t begin, end;
         bool written;

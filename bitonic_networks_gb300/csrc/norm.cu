@@ -28,7 +28,8 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kNormVectors = 4;                   // vectors of a thread in a step
 constexpr uint32_t kStep = kNormThreads * kNormVectors;     // vectors of a step
-constexpr int kFewTensors = 32, kManyTensors = 1000;
+// Tensors of a launch.  A table of 1000 takes 28 KB, which cost 3 us more to launch than one of 32.
+constexpr int kFewTensors = 32, kSomeTensors = 384, kManyTensors = 1000;
 constexpr int kStages = 3;
 constexpr uint32_t kNormCtas = 608;               // 4 to an SM of a GB300
 constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier
@@ -375,7 +376,8 @@ size_t norm_workspace_bytes(int64_t tensors) {
 }
 
 int launch_norm(const NormLaunch &L) {
-    return L.tensors <= kFewTensors ? launch_tables<kFewTensors>(L) : launch_tables<kManyTensors>(L);
+    if (L.tensors <= kFewTensors) return launch_tables<kFewTensors>(L);
+    return L.tensors <= kSomeTensors ? launch_tables<kSomeTensors>(L) : launch_tables<kManyTensors>(L);
 }
 
 }  // namespace gsort

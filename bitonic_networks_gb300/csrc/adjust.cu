@@ -10,15 +10,16 @@
 // and the gradient by x: 0 where the mask's bit is clear, else d * (seen ? (x > 0 ? 1 / r
 // : r) : 1).
 //
-// A CTA holds a piece of a row, a whole one where rows are many.  The tokens that
-// history or biases name in it are a set in shared memory: a bit for every token of
-// the piece, and the named ones before each word of bits, so that a named token has a
-// slot and the slots are no more than the history is long.  Counts are made in the slots by a
-// second look over the history.  The mask's words are laid beside the set's, so that a
-// vector's bits are all at one place.  Then the logits pass by once: a vector without a
-// bit costs a look at its bits and no more than a copy.  The memory bounds it: logits in,
-// logits out.  In place, vectors in which nothing changes are neither read nor
-// written.
+// A CTA holds a piece of a row, a whole one where rows are many.  Some of its warps pass
+// the logits by once, through a ring of bulk copies, and mask them.  The others meanwhile make
+// the set of the history's tokens in shared memory: a bit for every token of
+// the piece, and the members before each word of bits, so that a token has a
+// slot and the slots are no more than the history is long; counts are made in the slots
+// by a second look over the history, biases go to a hash table.  When the piece
+// is written, each token of the set is taken once, by whichever of its places in the history
+// comes first, and its logit (from the caches) is written anew.  The
+// memory bounds it: logits in, logits out.  In place, vectors in which nothing is masked
+// are neither read nor written.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -26,13 +27,17 @@
 namespace gsort {
 namespace {
 
-constexpr int kAdjustThreads = 512;
-constexpr int kAdjustVectors = 4;                 // 16-byte vectors in flight per thread, and as many of the next step
-constexpr int kHistoryLoads = 8;                  // tokens of the history in flight per thread
-constexpr size_t kAdjustMaxSmem = 112 * 1024;     // two CTAs to an SM
+constexpr int kMaxThreads = 512;
+constexpr int kStageVectors = 2;                  // vectors of a stage of the ring for each thread of the CTA
+constexpr int kMostStages = 4;
+constexpr int kHistoryLoads = 16;                 // tokens of the history in flight per thread while the set is made
+constexpr int kTakeLoads = 4;                     // and while its members are taken
+constexpr uint32_t kQueue = 32 * (kTakeLoads + 1);      // members that a warp has at hand
+constexpr size_t kAdjustMaxSmem = 108 * 1024;     // two CTAs of 512 threads to an SM
 constexpr int64_t kAdjustCtas = 304;              // that rows are cut into, where they are fewer
 constexpr uint32_t kSeenBefore = 0x80000000u;     // of a count: the token is in the prompt
 constexpr uint32_t kNowhere = 0xFFFFFFFFu;
+constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier
 
 template <typename T> struct AdjustArgs {
     const T *logits;         // the gradient's: null where no history is given
@@ -54,7 +59,11 @@ template <typename T> struct AdjustArgs {
     const uint32_t *allowed;
     int64_t allowed_stride;
     uint32_t pieces, tokens; // pieces of a row, of so many tokens (a multiple of 256) each
-    uint32_t slots, bias_slots;      // words of the sets' slots
+    uint32_t slots, table;   // words of the set's slots; entries of the biases' table, a power of two
+    uint32_t stages;         // of the ring; 0: none
+    uint32_t ring_words;     // of shared memory, for the ring and after it the queues
+    uint32_t streamers;      // threads that pass the logits by; the others see to what is named
+    bool narrow;             // counts and numbers of members in 16 bits
     bool vectors;            // rows of in and out lie the same way to 16 bytes
     bool in_place;
 };
@@ -68,13 +77,14 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t *words, uint32_t at, 
     return words[at >> 5] >> (at & 31) & ((1u << n) - 1);
 }
 
-// Tokens of a piece, by their distance from its first one, in shared memory.  With
-// less than 32768 members the words `before` and the counts in the slots take 16 bits.
+// Tokens of a piece, by their distance from its first one, in shared memory.
+constexpr bool is_narrow(int64_t length) { return length < 32768; }
+
 struct TokenSet {
     uint32_t *bits;      // null: no set
     uint32_t *before;    // members before each word of bits
-    uint32_t *slots;     // one for each member
-    bool narrow;
+    uint32_t *slots;     // a count for each member
+    bool narrow;         // `before` and counts in 16 bits
 
     __device__ __forceinline__ bool has(uint32_t at) const { return bits != nullptr && (bits[at >> 5] >> (at & 31) & 1); }
     __device__ __forceinline__ uint32_t member(uint32_t at) const {      // its number
@@ -85,87 +95,104 @@ struct TokenSet {
         const uint32_t bit = 1u << (at & 31);
         if (at != kNowhere && !(*const_cast<const volatile uint32_t *>(bits + (at >> 5)) & bit)) atomicOr(bits + (at >> 5), bit);
     }
-    // A token once more, in the prompt or behind it.
+    // A token of the history once more, in the prompt or behind it.
     __device__ __forceinline__ void count(uint32_t at, bool prompt) const {
         const uint32_t m = member(at), half = narrow ? 16 * (m & 1) : 0;
         uint32_t *word = slots + (narrow ? m / 2 : m);
         if (prompt) atomicOr(word, (narrow ? 0x8000u : kSeenBefore) << half);
         else atomicAdd(word, 1u << half);
     }
-    __device__ __forceinline__ uint32_t counted(uint32_t at) const {     // how often behind the prompt
+    // How often behind the prompt, with kSeenBefore; kNowhere for all but one of those who ask.
+    __device__ __forceinline__ uint32_t take(uint32_t at) const {
         const uint32_t m = member(at);
-        return narrow ? reinterpret_cast<const uint16_t *>(slots)[m] & 0x7FFFu : slots[m] & ~kSeenBefore;
+        if (!narrow) return atomicExch(slots + m, kNowhere);
+        const uint32_t half = 16 * (m & 1), c = atomicOr(slots + m / 2, 0xFFFFu << half) >> half & 0xFFFFu;
+        return c == 0xFFFFu ? kNowhere : (c & 0x7FFFu) | (c & 0x8000u) << 16;      // fewer than 32768: 0xFFFF is no count
+    }
+    // Whether the token was there still: the gradient needs no counts.
+    __device__ __forceinline__ bool take_bit(uint32_t at) const {
+        const uint32_t bit = 1u << (at & 31);
+        return atomicAnd(bits + (at >> 5), ~bit) & bit;
     }
 };
 
-__host__ __device__ constexpr bool is_narrow(int64_t members) { return members < 32768; }
+// Some warps of the CTA, for a barrier of their own.
+struct Crew {
+    uint32_t id, threads, rank;      // barrier, threads, and this thread among them
+    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+};
 
-// Counts the members before each word, and clears their slots (words of 1 or 2 to a
-// slot word).  Called by the whole CTA.
-__device__ __forceinline__ void number_members(const TokenSet &set, uint32_t words, uint32_t per_slot_word) {
-    __shared__ uint32_t s_sum[kAdjustThreads / 32];
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t per = (words + kAdjustThreads - 1) / kAdjustThreads, begin = min(tid * per, words), end = min(begin + per, words);
+// Counts the members before each word, and clears their slots.  Called by the whole crew.
+__device__ __forceinline__ void number_members(const TokenSet &set, uint32_t words, const Crew &crew) {
+    __shared__ uint32_t s_sum[kMaxThreads / 32];
+    const uint32_t threads = crew.threads, tid = crew.rank, lane = tid & 31, warp = tid >> 5;
+    const uint32_t per = (words + threads - 1) / threads, begin = min(tid * per, words), end = min(begin + per, words);
     uint32_t mine = 0;
     for (uint32_t w = begin; w < end; ++w) mine += __popc(set.bits[w]);
     const uint32_t upto = warp_inclusive_scan(mine, lane);
     if (lane == 31) s_sum[warp] = upto;
-    __syncthreads();
-    uint32_t sum = upto - mine, total = 0;
-#pragma unroll
-    for (int i = 0; i < kAdjustThreads / 32; ++i) {
-        const uint32_t n = s_sum[i];
-        if (i < static_cast<int>(warp)) sum += n;
-        total += n;
-    }
+    crew.sync();
+    const uint32_t warps = warp_inclusive_scan(lane < threads / 32 ? s_sum[lane] : 0, lane);      // sums up to each warp
+    const uint32_t total = __shfl_sync(kFullMask, warps, 31), earlier = __shfl_sync(kFullMask, warps, (warp + 31) & 31);
+    uint32_t sum = upto - mine + (warp > 0 ? earlier : 0);
     for (uint32_t w = begin; w < end; ++w) {
         if (set.narrow) reinterpret_cast<uint16_t *>(set.before)[w] = static_cast<uint16_t>(sum);
         else set.before[w] = sum;
         sum += __popc(set.bits[w]);
     }
-    for (uint32_t i = tid; i * per_slot_word < total; i += kAdjustThreads) set.slots[i] = 0;
-    __syncthreads();
+    const uint32_t slot_words = set.narrow ? (total + 1) / 2 : total;
+    for (uint32_t i = tid; i < slot_words; i += threads) set.slots[i] = 0;
+    crew.sync();
 }
 
-// The tokens `base` + thread, + threads, ... of a list, as distances from the piece's first one.
-__device__ __forceinline__ void load_tokens(const void *list, int bytes, int64_t row, uint32_t length, uint32_t base, int32_t begin,
-                                            int32_t end, int32_t first, uint32_t (&at)[kHistoryLoads]) {
-    uint32_t t[kHistoryLoads];       // what is no 32-bit number is no token
-    const uint32_t i0 = base + threadIdx.x;
-    if (bytes == 4) {
-        const uint32_t *p = static_cast<const uint32_t *>(list) + row + i0;
-#pragma unroll
-        for (int k = 0; k < kHistoryLoads; ++k) t[k] = i0 + k * kAdjustThreads < length ? p[k * kAdjustThreads] : kNowhere;
-    } else {
-        const uint64_t *p = static_cast<const uint64_t *>(list) + row + i0;
-#pragma unroll
-        for (int k = 0; k < kHistoryLoads; ++k) {
-            const uint64_t x = i0 + k * kAdjustThreads < length ? p[k * kAdjustThreads] : ~0ull;
-            t[k] = x >> 32 ? kNowhere : static_cast<uint32_t>(x);
+// The biased tokens of a piece, each with its last entry: an open hash table, at most half full.
+struct BiasTable {
+    uint2 *entries;      // token (kNowhere: free), entry + 1; null: no biases
+    uint32_t mask;
+
+    __device__ __forceinline__ uint32_t start(uint32_t at) const { return (at * 2654435761u >> 12) & mask; }
+    __device__ __forceinline__ void add(uint32_t at, uint32_t entry) const {
+        if (at == kNowhere) return;
+        for (uint32_t h = start(at), n = 0; n <= mask; h = (h + 1) & mask, ++n) {
+            const uint32_t was = atomicCAS(&entries[h].x, kNowhere, at);
+            if (was != kNowhere && was != at) continue;
+            atomicMax(&entries[h].y, entry + 1);
+            return;
         }
     }
-    const uint32_t span = static_cast<uint32_t>(end - begin);        // end <= 2^30: kNowhere is outside
-#pragma unroll
-    for (int k = 0; k < kHistoryLoads; ++k) at[k] = t[k] - static_cast<uint32_t>(begin) < span ? t[k] - static_cast<uint32_t>(first) : kNowhere;
-}
-
-// What a CTA knows of its piece of a row.
-struct Piece {
-    TokenSet seen, biased;
-    const float *bias;
-    uint32_t *allowed;         // bits of the piece's tokens, in shared memory; null: no mask
-    float repetition, presence, frequency;
-    int32_t first, begin, end; // the piece's first token (a vector may begin before the row), and its tokens
+    __device__ __forceinline__ uint32_t find(uint32_t at) const {        // entry + 1, 0: none
+        for (uint32_t h = start(at), n = 0; n <= mask; h = (h + 1) & mask, ++n) {
+            const uint2 e = entries[h];
+            if (e.x == at) return e.y;
+            if (e.x == kNowhere) return 0;
+        }
+        return 0;
+    }
 };
 
-__device__ __forceinline__ float adjusted(const Piece &p, float x, uint32_t at) {
-    if (p.seen.has(at)) {
-        const uint32_t n = p.seen.counted(at);
-        x = x > 0.0f ? x / p.repetition : x * p.repetition;
-        if (n != 0) x -= fmaf(p.frequency, static_cast<float>(n), p.presence);
+// A piece of a row: its first token (a vector may begin before the row), and its tokens.
+struct Range {
+    int32_t first, begin, end;
+};
+
+// The tokens i, i + step, ... of a list, as distances from the piece's first one.  What is no
+// 32-bit number is no token.
+template <int K>
+__device__ __forceinline__ void load_tokens(const void *list, int bytes, int64_t row, uint32_t length, uint32_t i, uint32_t step,
+                                            const Range &r, uint32_t (&at)[K]) {
+    const uint32_t words = bytes / 4;
+    const uint32_t *p = static_cast<const uint32_t *>(list) + (row + i) * words;
+    uint32_t high[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const bool there = i + k * step < length;
+        at[k] = there ? p[k * step * words] : kNowhere;
+        high[k] = there && words == 2 ? p[k * step * words + 1] : 0;
     }
-    if (p.biased.has(at)) x += p.bias[p.biased.slots[p.biased.member(at)] - 1];
-    return x;
+    const uint32_t span = static_cast<uint32_t>(r.end - r.begin);    // at most 2^30: kNowhere is outside
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        at[k] = high[k] == 0 && at[k] - static_cast<uint32_t>(r.begin) < span ? at[k] - static_cast<uint32_t>(r.first) : kNowhere;
 }
 
 // Elements whose bit is clear become -inf (or 0).
@@ -181,166 +208,243 @@ template <typename T, bool ZERO> __device__ __forceinline__ void mask_vector(uin
 }
 
 template <typename T, bool BACK>
-__global__ void __launch_bounds__(kAdjustThreads, 2) k_adjust(const AdjustArgs<T> a) {
-    constexpr int N = Wide<T>::kCount, U = kAdjustVectors;
+__global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a) {
+    constexpr int N = Wide<T>::kCount;
     constexpr uint32_t kAll = (1u << N) - 1;
-    extern __shared__ __align__(16) uint32_t s_words[];
-    const uint32_t row = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces, tid = threadIdx.x;
+    extern __shared__ __align__(128) uint32_t s_words[];
+    __shared__ __align__(8) uint64_t s_full[kMostStages];
+    __shared__ uint32_t s_failed;
+    const uint32_t row = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces, tid = threadIdx.x, threads = blockDim.x;
     const T *in = a.in + static_cast<int64_t>(row) * a.in_stride;
     T *out = a.out + static_cast<int64_t>(row) * a.out_stride;
     // elements between the 16-byte boundary at or before the row and the row
     const int32_t shift = a.vectors ? static_cast<int32_t>((reinterpret_cast<uintptr_t>(in) & 15) / sizeof(T)) : 0;
     const int64_t low = static_cast<int64_t>(piece) * a.tokens - shift;
     if (low >= a.vocab) return;
-    Piece p{};
-    p.first = static_cast<int32_t>(low);
-    p.begin = max(p.first, 0);
-    p.end = static_cast<int32_t>(min(low + a.tokens, static_cast<int64_t>(a.vocab)));
-    // vectors of the piece that are whole: not those that the row's start or end cuts
-    const uint32_t low_v = p.first < 0 ? 1 : 0, high_v = static_cast<uint32_t>(p.end - p.first) / N;
+    Range r;
+    r.first = static_cast<int32_t>(low);
+    r.begin = max(r.first, 0);
+    r.end = static_cast<int32_t>(min(low + a.tokens, static_cast<int64_t>(a.vocab)));
 
-    // the first vectors are on their way while the sets are made
-    uint4 q[U];
-    auto load = [&](uint32_t v0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t v = v0 + u * kAdjustThreads;
-            if (v >= low_v && v < high_v) q[u] = reinterpret_cast<const uint4 *>(in + p.first)[v];
-        }
-    };
-    const bool ahead = a.vectors && !a.in_place;
-    if (ahead) load(tid);
-
+    // shared memory: the ring (later the queues), the mask, then what is named
     const uint32_t words = a.tokens / 32;
-    uint32_t *space = s_words;
-    if (a.history != nullptr) {
-        p.seen.narrow = is_narrow(a.length);
-        p.seen.bits = space;
-        p.seen.before = space + words;
-        p.seen.slots = p.seen.before + (p.seen.narrow ? words / 2 : words);
-        space = BACK ? p.seen.before : p.seen.slots + a.slots;
-    }
+    uint4 *const ring = reinterpret_cast<uint4 *>(s_words);
+    uint32_t *const allowed = a.allowed ? s_words + a.ring_words : nullptr;
+    BiasTable biased{nullptr, a.table - 1};
+    TokenSet seen{nullptr, nullptr, nullptr, a.narrow};
+    uint32_t *space = s_words + a.ring_words + (a.allowed ? words : 0);
     if (!BACK && a.biases > 0) {
-        p.biased.narrow = is_narrow(a.biases);
-        p.biased.bits = space;
-        p.biased.before = space + words;
-        p.biased.slots = p.biased.before + (p.biased.narrow ? words / 2 : words);
-        p.bias = a.bias + static_cast<int64_t>(row) * a.bias_stride;
-        space = p.biased.slots + a.bias_slots;
+        biased.entries = reinterpret_cast<uint2 *>(space);
+        space += 2 * a.table;
     }
-    if (a.allowed != nullptr) {      // word w: the bits of the piece's tokens 32 w ..
-        const uint32_t *mask = a.allowed + static_cast<int64_t>(row) * a.allowed_stride;
-        const int32_t last = static_cast<int32_t>((a.vocab - 1) / 32);
-        p.allowed = space;
+    if (a.history != nullptr) {
+        seen.bits = space;
+        seen.before = space + words;
+        seen.slots = seen.before + (a.narrow ? words / 2 : words);
+    }
+    const int64_t history_row = static_cast<int64_t>(row) * a.history_stride, bias_row = static_cast<int64_t>(row) * a.bias_stride;
+    auto bias_at = [&](uint32_t i) {           // an entry's token as a distance from the piece's first one
+        const int64_t t = int_at(a.bias_tokens, a.bias_bytes, bias_row + i);
+        return t >= r.begin && t < r.end ? static_cast<uint32_t>(t - r.first) : kNowhere;
+    };
+
+    if (tid < a.streamers) {
+        // ------------------------------------------------ the logits, masked
+        const Crew crew{1, a.streamers, tid};
+        // vectors that are whole: not those that the row's start or end cuts
+        const uint32_t low_v = r.first < 0 ? 1 : 0, high_v = a.vectors ? static_cast<uint32_t>(r.end - r.first) / N : 0;
+        const uint4 *in_v = reinterpret_cast<const uint4 *>(in + r.first);     // read from low_v on
+        uint4 *out_v = reinterpret_cast<uint4 *>(out + r.first);
+        const uint32_t per_stage = threads * kStageVectors;
+        auto copy = [&](uint32_t k) {          // the ring's stage k: vectors low_v + k * per_stage ...; thread 0
+            const uint32_t from = low_v + k * per_stage;
+            if (from >= high_v) return;
+            const uint32_t bytes = min(per_stage, high_v - from) * 16, stage = k % a.stages;
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(&s_full[stage], bytes);
+            bulk_load(ring + stage * per_stage, in_v + from, bytes, &s_full[stage]);
+        };
+        if (tid == 0) {
+            s_failed = 0;
+            for (uint32_t k = 0; k < a.stages; ++k) mbar_init(&s_full[k], 1);
+            for (uint32_t k = 0; k < a.stages; ++k) copy(k);
+        }
+        if (allowed != nullptr) {              // word w: the bits of the piece's tokens 32 w ..
+            const uint32_t *mask = a.allowed + static_cast<int64_t>(row) * a.allowed_stride;
+            const int32_t last = static_cast<int32_t>((a.vocab - 1) / 32);
+            // Eight words' loads at once: behind the ring's copies each takes microseconds.  Words
+            // beside the mask's hold no token of the piece.
+            const uint32_t off = static_cast<uint32_t>(r.first) & 31;
+            const int32_t k0 = r.first >> 5;               // -1 where the first vector begins before the row
+            for (uint32_t w0 = tid; w0 < words; w0 += 8 * a.streamers) {
+                uint32_t here[8], next[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int32_t k = k0 + static_cast<int32_t>(w0 + j * a.streamers);
+                    here[j] = mask[min(max(k, 0), last)];
+                    next[j] = off != 0 ? mask[min(max(k + 1, 0), last)] : 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t w = w0 + j * a.streamers;
+                    if (w < words) allowed[w] = __funnelshift_r(here[j], next[j], off);
+                }
+            }
+        }
+        crew.sync();
+        // single elements: of the whole piece where rows lie differently, else of the two
+        // vectors that the row's start and end cut
+        const int32_t whole = a.vectors ? min(r.first + static_cast<int32_t>(low_v) * N, r.end) : r.end;
+        const int32_t rest = a.vectors ? max(r.first + static_cast<int32_t>(high_v) * N, whole) : r.end;
+        auto single = [&](int32_t e) { out[e] = !allowed || bits_at(allowed, e - r.first, 1) ? in[e] : from_f32<T>(BACK ? 0.0f : kNegInf); };
+        for (int32_t e = r.begin + static_cast<int32_t>(tid); e < whole; e += a.streamers) single(e);
+        for (int32_t e = rest + static_cast<int32_t>(tid); e < r.end; e += a.streamers) single(e);
+        for (uint32_t k = 0, v0 = low_v; v0 < high_v; ++k, v0 += per_stage) {
+            const uint4 *data = ring;
+            if (a.stages > 0) {
+                data += k % a.stages * per_stage;
+                if (!mbar_wait_bounded(&s_full[k % a.stages], (k / a.stages) & 1, kWaitLimit)) s_failed = 1;
+            }
 #pragma unroll 4
-        for (uint32_t w = tid; w < words; w += kAdjustThreads) {
-            const int32_t at = p.first + static_cast<int32_t>(w * 32), k = at >> 5;      // -8 < at
-            const uint32_t here = k >= 0 && k <= last ? mask[k] : 0, next = (at & 31) != 0 && k < last ? mask[k + 1] : 0;
-            space[w] = __funnelshift_r(here, next, at & 31);
+            for (uint32_t i = tid; i < min(per_stage, high_v - v0); i += a.streamers) {
+                const uint32_t v = v0 + i, allow = allowed ? bits_at(allowed, v * N, N) : kAll;
+                if (a.stages == 0 && allow == kAll) continue;      // in place
+                uint4 x = a.stages > 0 ? data[i] : in_v[v];
+                if (allowed) mask_vector<T, BACK>(x, allow);
+                out_v[v] = x;
+            }
+            if (a.stages > 0) {
+                crew.sync();
+                if (*const_cast<volatile uint32_t *>(&s_failed)) {     // a copy that does not come: what is left is no number
+                    for (uint32_t v = v0 + tid; v < high_v; v += a.streamers) out_v[v] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+                    for (uint32_t i = k; i < k + a.stages && low_v + i * per_stage < high_v; ++i)
+                        mbar_wait_bounded(&s_full[i % a.stages], (i / a.stages) & 1, kWaitLimit);
+                    break;
+                }
+                if (tid == 0) copy(k + a.stages);
+            }
         }
-        if (!p.seen.bits && !p.biased.bits) __syncthreads();
-    }
-    if (p.seen.bits || p.biased.bits) {
-        for (uint32_t w = tid; w < words; w += kAdjustThreads) {
-            if (p.seen.bits) p.seen.bits[w] = 0;
-            if (p.biased.bits) p.biased.bits[w] = 0;
+    } else {
+        // ------------------------------------------------ what is named
+        const Crew crew{2, threads - a.streamers, tid - a.streamers};
+        const uint32_t span = crew.threads * kHistoryLoads;
+        uint32_t at[kHistoryLoads], then[kHistoryLoads];
+        auto load = [&](uint32_t base, uint32_t (&to)[kHistoryLoads]) {
+            load_tokens(a.history, a.history_bytes, history_row, a.length, base + crew.rank, crew.threads, r, to);
+        };
+        if (seen.bits) {
+            load(0, at);
+            for (uint32_t w = crew.rank; w < words; w += crew.threads) seen.bits[w] = 0;
         }
-        __syncthreads();
-        const int64_t history_row = static_cast<int64_t>(row) * a.history_stride, bias_row = static_cast<int64_t>(row) * a.bias_stride;
-        uint32_t at[kHistoryLoads];
-        constexpr uint32_t kStep = kAdjustThreads * kHistoryLoads;
-        if (p.seen.bits) {
-            for (uint32_t base = 0; base < a.length; base += kStep) {
-                load_tokens(a.history, a.history_bytes, history_row, a.length, base, p.begin, p.end, p.first, at);
+        for (uint32_t i = crew.rank; biased.entries && i < a.table; i += crew.threads) biased.entries[i] = make_uint2(kNowhere, 0);
+        crew.sync();
+        for (uint32_t base = 0; seen.bits && base < a.length; base += span) {
+            if (base + span < a.length) load(base + span, then);       // while these are added
 #pragma unroll
-                for (int k = 0; k < kHistoryLoads; ++k) p.seen.add(at[k]);
+            for (int k = 0; k < kHistoryLoads; ++k) seen.add(at[k]);
+            if (base + span < a.length) {
+#pragma unroll
+                for (int k = 0; k < kHistoryLoads; ++k) at[k] = then[k];
             }
         }
-        if (p.biased.bits) {
-            for (uint32_t i = tid; i < a.biases; i += kAdjustThreads) {
-                const int64_t t = int_at(a.bias_tokens, a.bias_bytes, bias_row + i);
-                if (t >= p.begin && t < p.end) p.biased.add(static_cast<uint32_t>(t - p.first));
-            }
-        }
-        __syncthreads();
-        if (!BACK) {
-            if (p.seen.bits) {
-                number_members(p.seen, words, p.seen.narrow ? 2 : 1);
+        for (uint32_t i = crew.rank; biased.entries && i < a.biases; i += crew.threads) biased.add(bias_at(i), i);
+        crew.sync();
+        if constexpr (!BACK) {
+            if (seen.bits) {
                 const uint32_t prompt = a.prompt ? static_cast<uint32_t>(max(a.prompt[row], 0)) : 0;
-                for (uint32_t base = 0; base < a.length; base += kStep) {
-                    // a history of one step is still there
-                    if (a.length > kStep) load_tokens(a.history, a.history_bytes, history_row, a.length, base, p.begin, p.end, p.first, at);
+                if (a.length > span) load(0, at);                      // a history of one step is still there
+                number_members(seen, words, crew);
+                for (uint32_t base = 0; base < a.length; base += span) {
+                    if (base + span < a.length) load(base + span, then);
 #pragma unroll
-                    for (int k = 0; k < kHistoryLoads; ++k) {
-                        if (at[k] != kNowhere) p.seen.count(at[k], base + k * kAdjustThreads + tid < prompt);
+                    for (int k = 0; k < kHistoryLoads; ++k)
+                        if (at[k] != kNowhere) seen.count(at[k], base + k * crew.threads + crew.rank < prompt);
+                    if (base + span < a.length) {
+#pragma unroll
+                        for (int k = 0; k < kHistoryLoads; ++k) at[k] = then[k];
                     }
                 }
             }
-            if (p.biased.bits) {
-                number_members(p.biased, words, 1);
-                for (uint32_t i = tid; i < a.biases; i += kAdjustThreads) {
-                    const int64_t t = int_at(a.bias_tokens, a.bias_bytes, bias_row + i);
-                    if (t >= p.begin && t < p.end) atomicMax(p.biased.slots + p.biased.member(static_cast<uint32_t>(t - p.first)), i + 1);
+        }
+    }
+    if (a.streamers == threads) return;
+
+    // ---------------------------------------------- named tokens, anew
+    const float repetition = a.repetition ? a.repetition[row] : 1.0f;
+    const float presence = !BACK && a.presence ? a.presence[row] : 0.0f, frequency = !BACK && a.frequency ? a.frequency[row] : 0.0f;
+    const T *logits = BACK ? a.logits + static_cast<int64_t>(row) * a.logits_stride : nullptr;
+    uint32_t at[kTakeLoads];
+    if (seen.bits) load_tokens(a.history, a.history_bytes, history_row, a.length, tid, threads, r, at);
+    __syncthreads();
+    const uint32_t lane = tid & 31;
+    uint32_t queued = 0;
+    uint2 *const queue = reinterpret_cast<uint2 *>(s_words) + (tid >> 5) * kQueue;      // where the ring was
+    auto push = [&](uint32_t token, uint32_t count) {          // kNowhere: none
+        const uint32_t active = __ballot_sync(kFullMask, token != kNowhere);
+        if (token != kNowhere) {
+            queue[queued + __popc(active & lanemask_lt())] = make_uint2(token, count);
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(in + r.first + static_cast<int32_t>(token)));
+            if (BACK) asm volatile("prefetch.global.L1 [%0];" ::"l"(logits + r.first + static_cast<int32_t>(token)));
+        }
+        queued += __popc(active);
+    };
+    auto serve = [&](uint32_t least) {                         // 32 at a time, until fewer than `least` are left
+        __syncwarp();
+        while (queued >= least && queued > 0) {
+            const uint32_t n = min(queued, 32u);
+            queued -= n;
+            if (lane < n) {
+                const uint2 q = queue[queued + lane];
+                if (allowed == nullptr || bits_at(allowed, q.x, 1)) {
+                    const int32_t e = r.first + static_cast<int32_t>(q.x);
+                    float x = to_f32(in[e]);                   // in place, it holds its value still
+                    if (BACK) {
+                        x *= to_f32(logits[e]) > 0.0f ? 1.0f / repetition : repetition;
+                    } else {
+                        const uint32_t times = q.y & ~kSeenBefore, b = biased.entries ? biased.find(q.x) : 0;
+                        const float shift_by = b != 0 ? a.bias[bias_row + b - 1] : 0.0f;
+                        if (q.y != 0) x = x > 0.0f ? x / repetition : x * repetition;
+                        if (times != 0) x -= fmaf(frequency, static_cast<float>(times), presence);
+                        if (b != 0) x += shift_by;
+                    }
+                    out[e] = from_f32<T>(x);
                 }
             }
-            __syncthreads();
         }
-    }
-    p.repetition = a.repetition ? a.repetition[row] : 1.0f;
-    p.presence = a.presence ? a.presence[row] : 0.0f;
-    p.frequency = a.frequency ? a.frequency[row] : 0.0f;
-    const T *logits = BACK && p.seen.bits ? a.logits + static_cast<int64_t>(row) * a.logits_stride : nullptr;
-
-    // the value of a token that history or biases name
-    auto named = [&](float x, int32_t e) {
-        if (!BACK) return adjusted(p, x, static_cast<uint32_t>(e - p.first));
-        return to_f32(logits[e]) > 0.0f ? x * (1.0f / p.repetition) : x * p.repetition;
+        __syncwarp();
     };
-    auto single = [&](int32_t e) {
-        const uint32_t at = static_cast<uint32_t>(e - p.first);
-        const float x = to_f32(in[e]);
-        const bool allow = !p.allowed || bits_at(p.allowed, at, 1);
-        out[e] = from_f32<T>(!allow ? (BACK ? 0.0f : kNegInf) : p.seen.has(at) || p.biased.has(at) ? named(x, e) : x);
-    };
-    // Single elements: the whole piece where rows lie differently, else those of the two
-    // vectors that the row's start and end cut.
-    const int32_t whole = a.vectors ? p.first + static_cast<int32_t>(low_v) * N : p.end;
-    for (int32_t e = p.begin + static_cast<int32_t>(tid); e < min(whole, p.end); e += kAdjustThreads) single(e);
-    if (!a.vectors) return;
-    const int32_t rest = max(p.first + static_cast<int32_t>(high_v) * N, whole);
-    if (rest + static_cast<int32_t>(tid) < p.end) single(rest + static_cast<int32_t>(tid));
-    for (uint32_t v0 = tid; v0 < high_v; v0 += kAdjustThreads * U) {
-        uint4 x[U];
+    for (uint32_t base = 0; seen.bits && base < a.length; base += threads * kTakeLoads) {
+        uint32_t then[kTakeLoads];
+        const bool more = base + threads * kTakeLoads < a.length;
+        if (more) load_tokens(a.history, a.history_bytes, history_row, a.length, base + threads * kTakeLoads + tid, threads, r, then);
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = q[u];
-        if (ahead) load(v0 + kAdjustThreads * U);
-        // Vectors are masked and written as a whole; the few named tokens are gathered
-        // and written after them (their code stands here once: in the unrolled part, 32
-        // times, it did not fit the instruction cache, 2048 x 131072 490 us).
-        uint32_t names = 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t v = v0 + u * kAdjustThreads;
-            if (v < low_v || v >= high_v) continue;
-            uint32_t name = 0, allow = kAll;
-            if (p.seen.bits) name = bits_at(p.seen.bits, v * N, N);
-            if (p.biased.bits) name |= bits_at(p.biased.bits, v * N, N);
-            if (p.allowed) allow = bits_at(p.allowed, v * N, N);
-            names |= (name & allow) << (u * N);
-            if (a.in_place) {
-                if (allow == kAll) continue;
-                x[u] = reinterpret_cast<const uint4 *>(in + p.first)[v];
+        for (int k = 0; k < kTakeLoads; ++k) {
+            uint32_t token = at[k], count = 0;
+            if (token != kNowhere) {
+                if (BACK) {
+                    if (!seen.take_bit(token)) token = kNowhere;
+                } else {
+                    count = seen.take(token);
+                    if (count == kNowhere) token = kNowhere;
+                }
             }
-            if (p.allowed) mask_vector<T, BACK>(x[u], allow);
-            reinterpret_cast<uint4 *>(out + p.first)[v] = x[u];
+            push(token, count);
         }
-        while (names != 0) {
-            const uint32_t b = __ffs(names) - 1;
-            names &= names - 1;
-            const int32_t e = p.first + static_cast<int32_t>((v0 + b / N * kAdjustThreads) * N + b % N);
-            out[e] = from_f32<T>(named(to_f32(in[e]), e));     // in place, it holds its value still
+        serve(32);
+        if (more) {
+#pragma unroll
+            for (int k = 0; k < kTakeLoads; ++k) at[k] = then[k];
         }
     }
+    if (!BACK && biased.entries) {             // biased tokens that are not in the history, by their last entry
+        for (uint32_t base = 0; base < a.biases; base += threads) {
+            uint32_t token = base + tid < a.biases ? bias_at(base + tid) : kNowhere;
+            if (token != kNowhere && (seen.has(token) || biased.find(token) != base + tid + 1)) token = kNowhere;
+            push(token, 0);
+            serve(32);
+        }
+    }
+    serve(1);
 }
 
 }  // namespace
@@ -349,7 +453,10 @@ int launch_adjust(const AdjustLaunch &L) {
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int N = Wide<T>::kCount;
-        constexpr int64_t kLeast = kAdjustThreads * N;      // tokens of a piece: a vector for every thread
+        const int threads = getenv("AT") ? atoi(getenv("AT")) : 512;
+        const int64_t least = threads * N;         // tokens of a piece: a vector for every thread
+        const int64_t ctas = kAdjustCtas * (512 / threads);
+        const size_t most_smem = threads == 512 ? kAdjustMaxSmem : 51 * 1024;
         AdjustArgs<T> a{};
         a.logits = static_cast<const T *>(L.logits);
         a.in = static_cast<const T *>(L.in);
@@ -379,28 +486,40 @@ int launch_adjust(const AdjustLaunch &L) {
         a.vectors = ((reinterpret_cast<uintptr_t>(L.in) ^ reinterpret_cast<uintptr_t>(L.out)) & 15) == 0 &&
                     (L.rows == 1 || (L.in_stride - L.out_stride) % N == 0);
         // pieces that fill the device, smaller ones where their sets would take too much room
-        const int64_t want = std::max<int64_t>(kAdjustCtas / L.rows, 1), most = (L.vocab + kLeast - 1) / kLeast;
+        const int64_t want = std::max<int64_t>(ctas / L.rows, 1), most = (L.vocab + least - 1) / least;
         const int64_t pieces = std::min(want, most), span = L.vocab + (a.vectors ? N - 1 : 0);
         int64_t tokens = std::max<int64_t>(256, (std::min<int64_t>(span / pieces + 1, 1 << 18) + 255) / 256 * 256);
-        auto smem_bytes = [&] {
-            const int64_t words = tokens / 32;
+        const bool history = a.history != nullptr, biases = !L.backward && L.biases > 0, ring = a.vectors && !a.in_place;
+        const size_t stage = static_cast<size_t>(threads) * kStageVectors * 16, queues = history || biases ? threads / 32 * kQueue * 8 : 0;
+        a.streamers = history || biases ? (getenv("AS") ? atoi(getenv("AS")) * threads / 8 : threads / 2) : threads;
+        auto set_bytes = [&] {
+            const int64_t words = tokens / 32, members = std::min(tokens, L.length);
             a.tokens = static_cast<uint32_t>(tokens);
-            a.slots = static_cast<uint32_t>((std::min(tokens, L.length) + 1) / (is_narrow(L.length) ? 2 : 1));
-            a.bias_slots = static_cast<uint32_t>(std::min(tokens, L.biases));
-            int64_t all = L.allowed != nullptr ? words : 0;
-            if (a.history != nullptr) all += words + (L.backward ? 0 : (is_narrow(L.length) ? words / 2 : words) + a.slots);
-            if (!L.backward && L.biases > 0) all += words + (is_narrow(L.biases) ? words / 2 : words) + a.bias_slots;
+            a.narrow = is_narrow(L.length);
+            a.slots = static_cast<uint32_t>(a.narrow ? (members + 1) / 2 : members);
+            a.table = 1;
+            while (biases && a.table < 2 * std::min(tokens, L.biases)) a.table *= 2;
+            int64_t all = (L.allowed != nullptr ? words : 0) + (biases ? 2 * a.table : 0);
+            if (history) all += words + (L.backward ? 0 : (a.narrow ? words / 2 : words) + a.slots);
             return static_cast<size_t>(all) * 4;
         };
-        while (smem_bytes() > kAdjustMaxSmem) tokens = (tokens / 2 + 255) / 256 * 256;
+        const size_t least_ring = std::max(ring ? 2 * stage : 0, queues);
+        while (set_bytes() + least_ring > most_smem) tokens = (tokens / 2 + 255) / 256 * 256;
+        const size_t sets = set_bytes();
+        if (ring) {
+            const size_t stages = std::min<size_t>((most_smem - sets) / stage, kMostStages);
+            a.stages = static_cast<uint32_t>(std::min<size_t>(stages, (tokens / N * 16 + stage - 1) / stage));
+        }
+        const size_t ring_bytes = std::max(a.stages * stage, queues);
+        a.ring_words = static_cast<uint32_t>(ring_bytes / 4);
         a.pieces = static_cast<uint32_t>((span + tokens - 1) / tokens);
         const int64_t blocks = L.rows * a.pieces;
         if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
-        const size_t smem = smem_bytes();
+        const size_t smem = sets + ring_bytes;
         const void *kernel = L.backward ? reinterpret_cast<const void *>(k_adjust<T, true>) : reinterpret_cast<const void *>(k_adjust<T, false>);
-        if (smem > 48 * 1024 && set_smem_limit(kernel, kAdjustMaxSmem) != cudaSuccess) return static_cast<int>(GSORT_ECUDA);
-        if (L.backward) k_adjust<T, true><<<static_cast<uint32_t>(blocks), kAdjustThreads, smem, L.stream>>>(a);
-        else k_adjust<T, false><<<static_cast<uint32_t>(blocks), kAdjustThreads, smem, L.stream>>>(a);
+        if (smem > 40 * 1024 && set_smem_limit(kernel, kAdjustMaxSmem) != cudaSuccess) return static_cast<int>(GSORT_ECUDA);
+        if (L.backward) k_adjust<T, true><<<static_cast<uint32_t>(blocks), threads, smem, L.stream>>>(a);
+        else k_adjust<T, false><<<static_cast<uint32_t>(blocks), threads, smem, L.stream>>>(a);
         return cudaGetLastError() == cudaSuccess ? static_cast<int>(GSORT_OK) : static_cast<int>(GSORT_ECUDA);
     });
 }

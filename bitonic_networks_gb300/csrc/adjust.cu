@@ -16,8 +16,8 @@
 // the piece, and the members before each word of bits, so that a token has a
 // slot and the slots are no more than the history is long; counts are made in the slots
 // by a second look over the history, biases go to a hash table.  When the piece
-// is written, each token of the set is taken once, by whichever of its places in the history
-// comes first, and its logit (from the caches) is written anew.  The
+// is written, each token of the set is taken once, and its logit (from the caches) is
+// written anew.  The
 // memory bounds it: logits in, logits out.  In place, vectors in which nothing is masked
 // are neither read nor written.
 #include <algorithm>
@@ -27,14 +27,15 @@
 namespace gsort {
 namespace {
 
-constexpr int kMaxThreads = 512;
-constexpr int kStageVectors = 2;                  // vectors of a stage of the ring for each thread of the CTA
+constexpr int kMaxThreads = 1024;
+constexpr int kStageVectors = 2;                  // vectors of a stage of the ring for each thread of the CTA; 1 where room is short
 constexpr int kMostStages = 4;
-constexpr int kHistoryLoads = 16;                 // tokens of the history in flight per thread while the set is made
-constexpr int kTakeLoads = 4;                     // and while its members are taken
-constexpr uint32_t kQueue = 32 * (kTakeLoads + 1);      // members that a warp has at hand
-constexpr size_t kAdjustMaxSmem = 108 * 1024;     // two CTAs of 512 threads to an SM
-constexpr int64_t kAdjustCtas = 304;              // that rows are cut into, where they are fewer
+constexpr uint32_t kChunk = 1024, kChunks = 4;    // tokens of a chunk of a long history, and chunks on their way at once
+constexpr uint32_t kQueue = 64;                   // members of the set that a warp has room for, at least
+// A CTA of 512 threads has half an SM, one of 1024 a whole one: for histories that do not
+// fit beside the rest in the half.
+constexpr size_t kHalfSmem = 108 * 1024, kWholeSmem = 218 * 1024;
+constexpr int64_t kHalfCtas = 304, kWholeCtas = 152;      // that rows are cut into, where they are fewer
 constexpr uint32_t kSeenBefore = 0x80000000u;     // of a count: the token is in the prompt
 constexpr uint32_t kNowhere = 0xFFFFFFFFu;
 constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier
@@ -61,8 +62,10 @@ template <typename T> struct AdjustArgs {
     uint32_t pieces, tokens; // pieces of a row, of so many tokens (a multiple of 256) each
     uint32_t slots, table;   // words of the set's slots; entries of the biases' table, a power of two
     uint32_t stages;         // of the ring; 0: none
+    uint32_t stage_vectors;  // of a stage for each thread
     uint32_t ring_words;     // of shared memory, for the ring and after it the queues
     uint32_t streamers;      // threads that pass the logits by; the others see to what is named
+    bool history_whole;      // the history has room in shared memory
     bool narrow;             // counts and numbers of members in 16 bits
     bool vectors;            // rows of in and out lie the same way to 16 bytes
     bool in_place;
@@ -109,6 +112,13 @@ struct TokenSet {
         const uint32_t half = 16 * (m & 1), c = atomicOr(slots + m / 2, 0xFFFFu << half) >> half & 0xFFFFu;
         return c == 0xFFFFu ? kNowhere : (c & 0x7FFFu) | (c & 0x8000u) << 16;      // fewer than 32768: 0xFFFF is no count
     }
+    // The same, of a member that one thread asks for.
+    __device__ __forceinline__ uint32_t counted(uint32_t at) const {
+        const uint32_t m = member(at);
+        if (!narrow) return slots[m];
+        const uint32_t c = reinterpret_cast<const uint16_t *>(slots)[m];
+        return (c & 0x7FFFu) | (c & 0x8000u) << 16;
+    }
     // Whether the token was there still: the gradient needs no counts.
     __device__ __forceinline__ bool take_bit(uint32_t at) const {
         const uint32_t bit = 1u << (at & 31);
@@ -145,7 +155,7 @@ __device__ __forceinline__ void number_members(const TokenSet &set, uint32_t wor
     crew.sync();
 }
 
-// The biased tokens of a piece, each with its last entry: an open hash table, at most half full.
+// The biased tokens of a piece, each with its last entry: an open hash table, at most three quarters full.
 struct BiasTable {
     uint2 *entries;      // token (kNowhere: free), entry + 1; null: no biases
     uint32_t mask;
@@ -175,25 +185,44 @@ struct Range {
     int32_t first, begin, end;
 };
 
-// The tokens i, i + step, ... of a list, as distances from the piece's first one.  What is no
-// 32-bit number is no token.
-template <int K>
-__device__ __forceinline__ void load_tokens(const void *list, int bytes, int64_t row, uint32_t length, uint32_t i, uint32_t step,
-                                            const Range &r, uint32_t (&at)[K]) {
-    const uint32_t words = bytes / 4;
-    const uint32_t *p = static_cast<const uint32_t *>(list) + (row + i) * words;
-    uint32_t high[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const bool there = i + k * step < length;
-        at[k] = there ? p[k * step * words] : kNowhere;
-        high[k] = there && words == 2 ? p[k * step * words + 1] : 0;
+// The history in shared memory, whole or in chunks.  A thread copies tokens rank, rank +
+// threads, ... without registers, and looks at no others, so that it waits for its own copies
+// alone.
+struct History {
+    const char *row;         // the row's tokens
+    uint32_t *data;
+    uint32_t length, words;  // tokens; words of each
+    bool whole;              // a chunk is all of it
+
+    __device__ __forceinline__ uint32_t chunk() const { return whole ? length : kChunk; }
+    __device__ __forceinline__ uint32_t chunks() const { return whole ? 1 : (length + kChunk - 1) / kChunk; }
+    __device__ __forceinline__ uint32_t size(uint32_t c) const { return min(chunk(), length - c * kChunk); }
+    __device__ __forceinline__ uint32_t *slot(uint32_t c, uint32_t i) const { return data + ((c % kChunks) * kChunk + i) * words; }
+    __device__ __forceinline__ void fetch(uint32_t c, uint32_t rank, uint32_t threads) const {
+        if (c < chunks()) {
+            const char *from = row + static_cast<size_t>(c) * kChunk * words * 4;
+            for (uint32_t i = rank; i < size(c); i += threads) {
+                if (words == 1) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(slot(c, i))), "l"(from + i * 4) : "memory");
+                else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(slot(c, i))), "l"(from + i * 8) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    const uint32_t span = static_cast<uint32_t>(r.end - r.begin);    // at most 2^30: kNowhere is outside
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        at[k] = high[k] == 0 && at[k] - static_cast<uint32_t>(r.begin) < span ? at[k] - static_cast<uint32_t>(r.first) : kNowhere;
-}
+    __device__ __forceinline__ void start(uint32_t rank, uint32_t threads) const {
+        for (uint32_t c = 0; c + 1 < kChunks; ++c) fetch(c, rank, threads);
+    }
+    // The next chunk is asked for, and chunk c there.
+    __device__ __forceinline__ void next(uint32_t c, uint32_t rank, uint32_t threads) const {
+        fetch(c + kChunks - 1, rank, threads);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kChunks - 1) : "memory");
+    }
+    // A token as its distance from the piece's first one.  What is no 32-bit number is no token.
+    __device__ __forceinline__ uint32_t read(uint32_t c, uint32_t i, const Range &r) const {
+        const uint32_t *p = slot(c, i), t = p[0];
+        const bool inside = (words == 1 || p[1] == 0) && t - static_cast<uint32_t>(r.begin) < static_cast<uint32_t>(r.end - r.begin);
+        return inside ? t - static_cast<uint32_t>(r.first) : kNowhere;
+    }
+};
 
 // Elements whose bit is clear become -inf (or 0).
 template <typename T, bool ZERO> __device__ __forceinline__ void mask_vector(uint4 &q, uint32_t bits) {
@@ -208,7 +237,7 @@ template <typename T, bool ZERO> __device__ __forceinline__ void mask_vector(uin
 }
 
 template <typename T, bool BACK>
-__global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a) {
     constexpr int N = Wide<T>::kCount;
     constexpr uint32_t kAll = (1u << N) - 1;
     extern __shared__ __align__(128) uint32_t s_words[];
@@ -241,8 +270,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a
         seen.bits = space;
         seen.before = space + words;
         seen.slots = seen.before + (a.narrow ? words / 2 : words);
+        space = BACK ? seen.before : seen.slots + a.slots;
     }
-    const int64_t history_row = static_cast<int64_t>(row) * a.history_stride, bias_row = static_cast<int64_t>(row) * a.bias_stride;
+    const History history{static_cast<const char *>(a.history) + static_cast<int64_t>(row) * a.history_stride * a.history_bytes,
+                          space + (space - s_words) % 2, a.length, static_cast<uint32_t>(a.history_bytes) / 4, a.history_whole};
+    const int64_t bias_row = static_cast<int64_t>(row) * a.bias_stride;
     auto bias_at = [&](uint32_t i) {           // an entry's token as a distance from the piece's first one
         const int64_t t = int_at(a.bias_tokens, a.bias_bytes, bias_row + i);
         return t >= r.begin && t < r.end ? static_cast<uint32_t>(t - r.first) : kNowhere;
@@ -255,7 +287,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a
         const uint32_t low_v = r.first < 0 ? 1 : 0, high_v = a.vectors ? static_cast<uint32_t>(r.end - r.first) / N : 0;
         const uint4 *in_v = reinterpret_cast<const uint4 *>(in + r.first);     // read from low_v on
         uint4 *out_v = reinterpret_cast<uint4 *>(out + r.first);
-        const uint32_t per_stage = threads * kStageVectors;
+        const uint32_t per_stage = threads * a.stage_vectors;
         auto copy = [&](uint32_t k) {          // the ring's stage k: vectors low_v + k * per_stage ...; thread 0
             const uint32_t from = low_v + k * per_stage;
             if (from >= high_v) return;
@@ -264,18 +296,20 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a
             mbar_arrive_expect_tx(&s_full[stage], bytes);
             bulk_load(ring + stage * per_stage, in_v + from, bytes, &s_full[stage]);
         };
+        // the mask's words ask first: behind the ring's copies each load takes microseconds
+        const uint32_t *mask = a.allowed + static_cast<int64_t>(row) * a.allowed_stride;
+        const int32_t last = static_cast<int32_t>((a.vocab - 1) / 32);
+        const uint32_t off = static_cast<uint32_t>(r.first) & 31;
+        const int32_t k0 = r.first >> 5;       // -1 where the first vector begins before the row
+        for (uint32_t w = tid * 32; allowed && w < words + 32; w += 32 * a.streamers)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(mask + min(max(k0 + static_cast<int32_t>(w), 0), last)));
         if (tid == 0) {
             s_failed = 0;
             for (uint32_t k = 0; k < a.stages; ++k) mbar_init(&s_full[k], 1);
             for (uint32_t k = 0; k < a.stages; ++k) copy(k);
         }
         if (allowed != nullptr) {              // word w: the bits of the piece's tokens 32 w ..
-            const uint32_t *mask = a.allowed + static_cast<int64_t>(row) * a.allowed_stride;
-            const int32_t last = static_cast<int32_t>((a.vocab - 1) / 32);
-            // Eight words' loads at once: behind the ring's copies each takes microseconds.  Words
-            // beside the mask's hold no token of the piece.
-            const uint32_t off = static_cast<uint32_t>(r.first) & 31;
-            const int32_t k0 = r.first >> 5;               // -1 where the first vector begins before the row
+            // words beside the mask's hold no token of the piece
             for (uint32_t w0 = tid; w0 < words; w0 += 8 * a.streamers) {
                 uint32_t here[8], next[8];
 #pragma unroll
@@ -327,45 +361,32 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a
     } else {
         // ------------------------------------------------ what is named
         const Crew crew{2, threads - a.streamers, tid - a.streamers};
-        const uint32_t span = crew.threads * kHistoryLoads;
-        uint32_t at[kHistoryLoads], then[kHistoryLoads];
-        auto load = [&](uint32_t base, uint32_t (&to)[kHistoryLoads]) {
-            load_tokens(a.history, a.history_bytes, history_row, a.length, base + crew.rank, crew.threads, r, to);
-        };
-        if (seen.bits) {
-            load(0, at);
-            for (uint32_t w = crew.rank; w < words; w += crew.threads) seen.bits[w] = 0;
-        }
-        for (uint32_t i = crew.rank; biased.entries && i < a.table; i += crew.threads) biased.entries[i] = make_uint2(kNowhere, 0);
+        const uint32_t step = crew.threads, chunks = seen.bits ? history.chunks() : 0;
+        if (chunks > 0) history.start(crew.rank, step);
+        for (uint32_t w = crew.rank; seen.bits && w < words; w += step) seen.bits[w] = 0;
+        for (uint32_t i = crew.rank; biased.entries && i < a.table; i += step) biased.entries[i] = make_uint2(kNowhere, 0);
         crew.sync();
-        for (uint32_t base = 0; seen.bits && base < a.length; base += span) {
-            if (base + span < a.length) load(base + span, then);       // while these are added
-#pragma unroll
-            for (int k = 0; k < kHistoryLoads; ++k) seen.add(at[k]);
-            if (base + span < a.length) {
-#pragma unroll
-                for (int k = 0; k < kHistoryLoads; ++k) at[k] = then[k];
-            }
+        for (uint32_t c = 0; c < chunks; ++c) {
+            history.next(c, crew.rank, step);
+#pragma unroll 4
+            for (uint32_t i = crew.rank; i < history.size(c); i += step) seen.add(history.read(c, i, r));
         }
-        for (uint32_t i = crew.rank; biased.entries && i < a.biases; i += crew.threads) biased.add(bias_at(i), i);
+        for (uint32_t i = crew.rank; biased.entries && i < a.biases; i += step) biased.add(bias_at(i), i);
+        if (chunks > 0 && !history.whole) history.start(crew.rank, step);
         crew.sync();
-        if constexpr (!BACK) {
-            if (seen.bits) {
-                const uint32_t prompt = a.prompt ? static_cast<uint32_t>(max(a.prompt[row], 0)) : 0;
-                if (a.length > span) load(0, at);                      // a history of one step is still there
-                number_members(seen, words, crew);
-                for (uint32_t base = 0; base < a.length; base += span) {
-                    if (base + span < a.length) load(base + span, then);
-#pragma unroll
-                    for (int k = 0; k < kHistoryLoads; ++k)
-                        if (at[k] != kNowhere) seen.count(at[k], base + k * crew.threads + crew.rank < prompt);
-                    if (base + span < a.length) {
-#pragma unroll
-                        for (int k = 0; k < kHistoryLoads; ++k) at[k] = then[k];
-                    }
+        if (!BACK && chunks > 0) {
+            const uint32_t prompt = a.prompt ? static_cast<uint32_t>(max(a.prompt[row], 0)) : 0;
+            number_members(seen, words, crew);
+            for (uint32_t c = 0; c < chunks; ++c) {
+                if (!history.whole) history.next(c, crew.rank, step);
+#pragma unroll 4
+                for (uint32_t i = crew.rank; i < history.size(c); i += step) {
+                    const uint32_t at = history.read(c, i, r);
+                    if (at != kNowhere) seen.count(at, c * kChunk + i < prompt);
                 }
             }
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     if (a.streamers == threads) return;
 
@@ -373,53 +394,47 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a
     const float repetition = a.repetition ? a.repetition[row] : 1.0f;
     const float presence = !BACK && a.presence ? a.presence[row] : 0.0f, frequency = !BACK && a.frequency ? a.frequency[row] : 0.0f;
     const T *logits = BACK ? a.logits + static_cast<int64_t>(row) * a.logits_stride : nullptr;
-    uint32_t at[kTakeLoads];
-    if (seen.bits) load_tokens(a.history, a.history_bytes, history_row, a.length, tid, threads, r, at);
     __syncthreads();
     const uint32_t lane = tid & 31;
+    // A warp queues its tokens, and asks for their logits, before it writes any: one after another
+    // they would each wait for memory.
+    const uint32_t room = a.ring_words / 2 / (threads / 32);
     uint32_t queued = 0;
-    uint2 *const queue = reinterpret_cast<uint2 *>(s_words) + (tid >> 5) * kQueue;      // where the ring was
+    uint2 *const queue = reinterpret_cast<uint2 *>(s_words) + (tid >> 5) * room;      // where the ring was
+    auto serve = [&] {
+        __syncwarp();
+        for (uint32_t i = lane; i < queued; i += 32) {
+            const uint2 q = queue[i];
+            const int32_t e = r.first + static_cast<int32_t>(q.x);
+            float x = to_f32(in[e]);                           // in place, it holds its value still
+            if (BACK) {
+                x *= to_f32(logits[e]) > 0.0f ? 1.0f / repetition : repetition;
+            } else {
+                const uint32_t times = q.y & ~kSeenBefore, b = biased.entries ? biased.find(q.x) : 0;
+                const float by = b != 0 ? a.bias[bias_row + b - 1] : 0.0f;
+                if (q.y != 0) x = x > 0.0f ? x / repetition : x * repetition;
+                if (times != 0) x -= fmaf(frequency, static_cast<float>(times), presence);
+                if (b != 0) x += by;
+            }
+            out[e] = from_f32<T>(x);
+        }
+        queued = 0;
+        __syncwarp();
+    };
     auto push = [&](uint32_t token, uint32_t count) {          // kNowhere: none
-        const uint32_t active = __ballot_sync(kFullMask, token != kNowhere);
-        if (token != kNowhere) {
+        const bool real = token != kNowhere && (allowed == nullptr || bits_at(allowed, token, 1));
+        const uint32_t active = __ballot_sync(kFullMask, real);
+        if (real) {
             queue[queued + __popc(active & lanemask_lt())] = make_uint2(token, count);
             asm volatile("prefetch.global.L1 [%0];" ::"l"(in + r.first + static_cast<int32_t>(token)));
             if (BACK) asm volatile("prefetch.global.L1 [%0];" ::"l"(logits + r.first + static_cast<int32_t>(token)));
         }
         queued += __popc(active);
+        if (queued + 32 > room) serve();
     };
-    auto serve = [&](uint32_t least) {                         // 32 at a time, until fewer than `least` are left
-        __syncwarp();
-        while (queued >= least && queued > 0) {
-            const uint32_t n = min(queued, 32u);
-            queued -= n;
-            if (lane < n) {
-                const uint2 q = queue[queued + lane];
-                if (allowed == nullptr || bits_at(allowed, q.x, 1)) {
-                    const int32_t e = r.first + static_cast<int32_t>(q.x);
-                    float x = to_f32(in[e]);                   // in place, it holds its value still
-                    if (BACK) {
-                        x *= to_f32(logits[e]) > 0.0f ? 1.0f / repetition : repetition;
-                    } else {
-                        const uint32_t times = q.y & ~kSeenBefore, b = biased.entries ? biased.find(q.x) : 0;
-                        const float shift_by = b != 0 ? a.bias[bias_row + b - 1] : 0.0f;
-                        if (q.y != 0) x = x > 0.0f ? x / repetition : x * repetition;
-                        if (times != 0) x -= fmaf(frequency, static_cast<float>(times), presence);
-                        if (b != 0) x += shift_by;
-                    }
-                    out[e] = from_f32<T>(x);
-                }
-            }
-        }
-        __syncwarp();
-    };
-    for (uint32_t base = 0; seen.bits && base < a.length; base += threads * kTakeLoads) {
-        uint32_t then[kTakeLoads];
-        const bool more = base + threads * kTakeLoads < a.length;
-        if (more) load_tokens(a.history, a.history_bytes, history_row, a.length, base + threads * kTakeLoads + tid, threads, r, then);
-#pragma unroll
-        for (int k = 0; k < kTakeLoads; ++k) {
-            uint32_t token = at[k], count = 0;
+    if (seen.bits && a.length <= threads * 4) {  // a short history: the first of a token's places takes it
+        for (uint32_t i = tid; i - tid < a.length; i += threads) {
+            uint32_t token = i < a.length ? history.read(0, i, r) : kNowhere, count = 0;
             if (token != kNowhere) {
                 if (BACK) {
                     if (!seen.take_bit(token)) token = kNowhere;
@@ -430,10 +445,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a
             }
             push(token, count);
         }
-        serve(32);
-        if (more) {
-#pragma unroll
-            for (int k = 0; k < kTakeLoads; ++k) at[k] = then[k];
+    } else if (seen.bits) {                    // of a long one, a thread takes a word's members
+        for (uint32_t w = tid; w - tid < words; w += threads) {
+            uint32_t bits = w < words ? seen.bits[w] : 0;
+            while (__any_sync(kFullMask, bits != 0)) {
+                const uint32_t token = bits != 0 ? w * 32 + __ffs(bits) - 1 : kNowhere;
+                bits &= bits - 1;
+                push(token, !BACK && token != kNowhere ? seen.counted(token) : 0);
+            }
         }
     }
     if (!BACK && biased.entries) {             // biased tokens that are not in the history, by their last entry
@@ -441,10 +460,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_adjust(const AdjustArgs<T> a
             uint32_t token = base + tid < a.biases ? bias_at(base + tid) : kNowhere;
             if (token != kNowhere && (seen.has(token) || biased.find(token) != base + tid + 1)) token = kNowhere;
             push(token, 0);
-            serve(32);
         }
     }
-    serve(1);
+    serve();
 }
 
 }  // namespace
@@ -453,10 +471,6 @@ int launch_adjust(const AdjustLaunch &L) {
     return with_float_type(L.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int N = Wide<T>::kCount;
-        const int threads = getenv("AT") ? atoi(getenv("AT")) : 512;
-        const int64_t least = threads * N;         // tokens of a piece: a vector for every thread
-        const int64_t ctas = kAdjustCtas * (512 / threads);
-        const size_t most_smem = threads == 512 ? kAdjustMaxSmem : 51 * 1024;
         AdjustArgs<T> a{};
         a.logits = static_cast<const T *>(L.logits);
         a.in = static_cast<const T *>(L.in);
@@ -485,27 +499,46 @@ int launch_adjust(const AdjustLaunch &L) {
         // a row has the distance from the boundary of its array and `row` strides
         a.vectors = ((reinterpret_cast<uintptr_t>(L.in) ^ reinterpret_cast<uintptr_t>(L.out)) & 15) == 0 &&
                     (L.rows == 1 || (L.in_stride - L.out_stride) % N == 0);
-        // pieces that fill the device, smaller ones where their sets would take too much room
-        const int64_t want = std::max<int64_t>(ctas / L.rows, 1), most = (L.vocab + least - 1) / least;
-        const int64_t pieces = std::min(want, most), span = L.vocab + (a.vectors ? N - 1 : 0);
-        int64_t tokens = std::max<int64_t>(256, (std::min<int64_t>(span / pieces + 1, 1 << 18) + 255) / 256 * 256);
         const bool history = a.history != nullptr, biases = !L.backward && L.biases > 0, ring = a.vectors && !a.in_place;
-        const size_t stage = static_cast<size_t>(threads) * kStageVectors * 16, queues = history || biases ? threads / 32 * kQueue * 8 : 0;
-        a.streamers = history || biases ? (getenv("AS") ? atoi(getenv("AS")) * threads / 8 : threads / 2) : threads;
+        const int64_t span = L.vocab + (a.vectors ? N - 1 : 0);
+        int64_t tokens = 0;
+        uint32_t threads = 0;
+        size_t most_smem = 0, queues = 0;
         auto set_bytes = [&] {
             const int64_t words = tokens / 32, members = std::min(tokens, L.length);
             a.tokens = static_cast<uint32_t>(tokens);
             a.narrow = is_narrow(L.length);
             a.slots = static_cast<uint32_t>(a.narrow ? (members + 1) / 2 : members);
             a.table = 1;
-            while (biases && a.table < 2 * std::min(tokens, L.biases)) a.table *= 2;
+            while (biases && 3 * a.table < 4 * std::min(tokens, L.biases)) a.table *= 2;
             int64_t all = (L.allowed != nullptr ? words : 0) + (biases ? 2 * a.table : 0);
             if (history) all += words + (L.backward ? 0 : (a.narrow ? words / 2 : words) + a.slots);
+            if (history) all += 1 + (a.history_whole ? L.length : kChunks * kChunk) * (L.history_bytes / 4);
             return static_cast<size_t>(all) * 4;
         };
-        const size_t least_ring = std::max(ring ? 2 * stage : 0, queues);
-        while (set_bytes() + least_ring > most_smem) tokens = (tokens / 2 + 255) / 256 * 256;
-        const size_t sets = set_bytes();
+        auto stage_bytes = [&] { return static_cast<size_t>(threads) * a.stage_vectors * 16; };
+        auto fits = [&] { return set_bytes() + std::max(ring ? 2 * stage_bytes() : 0, queues) <= most_smem; };
+        // Pieces that fill the device; false where their sets take too much room.
+        auto plan = [&](uint32_t n, size_t smem, int64_t ctas) {
+            threads = n;
+            most_smem = smem;
+            queues = history || biases ? threads / 32 * kQueue * 8 : 0;
+            const int64_t least = static_cast<int64_t>(threads) * N;         // a vector for every thread
+            const int64_t pieces = std::min(std::max<int64_t>(ctas / L.rows, 1), (L.vocab + least - 1) / least);
+            tokens = std::max<int64_t>(256, (std::min<int64_t>(span / pieces + 1, 1 << 18) + 255) / 256 * 256);
+            a.stage_vectors = kStageVectors;
+            if (!fits()) a.stage_vectors = 1;
+            return fits();
+        };
+        a.history_whole = true;
+        if (!plan(512, kHalfSmem, kHalfCtas) && !plan(1024, kWholeSmem, kWholeCtas)) {
+            a.history_whole = L.length <= kChunks * kChunk;
+            while (!fits()) tokens = (tokens / 2 + 255) / 256 * 256;
+        }
+        // what is named takes longer where the history is long (256 x 100003 bf16, histories of 16384: 63 us
+        // with a quarter of the threads for the logits, 66 with half; 2048 x 131072 with 1024: 386 and 377)
+        a.streamers = !history && !biases ? threads : threads == 1024 ? threads / 4 : threads / 2;
+        const size_t sets = set_bytes(), stage = stage_bytes();
         if (ring) {
             const size_t stages = std::min<size_t>((most_smem - sets) / stage, kMostStages);
             a.stages = static_cast<uint32_t>(std::min<size_t>(stages, (tokens / N * 16 + stage - 1) / stage));
@@ -517,7 +550,7 @@ int launch_adjust(const AdjustLaunch &L) {
         if (blocks > 0x7FFFFFFF) return static_cast<int>(GSORT_ETOOBIG);
         const size_t smem = sets + ring_bytes;
         const void *kernel = L.backward ? reinterpret_cast<const void *>(k_adjust<T, true>) : reinterpret_cast<const void *>(k_adjust<T, false>);
-        if (smem > 40 * 1024 && set_smem_limit(kernel, kAdjustMaxSmem) != cudaSuccess) return static_cast<int>(GSORT_ECUDA);
+        if (smem > 40 * 1024 && set_smem_limit(kernel, kWholeSmem) != cudaSuccess) return static_cast<int>(GSORT_ECUDA);
         if (L.backward) k_adjust<T, true><<<static_cast<uint32_t>(blocks), threads, smem, L.stream>>>(a);
         else k_adjust<T, false><<<static_cast<uint32_t>(blocks), threads, smem, L.stream>>>(a);
         return cudaGetLastError() == cudaSuccess ? static_cast<int>(GSORT_OK) : static_cast<int>(GSORT_ECUDA);

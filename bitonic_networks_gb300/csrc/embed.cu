@@ -34,7 +34,7 @@ constexpr uint32_t kFillCtas = 608;                 // CTAs that keep a GB300 bu
 // A CTA that fills rows takes so many bytes: a table of 1 GB of 8 KB rows takes 146 us, 144 with
 // half, 151 with twice as many; with 65536 tokens, which make runs of absent rows short, the gradient
 // takes 384 us with its lookup, 393 with half.
-constexpr int64_t kFillBytes = 128 << 10;
+constexpr int64_t kFillBytes = 128 << 10, kWideRow = 2048;
 // Bytes that are filled while the tokens are sorted, by counting or in a cluster; what
 // is left is filled beside the sums.
 constexpr int64_t kBesideFew = 32 << 20, kBesideCounting = 64 << 20, kBesideCluster = 128 << 20;
@@ -123,20 +123,21 @@ struct FillArgs {
     uint32_t n;
 };
 
-// A CTA writes a span of bytes with what `word` has twice.
-__device__ __forceinline__ void fill_span(char *p, int64_t bytes, uint32_t word) {
-    const uint32_t tid = threadIdx.x;
+// THREADS threads write a span of bytes with what `word` has twice.
+template <uint32_t THREADS> __device__ __forceinline__ void fill_span(char *p, int64_t bytes, uint32_t word) {
+    const uint32_t rank = threadIdx.x % THREADS;
     const int64_t head = min(static_cast<int64_t>(-reinterpret_cast<intptr_t>(p) & 15), bytes);
     const int64_t vectors = (bytes - head) / 16, tail = head + vectors * 16;
-    if (tid < head / 2) reinterpret_cast<uint16_t *>(p)[tid] = static_cast<uint16_t>(word);
+    if (rank < head / 2) reinterpret_cast<uint16_t *>(p)[rank] = static_cast<uint16_t>(word);
     uint4 *v = reinterpret_cast<uint4 *>(p + head);
 #pragma unroll 4
-    for (int64_t i = tid; i < vectors; i += kEmbedThreads) v[i] = make_uint4(word, word, word, word);
-    if (tid < (bytes - tail) / 2) reinterpret_cast<uint16_t *>(p + tail)[tid] = static_cast<uint16_t>(word);
+    for (int64_t i = rank; i < vectors; i += THREADS) v[i] = make_uint4(word, word, word, word);
+    if (rank < (bytes - tail) / 2) reinterpret_cast<uint16_t *>(p + tail)[rank] = static_cast<uint16_t>(word);
 }
 
-// Fills the absent rows of CTA number `block`.  The CTA writes a run of them as a whole:
-// 400 MB of rows of 4004 bytes take 57 us so (7.0 TB/s), 63 with a run to each warp.
+// Fills the absent rows of CTA number `block`.  The CTA writes a run of them as a whole (400 MB
+// of rows of 4004 bytes take 57 us so, 7.0 TB/s, and 63 with a run to each warp), short rows by
+// warps.
 __device__ __forceinline__ void fill_absent(const FillArgs &a, uint32_t block) {
     __shared__ uint32_t s_bits[9];     // of 256 tokens, from any bit of the first word on
     const uint32_t base = block * a.rows, rows = min(a.rows, a.vocab - base), tid = threadIdx.x;
@@ -151,20 +152,29 @@ __device__ __forceinline__ void fill_absent(const FillArgs &a, uint32_t block) {
         }
         __syncthreads();
     }
-    // the first row from r on that is present (or absent), `rows` at most
-    auto find = [&](uint32_t r, bool present) {
-        while (r < rows) {
+    // the first row from r on that is present (or absent), `to` at most
+    auto find = [&](uint32_t r, uint32_t to, bool present) {
+        while (r < to) {
             const uint32_t at = shift + r, left = 32 - (at & 31);
             const uint32_t w = (present ? s_bits[at / 32] : ~s_bits[at / 32]) >> (at & 31);
-            if (w != 0) return min(r + __ffs(w) - 1, rows);        // zeros are shifted in
+            if (w != 0) return min(r + __ffs(w) - 1, to);          // zeros are shifted in
             r += left;
         }
-        return rows;
+        return to;
     };
-    for (uint32_t r = find(0, false); r < rows;) {
-        const uint32_t end = find(r, true), run = a.stride == a.row_bytes ? end - r : 1;   // without gaps, rows are one span
-        for (; r < end; r += run) fill_span(a.table + (base + static_cast<int64_t>(r)) * a.stride, run * a.row_bytes, 0);
-        r = find(end, false);
+    auto fill = [&](auto team, uint32_t from, uint32_t to) {
+        for (uint32_t r = find(from, to, false); r < to;) {
+            const uint32_t end = find(r, to, true), run = a.stride == a.row_bytes ? end - r : 1;   // without gaps, rows are one span
+            for (; r < end; r += run)
+                fill_span<decltype(team)::value>(a.table + (base + static_cast<int64_t>(r)) * a.stride, run * a.row_bytes, 0);
+            r = find(end, to, false);
+        }
+    };
+    if (a.row_bytes >= kWideRow) {
+        fill(std::integral_constant<uint32_t, kEmbedThreads>{}, 0, rows);
+    } else {
+        const uint32_t per = (rows + 7) / 8, from = min(tid / 32 * per, rows);
+        fill(std::integral_constant<uint32_t, 32>{}, from, min(from + per, rows));
     }
 }
 
@@ -180,7 +190,9 @@ __global__ void __launch_bounds__(256) k_fill_absent(const FillArgs a) {
 // its 32 tokens with an eighth of all (a broadcast from shared memory each).  The
 // CTAs behind those of the tokens fill absent rows.
 constexpr uint32_t kRankMax = 8192;
-constexpr uint32_t kFewTokens = 2048;      // every CTA that fills looks at them itself
+// Up to so many tokens, and more of them where few CTAs fill, each CTA that fills looks at the
+// tokens itself: two launches instead of five (3500 tokens, a table of 2890 x 120 f32: KEEP us).
+constexpr uint32_t kFewTokens = 2048, kFewFills = 1216;
 
 __global__ void __launch_bounds__(256) k_token_rank(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys,
                                                     uint32_t *order, uint32_t *status, uint32_t *counters, uint32_t count,
@@ -314,7 +326,8 @@ __global__ void __launch_bounds__(kEmbedThreads, 4) k_embed_sum(const EmbedSumAr
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // rows are filled meanwhile
     if (a.status != nullptr && *a.status != 0) {       // the sort gave up, its results are void: all rows are NaN
         for (uint32_t r = blockIdx.x; r < a.vocab; r += gridDim.x)
-            fill_span(reinterpret_cast<char *>(a.out + static_cast<int64_t>(r) * a.out_stride), static_cast<int64_t>(a.width) * sizeof(T), 0x7FFF7FFFu);
+            fill_span<kEmbedThreads>(reinterpret_cast<char *>(a.out + static_cast<int64_t>(r) * a.out_stride),
+                                     static_cast<int64_t>(a.width) * sizeof(T), 0x7FFF7FFFu);
         return;
     }
     __shared__ uint32_t s_key[kMaxChunk + 2], s_order[kMaxChunk];   // s_key[0]: the key before the chunk
@@ -576,7 +589,8 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
     fill.tokens = L.tokens;
     fill.token_bytes = L.token_bytes;
     fill.n = n;
-    fill.rows = static_cast<uint32_t>(std::min<int64_t>(256, std::max<int64_t>(1, kFillBytes / fill.row_bytes)));
+    // fewer of a small table, to fill the device
+    fill.rows = static_cast<uint32_t>(std::max<int64_t>(1, std::min({static_cast<int64_t>(256), kFillBytes / fill.row_bytes, std::max<int64_t>(8, vocab / kFillCtas)})));
     const uint32_t fill_ctas = L.accumulate ? 0 : (vocab + fill.rows - 1) / fill.rows;
     uint32_t *counters = reinterpret_cast<uint32_t *>(L.ws + plan.counters), *status = reinterpret_cast<uint32_t *>(L.ws + kHdrStatus);
     const uint64_t sums = static_cast<uint64_t>(plan.chunks) * plan.slabs;
@@ -587,10 +601,11 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
         fill.first = from;
         return from < to ? launch_early(k_fill_absent, to - from, L.stream, fill) : static_cast<int>(GSORT_OK);
     };
+    const bool few = n <= kFewTokens || (n <= kRankMax && static_cast<int64_t>(fill_ctas) * n <= static_cast<int64_t>(kFewFills) * kFewTokens);
     // of the CTAs that fill, those before the sums
-    const int64_t beside = n <= kFewTokens ? kBesideFew : n <= kRankMax ? kBesideCounting : cluster_sort_applies(n, 4, 0, kNoStall, 1) ? kBesideCluster : 0;
+    const int64_t beside = few ? kBesideFew : n <= kRankMax ? kBesideCounting : cluster_sort_applies(n, 4, 0, kNoStall, 1) ? kBesideCluster : 0;
     const uint32_t filled = n == 0 ? fill_ctas : static_cast<uint32_t>(std::min<int64_t>(fill_ctas, beside / (fill.row_bytes * fill.rows)));
-    if (n <= kFewTokens) {
+    if (few) {
         if (groups == 0 && fill_ctas == 0) return GSORT_OK;
         k_token_rank<<<groups + filled, 256, groups * 32 * 4, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys, order, status, counters, count, fill);
         if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(256) k_token_keys(const void *tokens, int byte
     if (i >= n) return;
     const uint32_t key = token_key(token_at(tokens, bytes, i), vocab);
     keys[i] = key;
-    if (positions != nullptr) positions[i] = i;
+    positions[i] = i;
     // frequent tokens find their bit set
     if (bits != nullptr && key < vocab && !(ld_relaxed(bits + key / 32) >> (key & 31) & 1)) atomicOr(bits + key / 32, 1u << (key & 31));
 }
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) k_fill_absent(const FillArgs a) {
 // CTAs behind those of the tokens fill absent rows.
 constexpr uint32_t kRankMax = 8192;
 // Up to so many tokens, and more of them where few CTAs fill, each CTA that fills looks at the
-// tokens itself: two launches instead of five (3500 tokens, a table of 2890 x 120 f32: KEEP us).
+// tokens itself: two launches instead of five (3500 tokens, a table of 2890 x 120 f32: 18 us, 24 with five).
 constexpr uint32_t kFewTokens = 2048, kFewFills = 1216;
 
 __global__ void __launch_bounds__(256) k_token_rank(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys,
@@ -204,7 +204,6 @@ __global__ void __launch_bounds__(256) k_token_rank(const void *tokens, int byte
         fill_absent(fill, blockIdx.x - groups);
         return;
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // rows are filled meanwhile
     if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;              // of the call: this sort cannot fail
     for (uint32_t c = blockIdx.x * 256 + threadIdx.x; c < count; c += groups * 256) counters[c] = 0;
     for (uint32_t i = threadIdx.x; i < groups * 32; i += 256)
@@ -242,6 +241,81 @@ __global__ void __launch_bounds__(256) k_token_rank(const void *tokens, int byte
         for (int w = 0; w < 8; ++w) rank += s_rank[w][lane];
         keys[rank] = mine;
         order[rank] = i;
+    }
+}
+
+// More of them are sorted in two steps.  Runs of 256 tokens, by counting within the run; bits, where they
+// are asked for, and the call's counters and status on the way.
+constexpr uint32_t kRun = 256;
+
+__global__ void __launch_bounds__(kRun) k_token_runs(const void *tokens, int bytes, uint32_t n, uint32_t vocab, uint32_t *keys, uint32_t *order,
+                                                     uint32_t *bits, uint32_t *status, uint32_t *counters, uint32_t count) {
+    __shared__ __align__(16) uint32_t s_keys[kRun];
+    const uint32_t tid = threadIdx.x, base = blockIdx.x * kRun, i = base + tid, group = tid / 32, lane = tid & 31;
+    for (uint32_t c = i; c < count; c += gridDim.x * kRun) counters[c] = 0;
+    if (i == 0) *status = 0;             // this sort cannot fail
+    const uint32_t mine = i < n ? token_key(token_at(tokens, bytes, i), vocab) : kNoKey;       // behind every token
+    s_keys[tid] = mine;
+    if (bits != nullptr && mine < vocab && !(ld_relaxed(bits + mine / 32) >> (mine & 31) & 1)) atomicOr(bits + mine / 32, 1u << (mine & 31));
+    __syncthreads();
+    uint32_t rank = 0;
+#pragma unroll 2
+    for (uint32_t g = 0; g < kRun / 32; ++g) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(s_keys + g * 32);
+        const uint32_t limit = mine + (g < group);         // equal ones before are counted
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+            const uint4 k = q[j];
+            if (g == group) {
+                rank += (k.x < mine || (k.x == mine && 4 * j < lane)) + (k.y < mine || (k.y == mine && 4 * j + 1 < lane)) +
+                        (k.z < mine || (k.z == mine && 4 * j + 2 < lane)) + (k.w < mine || (k.w == mine && 4 * j + 3 < lane));
+            } else {
+                rank += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+            }
+        }
+    }
+    if (i < n) {
+        keys[base + rank] = mine;
+        order[base + rank] = i;
+    }
+}
+
+// Joins the runs: a token's place is the number of tokens before it in every run, found by
+// halving.  A lane holds a token, a warp looks at an eighth of the runs.  (8000 tokens added to a
+// table of 32000 x 512 bf16 take 25 us so, 29 by counting among all of them.)
+__global__ void __launch_bounds__(256) k_token_join(const uint32_t *run_keys, const uint32_t *run_order, uint32_t n, uint32_t *keys, uint32_t *order) {
+    extern __shared__ __align__(16) uint32_t s_keys[];       // n
+    __shared__ uint32_t s_rank[8][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // rows are filled meanwhile
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, runs = (n + kRun - 1) / kRun;
+#pragma unroll 8
+    for (uint32_t i = threadIdx.x; i < n; i += 256) s_keys[i] = run_keys[i];
+    __syncthreads();
+    const uint32_t i = blockIdx.x * 32 + lane, own = blockIdx.x * 32 / kRun, mine = i < n ? s_keys[i] : 0;
+    uint32_t rank = 0;
+#pragma unroll 2
+    for (uint32_t b = warp; b < runs; b += 8) {
+        const uint32_t *run = s_keys + b * kRun;
+        const uint32_t size = min(kRun, n - b * kRun), limit = mine + (b < own);       // equal ones of earlier runs are before
+        if (b == own) {
+            rank += i - own * kRun;
+            continue;
+        }
+        uint32_t low = 0;                  // keys of the run below the limit
+#pragma unroll
+        for (uint32_t step = kRun / 2; step > 0; step /= 2)
+            if (low + step <= size && run[low + step - 1] < limit) low += step;
+        if (low < size && run[low] < limit) ++low;
+        rank += low;
+    }
+    s_rank[warp][lane] = rank;
+    __syncthreads();
+    if (warp == 0 && i < n) {
+        rank = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) rank += s_rank[w][lane];
+        keys[rank] = mine;
+        order[rank] = run_order[i];
     }
 }
 
@@ -509,13 +583,13 @@ EmbedPlan embed_plan(uint32_t n, uint32_t vocab, uint32_t width, int size) {
     if (n > kRankMax) {          // the sort's header comes first: its status is the call's
         p.radix = at;
         at += align_up(radix_layout(n, true, 4).total, kWsAlign);
-        p.order_in = at;
-        at += bytes;
     } else {
         at += kWsAlign;          // the status alone
     }
     if (n > kFewTokens) {
         p.keys_in = at;
+        at += bytes;
+        p.order_in = at;
         at += bytes;
         p.bits = at;
         at += align_up((static_cast<size_t>(vocab) + 31) / 32 * 4, kWsAlign);
@@ -601,7 +675,7 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
         fill.first = from;
         return from < to ? launch_early(k_fill_absent, to - from, L.stream, fill) : static_cast<int>(GSORT_OK);
     };
-    const bool few = n <= kFewTokens || (n <= kRankMax && static_cast<int64_t>(fill_ctas) * n <= static_cast<int64_t>(kFewFills) * kFewTokens);
+    const bool few = n <= kFewTokens || (n <= 2 * kFewTokens && static_cast<int64_t>(fill_ctas) * n <= static_cast<int64_t>(kFewFills) * kFewTokens);
     // of the CTAs that fill, those before the sums
     const int64_t beside = few ? kBesideFew : n <= kRankMax ? kBesideCounting : cluster_sort_applies(n, 4, 0, kNoStall, 1) ? kBesideCluster : 0;
     const uint32_t filled = n == 0 ? fill_ctas : static_cast<uint32_t>(std::min<int64_t>(fill_ctas, beside / (fill.row_bytes * fill.rows)));
@@ -611,15 +685,17 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
         if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
     } else {
         uint32_t *keys_in = reinterpret_cast<uint32_t *>(L.ws + plan.keys_in);
-        uint32_t *order_in = n > kRankMax ? reinterpret_cast<uint32_t *>(L.ws + plan.order_in) : nullptr;
+        uint32_t *order_in = reinterpret_cast<uint32_t *>(L.ws + plan.order_in);
         uint32_t *bits = L.accumulate ? nullptr : reinterpret_cast<uint32_t *>(L.ws + plan.bits);
         if (bits && cudaMemsetAsync(bits, 0, (static_cast<size_t>(vocab) + 31) / 32 * 4, L.stream) != cudaSuccess) return GSORT_ECUDA;
-        k_token_keys<<<(n + 255) / 256, 256, 0, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys_in, order_in, bits, counters, count);
-        if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
         if (n <= kRankMax) {
-            k_token_rank<<<groups, 256, groups * 32 * 4, L.stream>>>(keys_in, 4, n, vocab, keys, order, status, nullptr, 0, fill);
+            k_token_runs<<<(n + kRun - 1) / kRun, kRun, 0, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys_in, order_in, bits, status, counters, count);
+            if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
+            k_token_join<<<groups, 256, n * 4, L.stream>>>(keys_in, order_in, n, keys, order);
             if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
         } else {
+            k_token_keys<<<(n + 255) / 256, 256, 0, L.stream>>>(L.tokens, L.token_bytes, n, vocab, keys_in, order_in, bits, counters, count);
+            if (cudaGetLastError() != cudaSuccess) return GSORT_ECUDA;
             RadixLaunch R{};
             R.keys_in = keys_in;
             R.keys_out = keys;

@@ -670,8 +670,8 @@ struct TensorList {
         for (Py_ssize_t i = 0; i < n; ++i) {
             const Tensor &t = tensor(PySequence_Fast_GET_ITEM(fast, i), name);
             codes.push_back(float_code(t, name));
-            if (!t.is_cuda() || (device.has_value() && t.device() != *device))
-                refuse(PyExc_ValueError, "%s must be CUDA tensors of one device, got %s", name, text(t).c_str());
+            if (t.layout() != at::kStrided || !t.is_cuda() || (device.has_value() && t.device() != *device))
+                refuse(PyExc_ValueError, "%s must be strided CUDA tensors of one device, got %s", name, text(t).c_str());
             if (!t.is_non_overlapping_and_dense()) refuse(PyExc_ValueError, "%s must be dense, got %s with gaps or overlaps", name, text(t).c_str());
             if (t.requires_grad() && c10::GradMode::is_enabled())
                 refuse(PyExc_RuntimeError, "norm and clipping have no gradient: call them under torch.no_grad() or on detached tensors");

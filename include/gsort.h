@@ -462,7 +462,7 @@ int gsort_token_logprobs_backward(const float *d_grad_logprobs, const float *d_g
  * The gradient sums in 32 bits in an order that the tokens and the sizes give
  * (results are the same from run to run) and rounds once.  With more than 8192
  * tokens it uses the radix sort; where a wait of that gave up, gsort_check() of
- * the workspace says so and every row of d_grad_table is NaN.  The workspace may be NULL
+ * the workspace says so and the rows of tokens that occur are NaN.  The workspace may be NULL
  * where gsort_embed_tokens_backward_workspace_bytes() is 0 (no tokens). */
 int gsort_embed_tokens(const void *d_table, int dtype, int64_t vocab, int64_t width,
                        int64_t row_stride, const void *d_tokens, int token_bytes, int64_t tokens,

@@ -60,10 +60,44 @@ def test_sizes(dtype, vocab, length, biases, masked):
     check(*inputs(3, vocab, length, biases, masked, dtype))
 
 
-@pytest.mark.parametrize("rows,vocab,length", [(1, 40000, 5000), (150, 700, 33), (2, 100003, 20000)])
+@pytest.mark.parametrize("rows,vocab,length", [(1, 40000, 5000), (150, 700, 33), (2, 100003, 20000), (1, 3000, 40000), (2, 30000, 70000),
+                                               (3, 5000, 1024), (3, 5000, 4096), (3, 5000, 4097)])
 def test_long_histories(rows, vocab, length):
     for ints in (torch.int32, torch.int64):
         check(*inputs(rows, vocab, length, 300, True, torch.bfloat16, ints=ints))
+
+
+def test_integers_beyond_32_bits_are_no_tokens():
+    x = torch.randn(2, 100)
+    odd = torch.tensor([[3 + 2 ** 32, -2 ** 32 + 5, 2 ** 63 - 1, 7, -1]] * 2)
+    check(x, dict(history=odd, presence=torch.ones(2), repetition=torch.full((2,), 1.5), bias_tokens=odd, bias=torch.randn(2, 5)), None)
+
+
+def test_many_biases():
+    x, how, allowed = inputs(2, 30000, 50, 9000, True)
+    check(x, how, allowed)
+    spread = torch.arange(0, 30000, 11).repeat(2, 1)           # evenly spaced, all different
+    how.update(bias_tokens=spread, bias=torch.randn(spread.shape))
+    check(x, how, allowed)
+
+
+def test_dense_histories():
+    """Every token of the vocabulary, some again: the words of the set are full."""
+    x, how, allowed = inputs(2, 9000, 20000, 5, True)
+    how["history"] = (torch.arange(20000).repeat(2, 1) * 7 % 9000).int()
+    check(x, how, allowed)
+
+
+def test_more_rows_and_vocabulary_than_one_look_takes():
+    """Rows of several pieces, each of the largest size: the same row again and again is the row alone."""
+    x, how, allowed = inputs(1, 600_000, 3000, 40, True, torch.bfloat16)
+    one = call(x.cuda(), how, allowed)
+    rows = 310
+    many = {k: v.cuda().expand(rows, *v.shape[1:]).contiguous() for k, v in how.items()}
+    got = gs.adjust_logits(x.cuda().repeat(rows, 1), **many, allowed=pack(allowed).cuda().expand(rows, -1))
+    assert torch.equal(got, one.expand(rows, -1))
+    y, error, _ = adjust64(x, **how, allowed=allowed)
+    near(one, y, error)
 
 
 def test_one_token_again_and_again():
@@ -133,11 +167,12 @@ def test_strides(dtype, pad, off):
     d = torch.randn_like(want)
     g = back(d, x.cuda(), how, allowed)
     assert torch.equal(back(strided(d, pad, off), strided(x.cuda(), 3, 1), how, allowed, out=strided(d, 7, 1)), g)
-    wide = strided(how["history"].float(), 9).cuda().int()     # a wider buffer of histories
-    wide = torch.zeros(5, 250, dtype=torch.int32).cuda()
+    wide = torch.zeros(5, 250, dtype=torch.int32).cuda()       # wider buffers of histories and masks
     wide[:, :200] = how["history"].cuda()
+    words = torch.zeros(5, 300, dtype=torch.int32).cuda()
+    words[:, 1:283] = pack(allowed).cuda()
     lists = {**{k: v.cuda() for k, v in how.items()}, "history": wide[:, :200]}
-    assert torch.equal(gs.adjust_logits(xs, **lists, allowed=pack(allowed).cuda()), want)
+    assert torch.equal(gs.adjust_logits(xs, **lists, allowed=words[:, 1:283]), want)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -141,6 +141,17 @@ def test_dense_tensors_in_any_order_of_strides():
         check_clip([t, x], 1.0, out=[torch.empty_like(t), torch.empty_like(x)])
 
 
+def test_any_sequence_of_tensors():
+    x, y = torch.randn(100, device="cuda"), torch.randn(40, device="cuda")
+    want = gs.clip_gradients([x, y], 1.0)
+    for make_list in (tuple, iter, lambda ts: (t for t in ts)):
+        got = gs.clip_gradients(make_list([x, y]), 1.0, out=make_list([torch.empty_like(x), torch.empty_like(y)]))
+        assert isinstance(got.gradients, list) and torch.equal(got.norm, want.norm) and all(torch.equal(a, b) for a, b in zip(got.gradients, want.gradients))
+    with torch.inference_mode():
+        z = x.clone()
+        assert gs.clip_gradients([z], 1.0, out=[z]).gradients[0] is z
+
+
 def test_the_same_tensor_twice():
     x = torch.randn(1000, device="cuda")
     assert abs(float(gs.gradient_norm([x, x])) - math.sqrt(2) * norm64([x])) <= NORM * 2 * norm64([x])
@@ -166,7 +177,7 @@ def test_refusals():
         with pytest.raises(TypeError):
             call()
     for call in (lambda: gs.gradient_norm([]), lambda: gs.clip_gradients([], 1.0), lambda: gs.gradient_norm([x, y.cpu()]), lambda: gs.gradient_norm([x[::2]]),
-                 lambda: gs.gradient_norm([x.expand(3, 100)]), lambda: gs.clip_gradients([x], 1.0, out=[]), lambda: gs.clip_gradients([x], 1.0, out=[y]),
+                 lambda: gs.gradient_norm([x.expand(3, 100)]), lambda: gs.gradient_norm([x.to_sparse()]), lambda: gs.clip_gradients([x], 1.0, out=[]), lambda: gs.clip_gradients([x], 1.0, out=[y]),
                  lambda: gs.clip_gradients([x], 1.0, out=[x.half()]), lambda: gs.clip_gradients([x.view(10, 10)], 1.0, out=[torch.empty(10, 10, device="cuda").t()])):
         with pytest.raises(ValueError):
             call()

@@ -76,7 +76,7 @@ def test_decoding(example):
             count[torch.arange(5), last] += 1
 
 
-@pytest.mark.parametrize("n", [5, 3000, 9000])
+@pytest.mark.parametrize("n", [5, 3000, 9000, 70001])
 def test_steps_in_cuda_graphs(n):
     """A forward and backward pass and clipping, captured on a side stream and replayed on new
     inputs, beside an eager pass; two graphs captured into one pool replay one after another."""

@@ -92,7 +92,9 @@ __global__ void __launch_bounds__(kEmbedThreads) k_embed(const EmbedArgs<T> a) {
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, mul2(pair(a.scale, a.scale), Wide<T>::pair_of(q, i)));
         }
-        out.write(e, a.width, q);
+        // what is written is not read here again: the table's rows stay in L2 for tokens that come up again
+        if (MODE != kSingle && out.whole(e, a.width)) __stcs(reinterpret_cast<uint4 *>(out.row + e), q);
+        else out.write(e, a.width, q);
     }
 }
 

@@ -17,9 +17,13 @@
 // slot and the slots are no more than the history is long; counts are made in the slots
 // by a second look over the history, biases go to a hash table.  When the piece
 // is written, each token of the set is taken once, and its logit (from the caches) is
-// written anew.  The
-// memory bounds it: logits in, logits out.  In place, vectors in which nothing is masked
-// are neither read nor written.
+// written anew.  In place, vectors in which nothing is masked are neither read nor written.
+//
+// The memory bounds large calls: logits in, logits out.  2048 x 131072 bf16 with histories of 1024,
+// 64 biases and a mask take 183 us (6.1 TB/s of what is counted so), their gradient 184; 64 x
+// 131072 f32 with histories of 2048 16.4 us, of which 15 are what a copy with this grid takes.  Long
+// histories take longer than the logits: 256 x 100003 bf16 with 16384 tokens 61 us, the memory's
+// part 18, the rest looks over the history one after another.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -80,9 +84,10 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t *words, uint32_t at, 
     return words[at >> 5] >> (at & 31) & ((1u << n) - 1);
 }
 
-// Tokens of a piece, by their distance from its first one, in shared memory.
+// Histories whose counts fit 15 bits.
 constexpr bool is_narrow(int64_t length) { return length < 32768; }
 
+// Tokens of a piece, by their distance from its first one, in shared memory.
 struct TokenSet {
     uint32_t *bits;      // null: no set
     uint32_t *before;    // members before each word of bits

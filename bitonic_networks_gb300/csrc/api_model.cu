@@ -176,25 +176,48 @@ bool tensors_apart(const void *const *in, void *const *out, const int64_t *eleme
     return clear && (up || down) && (read_high <= low || high <= read_low || read_high == 0);
 }
 
+struct Range {
+    uintptr_t begin, end;
+    bool written;
+};
+
+// By address.  An allocator gives tensors in runs that go up or down: those are merged.
+void sort_runs(std::vector<Range> &v) {
+    auto before = [](const Range &x, const Range &y) { return x.begin < y.begin; };
+    std::vector<size_t> ends{0};         // of the runs
+    for (size_t i = 0, k; i < v.size(); i = k) {
+        k = i + 1;
+        if (k < v.size() && before(v[k], v[i])) {
+            while (k < v.size() && before(v[k], v[k - 1])) ++k;
+            std::reverse(v.begin() + i, v.begin() + k);
+        } else {
+            while (k < v.size() && !before(v[k], v[k - 1])) ++k;
+        }
+        ends.push_back(k);
+        if (ends.size() > v.size() / 8 + 8) return std::sort(v.begin(), v.end(), before);
+    }
+    while (ends.size() > 2) {
+        size_t kept = 1;
+        for (size_t i = 1; i < ends.size(); i += 2) {
+            const size_t last = std::min(i + 1, ends.size() - 1);
+            if (last > i) std::inplace_merge(v.begin() + ends[i - 1], v.begin() + ends[i], v.begin() + ends[last], before);
+            ends[kept++] = ends[last];
+        }
+        ends.resize(kept);
+    }
+}
+
 // Whether an output overlaps another output, the workspace, the norm or another tensor than the one
 // it is the clipped form of (or that one in part).
 bool tensors_clash(const void *const *in, void *const *out, const int64_t *elements, const int *dtypes, int64_t tensors, const Span &norm,
                    const Span &ws) {
     if (tensors_apart(in, out, elements, dtypes, tensors, norm, ws)) return false;
-    struct Range {
-        uintptr_t begin, end;
-        bool written;
-    };
-    // each of the two lists is mostly in order already, and taken as it comes
     std::vector<Range> lists[2];             // read (and written over, where the output is the input), written
     lists[0].reserve(tensors);
     lists[1].reserve(out != nullptr ? tensors + 2 : 2);
-    bool sorted[2] = {true, true};
     auto add = [&](int l, const void *p, uintptr_t n, bool written) {
         const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-        if (n == 0) return;
-        sorted[l] = sorted[l] && (lists[l].empty() || lists[l].back().begin <= a);
-        lists[l].push_back({a, a + n, written});
+        if (n > 0) lists[l].push_back({a, a + n, written});
     };
     for (int64_t i = 0; i < tensors; ++i) {
         const uintptr_t n = static_cast<uintptr_t>(elements[i]) * float_bytes(dtypes[i]);
@@ -204,8 +227,7 @@ bool tensors_clash(const void *const *in, void *const *out, const int64_t *eleme
     }
     add(1, norm.p, norm.bytes, true);
     add(1, ws.p, ws.bytes, true);
-    for (int l = 0; l < 2; ++l)
-        if (!sorted[l]) std::sort(lists[l].begin(), lists[l].end(), [](const Range &x, const Range &y) { return x.begin < y.begin; });
+    for (std::vector<Range> &list : lists) sort_runs(list);
     uintptr_t end = 0, written = 0;      // the furthest end of any range so far, and of a written one
     for (size_t i = 0, k = 0; i < lists[0].size() || k < lists[1].size();) {
         const bool first = k == lists[1].size() || (i < lists[0].size() && lists[0][i].begin < lists[1][k].begin);

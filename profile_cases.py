@@ -14,7 +14,9 @@ keys, hist and segsort take --dist uniform|and3|distinct16 (the key distribution
 Language-model operators: logprobs (--rows R --width V --top A), logprobs_grad, route and
 route_grad (--rows T --experts E --k K [--score S] [--renormalise] [--bias]), group (--rows T --k K
 --experts E --align A), dispatch, combine and combine_grad (--rows T --k K --experts E --width W
---align A); --dtype f32|bf16|f16.
+--align A); embed and embed_grad (--rows tokens --vocab V --width W, tokens as in a text), adjust and
+adjust_grad (--rows R --width vocabulary --history H --biases B, a mask of three quarters), norm and
+clip (--rows tensors --width elements of each); --dtype f32|bf16|f16.
 --time prints the median CUDA-event time of the timed calls (of a language-model operator's: the mean, back to back).
 Each call is followed by a device-status check; the process exits non-zero on
 any error, so a profiler only ever runs a command that finished cleanly.
@@ -33,9 +35,10 @@ sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 from bitonic_networks_gb300 import _lib, gsort, synth
 
 
-MODEL_OPS = ["logprobs", "logprobs_grad", "route", "route_grad", "group", "dispatch", "combine", "combine_grad"]
+MODEL_OPS = ["logprobs", "logprobs_grad", "route", "route_grad", "group", "dispatch", "combine", "combine_grad", "embed",
+             "embed_grad", "adjust", "adjust_grad", "norm", "clip"]
 
-MODEL_ARGS = ["rows", "width", "top", "experts", "k", "align", "dtype", "score", "renormalise", "bias"]
+MODEL_ARGS = ["rows", "width", "top", "experts", "k", "align", "dtype", "score", "renormalise", "bias", "vocab", "history", "biases"]
 
 
 def model_call(a):
@@ -46,6 +49,35 @@ def model_call(a):
     def normal(*shape, dtype={"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[a.dtype], by=1.0):
         return torch.empty(*shape, dtype=dtype, device="cuda").normal_(0.0, by, generator=gen)
 
+    def text(vocab, *shape):
+        """Tokens, the r-th most frequent one with a probability of about 1 / r."""
+        u = torch.rand(*shape, generator=gen, device="cuda", dtype=torch.float64)
+        return torch.randperm(vocab, generator=gen, device="cuda")[((vocab + 1.0) ** u).long().clamp(1, vocab) - 1]
+
+    if a.op.startswith("embed"):
+        tokens = text(a.vocab, a.rows)
+        if a.op == "embed":
+            table = normal(a.vocab, a.width)
+            return lambda: gs.embed_tokens(table, tokens)
+        d = normal(a.rows, a.width)
+        return lambda: gs.embed_tokens_backward(d, tokens, a.vocab)
+    if a.op.startswith("adjust"):
+        x, one = normal(a.rows, a.width, by=2.5), torch.ones(a.rows, device="cuda")
+        history = text(a.width, a.rows, a.history).int() if a.history else None
+        bits = torch.randint(-2 ** 31, 2 ** 31, (2, a.rows, (a.width + 31) // 32), generator=gen, device="cuda").int()
+        how = dict(history=history, repetition=1.1 * one if a.history else None, allowed=bits[0] | bits[1])
+        if a.op == "adjust_grad":
+            d = normal(a.rows, a.width)
+            return lambda: gs.adjust_logits_backward(d, x, **how)
+        if a.biases:
+            how.update(bias_tokens=text(a.width, a.rows, a.biases), bias=normal(a.rows, a.biases, dtype=torch.float32))
+        if a.history:
+            how.update(frequency=0.1 * one, presence=0.2 * one)
+        return lambda: gs.adjust_logits(x, **how)
+    if a.op in ("norm", "clip"):
+        tensors = [normal(a.width) for _ in range(a.rows)]
+        outs = [torch.empty_like(t) for t in tensors]
+        return lambda: gs.gradient_norm(tensors) if a.op == "norm" else gs.clip_gradients(tensors, 1.0, out=outs)
     if a.op.startswith("logprobs"):
         x, d = normal(a.rows, a.width, by=2.5), normal(a.rows, dtype=torch.float32)
         targets = torch.randint(a.width, (a.rows,), generator=gen, device="cuda")
@@ -73,7 +105,8 @@ def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("op", choices=["keys", "pairs", "fpairs", "compact", "segments", "hist", "sort",
                                    "segsort", "partition", "splitsort"] + MODEL_OPS)
-    for name, value in (("rows", 8192), ("width", 12000), ("top", 0), ("experts", 64), ("k", 6), ("align", 1)):
+    for name, value in (("rows", 8192), ("width", 12000), ("top", 0), ("experts", 64), ("k", 6), ("align", 1), ("vocab", 131072),
+                        ("history", 1024), ("biases", 0)):
         ap.add_argument("--" + name, type=int, default=value)
     ap.add_argument("--dtype", choices=["f32", "bf16", "f16"], default="bf16")
     ap.add_argument("--score", choices=["softmax", "sigmoid"], default="softmax")

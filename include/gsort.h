@@ -1,7 +1,8 @@
 /*
  * gsort.h -- C ABI of libgsort.so: GB300 (sm_103a) stable LSD radix sort,
  * stream compaction, segmented bitonic sort, and the selection and grouping
- * operators of language models (expert routing, token log probabilities).
+ * operators of language models (expert routing, token log probabilities,
+ * embedding, adjusted logits, gradient norm).
  *
  * Sources of the operations (reference pages, by title and section):
  *   [PMPP10]  "Parallel Patterns: Sorting on the GPU" (textbook chapter 10):

@@ -650,25 +650,28 @@ PyObject *adjust_logits_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // ------------------------------------------------------------ gradient norm
 // The tensors of a list: dense, on one device.
 struct TensorList {
-    PyObject *fast = nullptr;       // keeps the items
+    PyObject *items = nullptr;      // a tuple of the call's own: another thread may change the list meanwhile
     std::vector<const void *> data;
     std::vector<int64_t> sizes;
     std::vector<int> codes;
     std::optional<at::Device> device;
 
-    ~TensorList() { Py_XDECREF(fast); }
+    ~TensorList() { Py_XDECREF(items); }
     int64_t count() const { return static_cast<int64_t>(sizes.size()); }
-    const Tensor &at(int64_t i) const { return THPVariable_Unpack(PySequence_Fast_GET_ITEM(fast, i)); }
+    const Tensor &at(int64_t i) const { return THPVariable_Unpack(PyTuple_GET_ITEM(items, i)); }
 
     void read(PyObject *o, const char *name, const char *what) {
-        fast = PySequence_Fast(o, what);
+        PyObject *fast = PySequence_Fast(o, what);
         if (fast == nullptr) throw Refused{};
-        const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
+        items = PySequence_Tuple(fast);
+        Py_DECREF(fast);
+        if (items == nullptr) throw Refused{};
+        const Py_ssize_t n = PyTuple_GET_SIZE(items);
         data.reserve(n);
         sizes.reserve(n);
         codes.reserve(n);
         for (Py_ssize_t i = 0; i < n; ++i) {
-            const Tensor &t = tensor(PySequence_Fast_GET_ITEM(fast, i), name);
+            const Tensor &t = tensor(PyTuple_GET_ITEM(items, i), name);
             codes.push_back(float_code(t, name));
             if (t.layout() != at::kStrided || !t.is_cuda() || (device.has_value() && t.device() != *device))
                 refuse(PyExc_ValueError, "%s must be strided CUDA tensors of one device, got %s", name, text(t).c_str());
@@ -753,11 +756,11 @@ PyObject *clip_gradients(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         if (rc != GSORT_OK) return PyLong_FromLong(rc);
         PyObject *list;
-        if (o.fast != nullptr) {
+        if (o.items != nullptr) {
             // autograd refuses what it had saved of them
             for (int64_t i = 0; i < g.count(); ++i)
                 if (!o.at(i).is_inference()) o.at(i).unsafeGetTensorImpl()->bump_version();
-            list = PySequence_List(o.fast);
+            list = PySequence_List(o.items);
         } else {
             list = PyList_New(static_cast<Py_ssize_t>(g.count()));
             for (int64_t i = 0; list != nullptr && i < g.count(); ++i) {

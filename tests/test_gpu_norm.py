@@ -1,6 +1,7 @@
 """gradient_norm and clip_gradients against 64-bit sums: many tensors of odd sizes and
 mixed types, numbers whose squares leave the 32-bit range, in place, refusals."""
 import math
+import threading
 
 import pytest
 import torch
@@ -150,6 +151,32 @@ def test_any_sequence_of_tensors():
     with torch.inference_mode():
         z = x.clone()
         assert gs.clip_gradients([z], 1.0, out=[z]).gradients[0] is z
+
+
+def test_lists_that_another_thread_changes():
+    kept = [torch.randn(64, device="cuda") for _ in range(200)]
+    want = gs.clip_gradients(kept, 1.0)
+    gradients, out, stop = list(kept), [torch.empty_like(t) for t in kept], threading.Event()
+    whole_out = list(out)
+
+    def change():
+        while not stop.is_set():
+            for items, whole in ((gradients, kept), (out, whole_out)):
+                items.clear()
+                items.extend(whole)
+
+    thread = threading.Thread(target=change)
+    thread.start()
+    try:
+        for k in range(300):
+            try:
+                got = gs.clip_gradients(gradients, 1.0, out=out if k % 2 else None)
+            except ValueError:          # the call came upon an empty list
+                continue
+            assert len(got.gradients) == 200 and torch.equal(got.norm, want.norm) and torch.equal(got.gradients[-1], want.gradients[-1])
+    finally:
+        stop.set()
+        thread.join()
 
 
 def test_the_same_tensor_twice():

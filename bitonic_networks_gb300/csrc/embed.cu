@@ -402,7 +402,7 @@ template <typename T, int MODE>
 __global__ void __launch_bounds__(kEmbedThreads, 4) k_embed_sum(const EmbedSumArgs<T> a) {
     constexpr int N = Wide<T>::kCount, U = kLoads<MODE>;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // rows are filled meanwhile
-    if (a.status != nullptr && *a.status != 0) {       // the sort gave up, its results are void: all rows are NaN
+    if (a.status != nullptr && *a.status != 0) {       // the sort gave up, its results are void: rows are NaN (absent ones may be zeros)
         for (uint32_t r = blockIdx.x; r < a.vocab; r += gridDim.x)
             fill_span<kEmbedThreads>(reinterpret_cast<char *>(a.out + static_cast<int64_t>(r) * a.out_stride),
                                      static_cast<int64_t>(a.width) * sizeof(T), 0x7FFF7FFFu);

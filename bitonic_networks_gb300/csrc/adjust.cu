@@ -22,7 +22,7 @@
 // The memory bounds large calls: logits in, logits out.  2048 x 131072 bf16 with histories of 1024,
 // 64 biases and a mask take 183 us (6.1 TB/s of what is counted so), their gradient 184; 64 x
 // 131072 f32 with histories of 2048 16.4 us, of which 15 are what a copy with this grid takes.  Long
-// histories take longer than the logits: 256 x 100003 bf16 with 16384 tokens 61 us, the memory's
+// histories take longer than the logits: 256 x 100003 bf16 with 16384 tokens 55 us, the memory's
 // part 18, the rest looks over the history one after another.
 #include <algorithm>
 
@@ -415,9 +415,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a
             if (BACK) {
                 x *= to_f32(logits[e]) > 0.0f ? 1.0f / repetition : repetition;
             } else {
-                const uint32_t times = q.y & ~kSeenBefore, b = biased.entries ? biased.find(q.x) : 0;
+                const uint32_t count = q.y == kNowhere ? seen.counted(q.x) : q.y, times = count & ~kSeenBefore;
+                const uint32_t b = biased.entries ? biased.find(q.x) : 0;
                 const float by = b != 0 ? a.bias[bias_row + b - 1] : 0.0f;
-                if (q.y != 0) x = x > 0.0f ? x / repetition : x * repetition;
+                if (count != 0) x = x > 0.0f ? x / repetition : x * repetition;
                 if (times != 0) x -= fmaf(frequency, static_cast<float>(times), presence);
                 if (b != 0) x += by;
             }
@@ -426,13 +427,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a
         queued = 0;
         __syncwarp();
     };
+    auto ask = [&](uint32_t token) {
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(in + r.first + static_cast<int32_t>(token)));
+        if (BACK) asm volatile("prefetch.global.L1 [%0];" ::"l"(logits + r.first + static_cast<int32_t>(token)));
+    };
     auto push = [&](uint32_t token, uint32_t count) {          // kNowhere: none
         const bool real = token != kNowhere && (allowed == nullptr || bits_at(allowed, token, 1));
         const uint32_t active = __ballot_sync(kFullMask, real);
         if (real) {
             queue[queued + __popc(active & lanemask_lt())] = make_uint2(token, count);
-            asm volatile("prefetch.global.L1 [%0];" ::"l"(in + r.first + static_cast<int32_t>(token)));
-            if (BACK) asm volatile("prefetch.global.L1 [%0];" ::"l"(logits + r.first + static_cast<int32_t>(token)));
+            ask(token);
         }
         queued += __popc(active);
         if (queued + 32 > room) serve();
@@ -450,13 +454,21 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a
             }
             push(token, count);
         }
-    } else if (seen.bits) {                    // of a long one, a thread takes a word's members
-        for (uint32_t w = tid; w - tid < words; w += threads) {
-            uint32_t bits = w < words ? seen.bits[w] : 0;
+    } else if (seen.bits) {
+        // of a long one, a thread queues a word's members, whose counts are looked up when the queue is
+        // served (a push for each bit of the 32 words, few lanes at a time: 61 us where this takes 55)
+        for (uint32_t w = tid; w - lane < words; w += threads) {
+            uint32_t bits = w < words ? seen.bits[w] & (allowed ? allowed[w] : ~0u) : 0;
             while (__any_sync(kFullMask, bits != 0)) {
-                const uint32_t token = bits != 0 ? w * 32 + __ffs(bits) - 1 : kNowhere;
-                bits &= bits - 1;
-                push(token, !BACK && token != kNowhere ? seen.counted(token) : 0);
+                const uint32_t upto = warp_inclusive_scan(__popc(bits), lane), from = queued;
+                const bool fits = from + upto <= room;         // of the first lane that has any, at least
+                if (fits)
+                    for (uint32_t at = from + upto - __popc(bits); bits != 0; bits &= bits - 1)
+                        queue[at++] = make_uint2(w * 32 + __ffs(bits) - 1, kNowhere);
+                queued = __reduce_max_sync(kFullMask, fits ? from + upto : from);
+                __syncwarp();
+                for (uint32_t i = from + lane; i < queued; i += 32) ask(queue[i].x);
+                if (queued + 32 > room) serve();
             }
         }
     }

@@ -88,6 +88,20 @@ def test_dense_histories():
     check(x, how, allowed)
 
 
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_dense_histories_in_place(dtype, masked):
+    """Full words in one part of the row, single members in another, with the least room for them."""
+    x, how, allowed = inputs(2, 40000, 20000, 5, masked, dtype)
+    how["history"] = torch.cat([torch.arange(9000), torch.arange(9000, 40000, 37).repeat(13), torch.arange(100)]).repeat(2, 1).int()
+    y, error, factor = adjust64(x, **how, allowed=allowed)
+    xs = x.cuda()
+    near(call(xs, how, allowed, out=xs), y, error)
+    d = torch.randn(x.shape, generator=torch.Generator().manual_seed(9)).to(x.dtype)
+    ds, want = d.cuda(), d.double() * factor
+    near(back(ds, x.cuda(), how, allowed, out=ds), want, want.abs() * (UNIT[dtype] + 3 * U32) + 1e-37)
+
+
 def test_more_rows_and_vocabulary_than_one_look_takes():
     """Rows of several pieces, each of the largest size: the same row again and again is the row alone."""
     x, how, allowed = inputs(1, 600_000, 3000, 40, True, torch.bfloat16)

@@ -22,8 +22,8 @@
 // The memory bounds large calls: logits in, logits out.  2048 x 131072 bf16 with histories of 1024,
 // 64 biases and a mask take 183 us (6.1 TB/s of what is counted so), their gradient 184; 64 x
 // 131072 f32 with histories of 2048 16.4 us, of which 15 are what a copy with this grid takes.  Long
-// histories take longer than the logits: 256 x 100003 bf16 with 16384 tokens 55 us, the memory's
-// part 18, the rest looks over the history one after another.
+// histories take longer than the logits: 256 x 100003 bf16 with 16384 tokens 53 us, the memory's
+// part 18: an SM has two rows one after the other, and writes the named tokens of one before the next begins.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a
         }
     } else if (seen.bits) {
         // of a long one, a thread queues a word's members, whose counts are looked up when the queue is
-        // served (a push for each bit of the 32 words, few lanes at a time: 61 us where this takes 55)
+        // served (a push for each bit of the 32 words, few lanes at a time: 61 us where this takes 53)
         for (uint32_t w = tid; w - lane < words; w += threads) {
             uint32_t bits = w < words ? seen.bits[w] & (allowed ? allowed[w] : ~0u) : 0;
             while (__any_sync(kFullMask, bits != 0)) {

@@ -78,6 +78,12 @@ def _wants_grad(t) -> bool:
     return getattr(t, "requires_grad", False) and torch.is_grad_enabled()
 
 
+def _refuse_recorded(out, name: str):
+    """An output in a graph would keep the node that it has, whose gradient knows nothing of what is written."""
+    if _wants_grad(out):
+        raise RuntimeError(f"{name} with out takes part in no gradient: call it under torch.no_grad(), or with an out that requires none")
+
+
 def _written(out):
     """A tensor that a call has written: autograd refuses what it had saved of it."""
     if not out.is_inference():
@@ -293,7 +299,9 @@ def embed_tokens_backward(d_out: torch.Tensor, tokens: torch.Tensor, vocab: int,
     [*tokens.shape, width] (contiguous; with tokens of one dimension its rows may
     be strided): each token's rows summed in 32 bits in their order, times scale.
     Rows of tokens that do not occur are zero.  With accumulate the sums are added
-    to `out` [vocab, width], whose other rows stay as they are."""
+    to `out` [vocab, width], whose other rows stay as they are.  An `out` that
+    requires a gradient raises RuntimeError where gradients are recorded."""
+    _refuse_recorded(out, "embed_tokens_backward")
     grad = _checked(_ops.embed_tokens_backward(d_out, tokens, vocab, scale, out, accumulate, workspace),
                     "gsort_embed_tokens_backward")
     if out is not None:
@@ -338,11 +346,13 @@ def adjust_logits(logits: torch.Tensor, *, history: torch.Tensor | None = None, 
 
     history, biases and allowed may be expanded from one row.  `out` may be the
     logits themselves, which are then written only where they change; it takes
-    part in no gradient.  The result has a gradient by the logits; the adjustments
+    part in no gradient (RuntimeError where gradients are recorded and the logits or
+    `out` require one).  The result has a gradient by the logits; the adjustments
     have none.  Without `out`, result rows lie up to 15 bytes apart where the
     logits' rows do not follow each other."""
     if any(_wants_grad(t) for t in (repetition, presence, frequency, bias)):
         raise RuntimeError("penalties and biases have no gradient: detach them")
+    _refuse_recorded(out, "adjust_logits")
     if _wants_grad(logits):
         if out is not None:
             raise RuntimeError("adjust_logits with out takes part in no gradient: call it under torch.no_grad()")
@@ -358,8 +368,10 @@ def adjust_logits_backward(d_out: torch.Tensor, logits: torch.Tensor | None, *, 
                            repetition: torch.Tensor | None = None, allowed: torch.Tensor | None = None,
                            out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of adjust_logits by its logits, from that by its result.  `out`
-    may be d_out itself.  The logits are needed with a repetition only, for
+    may be d_out itself; one that requires a gradient raises RuntimeError where
+    gradients are recorded.  The logits are needed with a repetition only, for
     their signs."""
+    _refuse_recorded(out, "adjust_logits_backward")
     grad = _checked(_ops.adjust_logits_backward(d_out, logits, history, repetition, allowed, out),
                     "gsort_adjust_logits_backward")
     if out is not None:

@@ -312,3 +312,21 @@ def test_refusals():
         gs.adjust_logits_backward(x, None, history=how["history"], repetition=how["repetition"])
     with pytest.raises(gs.GsortError):
         gs.adjust_logits_backward(x.clone(), x, history=how["history"], repetition=how["repetition"], out=x)
+
+
+def test_an_output_in_a_graph_is_refused():
+    """It would keep its node, whose gradient knows nothing of the adjustments; under no_grad() it is the caller's to say so."""
+    x, how, allowed = inputs(4, 700, 60, 5, True)
+    leaf = x.cuda().requires_grad_()
+    y = leaf * 1.0
+    before = y.detach().clone()
+    for out in (y, leaf):
+        with pytest.raises(RuntimeError, match="no gradient"):
+            call(out.detach(), how, allowed, out=out)
+        with pytest.raises(RuntimeError, match="no gradient"):
+            back(torch.ones_like(before), x.cuda(), how, allowed, out=out)
+        with pytest.raises(RuntimeError, match="no gradient"):
+            gs.embed_tokens_backward(torch.ones(9, 700, device="cuda"), torch.zeros(9, dtype=torch.int64, device="cuda"), 4, out=out)
+    assert torch.equal(y, before) and torch.equal(leaf, before)
+    with torch.no_grad():
+        assert call(y, how, allowed, out=y) is y and torch.equal(y, call(before, how, allowed))

@@ -137,3 +137,20 @@ def test_torch_wrappers_refuse_before_the_device():
         gs.gradient_norm([])
     with pytest.raises(RuntimeError):
         gs.adjust_logits(x, history=t.view(4, 1).int(), repetition=torch.ones(4, requires_grad=True))
+
+
+def test_outputs_that_require_a_gradient_are_refused():
+    """Nothing of these calls is recorded: an output that is in a graph would go on with its old gradient."""
+    import torch
+
+    import bitonic_networks_gb300 as gs
+    x, t = torch.zeros(4, 64), torch.zeros(4, dtype=torch.int64)
+    leaf = torch.zeros(4, 64, requires_grad=True)
+    for out in (leaf, leaf * 1.0, (leaf * 1.0)[:]):
+        for call in (lambda: gs.adjust_logits(x, out=out), lambda: gs.adjust_logits(out.detach(), out=out),
+                     lambda: gs.adjust_logits_backward(x, None, out=out), lambda: gs.embed_tokens_backward(x, t, 4, out=out),
+                     lambda: gs.embed_tokens_backward(x, t, 4, out=out, accumulate=True)):
+            with pytest.raises(RuntimeError, match="no gradient"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+                call()

@@ -37,6 +37,7 @@ constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier
 constexpr uint64_t kSizeMask = (1ull << 56) - 1;
 // below it a thread's sum of squares may have lost what is under the 32-bit range
 constexpr float kTinySum = 1.2621774483536189e-29f;         // 2^-96
+constexpr double kLeastNormal = 1.1754943508222875e-38;     // 2^-126
 constexpr size_t kNormSmem = kStages * kStep * 16;
 
 template <int M> struct TensorTable {
@@ -250,14 +251,32 @@ __global__ void __launch_bounds__(kNormThreads) k_norm(const double *slots, uint
     if (threadIdx.x == 0) *out = static_cast<float>(norm);
 }
 
-template <typename T> __device__ __forceinline__ void scale_step(const Step &s, const uint4 *data, void *tensor, float by) {
+// What every element is multiplied by.  Where a norm is so far beyond its limit that the factor is no
+// normal 32-bit number, rounding would take its bits, or all of it: products are 64-bit there.
+struct Factor {
+    double exact;
+    float by;
+    bool below;
+
+    __device__ __forceinline__ explicit Factor(double c) : exact(c), by(static_cast<float>(c)), below(c != 0.0 && fabs(c) < kLeastNormal) {}
+    template <typename T> __device__ __forceinline__ T far(T x) const { return from_f32<T>(static_cast<float>(to_f32(x) * exact)); }
+    template <typename T> __device__ __forceinline__ T near(T x) const { return from_f32<T>(to_f32(x) * by); }
+};
+
+template <typename T> __device__ __forceinline__ void scale_step(const Step &s, const uint4 *data, void *tensor, const Factor &c) {
     constexpr int N = Wide<T>::kCount;
     char *to = static_cast<char *>(tensor) + s.begin;
-    if ((reinterpret_cast<uintptr_t>(to) & 15) != 0) {         // the output lies differently
-        const T *from = reinterpret_cast<const T *>(data);
-        for (uint32_t i = threadIdx.x; i < s.vectors * N; i += kNormThreads) reinterpret_cast<T *>(to)[i] = from_f32<T>(to_f32(from[i]) * by);
+    const T *from = reinterpret_cast<const T *>(data);
+    T *single = reinterpret_cast<T *>(to);
+    if (c.below) {
+        for (uint32_t i = threadIdx.x; i < s.vectors * N; i += kNormThreads) single[i] = c.far(from[i]);
         return;
     }
+    if ((reinterpret_cast<uintptr_t>(to) & 15) != 0) {         // the output lies differently
+        for (uint32_t i = threadIdx.x; i < s.vectors * N; i += kNormThreads) single[i] = c.near(from[i]);
+        return;
+    }
+    const float by = c.by;
 #pragma unroll
     for (int u = 0; u < kNormVectors; ++u) {
         const uint32_t v = threadIdx.x + u * kNormThreads;
@@ -280,18 +299,20 @@ k_clip(const __grid_constant__ TensorTable<M> t, const double *slots, uint32_t c
     if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
     // NaN stays: a gradient that is no number must not look like one
     const double part = norm > max_norm ? max_norm / norm : norm == norm ? 1.0 : norm;
-    const float by = static_cast<float>(scale * part);
-    auto changes = [&](uint32_t tensor) { return by != 1.0f || t.in[tensor] != t.out[tensor]; };     // else it is as it has to be
+    const Factor c(scale * part);
+    auto changes = [&](uint32_t tensor) { return c.by != 1.0f || t.in[tensor] != t.out[tensor]; };     // else it is as it has to be
     for_ends(t, [&](uint32_t tensor, uint32_t type, uint64_t first, uint32_t n) {
         with_type(type, [&](auto *p) {
             using T = std::remove_pointer_t<decltype(p)>;
-            for (uint32_t k = 0; changes(tensor) && k < n; ++k)
-                static_cast<T *>(t.out[tensor])[first + k] = from_f32<T>(to_f32(static_cast<const T *>(t.in[tensor])[first + k]) * by);
+            for (uint32_t k = 0; changes(tensor) && k < n; ++k) {
+                const T x = static_cast<const T *>(t.in[tensor])[first + k];
+                static_cast<T *>(t.out[tensor])[first + k] = c.below ? c.far(x) : c.near(x);
+            }
         });
     });
     const bool whole = ring.run([&](const Step &s, const uint4 *data) {
         if (changes(s.tensor))
-            with_type(s.type, [&](auto *p) { scale_step<std::remove_pointer_t<decltype(p)>>(s, data, t.out[s.tensor], by); });
+            with_type(s.type, [&](auto *p) { scale_step<std::remove_pointer_t<decltype(p)>>(s, data, t.out[s.tensor], c); });
     });
     if (!whole && norm_out != nullptr && threadIdx.x == 0) *norm_out = __uint_as_float(0x7FC00000u);
 }

@@ -392,6 +392,7 @@ def clip_gradients(gradients, max_norm: float, *, scale: float = 1.0, out=None) 
     """The gradients times scale, and times max_norm / norm where the norm of all
     of them (times scale) is above max_norm; with that norm.  `out` is a list of
     tensors like the gradients, or the gradients themselves (which are then not
-    written where nothing changes).  Nothing waits for the device: a norm that is
-    NaN makes every gradient NaN, an infinite one the finite gradients 0."""
+    written where nothing changes).  Nothing waits for the device: a NaN among them
+    makes every gradient NaN, an infinity the finite gradients 0.  A norm beyond
+    float32 is returned as infinity, and the gradients are clipped by what it is."""
     return ClippedGradients(*_checked(_ops.clip_gradients(gradients, max_norm, scale, out), "gsort_clip_gradients"))

@@ -524,9 +524,10 @@ int gsort_adjust_logits_backward(const void *d_grad_out, int dtype, int64_t rows
  *   norm           d_norm = sqrt(sum of the squares of all elements)
  *   clip           d_norm = |scale| * that, and every element times
  *                  scale * min(1, max_norm / norm), rounded once
- * Squares that leave the 32-bit range are summed in 64 bits.  A NaN makes the norm
- * and every output NaN; with an infinite one, and max_norm finite, finite elements
- * become 0 and infinite ones NaN.  max_norm >= 0 (infinity: scaling alone).  An output may be
+ * Squares that leave the 32-bit range are summed in 64 bits, and max_norm / norm is
+ * held in 64: a norm beyond the 32-bit range is infinite in d_norm, and elements are
+ * clipped by what it is.  A NaN makes the norm and every output NaN; with an infinite
+ * element, and max_norm finite, finite elements become 0 and infinite ones NaN.  max_norm >= 0 (infinity: scaling alone).  An output may be
  * its own input; other overlaps between outputs and inputs are refused. */
 size_t gsort_gradient_norm_workspace_bytes(int64_t tensors);
 

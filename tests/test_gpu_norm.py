@@ -221,3 +221,22 @@ def test_refusals():
         gs.clip_gradients([z], 1.0)
     with torch.no_grad():
         gs.clip_gradients([z], 1.0, out=[z])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("max_norm", [1.0, 1e-3, 1e-5])
+@pytest.mark.parametrize("n", [70001, 3])
+def test_norms_far_beyond_the_limit(dtype, max_norm, n):
+    """The factor is below the smallest normal 32-bit number: it must not lose bits, or become 0."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    sign = torch.where(torch.arange(n, device="cuda") % 2 == 0, 1.0, -1.0)
+    t = ((torch.rand(n, generator=g, device="cuda") * 0.25 + 0.75) * 3.3e38 * sign).to(dtype)
+    by = f32(max_norm) / norm64([t])
+    assert by < 2.0 ** -126
+    # squares beyond the 32-bit range are summed in 64 bits, so the factor is; the product rounds to 32 bits, then to the type
+    want = t.double() * by
+    error = want.abs() * (UNIT[dtype] + 2 * U32)
+    for out in (None, [torch.empty_like(t)], [torch.empty(n + 1, dtype=dtype, device="cuda")[1:]], [t]):
+        r = gs.clip_gradients([t], max_norm, out=out)
+        assert float(r.norm) == INF         # beyond 32 bits
+        assert bool(((r.gradients[0].double() - want).abs() <= error).all())

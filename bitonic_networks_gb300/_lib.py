@@ -168,6 +168,9 @@ SIGNATURES = {
     "gsort_gradient_norm": (ctypes.c_int, [
         ctypes.POINTER(ctypes.c_void_p), c_i64p, ctypes.POINTER(ctypes.c_int), ctypes.c_int64, ctypes.c_void_p,
         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "gsort_gradient_norm_ex": (ctypes.c_int, [
+        ctypes.POINTER(ctypes.c_void_p), c_i64p, ctypes.POINTER(ctypes.c_int), ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.POINTER(Options)]),
     "gsort_clip_gradients": (ctypes.c_int, [
         ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), c_i64p, ctypes.POINTER(ctypes.c_int),
         ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,

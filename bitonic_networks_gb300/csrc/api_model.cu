@@ -239,8 +239,20 @@ bool tensors_clash(const void *const *in, void *const *out, const int64_t *eleme
     return false;
 }
 
+// The options of an extended call that waits for bulk copies.
+int waits_of(const gsort_options *o, Waits *w) {
+    if (o == nullptr) return GSORT_OK;
+    if (o->variant != 0 || o->num_events < 0 || (o->num_events > 0 && o->events == nullptr)) return GSORT_EINVAL;
+    if (o->spin_limit != 0) w->polls = o->spin_limit;
+    if (o->stall_tile >= 0 && o->stall_tile < 0xFFFFFFFFll) w->stall = static_cast<uint32_t>(o->stall_tile);
+    return GSORT_OK;
+}
+
 int norm(const void *const *in, void *const *out, const int64_t *elements, const int *dtypes, int64_t tensors, float max_norm,
-         float scale, float *d_norm, void *ws, size_t ws_bytes, cudaStream_t stream) {
+         float scale, float *d_norm, void *ws, size_t ws_bytes, cudaStream_t stream, const gsort_options *options) {
+    NormLaunch L;
+    const int rc = waits_of(options, &L.waits);
+    if (rc != GSORT_OK) return rc;
     if (tensors < 0 || !std::isfinite(scale) || !(max_norm >= 0.0f)) return GSORT_EINVAL;
     if (tensors > GSORT_MAX_N) return GSORT_ETOOBIG;
     if (d_norm == nullptr || (tensors > 0 && (in == nullptr || elements == nullptr || dtypes == nullptr))) return GSORT_EINVAL;
@@ -262,7 +274,6 @@ int norm(const void *const *in, void *const *out, const int64_t *elements, const
     } catch (const std::bad_alloc &) {
         return GSORT_ETOOBIG;
     }
-    NormLaunch L;
     L.in = in;
     L.out = out;
     L.sizes = elements;
@@ -677,14 +688,20 @@ size_t gsort_gradient_norm_workspace_bytes(int64_t tensors) {
 int gsort_gradient_norm(const void *const *d_gradients, const int64_t *elements, const int *dtypes,
                         int64_t tensors, float *d_norm, void *d_ws, size_t ws_bytes,
                         cudaStream_t stream) {
-    return norm(d_gradients, nullptr, elements, dtypes, tensors, INFINITY, 1.0f, d_norm, d_ws, ws_bytes, stream);
+    return norm(d_gradients, nullptr, elements, dtypes, tensors, INFINITY, 1.0f, d_norm, d_ws, ws_bytes, stream, nullptr);
+}
+
+int gsort_gradient_norm_ex(const void *const *d_gradients, const int64_t *elements, const int *dtypes,
+                           int64_t tensors, float *d_norm, void *d_ws, size_t ws_bytes,
+                           cudaStream_t stream, const gsort_options *options) {
+    return norm(d_gradients, nullptr, elements, dtypes, tensors, INFINITY, 1.0f, d_norm, d_ws, ws_bytes, stream, options);
 }
 
 int gsort_clip_gradients(const void *const *d_gradients, void *const *d_out, const int64_t *elements,
                          const int *dtypes, int64_t tensors, float max_norm, float scale,
                          float *d_norm, void *d_ws, size_t ws_bytes, cudaStream_t stream) {
     if (tensors > 0 && d_out == nullptr) return GSORT_EINVAL;
-    return norm(d_gradients, d_out, elements, dtypes, tensors, max_norm, scale, d_norm, d_ws, ws_bytes, stream);
+    return norm(d_gradients, d_out, elements, dtypes, tensors, max_norm, scale, d_norm, d_ws, ws_bytes, stream, nullptr);
 }
 
 }  // extern "C"

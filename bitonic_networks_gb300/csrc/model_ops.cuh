@@ -164,6 +164,13 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// The waits of a call's kernels for their bulk copies: polls of one, and (testing) the CTA whose
+// waits run out at once.
+struct Waits {
+    uint32_t polls = kDefaultSpinLimit, stall = kNoStall;
+    __device__ __forceinline__ uint32_t of_cta() const { return blockIdx.x == stall ? 0 : polls; }
+};
+
 // --------------------------------------------------------- launch plans
 struct RouteLaunch {
     const void *logits;
@@ -320,6 +327,7 @@ struct NormLaunch {
     float scale, max_norm;
     float *norm;
     unsigned char *ws;
+    Waits waits;
     cudaStream_t stream;
 };
 size_t norm_workspace_bytes(int64_t tensors);

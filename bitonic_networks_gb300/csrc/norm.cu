@@ -33,7 +33,7 @@ constexpr uint32_t kStep = kNormThreads * kNormVectors;     // vectors of a step
 constexpr int kFewTensors = 32, kSomeTensors = 384, kManyTensors = 1000;
 constexpr int kStages = 3;
 constexpr uint32_t kNormCtas = 608;               // 4 to an SM of a GB300
-constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier
+constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier before the CTA is left
 constexpr uint64_t kSizeMask = (1ull << 56) - 1;
 // below it a thread's sum of squares may have lost what is under the 32-bit range
 constexpr float kTinySum = 1.2621774483536189e-29f;         // 2^-96
@@ -123,12 +123,14 @@ template <int M, bool BACKWARDS> struct Ring {
         mbar_arrive_expect_tx(&full[stage], s.vectors * 16);
         if (s.vectors > 0) bulk_load(data[stage], from, s.vectors * 16, &full[stage]);
     }
-    // Calls f(step, vectors) for every step; false if a copy did not come.
-    template <typename F> __device__ __forceinline__ bool run(F &&f) {
+    // Calls f(step, vectors) for every step; false if a copy did not come.  All threads leave at the
+    // same barrier: the end is read from the step, which was written before the last barrier, and a
+    // wait that ran out for one thread counts for all.
+    template <typename F> __device__ __forceinline__ bool run(uint32_t polls, F &&f) {
         for (uint32_t k = 0;; ++k) {
             const int stage = k % kStages;
-            const bool there = mbar_wait_bounded(&full[stage], (k / kStages) & 1, kWaitLimit);
-            if (there && steps[stage].vectors == 0) return true;
+            if (steps[stage].vectors == 0) return true;
+            const bool there = mbar_wait_bounded(&full[stage], (k / kStages) & 1, polls);
             if (there) f(steps[stage], data[stage]);
             if (__syncthreads_or(!there)) {        // leave once no copy can be under way any more
                 for (uint32_t i = k; i < k + kStages; ++i) mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1, kWaitLimit);
@@ -216,7 +218,7 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <int M>
-__global__ void __launch_bounds__(kNormThreads, 4) k_square_sums(const __grid_constant__ TensorTable<M> t, double *slots) {
+__global__ void __launch_bounds__(kNormThreads, 4) k_square_sums(const __grid_constant__ TensorTable<M> t, double *slots, const Waits waits) {
     let_next_start();
     Ring<M, false> ring = make_ring<M, false>(t);
     ring.start();
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kNormThreads, 4) k_square_sums(const __grid_co
             }
         });
     });
-    const bool whole = ring.run([&](const Step &s, const uint4 *data) {
+    const bool whole = ring.run(waits.of_cta(), [&](const Step &s, const uint4 *data) {
         with_type(s.type, [&](auto *p) { d += square_sum<std::remove_pointer_t<decltype(p)>>(s.vectors, data); });
     });
     if (!whole) d = __longlong_as_double(0x7FF8000000000000ll);      // a norm without all of its parts is none
@@ -310,7 +312,7 @@ k_clip(const __grid_constant__ TensorTable<M> t, const double *slots, uint32_t c
             }
         });
     });
-    const bool whole = ring.run([&](const Step &s, const uint4 *data) {
+    const bool whole = ring.run(kWaitLimit, [&](const Step &s, const uint4 *data) {
         if (changes(s.tensor))
             with_type(s.type, [&](auto *p) { scale_step<std::remove_pointer_t<decltype(p)>>(s, data, t.out[s.tensor], c); });
     });
@@ -373,7 +375,7 @@ template <int M> int launch_tables(const NormLaunch &L) {
         at += taken;
         if (t.tensors == 0) continue;
         const uint32_t ctas = ctas_of(t);
-        if ((rc = launch(k_square_sums<M>, ctas, kNormSmem, used > 0, L.stream, t, slots + used)) != GSORT_OK) return rc;
+        if ((rc = launch(k_square_sums<M>, ctas, kNormSmem, used > 0, L.stream, t, slots + used, L.waits)) != GSORT_OK) return rc;
         used += ctas;
     }
     if (L.out == nullptr || used == 0)

@@ -598,6 +598,13 @@ int gsort_compact_positive_ex(const float *d_in, float *d_out, int64_t n,
                               int64_t *d_num_kept, void *d_ws, size_t ws_bytes,
                               cudaStream_t stream, const gsort_options *options);
 
+/* Calls whose kernels wait for bulk copies of their inputs: spin_limit is the
+ * polls of one such wait (0 = default), and stall_tile (testing) a CTA whose waits run
+ * out at once.  Where a copy does not come the result says so: the norm is NaN. */
+int gsort_gradient_norm_ex(const void *const *d_gradients, const int64_t *elements, const int *dtypes,
+                           int64_t tensors, float *d_norm, void *d_ws, size_t ws_bytes,
+                           cudaStream_t stream, const gsort_options *options);
+
 /* Number of digit-pass launch configurations, and the name of one
  * ("warps x items per thread, ranking method"); NULL if out of range. */
 int gsort_radix_num_variants(void);

@@ -1,0 +1,62 @@
+"""Waits of the operators around the vocabulary and the gradients that run out: a testing option
+makes the waits of one CTA (of the sort: one tile) give up at once.  The kernels end, the result says
+that something is missing, other rows and the next call are right."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import bitonic_networks_gb300 as gs
+from bitonic_networks_gb300 import _lib
+from model_ref import DTYPES
+
+pytestmark = pytest.mark.gpu
+OK = 0
+CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def options(**fields):
+    return ctypes.byref(_lib.Options(fields.get("spin_limit", 0), fields.get("stall_tile", -1), None, 0, 0))
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def lists(tensors):
+    n = len(tensors)
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
+            (ctypes.c_int * n)(*[CODES[t.dtype] for t in tensors]))
+
+
+def norm_space(count):
+    return torch.empty(_lib.load().gsort_gradient_norm_workspace_bytes(count), dtype=torch.uint8, device="cuda")
+
+
+def norm(tensors, **fields):
+    at, sizes, codes = lists(tensors)
+    out, ws = torch.full((), 7.0, device="cuda"), norm_space(len(tensors))
+    assert _lib.load().gsort_gradient_norm_ex(at, sizes, codes, len(tensors), out.data_ptr(), ws.data_ptr(), ws.numel(), stream(),
+                                              options(**fields)) == OK
+    return float(out)
+
+
+# CTAs with several steps each, some with one; more tensors than one launch takes
+GRADIENTS = {"many steps": [30_000_001, 77, 5_000_000], "one step": [5000, 4096, 3], "two launches": [9000] * 1300}
+
+
+@pytest.mark.parametrize("name", GRADIENTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_norm_without_all_of_its_parts_is_nan(name, dtype):
+    tensors = [torch.randn(n, device="cuda").to(dtype) for n in GRADIENTS[name]]
+    want = float(gs.gradient_norm(tensors))
+    for stall in (0, 1):
+        assert math.isnan(norm(tensors, stall_tile=stall, spin_limit=100)), stall
+        assert float(gs.gradient_norm(tensors)) == want
+    assert norm(tensors) == want == norm(tensors, stall_tile=10 ** 6) == norm(tensors, spin_limit=1 << 22)
+
+
+def test_a_norm_without_copies_waits_for_nothing():
+    tensors = [torch.ones(3, device="cuda"), torch.ones(1, dtype=torch.bfloat16, device="cuda")]
+    assert norm(tensors, stall_tile=0) == 2.0

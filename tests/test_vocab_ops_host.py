@@ -154,3 +154,13 @@ def test_outputs_that_require_a_gradient_are_refused():
                 call()
             with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
                 call()
+
+
+def test_options_of_extended_calls(lib):
+    """What the options may hold is checked before anything else; NULL options are the defaults."""
+    from bitonic_networks_gb300 import _lib
+    bad = [_lib.Options(0, -1, None, 0, 1), _lib.Options(0, -1, None, -1, 0), _lib.Options(0, -1, None, 2, 0)]
+    i, s, t = (ctypes.c_void_p * 1)(A), (ctypes.c_int64 * 1)(10), (ctypes.c_int * 1)(0)
+    for o in bad:
+        assert lib.gsort_gradient_norm_ex(i, s, t, 1, C, W, 1 << 20, None, ctypes.byref(o)) == EINVAL
+    assert lib.gsort_gradient_norm_ex(i, s, t, 1, C, W, 8, None, None) == EWS

@@ -175,6 +175,10 @@ SIGNATURES = {
         ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), c_i64p, ctypes.POINTER(ctypes.c_int),
         ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
         ctypes.c_void_p]),
+    "gsort_clip_gradients_ex": (ctypes.c_int, [
+        ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p), c_i64p, ctypes.POINTER(ctypes.c_int),
+        ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+        ctypes.c_void_p, ctypes.POINTER(Options)]),
     "gsort_check": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "gsort_radix_num_variants": (ctypes.c_int, []),
     "gsort_radix_variant_name": (ctypes.c_char_p, [ctypes.c_int]),

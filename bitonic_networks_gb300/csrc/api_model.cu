@@ -704,4 +704,12 @@ int gsort_clip_gradients(const void *const *d_gradients, void *const *d_out, con
     return norm(d_gradients, d_out, elements, dtypes, tensors, max_norm, scale, d_norm, d_ws, ws_bytes, stream, nullptr);
 }
 
+int gsort_clip_gradients_ex(const void *const *d_gradients, void *const *d_out, const int64_t *elements,
+                            const int *dtypes, int64_t tensors, float max_norm, float scale,
+                            float *d_norm, void *d_ws, size_t ws_bytes, cudaStream_t stream,
+                            const gsort_options *options) {
+    if (tensors > 0 && d_out == nullptr) return GSORT_EINVAL;
+    return norm(d_gradients, d_out, elements, dtypes, tensors, max_norm, scale, d_norm, d_ws, ws_bytes, stream, options);
+}
+
 }  // extern "C"

@@ -74,6 +74,8 @@ struct Step {
     int64_t begin;
 };
 
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
 // The steps of a CTA, brought to shared memory in turn.
 template <int M, bool BACKWARDS> struct Ring {
     const TensorTable<M> &t;
@@ -91,11 +93,10 @@ template <int M, bool BACKWARDS> struct Ring {
         }
         __syncthreads();     // the barriers are there
     }
-    // Thread 0: the next step's copy into a stage.
-    __device__ __forceinline__ void copy(int stage) {
+    // Thread 0: the next step.
+    __device__ __forceinline__ Step next() {
         const uint32_t chunks = t.first[t.tensors];
         Step s{};
-        const char *from = nullptr;
         while (s.vectors == 0 && chunk < chunks) {
             const uint32_t c = BACKWARDS ? chunks - 1 - chunk : chunk;
             uint32_t i = 0, high = t.tensors - 1;
@@ -111,32 +112,47 @@ template <int M, bool BACKWARDS> struct Ring {
                 s.type = span.type;
                 s.vectors = static_cast<uint32_t>(min(span.vectors - v, static_cast<uint64_t>(kStep)));
                 s.begin = static_cast<int64_t>(span.head + v * 16);
-                from = static_cast<const char *>(t.in[i]) + s.begin;
             }
             if (++step == t.steps || v + kStep >= span.vectors) {
                 step = 0;
                 chunk += gridDim.x;
             }
         }
+        return s;
+    }
+    // Thread 0: the next step's copy into a stage.
+    __device__ __forceinline__ void copy(int stage) {
+        const Step s = next();
         steps[stage] = s;
         fence_proxy_async_smem();
         mbar_arrive_expect_tx(&full[stage], s.vectors * 16);
-        if (s.vectors > 0) bulk_load(data[stage], from, s.vectors * 16, &full[stage]);
+        if (s.vectors > 0) bulk_load(data[stage], static_cast<const char *>(t.in[s.tensor]) + s.begin, s.vectors * 16, &full[stage]);
     }
-    // Calls f(step, vectors) for every step; false if a copy did not come.  All threads leave at the
+    // Calls f(step, vectors) for every step; the number of the first step whose copy did not come, or kAll.  All threads leave at the
     // same barrier: the end is read from the step, which was written before the last barrier, and a
     // wait that ran out for one thread counts for all.
-    template <typename F> __device__ __forceinline__ bool run(uint32_t polls, F &&f) {
+    template <typename F> __device__ __forceinline__ uint32_t run(uint32_t polls, F &&f) {
         for (uint32_t k = 0;; ++k) {
             const int stage = k % kStages;
-            if (steps[stage].vectors == 0) return true;
+            if (steps[stage].vectors == 0) return kAll;
             const bool there = mbar_wait_bounded(&full[stage], (k / kStages) & 1, polls);
             if (there) f(steps[stage], data[stage]);
             if (__syncthreads_or(!there)) {        // leave once no copy can be under way any more
                 for (uint32_t i = k; i < k + kStages; ++i) mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1, kWaitLimit);
-                return false;
+                return k;
             }
             if (threadIdx.x == 0) copy(stage);
+        }
+    }
+    // After run has given up at step k: calls f(step) for it and all behind it.
+    template <typename F> __device__ __forceinline__ void rest(uint32_t k, F &&f) {
+        for (uint32_t i = k; i < k + kStages; ++i) f(steps[i % kStages]);
+        for (;;) {
+            __syncthreads();
+            if (threadIdx.x == 0) steps[0] = next();
+            __syncthreads();
+            if (steps[0].vectors == 0) return;
+            f(steps[0]);
         }
     }
 };
@@ -218,7 +234,7 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <int M>
-__global__ void __launch_bounds__(kNormThreads, 4) k_square_sums(const __grid_constant__ TensorTable<M> t, double *slots, const Waits waits) {
+__global__ void __launch_bounds__(kNormThreads, 4) k_square_sums(const __grid_constant__ TensorTable<M> t, double *slots, float *zero, const Waits waits) {
     let_next_start();
     Ring<M, false> ring = make_ring<M, false>(t);
     ring.start();
@@ -232,13 +248,14 @@ __global__ void __launch_bounds__(kNormThreads, 4) k_square_sums(const __grid_co
             }
         });
     });
-    const bool whole = ring.run(waits.of_cta(), [&](const Step &s, const uint4 *data) {
+    const uint32_t lost = ring.run(waits.of_cta(), [&](const Step &s, const uint4 *data) {
         with_type(s.type, [&](auto *p) { d += square_sum<std::remove_pointer_t<decltype(p)>>(s.vectors, data); });
     });
-    if (!whole) d = __longlong_as_double(0x7FF8000000000000ll);      // a norm without all of its parts is none
+    if (lost != kAll) d = __longlong_as_double(0x7FF8000000000000ll);      // a norm without all of its parts is none
     d = cta_sum(d);
     wait_for_last();         // so that who waits for this kernel has waited for those before it
     if (threadIdx.x == 0) slots[blockIdx.x] = d;
+    if (zero != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *zero = 0.0f;
 }
 
 __device__ __forceinline__ double norm_of(const double *slots, uint32_t count, float scale) {
@@ -290,15 +307,25 @@ template <typename T> __device__ __forceinline__ void scale_step(const Step &s, 
     }
 }
 
+// A step whose gradients did not come: its results are no numbers.
+__device__ __forceinline__ void void_step(const Step &s, void *tensor) {
+    uint16_t *to = reinterpret_cast<uint16_t *>(static_cast<char *>(tensor) + s.begin);
+    for (uint32_t i = threadIdx.x; i < s.vectors * 8; i += kNormThreads) to[i] = 0x7FFF;
+}
+
+// norm_out holds 0 before.  Its bits are only raised, so that the NaN of a CTA whose copies did not come
+// stays: NaN is above all numbers, and a norm is not below 0.
 template <int M>
 __global__ void __launch_bounds__(kNormThreads, 4)
-k_clip(const __grid_constant__ TensorTable<M> t, const double *slots, uint32_t count, float scale, float max_norm, float *norm_out) {
+k_clip(const __grid_constant__ TensorTable<M> t, const double *slots, uint32_t count, float scale, float max_norm, float *norm_out,
+       const Waits waits) {
     let_next_start();
     Ring<M, true> ring = make_ring<M, true>(t);
     ring.start();            // the gradients were there before the sums
     wait_for_last();
     const double norm = norm_of(slots, count, scale);
-    if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
+    uint32_t *const norm_bits = reinterpret_cast<uint32_t *>(norm_out);
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicMax(norm_bits, __float_as_uint(static_cast<float>(norm)));
     // NaN stays: a gradient that is no number must not look like one
     const double part = norm > max_norm ? max_norm / norm : norm == norm ? 1.0 : norm;
     const Factor c(scale * part);
@@ -312,11 +339,15 @@ k_clip(const __grid_constant__ TensorTable<M> t, const double *slots, uint32_t c
             }
         });
     });
-    const bool whole = ring.run(kWaitLimit, [&](const Step &s, const uint4 *data) {
+    const uint32_t lost = ring.run(waits.of_cta(), [&](const Step &s, const uint4 *data) {
         if (changes(s.tensor))
             with_type(s.type, [&](auto *p) { scale_step<std::remove_pointer_t<decltype(p)>>(s, data, t.out[s.tensor], c); });
     });
-    if (!whole && norm_out != nullptr && threadIdx.x == 0) *norm_out = __uint_as_float(0x7FC00000u);
+    if (lost == kAll) return;
+    if (threadIdx.x == 0) atomicMax(norm_bits, 0x7FC00000u);
+    ring.rest(lost, [&](const Step &s) {
+        if (s.vectors > 0 && changes(s.tensor)) void_step(s, t.out[s.tensor]);
+    });
 }
 
 // The tensors from `at` on, as many as fit, and how many of the list they are.
@@ -375,20 +406,20 @@ template <int M> int launch_tables(const NormLaunch &L) {
         at += taken;
         if (t.tensors == 0) continue;
         const uint32_t ctas = ctas_of(t);
-        if ((rc = launch(k_square_sums<M>, ctas, kNormSmem, used > 0, L.stream, t, slots + used, L.waits)) != GSORT_OK) return rc;
+        rc = launch(k_square_sums<M>, ctas, kNormSmem, used > 0, L.stream, t, slots + used, L.out != nullptr && used == 0 ? L.norm : nullptr,
+                    L.out == nullptr ? L.waits : Waits{});
+        if (rc != GSORT_OK) return rc;
         used += ctas;
     }
     if (L.out == nullptr || used == 0)
         return launch(k_norm, 1, 0, used > 0, L.stream, static_cast<const double *>(slots), used, L.scale, L.norm);
-    float *norm = L.norm;
     const bool one = L.tensors <= M;       // its table is still there
     for (at = 0; at < L.tensors;) {
         at += one ? L.tensors : fill_table(L, at, t);
         if (t.tensors == 0) continue;
         rc = launch(k_clip<M>, ctas_of(t), kNormSmem, true, L.stream, t, static_cast<const double *>(slots), used, L.scale,
-                    L.max_norm, norm);
+                    L.max_norm, L.norm, L.waits);
         if (rc != GSORT_OK) return rc;
-        norm = nullptr;
     }
     return GSORT_OK;
 }

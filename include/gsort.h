@@ -600,10 +600,16 @@ int gsort_compact_positive_ex(const float *d_in, float *d_out, int64_t n,
 
 /* Calls whose kernels wait for bulk copies of their inputs: spin_limit is the
  * polls of one such wait (0 = default), and stall_tile (testing) a CTA whose waits run
- * out at once.  Where a copy does not come the result says so: the norm is NaN. */
+ * out at once.  Where a copy does not come the result says so: the norm is NaN, and
+ * in clipping (whose options are those of its second read) so is what was not read. */
 int gsort_gradient_norm_ex(const void *const *d_gradients, const int64_t *elements, const int *dtypes,
                            int64_t tensors, float *d_norm, void *d_ws, size_t ws_bytes,
                            cudaStream_t stream, const gsort_options *options);
+
+int gsort_clip_gradients_ex(const void *const *d_gradients, void *const *d_out, const int64_t *elements,
+                            const int *dtypes, int64_t tensors, float max_norm, float scale,
+                            float *d_norm, void *d_ws, size_t ws_bytes, cudaStream_t stream,
+                            const gsort_options *options);
 
 /* Number of digit-pass launch configurations, and the name of one
  * ("warps x items per thread, ranking method"); NULL if out of range. */

@@ -60,3 +60,46 @@ def test_a_norm_without_all_of_its_parts_is_nan(name, dtype):
 def test_a_norm_without_copies_waits_for_nothing():
     tensors = [torch.ones(3, device="cuda"), torch.ones(1, dtype=torch.bfloat16, device="cuda")]
     assert norm(tensors, stall_tile=0) == 2.0
+
+
+def clip(tensors, out, max_norm, **fields):
+    at, sizes, codes = lists(tensors)
+    got, ws = torch.full((), 7.0, device="cuda"), norm_space(len(tensors))
+    assert _lib.load().gsort_clip_gradients_ex(at, lists(out)[0], sizes, codes, len(tensors), max_norm, 1.0, got.data_ptr(), ws.data_ptr(),
+                                               ws.numel(), stream(), options(**fields)) == OK
+    return float(got)
+
+
+def bits(t):
+    return t.view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+
+
+@pytest.mark.parametrize("name", GRADIENTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("off", [0, 1])
+def test_gradients_that_did_not_come_are_nan(name, dtype, off):
+    """Every result is what it should be or NaN, none is left as it was, and the norm tells of it."""
+    tensors = [torch.randn(n, device="cuda").to(dtype) for n in GRADIENTS[name]]
+    limit = 0.5 * float(gs.gradient_norm(tensors))
+    want = gs.clip_gradients(tensors, limit)
+    for stall in (0, 1):
+        for in_place in (False, True):
+            out = [t.clone() if in_place else torch.full((t.numel() + off,), 9.0, dtype=dtype, device="cuda")[off:] for t in tensors]
+            got = clip(out if in_place else tensors, out, limit, stall_tile=stall, spin_limit=100)
+            assert math.isnan(got), (stall, in_place)
+            lost = [int(t.isnan().sum()) for t in out]
+            assert all(bool((t.isnan() | (bits(t) == bits(w))).all()) for t, w in zip(out, want.gradients))
+            assert sum(lost) >= 4 and (name != "two launches" or (sum(lost[:1000]) > 0 and sum(lost[1000:]) > 0))
+            assert sum(lost) % (16 // out[0].element_size()) == 0          # whole vectors: tensors' ends come by themselves
+            assert sum(lost) < sum(t.numel() for t in out)
+    again = [torch.empty_like(t) for t in tensors]
+    for fields in ({}, dict(stall_tile=10 ** 6), dict(spin_limit=1 << 22)):
+        assert clip(tensors, again, limit, **fields) == float(want.norm)
+        assert all(torch.equal(bits(a), bits(w)) for a, w in zip(again, want.gradients))
+
+
+def test_gradients_that_stay_as_they_are_need_not_come():
+    tensors = [torch.randn(100_000, device="cuda"), torch.randn(33, device="cuda")]
+    before = [t.clone() for t in tensors]
+    assert math.isnan(clip(tensors, tensors, 1e9, stall_tile=0))
+    assert all(torch.equal(a, b) for a, b in zip(tensors, before))

@@ -163,4 +163,7 @@ def test_options_of_extended_calls(lib):
     i, s, t = (ctypes.c_void_p * 1)(A), (ctypes.c_int64 * 1)(10), (ctypes.c_int * 1)(0)
     for o in bad:
         assert lib.gsort_gradient_norm_ex(i, s, t, 1, C, W, 1 << 20, None, ctypes.byref(o)) == EINVAL
+        assert lib.gsort_clip_gradients_ex(i, i, s, t, 1, 1.0, 1.0, C, W, 1 << 20, None, ctypes.byref(o)) == EINVAL
     assert lib.gsort_gradient_norm_ex(i, s, t, 1, C, W, 8, None, None) == EWS
+    assert lib.gsort_clip_gradients_ex(i, i, s, t, 1, 1.0, 1.0, C, W, 8, None, None) == EWS
+    assert lib.gsort_clip_gradients_ex(i, None, s, t, 1, 1.0, 1.0, C, W, 1 << 20, None, None) == EINVAL

@@ -164,6 +164,13 @@ SIGNATURES = {
     "gsort_adjust_logits_backward": (ctypes.c_int, [
         ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
         ctypes.c_int64, ctypes.POINTER(Adjustments), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "gsort_adjust_logits_ex": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+        ctypes.POINTER(Adjustments), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.POINTER(Options)]),
+    "gsort_adjust_logits_backward_ex": (ctypes.c_int, [
+        ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.c_int64, ctypes.POINTER(Adjustments), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+        ctypes.POINTER(Options)]),
     "gsort_gradient_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64]),
     "gsort_gradient_norm": (ctypes.c_int, [
         ctypes.POINTER(ctypes.c_void_p), c_i64p, ctypes.POINTER(ctypes.c_int), ctypes.c_int64, ctypes.c_void_p,

@@ -42,7 +42,7 @@ constexpr size_t kHalfSmem = 108 * 1024, kWholeSmem = 218 * 1024;
 constexpr int64_t kHalfCtas = 304, kWholeCtas = 152;      // that rows are cut into, where they are fewer
 constexpr uint32_t kSeenBefore = 0x80000000u;     // of a count: the token is in the prompt
 constexpr uint32_t kNowhere = 0xFFFFFFFFu;
-constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier
+constexpr uint32_t kWaitLimit = 1u << 20;         // polls of a copy's barrier before its room is used anew
 
 template <typename T> struct AdjustArgs {
     const T *logits;         // the gradient's: null where no history is given
@@ -73,6 +73,7 @@ template <typename T> struct AdjustArgs {
     bool narrow;             // counts and numbers of members in 16 bits
     bool vectors;            // rows of in and out lie the same way to 16 bytes
     bool in_place;
+    Waits waits;             // for the ring's copies
 };
 
 __device__ __forceinline__ int64_t int_at(const void *p, int bytes, int64_t i) {
@@ -135,6 +136,13 @@ struct TokenSet {
 struct Crew {
     uint32_t id, threads, rank;      // barrier, threads, and this thread among them
     __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+    // The same, and whether x holds for any thread.
+    __device__ __forceinline__ bool sync_any(bool x) const {
+        uint32_t any;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(any) : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x)) : "memory");
+        return any != 0;
+    }
 };
 
 // Counts the members before each word, and clears their slots.  Called by the whole crew.
@@ -247,7 +255,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a
     constexpr uint32_t kAll = (1u << N) - 1;
     extern __shared__ __align__(128) uint32_t s_words[];
     __shared__ __align__(8) uint64_t s_full[kMostStages];
-    __shared__ uint32_t s_failed;
     const uint32_t row = blockIdx.x / a.pieces, piece = blockIdx.x % a.pieces, tid = threadIdx.x, threads = blockDim.x;
     const T *in = a.in + static_cast<int64_t>(row) * a.in_stride;
     T *out = a.out + static_cast<int64_t>(row) * a.out_stride;
@@ -309,7 +316,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a
         for (uint32_t w = tid * 32; allowed && w < words + 32; w += 32 * a.streamers)
             asm volatile("prefetch.global.L1 [%0];" ::"l"(mask + min(max(k0 + static_cast<int32_t>(w), 0), last)));
         if (tid == 0) {
-            s_failed = 0;
             for (uint32_t k = 0; k < a.stages; ++k) mbar_init(&s_full[k], 1);
             for (uint32_t k = 0; k < a.stages; ++k) copy(k);
         }
@@ -340,9 +346,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a
         for (int32_t e = rest + static_cast<int32_t>(tid); e < r.end; e += a.streamers) single(e);
         for (uint32_t k = 0, v0 = low_v; v0 < high_v; ++k, v0 += per_stage) {
             const uint4 *data = ring;
+            bool there = true;
             if (a.stages > 0) {
                 data += k % a.stages * per_stage;
-                if (!mbar_wait_bounded(&s_full[k % a.stages], (k / a.stages) & 1, kWaitLimit)) s_failed = 1;
+                there = mbar_wait_bounded(&s_full[k % a.stages], (k / a.stages) & 1, a.waits.of_cta());
             }
 #pragma unroll 4
             for (uint32_t i = tid; i < min(per_stage, high_v - v0); i += a.streamers) {
@@ -353,8 +360,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) k_adjust(const AdjustArgs<T> a
                 out_v[v] = x;
             }
             if (a.stages > 0) {
-                crew.sync();
-                if (*const_cast<volatile uint32_t *>(&s_failed)) {     // a copy that does not come: what is left is no number
+                if (crew.sync_any(!there)) {       // a copy that does not come: what is left is no number
                     for (uint32_t v = v0 + tid; v < high_v; v += a.streamers) out_v[v] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
                     for (uint32_t i = k; i < k + a.stages && low_v + i * per_stage < high_v; ++i)
                         mbar_wait_bounded(&s_full[i % a.stages], (i / a.stages) & 1, kWaitLimit);
@@ -513,6 +519,7 @@ int launch_adjust(const AdjustLaunch &L) {
         a.allowed = L.allowed;
         a.allowed_stride = L.allowed_stride;
         a.in_place = L.in == L.out;
+        a.waits = L.waits;
         // a row has the distance from the boundary of its array and `row` strides
         a.vectors = ((reinterpret_cast<uintptr_t>(L.in) ^ reinterpret_cast<uintptr_t>(L.out)) & 15) == 0 &&
                     (L.rows == 1 || (L.in_stride - L.out_stride) % N == 0);

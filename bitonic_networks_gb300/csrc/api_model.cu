@@ -75,12 +75,23 @@ int list_args(int64_t rows, int64_t width, int64_t stride) {
     return stride == 0 ? rows_args(1, width, width) : rows_args(rows, width, stride);
 }
 
+// The options of an extended call that waits for bulk copies.
+int waits_of(const gsort_options *o, Waits *w) {
+    if (o == nullptr) return GSORT_OK;
+    if (o->variant != 0 || o->num_events < 0 || (o->num_events > 0 && o->events == nullptr)) return GSORT_EINVAL;
+    if (o->spin_limit != 0) w->polls = o->spin_limit;
+    if (o->stall_tile >= 0 && o->stall_tile < 0xFFFFFFFFll) w->stall = static_cast<uint32_t>(o->stall_tile);
+    return GSORT_OK;
+}
+
 // The logits' adjustment (in: the logits) or its gradient (in: the gradient by the adjusted logits).
 int adjust(bool backward, const void *logits, int64_t logits_stride, const void *in, int64_t in_stride, int dtype, int64_t rows,
-           int64_t vocab, const gsort_adjustments *how, void *out, int64_t out_stride, cudaStream_t stream) {
+           int64_t vocab, const gsort_adjustments *how, void *out, int64_t out_stride, cudaStream_t stream, const gsort_options *options) {
     if (float_bytes(dtype) == 0 || how == nullptr) return GSORT_EINVAL;
     const gsort_adjustments &h = *how;
-    int rc = rows_args(rows, vocab, in_stride);
+    AdjustLaunch L;
+    int rc = waits_of(options, &L.waits);
+    if (rc == GSORT_OK) rc = rows_args(rows, vocab, in_stride);
     if (rc == GSORT_OK) rc = rows_args(rows, vocab, out_stride);
     const bool history = h.d_history != nullptr && h.length > 0 && (!backward || h.d_repetition != nullptr);
     if (rc == GSORT_OK && backward && history) rc = rows_args(rows, vocab, logits_stride);
@@ -111,7 +122,6 @@ int adjust(bool backward, const void *logits, int64_t logits_stride, const void 
                         h.d_allowed ? rows_span(h.d_allowed, rows, words, h.allowed_stride, 4) : Span{nullptr, 0}};
     const Span outs[] = {rows_span(out, rows, vocab, out_stride, size)};
     if (clash(ins, outs)) return GSORT_EINVAL;
-    AdjustLaunch L;
     L.backward = backward;
     L.logits = logits;
     L.in = in;
@@ -237,15 +247,6 @@ bool tensors_clash(const void *const *in, void *const *out, const int64_t *eleme
         if (r.written) written = std::max(written, r.end);
     }
     return false;
-}
-
-// The options of an extended call that waits for bulk copies.
-int waits_of(const gsort_options *o, Waits *w) {
-    if (o == nullptr) return GSORT_OK;
-    if (o->variant != 0 || o->num_events < 0 || (o->num_events > 0 && o->events == nullptr)) return GSORT_EINVAL;
-    if (o->spin_limit != 0) w->polls = o->spin_limit;
-    if (o->stall_tile >= 0 && o->stall_tile < 0xFFFFFFFFll) w->stall = static_cast<uint32_t>(o->stall_tile);
-    return GSORT_OK;
 }
 
 int norm(const void *const *in, void *const *out, const int64_t *elements, const int *dtypes, int64_t tensors, float max_norm,
@@ -671,14 +672,30 @@ int gsort_embed_tokens_backward(const void *d_grad_out, int dtype, int64_t token
 int gsort_adjust_logits(const void *d_logits, int dtype, int64_t rows, int64_t vocab,
                         int64_t row_stride, const gsort_adjustments *how, void *d_out,
                         int64_t out_stride, cudaStream_t stream) {
-    return adjust(false, nullptr, 0, d_logits, row_stride, dtype, rows, vocab, how, d_out, out_stride, stream);
+    return adjust(false, nullptr, 0, d_logits, row_stride, dtype, rows, vocab, how, d_out, out_stride, stream, nullptr);
+}
+
+int gsort_adjust_logits_ex(const void *d_logits, int dtype, int64_t rows, int64_t vocab,
+                           int64_t row_stride, const gsort_adjustments *how, void *d_out,
+                           int64_t out_stride, cudaStream_t stream, const gsort_options *options) {
+    return adjust(false, nullptr, 0, d_logits, row_stride, dtype, rows, vocab, how, d_out, out_stride, stream, options);
 }
 
 int gsort_adjust_logits_backward(const void *d_grad_out, int dtype, int64_t rows, int64_t vocab,
                                  int64_t grad_stride, const void *d_logits, int64_t row_stride,
                                  const gsort_adjustments *how, void *d_grad_logits,
                                  int64_t grad_logits_stride, cudaStream_t stream) {
-    return adjust(true, d_logits, row_stride, d_grad_out, grad_stride, dtype, rows, vocab, how, d_grad_logits, grad_logits_stride, stream);
+    return adjust(true, d_logits, row_stride, d_grad_out, grad_stride, dtype, rows, vocab, how, d_grad_logits, grad_logits_stride, stream,
+                  nullptr);
+}
+
+int gsort_adjust_logits_backward_ex(const void *d_grad_out, int dtype, int64_t rows, int64_t vocab,
+                                    int64_t grad_stride, const void *d_logits, int64_t row_stride,
+                                    const gsort_adjustments *how, void *d_grad_logits,
+                                    int64_t grad_logits_stride, cudaStream_t stream,
+                                    const gsort_options *options) {
+    return adjust(true, d_logits, row_stride, d_grad_out, grad_stride, dtype, rows, vocab, how, d_grad_logits, grad_logits_stride, stream,
+                  options);
 }
 
 size_t gsort_gradient_norm_workspace_bytes(int64_t tensors) {

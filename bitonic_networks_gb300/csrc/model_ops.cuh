@@ -314,6 +314,7 @@ struct AdjustLaunch {
     int bias_bytes;
     const uint32_t *allowed; // null: none
     int64_t allowed_stride;
+    Waits waits;
     cudaStream_t stream;
 };
 int launch_adjust(const AdjustLaunch &L);

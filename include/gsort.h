@@ -600,8 +600,20 @@ int gsort_compact_positive_ex(const float *d_in, float *d_out, int64_t n,
 
 /* Calls whose kernels wait for bulk copies of their inputs: spin_limit is the
  * polls of one such wait (0 = default), and stall_tile (testing) a CTA whose waits run
- * out at once.  Where a copy does not come the result says so: the norm is NaN, and
- * in clipping (whose options are those of its second read) so is what was not read. */
+ * out at once.  Where a copy does not come the result says so: adjusted logits of the
+ * CTA's part of a row are NaN from there on, masked ones too (but not those of the
+ * history, biased ones and a row's cut ends, which are read by themselves), the norm is
+ * NaN, and in clipping (whose options are those of its second read) so is what was not read. */
+int gsort_adjust_logits_ex(const void *d_logits, int dtype, int64_t rows, int64_t vocab,
+                           int64_t row_stride, const gsort_adjustments *how, void *d_out,
+                           int64_t out_stride, cudaStream_t stream, const gsort_options *options);
+
+int gsort_adjust_logits_backward_ex(const void *d_grad_out, int dtype, int64_t rows, int64_t vocab,
+                                    int64_t grad_stride, const void *d_logits, int64_t row_stride,
+                                    const gsort_adjustments *how, void *d_grad_logits,
+                                    int64_t grad_logits_stride, cudaStream_t stream,
+                                    const gsort_options *options);
+
 int gsort_gradient_norm_ex(const void *const *d_gradients, const int64_t *elements, const int *dtypes,
                            int64_t tensors, float *d_norm, void *d_ws, size_t ws_bytes,
                            cudaStream_t stream, const gsort_options *options);

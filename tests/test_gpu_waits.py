@@ -103,3 +103,52 @@ def test_gradients_that_stay_as_they_are_need_not_come():
     before = [t.clone() for t in tensors]
     assert math.isnan(clip(tensors, tensors, 1e9, stall_tile=0))
     assert all(torch.equal(a, b) for a, b in zip(tensors, before))
+
+
+def adjust(x, how, allowed, out, d=None, **fields):
+    h = how["history"]
+    a = _lib.Adjustments(d_history=h.data_ptr(), length=h.shape[1], history_stride=h.shape[1], history_bytes=h.element_size(),
+                         d_repetition=how["repetition"].data_ptr(), d_bias_tokens=how["bias_tokens"].data_ptr(), d_bias=how["bias"].data_ptr(),
+                         biases=how["bias"].shape[1], bias_stride=how["bias"].shape[1], bias_bytes=how["bias_tokens"].element_size(),
+                         d_allowed=allowed.data_ptr(), allowed_stride=allowed.shape[1])
+    rows, vocab = x.shape
+    if d is None:
+        rc = _lib.load().gsort_adjust_logits_ex(x.data_ptr(), CODES[x.dtype], rows, vocab, vocab, ctypes.byref(a), out.data_ptr(), vocab, stream(),
+                                                options(**fields))
+    else:
+        rc = _lib.load().gsort_adjust_logits_backward_ex(d.data_ptr(), CODES[x.dtype], rows, vocab, vocab, x.data_ptr(), vocab, ctypes.byref(a),
+                                                         out.data_ptr(), vocab, stream(), options(**fields))
+    assert rc == OK
+    return out
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,vocab,length,whole", [(3, 60011, 40, False), (400, 9001, 300, True), (200, 40000, 9000, True), (310, 300000, 50, True)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_logits_that_did_not_come_are_nan(dtype, rows, vocab, length, whole, backward):
+    """Other rows are right, and so is what is read by itself; `whole`: a row is one CTA's."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x, d = (torch.randn(rows, vocab, generator=g, device="cuda").to(dtype) for _ in range(2))
+    how = dict(history=torch.randint(vocab, (rows, length), generator=g, device="cuda"), repetition=torch.rand(rows, generator=g, device="cuda") + 0.5,
+               bias_tokens=torch.randint(vocab, (rows, 7), generator=g, device="cuda"), bias=torch.randn(rows, 7, generator=g, device="cuda"))
+    allowed = torch.full((rows, (vocab + 31) // 32), -1, dtype=torch.int32, device="cuda")
+    grad = d if backward else None
+    want = gs.adjust_logits_backward(d, x, history=how["history"], repetition=how["repetition"], allowed=allowed) if backward else \
+        gs.adjust_logits(x, **how, allowed=allowed)
+    for stall in (0, 7):
+        got = adjust(x, how, allowed, torch.full_like(x, 9.0), grad, stall_tile=stall, spin_limit=100)
+        lost = got.isnan().sum(1)
+        assert int((lost > 0).sum()) == 1 and (not whole or vocab == 300000 or int(lost[stall]) > 0), lost
+        row = int(lost.argmax())
+        assert bool((got.isnan() | (bits(got) == bits(want))).all())
+        named = how["history"][row] if backward else torch.cat([how["history"][row], how["bias_tokens"][row]])
+        assert not bool(got[row, named].isnan().any())
+        if whole and vocab < 300000:            # all but those and the row's cut ends
+            others = torch.ones(vocab, dtype=torch.bool, device="cuda")
+            others[named] = False
+            vector = 16 // x.element_size()
+            assert int(lost[row]) >= int(others.sum()) - 2 * (vector - 1)
+    for fields in ({}, dict(stall_tile=10 ** 6), dict(spin_limit=1 << 22)):
+        assert torch.equal(bits(adjust(x, how, allowed, torch.full_like(x, 9.0), grad, **fields)), bits(want))
+    into = (d if backward else x).clone()
+    assert torch.equal(bits(adjust(x if backward else into, how, allowed, into, into if backward else None, stall_tile=0)), bits(want))     # in place nothing is copied

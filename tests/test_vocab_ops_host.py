@@ -161,9 +161,15 @@ def test_options_of_extended_calls(lib):
     from bitonic_networks_gb300 import _lib
     bad = [_lib.Options(0, -1, None, 0, 1), _lib.Options(0, -1, None, -1, 0), _lib.Options(0, -1, None, 2, 0)]
     i, s, t = (ctypes.c_void_p * 1)(A), (ctypes.c_int64 * 1)(10), (ctypes.c_int * 1)(0)
+    how = _lib.Adjustments()
     for o in bad:
         assert lib.gsort_gradient_norm_ex(i, s, t, 1, C, W, 1 << 20, None, ctypes.byref(o)) == EINVAL
         assert lib.gsort_clip_gradients_ex(i, i, s, t, 1, 1.0, 1.0, C, W, 1 << 20, None, ctypes.byref(o)) == EINVAL
+        assert lib.gsort_adjust_logits_ex(A, 0, 4, 100, 100, how, C, 100, None, ctypes.byref(o)) == EINVAL
+        assert lib.gsort_adjust_logits_backward_ex(A, 0, 4, 100, 100, None, 0, how, C, 100, None, ctypes.byref(o)) == EINVAL
     assert lib.gsort_gradient_norm_ex(i, s, t, 1, C, W, 8, None, None) == EWS
     assert lib.gsort_clip_gradients_ex(i, i, s, t, 1, 1.0, 1.0, C, W, 8, None, None) == EWS
     assert lib.gsort_clip_gradients_ex(i, None, s, t, 1, 1.0, 1.0, C, W, 1 << 20, None, None) == EINVAL
+    assert lib.gsort_adjust_logits_ex(A, 0, 4, 100, 99, how, C, 100, None, None) == EINVAL
+    assert lib.gsort_adjust_logits_ex(None, 0, 0, 100, 100, how, None, 100, None, None) == OK
+    assert lib.gsort_adjust_logits_backward_ex(None, 0, 0, 100, 100, None, 0, how, None, 100, None, None) == OK

@@ -75,7 +75,7 @@ int list_args(int64_t rows, int64_t width, int64_t stride) {
     return stride == 0 ? rows_args(1, width, width) : rows_args(rows, width, stride);
 }
 
-// The options of an extended call that waits for bulk copies.
+// The options of an extended call: limits of its waits.
 int waits_of(const gsort_options *o, Waits *w) {
     if (o == nullptr) return GSORT_OK;
     if (o->variant != 0 || o->num_events < 0 || (o->num_events > 0 && o->events == nullptr)) return GSORT_EINVAL;
@@ -622,17 +622,28 @@ int gsort_embed_tokens(const void *d_table, int dtype, int64_t vocab, int64_t wi
     return launch_embed(L);
 }
 
-size_t gsort_embed_tokens_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int dtype) {
-    if (tokens < 1 || embed_args(dtype, vocab, width, tokens, 4, 1.0f) != GSORT_OK) return 0;
-    return embed_workspace_bytes(tokens, vocab, width, dtype);
-}
-
 int gsort_embed_tokens_backward(const void *d_grad_out, int dtype, int64_t tokens, int64_t width,
                                 int64_t grad_stride, const void *d_tokens, int token_bytes,
                                 int64_t vocab, float scale, int accumulate, void *d_grad_table,
                                 int64_t table_stride, void *d_ws, size_t ws_bytes,
                                 cudaStream_t stream) {
-    int rc = embed_args(dtype, vocab, width, tokens, token_bytes, scale);
+    return gsort_embed_tokens_backward_ex(d_grad_out, dtype, tokens, width, grad_stride, d_tokens, token_bytes, vocab, scale, accumulate,
+                                          d_grad_table, table_stride, d_ws, ws_bytes, stream, nullptr);
+}
+
+size_t gsort_embed_tokens_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width, int dtype) {
+    if (tokens < 1 || embed_args(dtype, vocab, width, tokens, 4, 1.0f) != GSORT_OK) return 0;
+    return embed_workspace_bytes(tokens, vocab, width, dtype);
+}
+
+int gsort_embed_tokens_backward_ex(const void *d_grad_out, int dtype, int64_t tokens, int64_t width,
+                                   int64_t grad_stride, const void *d_tokens, int token_bytes,
+                                   int64_t vocab, float scale, int accumulate, void *d_grad_table,
+                                   int64_t table_stride, void *d_ws, size_t ws_bytes,
+                                   cudaStream_t stream, const gsort_options *options) {
+    EmbedBackwardLaunch L;
+    int rc = waits_of(options, &L.waits);
+    if (rc == GSORT_OK) rc = embed_args(dtype, vocab, width, tokens, token_bytes, scale);
     if (rc == GSORT_OK) rc = rows_args(tokens, width, grad_stride);
     if (rc == GSORT_OK) rc = rows_args(vocab, width, table_stride);
     if (rc != GSORT_OK) return rc;
@@ -650,7 +661,6 @@ int gsort_embed_tokens_backward(const void *d_grad_out, int dtype, int64_t token
     if (clash(in, out)) return GSORT_EINVAL;
     DeviceInfo dev;
     if (device_info(&dev) != GSORT_OK) return GSORT_ECUDA;
-    EmbedBackwardLaunch L;
     L.d_out = d_grad_out;
     L.dtype = dtype;
     L.n = tokens;

@@ -329,12 +329,13 @@ template <typename T> struct EmbedSumArgs {
     const uint4 *safe;
     T *out;
     const uint32_t *keys, *order;    // sorted
+    const void *tokens;
     const uint32_t *status;          // of the sort; null: it cannot fail
     float *partials;                 // [chunks][2][slabs * lanes][N]: sums up to a chunk's end and from its start
     uint32_t *counters;              // [chunks][slabs], zeros: parts of a run that began in the chunk
     int64_t d_stride, out_stride;
     float scale;
-    bool accumulate;
+    bool accumulate, wide;           // wide: tokens of 8 bytes (as an int of its own it made ptxas spill: shifted rows 3 % slower)
     uint32_t n, vocab, width, vectors;
     uint32_t log_lanes, slabs;       // 2^log_lanes lanes hold a vector each; slabs of them make a row
     uint32_t per;                    // positions of a group of lanes
@@ -398,14 +399,22 @@ template <typename T, int MODE> struct RowSum {
     }
 };
 
+// Rows of tokens that occur become NaN.
+template <typename T> __device__ __forceinline__ void void_rows(const EmbedSumArgs<T> &a) {
+    for (uint32_t i = blockIdx.x; i < a.n; i += gridDim.x) {
+        const uint32_t key = token_key(token_at(a.tokens, a.wide ? 8 : 4, i), a.vocab);
+        if (key < a.vocab)
+            fill_span<kEmbedThreads>(reinterpret_cast<char *>(a.out + static_cast<int64_t>(key) * a.out_stride),
+                                     static_cast<int64_t>(a.width) * sizeof(T), 0x7FFF7FFFu);
+    }
+}
+
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kEmbedThreads, 4) k_embed_sum(const EmbedSumArgs<T> a) {
     constexpr int N = Wide<T>::kCount, U = kLoads<MODE>;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");       // rows are filled meanwhile
-    if (a.status != nullptr && *a.status != 0) {       // the sort gave up, its results are void: rows are NaN (absent ones may be zeros)
-        for (uint32_t r = blockIdx.x; r < a.vocab; r += gridDim.x)
-            fill_span<kEmbedThreads>(reinterpret_cast<char *>(a.out + static_cast<int64_t>(r) * a.out_stride),
-                                     static_cast<int64_t>(a.width) * sizeof(T), 0x7FFF7FFFu);
+    if (a.status != nullptr && *a.status != 0) {       // the sort gave up, its results are void: rows of tokens that occur are NaN
+        void_rows(a);
         return;
     }
     __shared__ uint32_t s_key[kMaxChunk + 2], s_order[kMaxChunk];   // s_key[0]: the key before the chunk
@@ -681,7 +690,7 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
     };
     const bool few = n <= kFewTokens || (n <= 2 * kFewTokens && static_cast<int64_t>(fill_ctas) * n <= static_cast<int64_t>(kFewFills) * kFewTokens);
     // of the CTAs that fill, those before the sums
-    const int64_t beside = few ? kBesideFew : n <= kRankMax ? kBesideCounting : cluster_sort_applies(n, 4, 0, kNoStall, 1) ? kBesideCluster : 0;
+    const int64_t beside = few ? kBesideFew : n <= kRankMax ? kBesideCounting : cluster_sort_applies(n, 4, 0, L.waits.stall, 1) ? kBesideCluster : 0;
     const uint32_t filled = n == 0 ? fill_ctas : static_cast<uint32_t>(std::min<int64_t>(fill_ctas, beside / (fill.row_bytes * fill.rows)));
     if (few) {
         if (groups == 0 && fill_ctas == 0) return GSORT_OK;
@@ -709,8 +718,8 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
             R.kind = GSORT_KEY_U32;
             R.end_bit = 32 - __builtin_clz(vocab);       // what is no token has the key `vocab`
             R.ws = L.ws + plan.radix;
-            R.spin_limit = kDefaultSpinLimit;
-            R.stall_tile = kNoStall;
+            R.spin_limit = L.waits.polls;
+            R.stall_tile = L.waits.stall;
             R.stream = L.stream;
             R.sm_count = L.sm_count;
             R.next_early = fill_ctas > 0;
@@ -730,6 +739,8 @@ int launch_embed_backward(const EmbedBackwardLaunch &L) {
         a.keys = keys;
         a.order = order;
         a.status = n > kRankMax ? status : nullptr;
+        a.tokens = L.tokens;
+        a.wide = L.token_bytes == 8;
         a.partials = reinterpret_cast<float *>(L.ws + plan.partials);
         a.counters = counters;
         a.d_stride = L.d_stride;

@@ -165,7 +165,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // The waits of a call's kernels for their bulk copies: polls of one, and (testing) the CTA whose
-// waits run out at once.
+// waits run out at once.  Where a call sorts: polls of a look-back, and the tile that publishes nothing.
 struct Waits {
     uint32_t polls = kDefaultSpinLimit, stall = kNoStall;
     __device__ __forceinline__ uint32_t of_cta() const { return blockIdx.x == stall ? 0 : polls; }
@@ -290,6 +290,7 @@ struct EmbedBackwardLaunch {
     void *d_table;
     int64_t table_stride;
     unsigned char *ws;
+    Waits waits;             // of the sort
     cudaStream_t stream;
     int sm_count;
 };

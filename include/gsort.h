@@ -463,8 +463,9 @@ int gsort_token_logprobs_backward(const float *d_grad_logprobs, const float *d_g
  * The gradient sums in 32 bits in an order that the tokens and the sizes give
  * (results are the same from run to run) and rounds once.  With more than 8192
  * tokens it uses the radix sort; where a wait of that gave up, gsort_check() of
- * the workspace says so and the rows of tokens that occur are NaN.  The workspace may be NULL
- * where gsort_embed_tokens_backward_workspace_bytes() is 0 (no tokens). */
+ * the workspace says so and the rows of tokens that occur are NaN, the others as
+ * they would be.  The workspace may be NULL where
+ * gsort_embed_tokens_backward_workspace_bytes() is 0 (no tokens). */
 int gsort_embed_tokens(const void *d_table, int dtype, int64_t vocab, int64_t width,
                        int64_t row_stride, const void *d_tokens, int token_bytes, int64_t tokens,
                        float scale, void *d_out, cudaStream_t stream);
@@ -597,6 +598,13 @@ int gsort_segmented_sort_ex(const void *d_keys_in, void *d_keys_out,
 int gsort_compact_positive_ex(const float *d_in, float *d_out, int64_t n,
                               int64_t *d_num_kept, void *d_ws, size_t ws_bytes,
                               cudaStream_t stream, const gsort_options *options);
+
+/* spin_limit and stall_tile are those of the radix sort that more than 8192 tokens take. */
+int gsort_embed_tokens_backward_ex(const void *d_grad_out, int dtype, int64_t tokens, int64_t width,
+                                   int64_t grad_stride, const void *d_tokens, int token_bytes,
+                                   int64_t vocab, float scale, int accumulate, void *d_grad_table,
+                                   int64_t table_stride, void *d_ws, size_t ws_bytes,
+                                   cudaStream_t stream, const gsort_options *options);
 
 /* Calls whose kernels wait for bulk copies of their inputs: spin_limit is the
  * polls of one such wait (0 = default), and stall_tile (testing) a CTA whose waits run

@@ -12,7 +12,7 @@ from bitonic_networks_gb300 import _lib
 from model_ref import DTYPES
 
 pytestmark = pytest.mark.gpu
-OK = 0
+OK, ETIMEOUT = 0, -6
 CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -152,3 +152,38 @@ def test_logits_that_did_not_come_are_nan(dtype, rows, vocab, length, whole, bac
         assert torch.equal(bits(adjust(x, how, allowed, torch.full_like(x, 9.0), grad, **fields)), bits(want))
     into = (d if backward else x).clone()
     assert torch.equal(bits(adjust(x if backward else into, how, allowed, into, into if backward else None, stall_tile=0)), bits(want))     # in place nothing is copied
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,vocab,width", [(30000, 5000, 40), (70001, 900, 33), (300001, 70000, 8)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_a_sort_of_tokens_that_gives_up(dtype, n, vocab, width, accumulate):
+    """Rows of tokens that occur are NaN, others zero or as they were, and the workspace tells of it.  One cooperative kernel
+    sorts up to 2^18 tokens here, passes with look-backs more."""
+    lib, g = _lib.load(), torch.Generator(device="cuda").manual_seed(n)
+    tokens = torch.randint(vocab, (n,), generator=g, device="cuda") // 3 * 3         # a third of the rows
+    tokens[:50] = -1
+    tokens[50:60] = vocab
+    d, old = torch.randn(n, width, generator=g, device="cuda").to(dtype), torch.randn(vocab, width + 3, generator=g, device="cuda").to(dtype)
+    ws = torch.empty(gs.embed_workspace_bytes(n, vocab, width, dtype), dtype=torch.uint8, device="cuda")
+    held = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+    held[tokens[60:]] = True
+
+    def call(**fields):
+        out = old.clone()
+        rc = lib.gsort_embed_tokens_backward_ex(d.data_ptr(), CODES[dtype], n, width, width, tokens.data_ptr(), 8, vocab, 1.0, int(accumulate),
+                                                out.data_ptr(), width + 3, ws.data_ptr(), ws.numel(), stream(), options(**fields))
+        assert rc == OK
+        return out, lib.gsort_check(ws.data_ptr(), stream())
+
+    want, status = call()
+    assert status == OK and not bool(want.isnan().any())
+    for stall in (0, 1):
+        got, status = call(stall_tile=stall, spin_limit=2000)
+        assert status == ETIMEOUT
+        assert bool(got[held, :width].isnan().all())
+        assert torch.equal(bits(got[~held].contiguous()), bits(want[~held].contiguous())) and torch.equal(got[:, width:], old[:, width:])
+        if accumulate:
+            assert torch.equal(got[~held], old[~held])
+        again, status = call()
+        assert status == OK and torch.equal(bits(again), bits(want))

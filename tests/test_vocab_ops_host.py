@@ -166,10 +166,13 @@ def test_options_of_extended_calls(lib):
         assert lib.gsort_gradient_norm_ex(i, s, t, 1, C, W, 1 << 20, None, ctypes.byref(o)) == EINVAL
         assert lib.gsort_clip_gradients_ex(i, i, s, t, 1, 1.0, 1.0, C, W, 1 << 20, None, ctypes.byref(o)) == EINVAL
         assert lib.gsort_adjust_logits_ex(A, 0, 4, 100, 100, how, C, 100, None, ctypes.byref(o)) == EINVAL
+        assert lib.gsort_embed_tokens_backward_ex(A, 0, 4, 8, 8, B, 4, 10, 1.0, 0, C, 8, W, 1 << 30, None, ctypes.byref(o)) == EINVAL
         assert lib.gsort_adjust_logits_backward_ex(A, 0, 4, 100, 100, None, 0, how, C, 100, None, ctypes.byref(o)) == EINVAL
     assert lib.gsort_gradient_norm_ex(i, s, t, 1, C, W, 8, None, None) == EWS
     assert lib.gsort_clip_gradients_ex(i, i, s, t, 1, 1.0, 1.0, C, W, 8, None, None) == EWS
     assert lib.gsort_clip_gradients_ex(i, None, s, t, 1, 1.0, 1.0, C, W, 1 << 20, None, None) == EINVAL
     assert lib.gsort_adjust_logits_ex(A, 0, 4, 100, 99, how, C, 100, None, None) == EINVAL
     assert lib.gsort_adjust_logits_ex(None, 0, 0, 100, 100, how, None, 100, None, None) == OK
+    assert lib.gsort_embed_tokens_backward_ex(A, 0, 4, 8, 8, B, 4, 10, 1.0, 0, C, 8, W, 16, None, None) == EWS
+    assert lib.gsort_embed_tokens_backward_ex(None, 0, 0, 8, 8, None, 4, 10, 1.0, 1, C, 8, None, 0, None, None) == OK
     assert lib.gsort_adjust_logits_backward_ex(None, 0, 0, 100, 100, None, 0, how, None, 100, None, None) == OK

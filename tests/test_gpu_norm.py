@@ -240,3 +240,20 @@ def test_norms_far_beyond_the_limit(dtype, max_norm, n):
         r = gs.clip_gradients([t], max_norm, out=out)
         assert float(r.norm) == INF         # beyond 32 bits
         assert bool(((r.gradients[0].double() - want).abs() <= error).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("value", [None, 1.1, 0.7, 1 / 3, 0.013])
+@pytest.mark.parametrize("n", [3, 4096, 16384, 1_000_003, 30_000_000])
+def test_the_norm_is_as_near_as_a_steps_sums_allow(dtype, value, n):
+    """Of a step a thread has 4 vectors: 4 chains of 4 products (f32) or 8 (16 bits), joined by 2 additions: 6 or 10 roundings
+    of numbers of one sign, half of that under the root.  All else is 64-bit, and the norm rounds once.  Equal numbers
+    round alike in every chain, so that errors do not cancel."""
+    if value is None:
+        t = torch.rand(n, generator=torch.Generator(device="cuda").manual_seed(n), device="cuda").add_(0.5).to(dtype)
+    else:
+        t = torch.full((n,), value, device="cuda").to(dtype)
+    want = norm64([t])
+    near = ((3 if dtype == torch.float32 else 5) + 1) * U32 * 1.0001         # the rest is of second order
+    assert abs(float(gs.gradient_norm([t])) - want) <= near * want
+    assert abs(float(gs.clip_gradients([t], 1.0).norm) - want) <= near * want

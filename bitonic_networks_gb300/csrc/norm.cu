@@ -134,8 +134,8 @@ template <int M, bool BACKWARDS> struct Ring {
     template <typename F> __device__ __forceinline__ uint32_t run(uint32_t polls, F &&f) {
         for (uint32_t k = 0;; ++k) {
             const int stage = k % kStages;
-            if (steps[stage].vectors == 0) return kAll;
             const bool there = mbar_wait_bounded(&full[stage], (k / kStages) & 1, polls);
+            if (steps[stage].vectors == 0) return kAll;
             if (there) f(steps[stage], data[stage]);
             if (__syncthreads_or(!there)) {        // leave once no copy can be under way any more
                 for (uint32_t i = k; i < k + kStages; ++i) mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1, kWaitLimit);
@@ -258,59 +258,64 @@ __global__ void __launch_bounds__(kNormThreads, 4) k_square_sums(const __grid_co
     if (zero != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *zero = 0.0f;
 }
 
-__device__ __forceinline__ double norm_of(const double *slots, uint32_t count, float scale) {
+__device__ __forceinline__ double sum_of(const double *slots, uint32_t count) {
     double d = 0.0;
     for (uint32_t i = threadIdx.x; i < count; i += kNormThreads) d += slots[i];
-    return fabs(static_cast<double>(scale)) * sqrt(cta_sum(d));
+    return cta_sum(d);
 }
+
+__device__ __forceinline__ double norm_of(double squares, float scale) { return fabs(static_cast<double>(scale)) * sqrt(squares); }
 
 __global__ void __launch_bounds__(kNormThreads) k_norm(const double *slots, uint32_t count, float scale, float *out) {
     wait_for_last();
-    const double norm = norm_of(slots, count, scale);
-    if (threadIdx.x == 0) *out = static_cast<float>(norm);
+    const double squares = sum_of(slots, count);
+    if (threadIdx.x == 0) *out = static_cast<float>(norm_of(squares, scale));
 }
 
-// What every element is multiplied by.  Where a norm is so far beyond its limit that the factor is no
-// normal 32-bit number, rounding would take its bits, or all of it: products are 64-bit there.
+// What every element is multiplied by, one number after the other.  Where a norm is so far beyond its
+// limit that the factor is no normal 32-bit number, rounding it would take its bits, or all of
+// it: it is cut in two there, 2^-126 and a number that is not above 1.  The first product is exact, or
+// below the normal range, where the second one is then too.
 struct Factor {
-    double exact;
-    float by;
-    bool below;
+    float first, by;
 
-    __device__ __forceinline__ explicit Factor(double c) : exact(c), by(static_cast<float>(c)), below(c != 0.0 && fabs(c) < kLeastNormal) {}
-    template <typename T> __device__ __forceinline__ T far(T x) const { return from_f32<T>(static_cast<float>(to_f32(x) * exact)); }
-    template <typename T> __device__ __forceinline__ T near(T x) const { return from_f32<T>(to_f32(x) * by); }
+    __device__ __forceinline__ void set(double c) {
+        const bool low = fabs(c) < kLeastNormal && c != 0.0;
+        first = low ? static_cast<float>(kLeastNormal) : 1.0f;
+        by = static_cast<float>(low ? c * (1.0 / kLeastNormal) : c);
+    }
+    __device__ __forceinline__ bool one() const { return first == 1.0f && by == 1.0f; }
+    __device__ __forceinline__ float of(float x) const { return x * first * by; }
+    __device__ __forceinline__ Pair of(Pair x) const { return mul2(mul2(x, pair(first, first)), pair(by, by)); }
 };
 
 template <typename T> __device__ __forceinline__ void scale_step(const Step &s, const uint4 *data, void *tensor, const Factor &c) {
     constexpr int N = Wide<T>::kCount;
     char *to = static_cast<char *>(tensor) + s.begin;
-    const T *from = reinterpret_cast<const T *>(data);
-    T *single = reinterpret_cast<T *>(to);
-    if (c.below) {
-        for (uint32_t i = threadIdx.x; i < s.vectors * N; i += kNormThreads) single[i] = c.far(from[i]);
-        return;
-    }
     if ((reinterpret_cast<uintptr_t>(to) & 15) != 0) {         // the output lies differently
-        for (uint32_t i = threadIdx.x; i < s.vectors * N; i += kNormThreads) single[i] = c.near(from[i]);
+        const T *from = reinterpret_cast<const T *>(data);
+        for (uint32_t i = threadIdx.x; i < s.vectors * N; i += kNormThreads) reinterpret_cast<T *>(to)[i] = from_f32<T>(c.of(to_f32(from[i])));
         return;
     }
-    const float by = c.by;
 #pragma unroll
     for (int u = 0; u < kNormVectors; ++u) {
         const uint32_t v = threadIdx.x + u * kNormThreads;
         if (v >= s.vectors) break;
         uint4 q = data[v];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, mul2(Wide<T>::pair_of(q, i), pair(by, by)));
+        for (int i = 0; i < N / 2; ++i) Wide<T>::set_pair(q, i, c.of(Wide<T>::pair_of(q, i)));
         reinterpret_cast<uint4 *>(to)[v] = q;
     }
 }
 
-// A step whose gradients did not come: its results are no numbers.
-__device__ __forceinline__ void void_step(const Step &s, void *tensor) {
-    uint16_t *to = reinterpret_cast<uint16_t *>(static_cast<char *>(tensor) + s.begin);
-    for (uint32_t i = threadIdx.x; i < s.vectors * 8; i += kNormThreads) to[i] = 0x7FFF;
+// The gradients of step k and behind did not come: results are no numbers, but for tensors that
+// stay as they are (`same`: those that are their own output).
+template <int M> __device__ __forceinline__ void void_rest(Ring<M, true> &ring, uint32_t k, bool same) {
+    ring.rest(k, [&](const Step &s) {
+        if (s.vectors == 0 || (same && ring.t.in[s.tensor] == ring.t.out[s.tensor])) return;
+        uint16_t *to = reinterpret_cast<uint16_t *>(static_cast<char *>(ring.t.out[s.tensor]) + s.begin);
+        for (uint32_t i = threadIdx.x; i < s.vectors * 8; i += kNormThreads) to[i] = 0x7FFF;
+    });
 }
 
 // norm_out holds 0 before.  Its bits are only raised, so that the NaN of a CTA whose copies did not come
@@ -323,20 +328,24 @@ k_clip(const __grid_constant__ TensorTable<M> t, const double *slots, uint32_t c
     Ring<M, true> ring = make_ring<M, true>(t);
     ring.start();            // the gradients were there before the sums
     wait_for_last();
-    const double norm = norm_of(slots, count, scale);
+    __shared__ Factor s_factor;
+    const double squares = sum_of(slots, count);
     uint32_t *const norm_bits = reinterpret_cast<uint32_t *>(norm_out);
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicMax(norm_bits, __float_as_uint(static_cast<float>(norm)));
-    // NaN stays: a gradient that is no number must not look like one
-    const double part = norm > max_norm ? max_norm / norm : norm == norm ? 1.0 : norm;
-    const Factor c(scale * part);
-    auto changes = [&](uint32_t tensor) { return c.by != 1.0f || t.in[tensor] != t.out[tensor]; };     // else it is as it has to be
+    if (threadIdx.x == 0) {  // 64-bit operations are slow: 2^24 f32 elements in 300 tensors take 38.9 us so, 44.0 where every thread does them
+        const double norm = norm_of(squares, scale);
+        if (blockIdx.x == 0) atomicMax(norm_bits, __float_as_uint(static_cast<float>(norm)));
+        // NaN stays: a gradient that is no number must not look like one
+        const double part = norm > max_norm ? max_norm / norm : norm == norm ? 1.0 : norm;
+        s_factor.set(scale * part);
+    }
+    __syncthreads();
+    const Factor c = s_factor;
+    auto changes = [&](uint32_t tensor) { return !c.one() || t.in[tensor] != t.out[tensor]; };     // else it is as it has to be
     for_ends(t, [&](uint32_t tensor, uint32_t type, uint64_t first, uint32_t n) {
         with_type(type, [&](auto *p) {
             using T = std::remove_pointer_t<decltype(p)>;
-            for (uint32_t k = 0; changes(tensor) && k < n; ++k) {
-                const T x = static_cast<const T *>(t.in[tensor])[first + k];
-                static_cast<T *>(t.out[tensor])[first + k] = c.below ? c.far(x) : c.near(x);
-            }
+            for (uint32_t k = 0; changes(tensor) && k < n; ++k)
+                static_cast<T *>(t.out[tensor])[first + k] = from_f32<T>(c.of(to_f32(static_cast<const T *>(t.in[tensor])[first + k])));
         });
     });
     const uint32_t lost = ring.run(waits.of_cta(), [&](const Step &s, const uint4 *data) {
@@ -345,9 +354,7 @@ k_clip(const __grid_constant__ TensorTable<M> t, const double *slots, uint32_t c
     });
     if (lost == kAll) return;
     if (threadIdx.x == 0) atomicMax(norm_bits, 0x7FC00000u);
-    ring.rest(lost, [&](const Step &s) {
-        if (s.vectors > 0 && changes(s.tensor)) void_step(s, t.out[s.tensor]);
-    });
+    void_rest(ring, lost, c.one());
 }
 
 // The tensors from `at` on, as many as fit, and how many of the list they are.

@@ -20,10 +20,12 @@
 // written anew.  In place, vectors in which nothing is masked are neither read nor written.
 //
 // The memory bounds large calls: logits in, logits out.  2048 x 131072 bf16 with histories of 1024,
-// 64 biases and a mask take 183 us (6.1 TB/s of what is counted so), their gradient 184; 64 x
-// 131072 f32 with histories of 2048 16.4 us, of which 15 are what a copy with this grid takes.  Long
-// histories take longer than the logits: 256 x 100003 bf16 with 16384 tokens 53 us, the memory's
+// 64 biases and a mask take 376 us with their gradient (5.8 TB/s of what is counted so); 64 x
+// 131072 f32 with histories of 2048 16.4 us, of which 13.5 are what the call takes with nothing to adjust.  Long
+// histories take longer than the logits: 256 x 100003 bf16 with 16384 tokens 54 us, the memory's
 // part 18: an SM has two rows one after the other, and writes the named tokens of one before the next begins.
+// In place, what is masked is read too, behind the mask's words: where a grammar leaves one token of
+// 1000, 64 x 131072 f32 take 20.6 us in place and 14.5 with an output of their own.
 #include <algorithm>
 
 #include "model_ops.cuh"
@@ -559,8 +561,9 @@ int launch_adjust(const AdjustLaunch &L) {
             a.history_whole = L.length <= kChunks * kChunk;
             while (!fits()) tokens = (tokens / 2 + 255) / 256 * 256;
         }
-        // what is named takes longer where the history is long (256 x 100003 bf16, histories of 16384: 63 us
-        // with a quarter of the threads for the logits, 66 with half; 2048 x 131072 with 1024: 386 and 377)
+        // what is named takes longer where the history is long (256 x 100003 bf16, histories of 16384: 57 us
+        // with a quarter of 1024 threads for the logits, 59 with half; 2048 x 131072 with 1024 and its
+        // gradient: 376 with half of 512, 385 with a quarter; graph replays)
         a.streamers = !history && !biases ? threads : threads == 1024 ? threads / 4 : threads / 2;
         const size_t sets = set_bytes(), stage = stage_bytes();
         if (ring) {

@@ -12,10 +12,10 @@
 // runs (in a text one position in twenty may hold the same token), rare ones a run
 // of one position, and a piece costs the same either way.  Within a piece a group
 // of lanes walks its positions with several rows' loads in flight; runs that cross
-// its ends leave partial sums, which are joined in shared memory within a CTA and
-// through the workspace between CTAs, always in the order of the positions.  Every
-// row of d_out is read once and every row of d_table written once, so the memory
-// bounds it: 65536 rows of 4096 bf16 into 131072 take 270 us (6.0 TB/s), their
+// its ends leave partial sums, which are joined in shared memory within a CTA, in the
+// order of the positions, and through the workspace between CTAs, in an order that is
+// fixed as well (below).  Every row of d_out is read once and every row of d_table
+// written once, so the memory bounds it: 65536 rows of 4096 bf16 into 131072 take 270 us (6.0 TB/s), their
 // lookup 111 (6.3).  Sums are 32-bit, rounded once.  Rows of tokens that do not
 // occur are filled with zeros while the tokens are sorted, which takes few SMs, and
 // while the sums run.
@@ -506,7 +506,8 @@ __global__ void __launch_bounds__(kEmbedThreads, 4) k_embed_sum(const EmbedSumAr
         else if (v < a.vectors) sum.write(a, key, v);
     }
     // A run that crosses ends of chunks has a part in each of them.  The CTA that
-    // writes the last of these joins them, in their order.
+    // writes the last of these joins them: each group of lanes every units-th part, then the
+    // groups' sums one after the other.  Tokens and sizes give that order, not the CTAs' times.
     const uint32_t front = s_key[1], back = s_key[count], next = s_key[count + 1];
     const bool before = s_key[0] == front && front < a.vocab;
     const bool behind = next == back && back < a.vocab;

@@ -16,8 +16,9 @@
 //
 // The memory bounds both kernels.  Clipping reads everything twice, as the norm has to be
 // known before the first product; it takes the chunks backwards, so that what was
-// read last comes from the caches.  2^30 bf16 elements in 200 tensors: norm 315 us (6.8 TB/s),
-// clipping 1000 us in all (6.4 TB/s of three passes).
+// read last comes from the caches.  2^30 bf16 elements in 200 tensors: norm 312 us (6.9 TB/s),
+// clipping 990 us in all (6.5 TB/s of three passes).  In place and not clipped nothing is written, but
+// all is read twice: 615 us.
 #include <algorithm>
 #include <cmath>
 

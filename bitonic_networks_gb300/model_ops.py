@@ -297,7 +297,8 @@ def embed_tokens_backward(d_out: torch.Tensor, tokens: torch.Tensor, vocab: int,
                           workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of embed_tokens by its table of `vocab` rows, for d_out
     [*tokens.shape, width] (contiguous; with tokens of one dimension its rows may
-    be strided): each token's rows summed in 32 bits in their order, times scale.
+    be strided): each token's rows summed in 32 bits, in an order that tokens and sizes
+    give (the same from call to call), times scale.
     Rows of tokens that do not occur are zero.  With accumulate the sums are added
     to `out` [vocab, width], whose other rows stay as they are.  An `out` that
     requires a gradient raises RuntimeError where gradients are recorded."""
@@ -344,7 +345,8 @@ def adjust_logits(logits: torch.Tensor, *, history: torch.Tensor | None = None, 
     has bit v % 32 of word v // 32 set where token v may follow; the others become
     -inf, which token_logprobs takes as masked.
 
-    history, biases and allowed may be expanded from one row.  `out` may be the
+    For biases before the penalties, make two calls: one with the biases, then one
+    in place with the rest.  history, biases and allowed may be expanded from one row.  `out` may be the
     logits themselves, which are then written only where they change; it takes
     part in no gradient (RuntimeError where gradients are recorded and the logits or
     `out` require one).  The result has a gradient by the logits; the adjustments

@@ -257,3 +257,25 @@ def test_the_norm_is_as_near_as_a_steps_sums_allow(dtype, value, n):
     near = ((3 if dtype == torch.float32 else 5) + 1) * U32 * 1.0001         # the rest is of second order
     assert abs(float(gs.gradient_norm([t])) - want) <= near * want
     assert abs(float(gs.clip_gradients([t], 1.0).norm) - want) <= near * want
+
+
+@pytest.mark.parametrize("count", [3, 1200])
+def test_replays_on_smaller_gradients(count):
+    """Each replay gives the norm of what is there then, not of what was there before."""
+    tensors = [torch.randn(5000, device="cuda") for _ in range(count)]
+    out = [torch.empty_like(t) for t in tensors]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gs.clip_gradients(tensors, 1.0, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = gs.clip_gradients(tensors, 1.0, out=out)
+    for by in (1.0, 1e-3, 0.0, float("nan"), 1.0):
+        for t in tensors:
+            t.normal_().mul_(by)
+        graph.replay()
+        want = gs.clip_gradients(tensors, 1.0)
+        assert torch.equal(held.norm.view(torch.int32), want.norm.view(torch.int32))
+        assert all(torch.equal(a.view(torch.int32), b.view(torch.int32)) for a, b in zip(out, want.gradients))
